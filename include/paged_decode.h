@@ -626,6 +626,128 @@ PA_API int quest_decode_fp8_block(pa_bf16 *out, int32_t *selected, const pa_bf16
                                   int topk, float scale, int max_ctas, void *workspace,
                                   size_t workspace_bytes, void *stream);
 
+/* --------------------------------- decode over a part of the cache ----
+ * Three additions next to the dense and the Quest decode: attention over a
+ * sliding window with visible first tokens, attention of a batch over shared
+ * prefixes, and eviction by accumulated attention weight. Layouts, block
+ * tables, masking of bad metadata, workspaces (zero-filled once; calls that
+ * overlap in time need different ones; pa_workspace_status reads their
+ * status) and errors as pa_decode; scale must be finite. */
+
+/* Sliding-window decode: as pa_decode, but sequence b's query sees only the
+ * tokens t < ctx_b with
+ *     t < sinks   or   t >= ctx_b - window
+ * (its first `sinks` tokens and its last `window` ones, the newest token
+ * included). window >= 1, sinks >= 0; with window >= ctx_b it is pa_decode.
+ * Table entries of blocks that hold no visible token are not used, so those
+ * blocks may have been freed (entry -1). */
+PA_API size_t pa_decode_window_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim);
+
+PA_API int pa_decode_window(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *key_cache,
+                            const pa_bf16 *value_cache, const int32_t *block_tables, int max_blocks_per_seq,
+                            const int32_t *context_lens, int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                            int block_size, int64_t num_blocks, int window, int sinks, float scale, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* pa_decode_window over an 8-bit cache with per-KV-head scales (as
+ * pa_decode_fp8). Workspace: pa_decode_window_workspace_size. */
+PA_API int pa_decode_window_fp8(pa_bf16 *out, const pa_bf16 *query, const pa_e4m3 *key_cache,
+                                const pa_e4m3 *value_cache, const float *k_scale, const float *v_scale,
+                                const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                                int batch, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                int64_t num_blocks, int window, int sinks, float scale, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/* pa_decode_window over an 8-bit cache with per-block scales (as
+ * pa_decode_fp8_block). */
+PA_API int pa_decode_window_fp8_block(pa_bf16 *out, const pa_bf16 *query, const pa_e4m3 *key_cache,
+                                      const pa_e4m3 *value_cache, const float *k_bscale, const float *v_bscale,
+                                      const int32_t *block_tables, int max_blocks_per_seq,
+                                      const int32_t *context_lens, int batch, int num_q_heads, int num_kv_heads,
+                                      int head_dim, int block_size, int64_t num_blocks, int window, int sinks,
+                                      float scale, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Several query rows per sequence, from speculative tokens to prefill chunks:
+ * rows and cu_seqlens_q as pa_decode_multi. Row i of sequence b sees the
+ * tokens t < lim with t < sinks or t >= lim - window, where
+ * lim = context_lens[b] - q_len + i + 1; a row with lim <= 0 gets a zero
+ * output; rows of no sequence (total_q > cu_seqlens_q[batch]) are left as
+ * they are. total_q <= 1048576, batch <= 4096; a malformed cu_seqlens_q
+ * gives undefined rows, never a fault. bf16 cache. */
+PA_API size_t pa_decode_window_multi_workspace_size(int batch, int total_q, int num_q_heads, int num_kv_heads,
+                                                    int head_dim);
+
+PA_API int pa_decode_window_multi(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *key_cache,
+                                  const pa_bf16 *value_cache, const int32_t *block_tables, int max_blocks_per_seq,
+                                  const int32_t *cu_seqlens_q, const int32_t *context_lens, int batch, int total_q,
+                                  int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                  int64_t num_blocks, int window, int sinks, float scale, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+/* Decode attention of a batch whose sequences share long prefixes (one query
+ * token per sequence): sequences cu_group[g] .. cu_group[g+1]-1 form group g
+ * and all begin with the same prefix_lens[g] tokens, which are in the blocks
+ * prefix_tables[g][0..max_prefix_blocks). Sequence b sees its group's prefix
+ * and then its own tokens t < context_lens[b], in the blocks of
+ * block_tables[b] (which do not repeat the prefix's). The prefix length need
+ * not be a multiple of the block size. A group's prefix is read once for all
+ * its sequences. cu_group is [num_groups + 1] int32 on the device, ascending
+ * from 0; a sequence of no group has no prefix; a sequence with neither
+ * prefix nor own tokens gets a zero output. num_groups <= 4096. bf16 cache. */
+PA_API size_t pa_decode_prefix_workspace_size(int batch, int num_groups, int num_q_heads, int num_kv_heads,
+                                              int head_dim);
+
+PA_API int pa_decode_prefix(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *key_cache,
+                            const pa_bf16 *value_cache, const int32_t *prefix_tables, int max_prefix_blocks,
+                            const int32_t *prefix_lens, const int32_t *cu_group, int num_groups,
+                            const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                            int batch, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                            int64_t num_blocks, float scale, void *workspace, size_t workspace_bytes, void *stream);
+
+/* pa_decode that also adds up the attention every cached token receives:
+ *   weights[p][g][o] += sum over the query heads h of KV head g of
+ *                       softmax_t(scale * query[b][h] . K[b][t])   at token t
+ * for every sequence b and token t < context_lens[b] at block
+ * p = block_tables[b][t / BS], offset o = t % BS. weights is [NB][Hkv][BS]
+ * fp32, 16-byte aligned, kept by the caller beside the cache. Blocks that
+ * several sequences share receive the sum over them (in no fixed order, so
+ * the last bits may differ between calls). bf16 cache. */
+PA_API size_t pa_decode_weights_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                                               int max_blocks_per_seq);
+
+PA_API int pa_decode_weights(pa_bf16 *out, float *weights, const pa_bf16 *query, const pa_bf16 *key_cache,
+                             const pa_bf16 *value_cache, const int32_t *block_tables, int max_blocks_per_seq,
+                             const int32_t *context_lens, int batch, int num_q_heads, int num_kv_heads,
+                             int head_dim, int block_size, int64_t num_blocks, float scale, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/* The weights of newly written tokens: weights[slot / BS][g][slot % BS] = 0
+ * for every slot of one ReshapeAndCache call (same skip rules). */
+PA_API int pa_reset_weights(float *weights, const int64_t *slot_mapping, int64_t num_tokens, int num_kv_heads,
+                            int block_size, int64_t num_blocks, void *stream);
+
+/* Eviction: of each sequence's n = context_lens[b] tokens, at most `budget`
+ * are kept per KV head: all if n <= budget, else the min(recent, budget)
+ * newest ones and, of the others, those with the largest weights (compared in
+ * IEEE totalOrder, ties to the lower position). KV heads keep different
+ * tokens. Per KV head the kept tokens, in ascending order of position, are
+ * copied to positions 0, 1, ... of the sequence's destination blocks
+ * dst_tables[b][0..max_dst_blocks): K and V rows and weights. Written besides:
+ *   kept     [B][Hkv][budget] int32: their old positions, padded with -1;
+ *   new_lens [B] int32: min(n, budget), the sequence's new length.
+ * After the call the sequence continues on its destination blocks (a Quest
+ * cache: after quest_rebuild_meta on them) and its old ones can be freed.
+ * No destination block may be a source block of the call (context_lens
+ * tokens of any sequence) or another destination, and new_lens may not be
+ * context_lens; destination slots from position new_lens[b] on are left as
+ * they are. Tokens of a block whose table entry is outside the pool count as
+ * smaller than every weight; rows from or to such blocks are not copied.
+ * max_dst_blocks * block_size >= budget. bf16 cache; no workspace. */
+PA_API int pa_evict(int32_t *kept, int32_t *new_lens, pa_bf16 *key_cache, pa_bf16 *value_cache, float *weights,
+                    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                    const int32_t *dst_tables, int max_dst_blocks, int batch, int num_kv_heads, int head_dim,
+                    int block_size, int64_t num_blocks, int budget, int recent, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

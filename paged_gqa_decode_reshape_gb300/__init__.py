@@ -11,8 +11,11 @@ Names follow the C ABI: ``pa_reshape_and_cache``, ``pa_decode``,
 ``quest_update_meta``, ``quest_reshape_and_cache`` (both write steps in one
 launch), ``quest_rebuild_meta``, ``quest_select_topk``,
 ``quest_sparse_decode``; ``pa_decode_multi`` for several query rows per
-sequence; the ``*_fp8`` variants for an 8-bit (E4M3) cache; plus the
-workspace-size queries and checks.
+sequence; the ``*_fp8`` variants for an 8-bit (E4M3) cache;
+``pa_decode_window`` (``_multi``, ``_fp8``, ``_fp8_block``) over a sliding
+window and first tokens; ``pa_decode_prefix`` over shared prefixes;
+``pa_decode_weights``, ``pa_reset_weights`` and ``pa_evict`` for eviction by
+accumulated attention weight; plus the workspace-size queries and checks.
 """
 
 from __future__ import annotations
@@ -45,6 +48,10 @@ __all__ = [
     "pa_reshape_and_cache_fp8_block", "quest_reshape_and_cache_fp8_block", "quest_select_topk_fp8_block",
     "pa_decode_fp8_block", "pa_decode_fp8_block_budget", "quest_sparse_decode_fp8_block", "quest_decode_fp8_block",
     "pa_reshape_and_decode", "quest_reshape_and_decode",
+    "pa_decode_window_workspace_size", "pa_decode_window", "pa_decode_window_fp8", "pa_decode_window_fp8_block",
+    "pa_decode_window_multi_workspace_size", "pa_decode_window_multi",
+    "pa_decode_prefix_workspace_size", "pa_decode_prefix",
+    "pa_decode_weights_workspace_size", "pa_decode_weights", "pa_reset_weights", "pa_evict",
     "pa_workspace_status", "pa_check_metadata", "Workspace",
 ]
 
@@ -165,6 +172,35 @@ def load_library(path: Optional[str] = None):
         L.quest_sparse_decode_fp8_block.restype = i32
         L.quest_decode_fp8_block.argtypes = L.quest_decode_fp8.argtypes
         L.quest_decode_fp8_block.restype = i32
+        L.pa_decode_window_workspace_size.argtypes = [i32, i32, i32, i32]
+        L.pa_decode_window_workspace_size.restype = sz
+        L.pa_decode_window.argtypes = [vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i64, i32, i32, f32,
+                                       vp, sz, vp]
+        L.pa_decode_window.restype = i32
+        L.pa_decode_window_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i64, i32,
+                                           i32, f32, vp, sz, vp]
+        L.pa_decode_window_fp8.restype = i32
+        L.pa_decode_window_fp8_block.argtypes = L.pa_decode_window_fp8.argtypes
+        L.pa_decode_window_fp8_block.restype = i32
+        L.pa_decode_window_multi_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+        L.pa_decode_window_multi_workspace_size.restype = sz
+        L.pa_decode_window_multi.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, i64,
+                                             i32, i32, f32, vp, sz, vp]
+        L.pa_decode_window_multi.restype = i32
+        L.pa_decode_prefix_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+        L.pa_decode_prefix_workspace_size.restype = sz
+        L.pa_decode_prefix.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, i32, vp, i32, vp, i32, i32, i32, i32, i32,
+                                       i64, f32, vp, sz, vp]
+        L.pa_decode_prefix.restype = i32
+        L.pa_decode_weights_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+        L.pa_decode_weights_workspace_size.restype = sz
+        L.pa_decode_weights.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i64, f32, vp, sz,
+                                        vp]
+        L.pa_decode_weights.restype = i32
+        L.pa_reset_weights.argtypes = [vp, vp, i64, i32, i32, i64, vp]
+        L.pa_reset_weights.restype = i32
+        L.pa_evict.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i64, i32, i32, vp]
+        L.pa_evict.restype = i32
         _lib = L
         return _lib
 
@@ -1015,3 +1051,248 @@ def quest_reshape_and_decode(out: torch.Tensor, selected: torch.Tensor, query: t
                                                *a[3:])
     return _quest_decode(fn, "quest_reshape_and_decode", out, selected, query, kmin, kmax, key_cache,
                          value_cache, block_tables, context_lens, topk, scale, max_ctas, workspace, (), checks)
+
+
+# ------------------------------------------- decode over a part of the cache
+
+
+class _Scratch(Workspace):
+    """A Workspace for calls that may be captured into CUDA graphs: a buffer
+    that has been handed out is kept for good (a captured graph may hold its
+    address), and none is allocated during a capture."""
+
+    def __init__(self):
+        super().__init__()
+        self._kept = []
+
+    def get(self, device: torch.device, nbytes: int) -> torch.Tensor:
+        key = device.index if device.index is not None else torch.cuda.current_device()
+        buf = self._buf.get(key)
+        if buf is not None and buf.numel() >= nbytes:
+            return buf
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError(f"no workspace of {nbytes} bytes yet: make one such call before the capture, or pass "
+                               "workspace=")
+        if buf is not None:
+            self._kept.append(buf)
+        # grown by half as much again, so that growing step by step keeps few buffers
+        n = max(nbytes, 256, buf.numel() * 3 // 2 if buf is not None else 0)
+        self._buf[key] = torch.zeros(n, dtype=torch.uint8, device=device)
+        return self._buf[key]
+
+
+_subset_ws = _Scratch()
+
+
+def _tokens(n, name: str) -> int:
+    """A token count for the C ABI; anything above int32 is no limit at all."""
+    n = int(n)
+    if n < 0:
+        raise ValueError(f"{name} must not be negative")
+    return min(n, 2 ** 31 - 1)
+
+
+def _scratch(workspace: Optional[torch.Tensor], dev: torch.device, nbytes: int):
+    """(pointer, bytes) of the caller's workspace or of the binding's own."""
+    if workspace is None:
+        workspace = _subset_ws.get(dev, nbytes)
+    else:
+        if not isinstance(workspace, torch.Tensor):
+            raise TypeError("workspace must be a torch.Tensor")
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def pa_decode_window_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    return int(load_library().pa_decode_window_workspace_size(batch, num_q_heads, num_kv_heads, head_dim))
+
+
+def pa_decode_window_multi_workspace_size(batch: int, total_q: int, num_q_heads: int, num_kv_heads: int,
+                                          head_dim: int) -> int:
+    return int(load_library().pa_decode_window_multi_workspace_size(batch, total_q, num_q_heads, num_kv_heads,
+                                                                    head_dim))
+
+
+def pa_decode_prefix_workspace_size(batch: int, num_groups: int, num_q_heads: int, num_kv_heads: int,
+                                    head_dim: int) -> int:
+    return int(load_library().pa_decode_prefix_workspace_size(batch, num_groups, num_q_heads, num_kv_heads, head_dim))
+
+
+def pa_decode_weights_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                     max_blocks_per_seq: int) -> int:
+    return int(load_library().pa_decode_weights_workspace_size(batch, num_q_heads, num_kv_heads, head_dim,
+                                                               max_blocks_per_seq))
+
+
+def pa_decode_window(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Tensor,
+                     block_tables: torch.Tensor, context_lens: torch.Tensor, window: int, sinks: int, scale: float,
+                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Decode attention over each sequence's first `sinks` and last `window` tokens; writes out [B, Hq, D] (bf16)."""
+    L = load_library()
+    dev, B, Hq, Hkv, D, BS, NB, MBS = _attention_checks(out, query, key_cache, value_cache, block_tables,
+                                                        context_lens)
+    window, sinks = _tokens(window, "window"), _tokens(sinks, "sinks")
+    with torch.cuda.device(dev):
+        ws, nbytes = _scratch(workspace, dev, L.pa_decode_window_workspace_size(B, Hq, Hkv, D))
+        _check("pa_decode_window",
+               L.pa_decode_window(_ptr(out), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(block_tables), MBS,
+                                  _ptr(context_lens), B, Hq, Hkv, D, BS, NB, window, sinks, float(scale),
+                                  ws, nbytes, _stream(dev)))
+    return out
+
+
+def _window_fp8(name, per_block, out, query, key_cache, value_cache, k_scale, v_scale, block_tables, context_lens,
+                window, sinks, scale, workspace):
+    L = load_library()
+    dev, B, Hq, Hkv, D, BS, NB, MBS = _attention_checks_fp8(out, query, key_cache, value_cache, block_tables,
+                                                            context_lens, k_scale, v_scale, per_block)
+    window, sinks = _tokens(window, "window"), _tokens(sinks, "sinks")
+    with torch.cuda.device(dev):
+        ws, nbytes = _scratch(workspace, dev, L.pa_decode_window_workspace_size(B, Hq, Hkv, D))
+        _check(name, getattr(L, name)(_ptr(out), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(k_scale),
+                                      _ptr(v_scale), _ptr(block_tables), MBS, _ptr(context_lens), B, Hq, Hkv, D, BS,
+                                      NB, window, sinks, float(scale), ws, nbytes, _stream(dev)))
+    return out
+
+
+def pa_decode_window_fp8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Tensor,
+                         k_scale: torch.Tensor, v_scale: torch.Tensor, block_tables: torch.Tensor,
+                         context_lens: torch.Tensor, window: int, sinks: int, scale: float,
+                         workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """pa_decode_window over an 8-bit cache with per-KV-head scales."""
+    return _window_fp8("pa_decode_window_fp8", False, out, query, key_cache, value_cache, k_scale, v_scale,
+                       block_tables, context_lens, window, sinks, scale, workspace)
+
+
+def pa_decode_window_fp8_block(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                               value_cache: torch.Tensor, k_bscale: torch.Tensor, v_bscale: torch.Tensor,
+                               block_tables: torch.Tensor, context_lens: torch.Tensor, window: int, sinks: int,
+                               scale: float, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """pa_decode_window over an 8-bit cache with per-block scales."""
+    return _window_fp8("pa_decode_window_fp8_block", True, out, query, key_cache, value_cache, k_bscale, v_bscale,
+                       block_tables, context_lens, window, sinks, scale, workspace)
+
+
+def pa_decode_window_multi(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                           value_cache: torch.Tensor, block_tables: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                           context_lens: torch.Tensor, window: int, sinks: int, scale: float,
+                           workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Windowed attention of several query rows per sequence: query / out [total_q, Hq, D], rows of sequence b
+    cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1, right-aligned causal masks."""
+    L = load_library()
+    _need(key_cache, "key_cache", torch.bfloat16, 4)
+    dev = key_cache.device
+    _need(value_cache, "value_cache", torch.bfloat16, 4, dev)
+    _need(query, "query", torch.bfloat16, 3, dev)
+    _need(out, "out", torch.bfloat16, 3, dev)
+    T, Hq, D = query.shape
+    NB, BS, Hkv, D2 = key_cache.shape
+    if D != D2 or value_cache.shape != key_cache.shape or out.shape != query.shape:
+        raise ValueError("shape mismatch between query/out and the caches")
+    _need(block_tables, "block_tables", torch.int32, 2, dev)
+    _need(context_lens, "context_lens", torch.int32, 1, dev)
+    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1, dev)
+    B, MBS = block_tables.shape
+    if context_lens.shape[0] != B or cu_seqlens_q.shape[0] != B + 1:
+        raise ValueError("block_tables / context_lens / cu_seqlens_q batch mismatch")
+    window, sinks = _tokens(window, "window"), _tokens(sinks, "sinks")
+    with torch.cuda.device(dev):
+        ws, nbytes = _scratch(workspace, dev, L.pa_decode_window_multi_workspace_size(B, T, Hq, Hkv, D))
+        _check("pa_decode_window_multi",
+               L.pa_decode_window_multi(_ptr(out), _ptr(query), _ptr(key_cache), _ptr(value_cache),
+                                        _ptr(block_tables), MBS, _ptr(cu_seqlens_q), _ptr(context_lens), B, T, Hq,
+                                        Hkv, D, BS, NB, window, sinks, float(scale), ws, nbytes,
+                                        _stream(dev)))
+    return out
+
+
+def pa_decode_prefix(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Tensor,
+                     prefix_tables: torch.Tensor, prefix_lens: torch.Tensor, cu_group: torch.Tensor,
+                     block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Decode attention of a batch with shared prefixes: sequences cu_group[g] .. cu_group[g + 1] - 1 see the
+    prefix_lens[g] tokens of prefix_tables[g], then their own context_lens[b] tokens of block_tables[b]."""
+    L = load_library()
+    dev, B, Hq, Hkv, D, BS, NB, MBS = _attention_checks(out, query, key_cache, value_cache, block_tables,
+                                                        context_lens)
+    _need(prefix_tables, "prefix_tables", torch.int32, 2, dev)
+    _need(prefix_lens, "prefix_lens", torch.int32, 1, dev)
+    _need(cu_group, "cu_group", torch.int32, 1, dev)
+    NG, PMBS = prefix_tables.shape
+    if prefix_lens.shape[0] != NG or cu_group.shape[0] != NG + 1:
+        raise ValueError("prefix_tables / prefix_lens / cu_group mismatch")
+    with torch.cuda.device(dev):
+        ws, nbytes = _scratch(workspace, dev, L.pa_decode_prefix_workspace_size(B, NG, Hq, Hkv, D))
+        _check("pa_decode_prefix",
+               L.pa_decode_prefix(_ptr(out), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(prefix_tables),
+                                  PMBS, _ptr(prefix_lens), _ptr(cu_group), NG, _ptr(block_tables), MBS,
+                                  _ptr(context_lens), B, Hq, Hkv, D, BS, NB, float(scale), ws, nbytes, _stream(dev)))
+    return out
+
+
+def _need_weights(weights, NB, Hkv, BS, dev):
+    _need(weights, "weights", torch.float32, 3, dev)
+    if weights.shape != (NB, Hkv, BS):
+        raise ValueError("weights must be [NB, Hkv, BS]")
+
+
+def pa_decode_weights(out: torch.Tensor, weights: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                      value_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                      scale: float, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """pa_decode that also adds each cached token's attention weight, summed over its KV head's query heads, to
+    weights [NB, Hkv, BS] (fp32)."""
+    L = load_library()
+    dev, B, Hq, Hkv, D, BS, NB, MBS = _attention_checks(out, query, key_cache, value_cache, block_tables,
+                                                        context_lens)
+    _need_weights(weights, NB, Hkv, BS, dev)
+    with torch.cuda.device(dev):
+        ws, nbytes = _scratch(workspace, dev, L.pa_decode_weights_workspace_size(B, Hq, Hkv, D, MBS))
+        _check("pa_decode_weights",
+               L.pa_decode_weights(_ptr(out), _ptr(weights), _ptr(query), _ptr(key_cache), _ptr(value_cache),
+                                   _ptr(block_tables), MBS, _ptr(context_lens), B, Hq, Hkv, D, BS, NB, float(scale),
+                                   ws, nbytes, _stream(dev)))
+    return out
+
+
+def pa_reset_weights(weights: torch.Tensor, slot_mapping: torch.Tensor) -> None:
+    """Zero the accumulated weights [NB, Hkv, BS] of a write's slots."""
+    L = load_library()
+    _need(weights, "weights", torch.float32, 3)
+    dev = weights.device
+    _need(slot_mapping, "slot_mapping", torch.int64, 1, dev)
+    NB, Hkv, BS = weights.shape
+    with torch.cuda.device(dev):
+        _check("pa_reset_weights",
+               L.pa_reset_weights(_ptr(weights), _ptr(slot_mapping), slot_mapping.shape[0], Hkv, BS, NB,
+                                  _stream(dev)))
+
+
+def pa_evict(kept: torch.Tensor, new_lens: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Tensor,
+             weights: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+             dst_tables: torch.Tensor, recent: int) -> None:
+    """Keep at most kept.shape[2] tokens per (sequence, KV head), the `recent` newest and the largest weights of the
+    rest, and copy them to the blocks of dst_tables; writes kept [B, Hkv, budget] and new_lens [B]."""
+    L = load_library()
+    _need(key_cache, "key_cache", torch.bfloat16, 4)
+    dev = key_cache.device
+    _need(value_cache, "value_cache", torch.bfloat16, 4, dev)
+    NB, BS, Hkv, D = key_cache.shape
+    _need_weights(weights, NB, Hkv, BS, dev)
+    _need(block_tables, "block_tables", torch.int32, 2, dev)
+    _need(context_lens, "context_lens", torch.int32, 1, dev)
+    _need(dst_tables, "dst_tables", torch.int32, 2, dev)
+    _need(kept, "kept", torch.int32, 3, dev)
+    _need(new_lens, "new_lens", torch.int32, 1, dev)
+    B, MBS = block_tables.shape
+    if value_cache.shape != key_cache.shape:
+        raise ValueError("shape mismatch between the caches")
+    if context_lens.shape[0] != B or dst_tables.shape[0] != B or new_lens.shape[0] != B or kept.shape[:2] != (B, Hkv):
+        raise ValueError("block_tables / context_lens / dst_tables / kept / new_lens mismatch")
+    if new_lens.data_ptr() == context_lens.data_ptr():
+        raise ValueError("new_lens must not be context_lens")
+    with torch.cuda.device(dev):
+        _check("pa_evict",
+               L.pa_evict(_ptr(kept), _ptr(new_lens), _ptr(key_cache), _ptr(value_cache), _ptr(weights),
+                          _ptr(block_tables), MBS, _ptr(context_lens), _ptr(dst_tables), dst_tables.shape[1], B, Hkv,
+                          D, BS, NB, kept.shape[2], _tokens(recent, "recent"), _stream(dev)))

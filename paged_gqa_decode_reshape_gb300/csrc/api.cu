@@ -7,6 +7,7 @@
 
 #include "../../include/paged_decode.h"
 #include "kernels.h"
+#include "subset.h"
 
 using namespace pa;
 
@@ -813,3 +814,233 @@ extern "C" PA_API void pa_fault_test_configure(int stop_item, uint64_t wait_ns) 
     g_stop_item.store(stop_item < 0 ? INT_MAX : stop_item, std::memory_order_relaxed);
 }
 #endif
+
+/* ------------------------------------- decode over a part of the cache ---- */
+
+namespace {
+
+// argument checks shared by the decode operators of this section (rows: query rows)
+int check_subset_args(const void *out, const void *q, const void *kc, const void *vc, const int32_t *bt, int MBS,
+                      const int32_t *ctx, int nseq, int64_t rows, int64_t max_rows, int Hq, int Hkv, int D, int BS,
+                      int64_t NB, float scale, const void *ws) {
+    // the scale, pointer, shape and alignment rules of every decode call
+    const int rc = check_attention_args(out, q, kc, vc, bt, MBS, ctx, nseq, Hq, Hkv, D, BS, NB, scale, ws);
+    if (rc != PA_OK) return rc;
+    if (!(scale <= 3.4028234e38f)) return PA_ERR_INVALID_ARG;  // infinite
+    if (rows <= 0) return PA_ERR_INVALID_ARG;
+    if (rows > max_rows || rows * Hq > INT_MAX || Hkv > 65535) return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+SubsetArgs subset_args(pa_bf16 *out, const pa_bf16 *query, const void *kc, const void *vc, const int32_t *bt, int MBS,
+                       const int32_t *ctx, int nseq, int rows, int Hq, int Hkv, int64_t NB, float scale) {
+    SubsetArgs a{};
+    a.q = query;
+    a.out = out;
+    a.kc = kc;
+    a.vc = vc;
+    a.bt = bt;
+    a.ctx = ctx;
+    a.NB = NB;
+    a.MBS = MBS;
+    a.nseq = nseq;
+    a.rows = rows;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.G = Hq / Hkv;
+    a.window = INT_MAX;
+    a.sinks = 0;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    return a;
+}
+
+int run_window(pa_bf16 *out, const pa_bf16 *query, const void *kc, const void *vc, const float *k_scale,
+               const float *v_scale, CacheKind kind, const int32_t *bt, int MBS, const int32_t *cu_q,
+               const int32_t *ctx, int nseq, int rows, int Hq, int Hkv, int D, int BS, int64_t NB, int window,
+               int sinks, float scale, void *workspace, size_t workspace_bytes, size_t need, void *stream) {
+    const int rc = check_subset_args(out, query, kc, vc, bt, MBS, ctx, nseq, rows, cu_q ? kMaxWindowRows : kMaxBatch,
+                                     Hq, Hkv, D, BS, NB, scale, workspace);
+    if (rc != PA_OK) return rc;
+    if (window < 1 || sinks < 0) return PA_ERR_INVALID_ARG;
+    if (kind != kCacheBf16) {
+        if (!k_scale || !v_scale) return PA_ERR_INVALID_ARG;
+        if (D != 128) return PA_ERR_UNSUPPORTED;
+    }
+    if (workspace_bytes < need) return PA_ERR_WORKSPACE;
+    SubsetArgs a = subset_args(out, query, kc, vc, bt, MBS, ctx, nseq, rows, Hq, Hkv, NB, scale);
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.cu_q = cu_q;
+    a.window = window;
+    a.sinks = sinks;
+    const cudaError_t e = launch_subset_decode(a, D, kind, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pa_decode_window_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim) {
+    return pa_decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim);
+}
+
+int pa_decode_window(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *key_cache, const pa_bf16 *value_cache,
+                     const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens, int batch,
+                     int num_q_heads, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, int window,
+                     int sinks, float scale, void *workspace, size_t workspace_bytes, void *stream) {
+    return run_window(out, query, key_cache, value_cache, nullptr, nullptr, kCacheBf16, block_tables,
+                      max_blocks_per_seq, nullptr, context_lens, batch, batch, num_q_heads, num_kv_heads, head_dim,
+                      block_size, num_blocks, window, sinks, scale, workspace, workspace_bytes,
+                      pa_decode_window_workspace_size(batch, num_q_heads, num_kv_heads, head_dim), stream);
+}
+
+int pa_decode_window_fp8(pa_bf16 *out, const pa_bf16 *query, const pa_e4m3 *key_cache, const pa_e4m3 *value_cache,
+                         const float *k_scale, const float *v_scale, const int32_t *block_tables,
+                         int max_blocks_per_seq, const int32_t *context_lens, int batch, int num_q_heads,
+                         int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, int window, int sinks,
+                         float scale, void *workspace, size_t workspace_bytes, void *stream) {
+    return run_window(out, query, key_cache, value_cache, k_scale, v_scale, kCacheE4m3, block_tables,
+                      max_blocks_per_seq, nullptr, context_lens, batch, batch, num_q_heads, num_kv_heads, head_dim,
+                      block_size, num_blocks, window, sinks, scale, workspace, workspace_bytes,
+                      pa_decode_window_workspace_size(batch, num_q_heads, num_kv_heads, head_dim), stream);
+}
+
+int pa_decode_window_fp8_block(pa_bf16 *out, const pa_bf16 *query, const pa_e4m3 *key_cache,
+                               const pa_e4m3 *value_cache, const float *k_bscale, const float *v_bscale,
+                               const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                               int batch, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                               int64_t num_blocks, int window, int sinks, float scale, void *workspace,
+                               size_t workspace_bytes, void *stream) {
+    return run_window(out, query, key_cache, value_cache, k_bscale, v_bscale, kCacheE4m3Block, block_tables,
+                      max_blocks_per_seq, nullptr, context_lens, batch, batch, num_q_heads, num_kv_heads, head_dim,
+                      block_size, num_blocks, window, sinks, scale, workspace, workspace_bytes,
+                      pa_decode_window_workspace_size(batch, num_q_heads, num_kv_heads, head_dim), stream);
+}
+
+size_t pa_decode_window_multi_workspace_size(int batch, int total_q, int num_q_heads, int num_kv_heads,
+                                             int head_dim) {
+    if (total_q <= 0 || total_q > kMaxWindowRows) return 0;
+    return pa_decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim);
+}
+
+int pa_decode_window_multi(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *key_cache, const pa_bf16 *value_cache,
+                           const int32_t *block_tables, int max_blocks_per_seq, const int32_t *cu_seqlens_q,
+                           const int32_t *context_lens, int batch, int total_q, int num_q_heads, int num_kv_heads,
+                           int head_dim, int block_size, int64_t num_blocks, int window, int sinks, float scale,
+                           void *workspace, size_t workspace_bytes, void *stream) {
+    if (!cu_seqlens_q) return PA_ERR_INVALID_ARG;
+    return run_window(out, query, key_cache, value_cache, nullptr, nullptr, kCacheBf16, block_tables,
+                      max_blocks_per_seq, cu_seqlens_q, context_lens, batch, total_q, num_q_heads, num_kv_heads,
+                      head_dim, block_size, num_blocks, window, sinks, scale, workspace, workspace_bytes,
+                      pa_decode_window_multi_workspace_size(batch, total_q, num_q_heads, num_kv_heads, head_dim),
+                      stream);
+}
+
+size_t pa_decode_prefix_workspace_size(int batch, int num_groups, int num_q_heads, int num_kv_heads, int head_dim) {
+    if (num_groups <= 0 || num_groups > kMaxBatch) return 0;
+    return pa_decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim);
+}
+
+int pa_decode_prefix(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *key_cache, const pa_bf16 *value_cache,
+                     const int32_t *prefix_tables, int max_prefix_blocks, const int32_t *prefix_lens,
+                     const int32_t *cu_group, int num_groups, const int32_t *block_tables, int max_blocks_per_seq,
+                     const int32_t *context_lens, int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                     int block_size, int64_t num_blocks, float scale, void *workspace, size_t workspace_bytes,
+                     void *stream) {
+    const int rc = check_subset_args(out, query, key_cache, value_cache, block_tables, max_blocks_per_seq,
+                                     context_lens, batch, batch, kMaxBatch, num_q_heads, num_kv_heads, head_dim,
+                                     block_size, num_blocks, scale, workspace);
+    if (rc != PA_OK) return rc;
+    if (!prefix_tables || !prefix_lens || !cu_group || num_groups <= 0 || max_prefix_blocks <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_groups > kMaxBatch || int64_t(max_prefix_blocks) * block_size > int64_t(1) << 30)
+        return PA_ERR_UNSUPPORTED;
+    if (workspace_bytes < pa_decode_prefix_workspace_size(batch, num_groups, num_q_heads, num_kv_heads, head_dim))
+        return PA_ERR_WORKSPACE;
+    SubsetArgs a = subset_args(out, query, key_cache, value_cache, block_tables, max_blocks_per_seq, context_lens,
+                               batch, batch, num_q_heads, num_kv_heads, num_blocks, scale);
+    a.pt = prefix_tables;
+    a.PMBS = max_prefix_blocks;
+    a.plen = prefix_lens;
+    a.cu_g = cu_group;
+    a.ngroups = num_groups;
+    const cudaError_t e = launch_subset_decode(a, head_dim, kCacheBf16, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+size_t pa_decode_weights_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                                        int max_blocks_per_seq) {
+    if (max_blocks_per_seq <= 0 || int64_t(max_blocks_per_seq) * kBlockSize > int64_t(1) << 30) return 0;
+    return pa_decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim);
+}
+
+int pa_decode_weights(pa_bf16 *out, float *weights, const pa_bf16 *query, const pa_bf16 *key_cache,
+                      const pa_bf16 *value_cache, const int32_t *block_tables, int max_blocks_per_seq,
+                      const int32_t *context_lens, int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                      int block_size, int64_t num_blocks, float scale, void *workspace, size_t workspace_bytes,
+                      void *stream) {
+    const int rc = check_subset_args(out, query, key_cache, value_cache, block_tables, max_blocks_per_seq,
+                                     context_lens, batch, batch, kMaxBatch, num_q_heads, num_kv_heads, head_dim,
+                                     block_size, num_blocks, scale, workspace);
+    if (rc != PA_OK) return rc;
+    if (!weights || !aligned16(weights)) return PA_ERR_INVALID_ARG;
+    if (workspace_bytes <
+        pa_decode_weights_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq))
+        return PA_ERR_WORKSPACE;
+    SubsetArgs a = subset_args(out, query, key_cache, value_cache, block_tables, max_blocks_per_seq, context_lens,
+                               batch, batch, num_q_heads, num_kv_heads, num_blocks, scale);
+    a.weights = weights;
+    const cudaError_t e = launch_subset_decode(a, head_dim, kCacheBf16, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+int pa_reset_weights(float *weights, const int64_t *slot_mapping, int64_t num_tokens, int num_kv_heads,
+                     int block_size, int64_t num_blocks, void *stream) {
+    if (num_tokens < 0 || num_kv_heads <= 0 || block_size <= 0 || num_blocks <= 0) return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PA_OK;
+    if (!weights || !slot_mapping) return PA_ERR_INVALID_ARG;
+    if (block_size != kBlockSize || num_tokens > (int64_t(1) << 31) - 1 || num_kv_heads > 65535)
+        return PA_ERR_UNSUPPORTED;
+    const cudaError_t e = launch_reset_weights(weights, slot_mapping, num_tokens, num_kv_heads, num_blocks,
+                                               static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+int pa_evict(int32_t *kept, int32_t *new_lens, pa_bf16 *key_cache, pa_bf16 *value_cache, float *weights,
+             const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+             const int32_t *dst_tables, int max_dst_blocks, int batch, int num_kv_heads, int head_dim,
+             int block_size, int64_t num_blocks, int budget, int recent, void *stream) {
+    if (!kept || !new_lens || !key_cache || !value_cache || !weights || !block_tables || !context_lens || !dst_tables)
+        return PA_ERR_INVALID_ARG;
+    if (batch <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || num_blocks <= 0 ||
+        max_blocks_per_seq <= 0 || max_dst_blocks <= 0 || budget <= 0 || recent < 0)
+        return PA_ERR_INVALID_ARG;
+    if (!shape_supported(head_dim, block_size) || batch > kMaxBatch || num_kv_heads > 65535)
+        return PA_ERR_UNSUPPORTED;
+    if (int64_t(max_blocks_per_seq) * block_size > int64_t(1) << 30 || num_blocks > (int64_t(1) << 31) - 1)
+        return PA_ERR_UNSUPPORTED;
+    if (int64_t(max_dst_blocks) * block_size < budget) return PA_ERR_INVALID_ARG;  // no room for the kept tokens
+    if (int64_t(batch) * num_kv_heads * budget > int64_t(1) << 33) return PA_ERR_UNSUPPORTED;
+    if (!aligned16(key_cache) || !aligned16(value_cache) || !aligned16(weights)) return PA_ERR_INVALID_ARG;
+    EvictArgs a{};
+    a.kept = kept;
+    a.new_lens = new_lens;
+    a.kc = key_cache;
+    a.vc = value_cache;
+    a.weights = weights;
+    a.bt = block_tables;
+    a.ctx = context_lens;
+    a.dst = dst_tables;
+    a.NB = num_blocks;
+    a.MBS = max_blocks_per_seq;
+    a.DMBS = max_dst_blocks;
+    a.B = batch;
+    a.Hkv = num_kv_heads;
+    a.budget = budget;
+    a.recent = recent;
+    const cudaError_t e = launch_evict(a, head_dim, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+}  // extern "C"

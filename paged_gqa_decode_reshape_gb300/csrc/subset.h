@@ -1,0 +1,49 @@
+// subset.h -- internal interface of the decode operators that read a part of
+// the cache, or share it between sequences, and of eviction (subset_decode.cu,
+// evict.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace pa {
+
+constexpr int kMaxWindowRows = 1 << 20;  // query rows of a windowed multi-token call
+
+enum CacheKind { kCacheBf16 = 0, kCacheE4m3 = 1, kCacheE4m3Block = 2 };
+
+// Attention of query rows over the tokens a row sees:
+//   its sequence's prefix (pt / plen: the prefix blocks of its group), then
+//   its own tokens t < lim with t < sinks or t >= lim - window.
+struct SubsetArgs {
+    const uint16_t *q;            // [rows][Hq][D] bf16
+    uint16_t *out;                // [rows][Hq][D] bf16
+    const void *kc, *vc;          // the caches, in the layout of `kind`
+    const float *k_scale, *v_scale;
+    const int32_t *bt, *ctx;      // [nseq][MBS], [nseq]
+    const int32_t *cu_q;          // [nseq + 1] query-row offsets; null: one row per sequence
+    const int32_t *pt, *plen;     // [ngroups][PMBS], [ngroups] prefixes; null: none
+    const int32_t *cu_g;          // [ngroups + 1] sequence offsets of the groups
+    float *weights;               // [NB][Hkv][16]: accumulated attention weights; null: none
+    int64_t NB;
+    int MBS, PMBS, nseq, ngroups, rows, Hq, Hkv, G;
+    int window, sinks;            // window: INT_MAX when everything before lim is seen
+    float scale_log2;             // softmax scale * log2(e)
+};
+
+cudaError_t launch_subset_decode(const SubsetArgs &a, int head_dim, CacheKind kind, cudaStream_t stream);
+
+struct EvictArgs {
+    int32_t *kept, *new_lens;     // [B][Hkv][budget], [B]
+    uint16_t *kc, *vc;            // [NB][16][Hkv][D] bf16
+    float *weights;               // [NB][Hkv][16]
+    const int32_t *bt, *ctx, *dst;  // [B][MBS], [B], [B][DMBS]
+    int64_t NB;
+    int MBS, DMBS, B, Hkv, budget, recent;
+};
+
+cudaError_t launch_evict(const EvictArgs &a, int head_dim, cudaStream_t stream);
+cudaError_t launch_reset_weights(float *weights, const int64_t *slots, int64_t T, int Hkv, int64_t NB,
+                                 cudaStream_t stream);
+
+}  // namespace pa
