@@ -854,6 +854,57 @@ SubsetArgs subset_args(pa_bf16 *out, const pa_bf16 *query, const void *kc, const
     return a;
 }
 
+// Workspace of the streaming kernel: status word, arrival counters and two
+// piece slots per CTA, then (accumulated weights) normalisers and logits.
+struct StreamWorkspace {
+    size_t part, lse, logits, bytes;
+};
+
+int stream_workspace(StreamWorkspace *w, int *sms, int B, int Hq, int D, int64_t logit_blocks) {
+    DecodeGeometry geo;
+    const cudaError_t e = decode_geometry(D, &geo);
+    if (e != cudaSuccess) return cuda_fail(e);
+    const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    *sms = geo.grid;
+    w->part = 256 + up(size_t(geo.grid) * 4);
+    w->lse = w->part + up(size_t(geo.grid) * 2 * stream_part_floats(D) * 4);
+    w->logits = w->lse + (logit_blocks ? up(size_t(B) * Hq * 4) : 0);
+    w->bytes = w->logits + up(size_t(B) * Hq * logit_blocks * kBlockSize * 4);
+    return PA_OK;
+}
+
+size_t stream_workspace_bytes(int batch, int Hq, int Hkv, int D, int64_t logit_blocks) {
+    if (batch <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || batch > kMaxBatch) return 0;
+    if (!shape_supported(D, kBlockSize) || Hq / Hkv > kMaxGroup || Hkv > 65535) return 0;
+    StreamWorkspace w;
+    int sms;
+    return stream_workspace(&w, &sms, batch, Hq, D, logit_blocks) == PA_OK ? w.bytes : 0;
+}
+
+// the streaming kernel's launch, after the argument checks
+int run_stream(SubsetArgs a, int D, CacheKind kind, void *workspace, size_t workspace_bytes, void *stream) {
+    StreamWorkspace w;
+    int sms = 0;
+    int rc = stream_workspace(&w, &sms, a.nseq, a.Hq, D, a.weights ? a.MBS : 0);
+    if (rc != PA_OK) return rc;
+    if (workspace_bytes < w.bytes) return PA_ERR_WORKSPACE;
+    uint8_t *p = static_cast<uint8_t *>(workspace);
+    a.status = reinterpret_cast<int32_t *>(p);
+    a.counters = reinterpret_cast<int32_t *>(p + 256);
+    a.part = reinterpret_cast<float *>(p + w.part);
+    a.lse = reinterpret_cast<float *>(p + w.lse);
+    a.logits = reinterpret_cast<float *>(p + w.logits);
+    a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+    a.stop_item = g_stop_item.load(std::memory_order_relaxed);
+    const bool fp8 = kind != kCacheBf16;
+    CUtensorMap tk, tv;
+    if ((rc = make_cache_map(&tk, a.kc, a.Hkv, D, kBlockSize, a.NB, fp8)) != PA_OK) return rc;
+    if (fp8) std::memset(&tv, 0, sizeof tv);  // an E4M3 V tile is contiguous: plain bulk copies
+    else if ((rc = make_cache_map(&tv, a.vc, a.Hkv, D, kBlockSize, a.NB)) != PA_OK) return rc;
+    const cudaError_t e = launch_stream_decode(tk, tv, a, D, kind, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
 int run_window(pa_bf16 *out, const pa_bf16 *query, const void *kc, const void *vc, const float *k_scale,
                const float *v_scale, CacheKind kind, const int32_t *bt, int MBS, const int32_t *cu_q,
                const int32_t *ctx, int nseq, int rows, int Hq, int Hkv, int D, int BS, int64_t NB, int window,
@@ -866,14 +917,15 @@ int run_window(pa_bf16 *out, const pa_bf16 *query, const void *kc, const void *v
         if (!k_scale || !v_scale) return PA_ERR_INVALID_ARG;
         if (D != 128) return PA_ERR_UNSUPPORTED;
     }
-    if (workspace_bytes < need) return PA_ERR_WORKSPACE;
     SubsetArgs a = subset_args(out, query, kc, vc, bt, MBS, ctx, nseq, rows, Hq, Hkv, NB, scale);
     a.k_scale = k_scale;
     a.v_scale = v_scale;
     a.cu_q = cu_q;
     a.window = window;
     a.sinks = sinks;
-    const cudaError_t e = launch_subset_decode(a, D, kind, static_cast<cudaStream_t>(stream));
+    if (!cu_q) return run_stream(a, D, kind, workspace, workspace_bytes, stream);
+    if (workspace_bytes < need) return PA_ERR_WORKSPACE;
+    const cudaError_t e = launch_subset_decode(a, D, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 
@@ -882,7 +934,7 @@ int run_window(pa_bf16 *out, const pa_bf16 *query, const void *kc, const void *v
 extern "C" {
 
 size_t pa_decode_window_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim) {
-    return pa_decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim);
+    return stream_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, 0);
 }
 
 int pa_decode_window(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *key_cache, const pa_bf16 *value_cache,
@@ -892,7 +944,7 @@ int pa_decode_window(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *key_cach
     return run_window(out, query, key_cache, value_cache, nullptr, nullptr, kCacheBf16, block_tables,
                       max_blocks_per_seq, nullptr, context_lens, batch, batch, num_q_heads, num_kv_heads, head_dim,
                       block_size, num_blocks, window, sinks, scale, workspace, workspace_bytes,
-                      pa_decode_window_workspace_size(batch, num_q_heads, num_kv_heads, head_dim), stream);
+                      0, stream);
 }
 
 int pa_decode_window_fp8(pa_bf16 *out, const pa_bf16 *query, const pa_e4m3 *key_cache, const pa_e4m3 *value_cache,
@@ -903,7 +955,7 @@ int pa_decode_window_fp8(pa_bf16 *out, const pa_bf16 *query, const pa_e4m3 *key_
     return run_window(out, query, key_cache, value_cache, k_scale, v_scale, kCacheE4m3, block_tables,
                       max_blocks_per_seq, nullptr, context_lens, batch, batch, num_q_heads, num_kv_heads, head_dim,
                       block_size, num_blocks, window, sinks, scale, workspace, workspace_bytes,
-                      pa_decode_window_workspace_size(batch, num_q_heads, num_kv_heads, head_dim), stream);
+                      0, stream);
 }
 
 int pa_decode_window_fp8_block(pa_bf16 *out, const pa_bf16 *query, const pa_e4m3 *key_cache,
@@ -915,7 +967,7 @@ int pa_decode_window_fp8_block(pa_bf16 *out, const pa_bf16 *query, const pa_e4m3
     return run_window(out, query, key_cache, value_cache, k_bscale, v_bscale, kCacheE4m3Block, block_tables,
                       max_blocks_per_seq, nullptr, context_lens, batch, batch, num_q_heads, num_kv_heads, head_dim,
                       block_size, num_blocks, window, sinks, scale, workspace, workspace_bytes,
-                      pa_decode_window_workspace_size(batch, num_q_heads, num_kv_heads, head_dim), stream);
+                      0, stream);
 }
 
 size_t pa_decode_window_multi_workspace_size(int batch, int total_q, int num_q_heads, int num_kv_heads,
@@ -965,14 +1017,14 @@ int pa_decode_prefix(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *key_cach
     a.plen = prefix_lens;
     a.cu_g = cu_group;
     a.ngroups = num_groups;
-    const cudaError_t e = launch_subset_decode(a, head_dim, kCacheBf16, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_subset_decode(a, head_dim, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 
 size_t pa_decode_weights_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim,
                                         int max_blocks_per_seq) {
     if (max_blocks_per_seq <= 0 || int64_t(max_blocks_per_seq) * kBlockSize > int64_t(1) << 30) return 0;
-    return pa_decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim);
+    return stream_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq);
 }
 
 int pa_decode_weights(pa_bf16 *out, float *weights, const pa_bf16 *query, const pa_bf16 *key_cache,
@@ -985,14 +1037,10 @@ int pa_decode_weights(pa_bf16 *out, float *weights, const pa_bf16 *query, const 
                                      block_size, num_blocks, scale, workspace);
     if (rc != PA_OK) return rc;
     if (!weights || !aligned16(weights)) return PA_ERR_INVALID_ARG;
-    if (workspace_bytes <
-        pa_decode_weights_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq))
-        return PA_ERR_WORKSPACE;
     SubsetArgs a = subset_args(out, query, key_cache, value_cache, block_tables, max_blocks_per_seq, context_lens,
                                batch, batch, num_q_heads, num_kv_heads, num_blocks, scale);
     a.weights = weights;
-    const cudaError_t e = launch_subset_decode(a, head_dim, kCacheBf16, static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? PA_OK : cuda_fail(e);
+    return run_stream(a, head_dim, kCacheBf16, workspace, workspace_bytes, stream);
 }
 
 int pa_reset_weights(float *weights, const int64_t *slot_mapping, int64_t num_tokens, int num_kv_heads,

@@ -1,0 +1,649 @@
+// stream_decode.cu -- one-query-row decode over a part of the cache (sm_103a):
+// the sliding window with sinks, the dense decode that also stores its logits
+// (for the accumulated weights), and the own tokens of a sequence whose
+// prefix was attended to separately.
+//
+// For KV head g of sequence b and the query heads h of its group, over the
+// tokens t the row sees (z_t = scale * log2(e) * q_h . K_t):
+//   out_h = sum_t 2^(z_t - m) V_t / sum_t 2^(z_t - m),   m = max_t z_t.
+//
+// Bound: every visible K/V byte is read once, at about 2 G flops per byte, so
+// HBM bandwidth bounds long calls and latency short ones.
+//
+//  * Work list. A (sequence, KV head) is a segment with one item per 16-token
+//    block that holds a visible token (sink blocks, then window blocks; at
+//    least one item, so that every output row is written). The segments are
+//    concatenated and cut into equal ranges, one per CTA, so that ragged
+//    lengths load the SMs evenly.
+//  * Each warp is its own producer: item k of warp w is position
+//    pos0 + w + NW k of the range, copied by TMA (K and V in 64-dim halves,
+//    128-byte swizzle; E4M3: K box and V tile) into the warp's private ring of
+//    R stages, which only this warp fills and empties. No warp waits for
+//    another between segment ends, and copies run ahead across them.
+//  * Math as mma.sync m16n8k16 on S^T = K Q^T and O^T += V^T P^T: tokens (then
+//    dims) are the 16 rows, the up to 8 heads of the group the 8 columns, so
+//    a K/V byte serves the whole group. tcgen05's smallest M of 64 would be
+//    filled, but its results come back through TMEM to warps that would
+//    wait for them; at 2 G flops per byte the tensor pipes are nearly idle.
+//  * Two blocks (32 tokens) per softmax step; a 16-bit mask per block says
+//    which tokens are seen, masked V lanes are zeroed (they may hold NaN).
+//  * At a segment's end the warps' states are merged in shared memory by all
+//    threads. A segment cut between CTAs leaves (O, m, l) per piece in the
+//    workspace, and the CTA that completes its arrival counter merges them,
+//    in piece order: the result does not depend on who is last.
+#include <climits>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "subset.h"
+
+namespace pa {
+namespace {
+
+constexpr int kPreCap = 1024;  // entries of the items-per-sequence prefix in shared memory
+
+template <int D, CacheKind KIND>
+struct StreamCfg {
+    static constexpr bool F8 = KIND != kCacheBf16;
+    static_assert(!F8 || D == 128, "the E4M3 cache path is for head_dim 128");
+    static constexpr int NW = 6;                          // warps
+    static constexpr int KT = kBlockSize * D * (F8 ? 1 : 2);  // bytes of a K (or V) tile of one block
+    static constexpr int STAGE = 2 * KT;
+    static constexpr int RING = 32 * 1024;                // bytes in flight per warp
+    static constexpr int R = RING / STAGE;                // stages per warp
+    static constexpr int NKK = D / 16;
+    static constexpr int HALF = kBlockSize * 128;         // bytes of one 64-dim half tile (bf16)
+    static constexpr int ROW = D + 4;                     // floats per head row of a warp's state (conflict-free)
+    static constexpr int SCR = 8 * ROW;
+    static constexpr int PART = 8 * D + 16;               // floats per partial: O[8][D], m[8], l[8]
+    static constexpr int THREADS = NW * 32;
+    static constexpr size_t off_bars = size_t(NW) * RING;
+    static constexpr size_t off_scr = off_bars + size_t(NW) * R * 8;
+    static constexpr size_t off_ml = off_scr + size_t(NW) * SCR * 4;
+    static constexpr size_t off_flag = off_ml + size_t(NW) * 16 * 4;
+    static constexpr size_t off_pre = off_flag + 16;
+    static constexpr size_t SMEM = 1024 + off_pre + (kPreCap + 1) * 4 + 12;
+};
+
+// a sequence's visible tokens [0, s1) and [lo, lim), as items
+struct Span {
+    int lim, s1, lo, nb1, jw, n;  // nb1 sink blocks, then blocks jw, jw + 1, ...; n items (at least one)
+};
+
+__device__ __forceinline__ Span span_of(const SubsetArgs &a, int b) {
+    Span s;
+    s.lim = min(max(__ldg(a.ctx + b), 0), a.MBS * kBlockSize);
+    s.s1 = min(a.sinks, s.lim);
+    s.lo = max(s.s1, a.window >= s.lim ? 0 : s.lim - a.window);
+    s.nb1 = (s.s1 + kBlockSize - 1) / kBlockSize;
+    s.jw = max(s.lo / kBlockSize, s.nb1);
+    s.n = max(s.nb1 + max((s.lim + kBlockSize - 1) / kBlockSize - s.jw, 0), 1);
+    return s;
+}
+
+// bits of the offsets t - t0 of tokens t in [a, b)
+__device__ __forceinline__ uint32_t bits_between(int a, int b, int t0) {
+    const int x = min(max(a - t0, 0), 16), y = min(max(b - t0, 0), 16);
+    return y > x ? ((1u << y) - 1u) & ~((1u << x) - 1u) : 0u;
+}
+
+template <int D, CacheKind KIND, bool LOGITS>
+__global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
+    stream_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         const SubsetArgs a) {
+    using C = StreamCfg<D, KIND>;
+    constexpr int NW = C::NW, R = C::R, NKK = C::NKK, BS = kBlockSize;
+    constexpr bool F8 = C::F8, PSC = KIND == kCacheE4m3Block;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *bp = smem_raw + (base - raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int Hkv = a.Hkv, G = a.G;
+    float *scr = reinterpret_cast<float *>(bp + C::off_scr);
+    float *sm_ml = reinterpret_cast<float *>(bp + C::off_ml);  // [NW][16]: m[8], l[8]
+    volatile int *flag = reinterpret_cast<volatile int *>(bp + C::off_flag);
+    int *pre = reinterpret_cast<int *>(bp + C::off_pre);
+    const uint32_t ring = base + uint32_t(warp) * C::RING;
+    const uint32_t bars = base + uint32_t(C::off_bars) + uint32_t(warp) * R * 8;
+
+    pdl_trigger();
+    if (tid == 0) {
+        prefetch_tensormap(&tm_k);
+        if (!F8) prefetch_tensormap(&tm_v);
+    }
+    if (lane == 0) {
+        for (int s = 0; s < R; ++s) mbar_init(bars + s * 8, 1);
+        fence_barrier_init();
+    }
+    // ---- items of groups of `str` sequences and their prefix sums
+    const int str = (a.nseq + kPreCap - 1) / kPreCap, np = (a.nseq + str - 1) / str;
+    for (int i = tid; i < np; i += C::THREADS) {
+        int n = 0;
+        for (int b = i * str; b < min((i + 1) * str, a.nseq); ++b) n += span_of(a, b).n;
+        pre[i + 1] = n;
+    }
+    if (tid == 0) pre[0] = 0;
+    __syncthreads();
+    if (warp == 0) {
+        int carry = 0;
+        for (int i0 = 0; i0 < np; i0 += 32) {
+            int v = i0 + lane < np ? pre[i0 + lane + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            if (i0 + lane < np) pre[i0 + lane + 1] = carry + v;
+            carry += __shfl_sync(0xffffffffu, v, 31);
+        }
+    }
+    __syncthreads();
+    const int64_t total = int64_t(Hkv) * pre[np];
+    const int64_t L = max((total + gridDim.x - 1) / gridDim.x, int64_t(a.min_items));
+    const int64_t pos0 = int64_t(blockIdx.x) * L, pos1 = min(total, pos0 + L);
+    if (pos0 >= pos1) return;  // whole CTA: nothing to do
+    const int n_items = int(pos1 - pos0);
+
+    // the sequence of global position p, and p's offset inside its items
+    auto locate = [&](int64_t p, Span &s, int64_t &rem) -> int {
+        int lo = 0, hi = np;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (int64_t(Hkv) * pre[mid] <= p) lo = mid; else hi = mid;
+        }
+        int b = lo * str;
+        rem = p - int64_t(Hkv) * pre[lo];
+        s = span_of(a, b);
+        while (rem >= int64_t(Hkv) * s.n) {
+            rem -= int64_t(Hkv) * s.n;
+            s = span_of(a, ++b);
+        }
+        return b;
+    };
+
+    // ---- a window of 32 of this warp's items, one per lane
+    struct Win {
+        int phys;       // physical block, or -1: nothing to read
+        uint32_t what;  // token mask, KV head << 16
+        int j;          // logical block (LOGITS)
+        float sk, sv;   // scales of the block (per-block scales)
+    };
+    const int kn = n_items > warp ? (n_items - warp + NW - 1) / NW : 0;  // this warp's items
+    auto resolve = [&](int k0) -> Win {
+        Win w{-1, 0u, 0, 0.f, 0.f};
+        const int k = k0 + lane;
+        if (k >= kn) return w;
+        Span s;
+        int64_t rem;
+        const int b = locate(pos0 + warp + int64_t(NW) * k, s, rem);
+        const int kvh = int(rem / s.n), e = int(rem - int64_t(kvh) * s.n);
+        const int j = e < s.nb1 ? e : e - s.nb1 + s.jw;
+        const uint32_t m = bits_between(0, s.s1, j * BS) | bits_between(s.lo, s.lim, j * BS);
+        w.what = uint32_t(kvh) << 16;
+        w.j = j;
+        if (m) {
+            const int ph = __ldg(a.bt + int64_t(b) * a.MBS + j);
+            if (ph >= 0 && int64_t(ph) < a.NB) {
+                w.phys = ph;
+                w.what |= m;
+            }
+        }
+        return w;
+    };
+    auto scales = [&](Win &w) {
+        if (PSC && w.phys >= 0) {
+            const int64_t i = int64_t(w.phys) * Hkv + (w.what >> 16);
+            w.sk = __ldg(a.k_scale + i);
+            w.sv = __ldg(a.v_scale + i);
+        }
+    };
+    pdl_wait();
+    Win cur = resolve(0), nxt = resolve(32);
+    scales(cur);
+    scales(nxt);
+    int wbase = 0;        // first item of cur
+    uint32_t armed = 0;   // bit s: parity of the fills of stage s so far
+    uint32_t phase = 0;   // bit s: parity of the fill of stage s that is waited for next
+    bool dead = false;    // a wait gave up: no further copies or waits
+    const uint64_t policy = l2_policy_evict_first();
+    // start the copy of item i (i < kn, in cur or nxt) into its stage
+    auto issue = [&](int i) {
+        const bool c = i < wbase + 32;
+        const int phys = __shfl_sync(0xffffffffu, c ? cur.phys : nxt.phys, i & 31);
+        const uint32_t what = __shfl_sync(0xffffffffu, c ? cur.what : nxt.what, i & 31);
+        if (phys < 0 || dead || i >= a.stop_item) return;
+        const uint32_t st = uint32_t(i) % R;
+        armed ^= 1u << st;
+        const uint32_t fb = bars + st * 8, dst = ring + st * C::STAGE;
+        const int kvh = int(what >> 16);
+        if (lane == 0) mbar_arrive_expect_tx(fb, C::STAGE);
+        __syncwarp();
+        if constexpr (F8) {
+            if (lane == 0) tma_load_4d(dst, &tm_k, fb, 0, kvh, 0, phys, policy);
+            if (lane == 1)
+                bulk_load_1d(dst + C::KT, static_cast<const uint8_t *>(a.vc) + (int64_t(phys) * Hkv + kvh) * C::KT,
+                             C::KT, fb, policy);
+        } else {
+            constexpr int HV = D / 64;
+            if (lane < 2 * HV)
+                tma_load_4d(dst + (lane / HV) * C::KT + (lane % HV) * C::HALF, lane / HV ? &tm_v : &tm_k, fb,
+                            (lane % HV) * 64, kvh, 0, phys, policy);
+        }
+    };
+
+    const int g = lane >> 2, q4 = lane & 3;
+    float scale_log2 = a.scale_log2, vref = 0.f;  // as in the dense decode: acc holds O / vref (E4M3)
+    uint32_t qb[NKK][2];
+    uint2 qn[NKK];  // the next segment's query, on its way
+    float acc[NKK][4], m0, m1, l0, l1;
+    auto fetch_q = [&](int b, int kvh) {
+        const uint32_t *row = reinterpret_cast<const uint32_t *>(a.q + (int64_t(b) * a.Hq + kvh * G + (g < G ? g : 0)) * D);
+#pragma unroll
+        for (int kk = 0; kk < NKK; ++kk) {
+            if constexpr (F8) qn[kk] = __ldg(reinterpret_cast<const uint2 *>(row + 8 * kk + 2 * q4));
+            else qn[kk] = make_uint2(__ldg(row + 8 * kk + q4), __ldg(row + 8 * kk + 4 + q4));
+        }
+    };
+    auto begin_segment = [&](int kvh) {
+#pragma unroll
+        for (int kk = 0; kk < NKK; ++kk) {
+            const uint2 v = g < G ? qn[kk] : make_uint2(0u, 0u);
+            qb[kk][0] = F8 ? pack_f16x2(bf16_lo(v.x), bf16_hi(v.x)) : v.x;
+            qb[kk][1] = F8 ? pack_f16x2(bf16_lo(v.y), bf16_hi(v.y)) : v.y;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[kk][e] = 0.f;
+        }
+        m0 = m1 = -INFINITY;
+        l0 = l1 = 0.f;
+        if constexpr (KIND == kCacheE4m3) {
+            scale_log2 = a.scale_log2 * __ldg(a.k_scale + kvh);
+            vref = __ldg(a.v_scale + kvh);
+        }
+        if constexpr (PSC) vref = 0.f;
+    };
+    // S^T = K Q^T for the 16 tokens of a staged block
+    auto qk = [&](uint32_t kb, float (&sc)[4]) {
+        float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+        const int rk = (lane & 7) + (((lane >> 3) & 1) << 3);
+        if constexpr (F8) {
+            // four codes per lane and 16-byte chunk: k = 2 q4 + e stands for dim 4 q4 + e, k = 2 q4 + 8 + e
+            // for dim 4 q4 + 2 + e (the query fragments are in the same order)
+#pragma unroll
+            for (int c2 = 0; c2 < NKK / 2; ++c2) {
+                const int ch = 2 * c2 + (lane >> 4);
+                uint32_t r0, r1, r2, r3, l0_, h0_, l1_, h1_, l2_, h2_, l3_, h3_;
+                ldsm_x4(kb + rk * 128 + ((ch ^ (lane & 7)) << 4), r0, r1, r2, r3);
+                e4m3x4_to_f16x2x2(r0, l0_, h0_);
+                e4m3x4_to_f16x2x2(r1, l1_, h1_);
+                e4m3x4_to_f16x2x2(r2, l2_, h2_);
+                e4m3x4_to_f16x2x2(r3, l3_, h3_);
+                mma_f16(sa, l0_, l1_, h0_, h1_, qb[2 * c2][0], qb[2 * c2][1]);
+                mma_f16(sb, l2_, l3_, h2_, h3_, qb[2 * c2 + 1][0], qb[2 * c2 + 1][1]);
+            }
+        } else {
+#pragma unroll
+            for (int kk = 0; kk < NKK; ++kk) {
+                const int ch = ((kk & 3) << 1) + (lane >> 4);
+                uint32_t a0, a1, a2, a3;
+                ldsm_x4(kb + (kk >> 2) * C::HALF + rk * 128 + ((ch ^ (lane & 7)) << 4), a0, a1, a2, a3);
+                if (kk & 1) mma_bf16(sb, a0, a1, a2, a3, qb[kk][0], qb[kk][1]);
+                else mma_bf16(sa, a0, a1, a2, a3, qb[kk][0], qb[kk][1]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[e] = sa[e] + sb[e];
+    };
+    // O^T += V^T P^T for a staged block; V lanes of unseen tokens zeroed
+    auto pv = [&](uint32_t vb, uint32_t p01, uint32_t p23, uint32_t mask) {
+        const uint32_t pb0 = movmatrix_trans(p01), pb1 = movmatrix_trans(p23);
+        uint32_t mlo = 0xffffffffu, mhi = 0xffffffffu;
+        if (mask != 0xffffu) {
+            const uint32_t t = mask >> (2 * q4);
+            mlo = (t & 1u ? 0x0000ffffu : 0u) | (t & 2u ? 0xffff0000u : 0u);
+            mhi = (t & 0x100u ? 0x0000ffffu : 0u) | (t & 0x200u ? 0xffff0000u : 0u);
+        }
+        if constexpr (F8) {
+#pragma unroll
+            for (int c2 = 0; c2 < NKK / 2; ++c2) {
+                uint32_t r0, r1, r2, r3, a0, a1, a2, a3, b0, b1, b2, b3;
+                ldsm_x4(vb + (32 * c2 + lane) * 16, r0, r1, r2, r3);
+                e4m3x4_to_f16x2x2(r0, a0, a2);
+                e4m3x4_to_f16x2x2(r1, a1, a3);
+                e4m3x4_to_f16x2x2(r2, b0, b2);
+                e4m3x4_to_f16x2x2(r3, b1, b3);
+                mma_f16(acc[2 * c2], a0 & mlo, a1 & mlo, a2 & mhi, a3 & mhi, pb0, pb1);
+                mma_f16(acc[2 * c2 + 1], b0 & mlo, b1 & mlo, b2 & mhi, b3 & mhi, pb0, pb1);
+            }
+        } else {
+            const int rv = (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+            for (int mt = 0; mt < NKK; ++mt) {
+                const int ch = ((mt & 3) << 1) + ((lane >> 3) & 1);
+                uint32_t a0, a1, a2, a3;
+                ldsm_x4_trans(vb + (mt >> 2) * C::HALF + rv * 128 + ((ch ^ (lane & 7)) << 4), a0, a1, a2, a3);
+                mma_bf16(acc[mt], a0 & mlo, a1 & mlo, a2 & mhi, a3 & mhi, pb0, pb1);
+            }
+        }
+    };
+    // one online-softmax step over up to two staged blocks (mask 0: none);
+    // ca, cb: their K and V scales (per-block scales)
+    auto step = [&](uint32_t s0a, uint32_t ma, float2 ca, uint32_t s1a, uint32_t mb, float2 cb, float *la, float *lb) {
+        float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+        if (ma) qk(s0a, s0);
+        if (mb) qk(s1a, s1);
+        float sla = scale_log2, slb = scale_log2, vr = 1.f, ra = 1.f, rb = 1.f;
+        if constexpr (PSC) {
+            // acc is in units of vref, the largest V scale so far; a block's P
+            // enters times its scale over vref (powers of two: exact down to
+            // the f16 subnormals)
+            sla *= ca.x;
+            slb *= cb.x;
+            float vnew = vref;
+            if (ma) vnew = fmaxf(vnew, ca.y);
+            if (mb) vnew = fmaxf(vnew, cb.y);
+            // a block never written has scale 0 and holds zeros
+            const float rv = vnew > 0.f ? rcp_pow2(vnew) : 0.f;
+            vr = vref * rv;
+            if (vref == vnew) vr = 1.f;
+            vref = vnew;
+            ra = ca.y * rv;
+            rb = cb.y * rv;
+        }
+        float x[4], y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int t = e < 2 ? g : g + 8;
+            x[e] = (ma >> t) & 1u ? s0[e] * sla : -INFINITY;
+            y[e] = (mb >> t) & 1u ? s1[e] * slb : -INFINITY;
+        }
+        if constexpr (LOGITS) {  // [G][16] per block: heads 2 q4, 2 q4 + 1 of tokens g, g + 8
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int h = 2 * q4 + (e & 1), t = e < 2 ? g : g + 8;
+                if (h < G && ma) __stcg(la + h * BS + t, x[e]);
+                if (h < G && mb) __stcg(lb + h * BS + t, y[e]);
+            }
+        }
+        float bm0 = fmaxf(fmaxf(x[0], x[2]), fmaxf(y[0], y[2]));
+        float bm1 = fmaxf(fmaxf(x[1], x[3]), fmaxf(y[1], y[3]));
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+            bm0 = fmaxf(bm0, __shfl_xor_sync(0xffffffffu, bm0, o));
+            bm1 = fmaxf(bm1, __shfl_xor_sync(0xffffffffu, bm1, o));
+        }
+        const float mn0 = fmaxf(m0, bm0), mn1 = fmaxf(m1, bm1);
+        const float r0 = mn0 == -INFINITY ? 0.f : mn0, r1 = mn1 == -INFINITY ? 0.f : mn1;
+        const bool grow = mn0 != m0 || mn1 != m1;
+        float al0 = fast_exp2(m0 - r0), al1 = fast_exp2(m1 - r1);
+        m0 = mn0;
+        m1 = mn1;
+        float p[4], q[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            p[e] = fast_exp2(x[e] - (e & 1 ? r1 : r0));
+            q[e] = fast_exp2(y[e] - (e & 1 ? r1 : r0));
+        }
+        auto pk = [](float lo, float hi) { return F8 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi); };
+        const uint32_t p01 = pk(p[0], p[1]), p23 = pk(p[2], p[3]), q01 = pk(q[0], q[1]), q23 = pk(q[2], q[3]);
+        if constexpr (!LOGITS) {
+            // the normaliser sums the values that meet V, so a constant V comes out exactly
+            auto lo = [](uint32_t v) { return F8 ? f16_lo(v) : bf16_lo(v); };
+            auto hi = [](uint32_t v) { return F8 ? f16_hi(v) : bf16_hi(v); };
+            p[0] = lo(p01), p[1] = hi(p01), p[2] = lo(p23), p[3] = hi(p23);
+            q[0] = lo(q01), q[1] = hi(q01), q[2] = lo(q23), q[3] = hi(q23);
+        }  // LOGITS: the weights are fp32, so is their normaliser
+        l0 = l0 * al0 + ((p[0] + p[2]) + (q[0] + q[2]));
+        l1 = l1 * al1 + ((p[1] + p[3]) + (q[1] + q[3]));
+        if (PSC) {
+            al0 *= vr;
+            al1 *= vr;
+        }
+        if (__any_sync(0xffffffffu, grow) || (PSC && vr != 1.f)) {
+#pragma unroll
+            for (int mt = 0; mt < NKK; ++mt) {
+                acc[mt][0] *= al0;
+                acc[mt][1] *= al1;
+                acc[mt][2] *= al0;
+                acc[mt][3] *= al1;
+            }
+        }
+        if (ma) pv(s0a + C::KT, PSC ? scale_f16x2(p01, ra) : p01, PSC ? scale_f16x2(p23, ra) : p23, ma);
+        if (mb) pv(s1a + C::KT, PSC ? scale_f16x2(q01, rb) : q01, PSC ? scale_f16x2(q23, rb) : q23, mb);
+    };
+
+    // the finished row: O relative to the maximum M with normaliser Ls, head h, dims d .. d + 3
+    auto emit = [&](int b, int kvh, int h, int d, float M, float Ls, float4 O) {
+        const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+        const int64_t row = int64_t(b) * a.Hq + kvh * G + h;
+        *reinterpret_cast<uint2 *>(a.out + row * D + d) =
+            make_uint2(pack_bf16x2(O.x * inv, O.y * inv), pack_bf16x2(O.z * inv, O.w * inv));
+        // a row without tokens: every weight 2^(z - inf) = 0 (it has none)
+        if (LOGITS && d == 0) a.lse[row] = Ls > 0.f ? M + log2f(Ls) : INFINITY;
+    };
+
+    auto wait_item = [&](int k) {
+        const uint32_t st = uint32_t(k) % R;
+        if (!dead && !mbar_wait_bounded(bars + st * 8, (phase >> st) & 1u, a.wait_ns)) {
+            dead = true;
+            if (lane == 0) atomicOr(a.status, kStatusTimeout);
+        }
+        dead = __any_sync(0xffffffffu, dead);
+        phase ^= 1u << st;
+    };
+
+    int issued = min(kn, R);
+    for (int i = 0; i < issued; ++i) issue(i);
+
+    // ---- the segments of this CTA's range
+    int64_t p = pos0, rem;
+    Span sp;
+    int b = locate(p, sp, rem);
+    int kvh = int(rem / sp.n);
+    int64_t s0 = p - (rem - int64_t(kvh) * sp.n);  // global position of the segment's first item
+    fetch_q(b, kvh);
+    int k = 0;
+    while (true) {
+        const int64_t e0 = s0 + sp.n;
+        const int64_t pe = min(e0, pos1);
+        const int k1 = min(kn, int(max(int64_t(0), (pe - pos0 - warp + NW - 1) / NW)));  // this warp's items before pe
+        const int cb = b, ckvh = kvh;
+        const int64_t cs0 = s0;
+        begin_segment(kvh);
+        // the next segment, and its query
+        const bool more = pe < pos1;
+        if (more) {
+            s0 = e0;
+            if (++kvh == Hkv) {
+                kvh = 0;
+                sp = span_of(a, ++b);
+            }
+            fetch_q(b, kvh);
+        }
+        while (k < k1) {
+            if (k >= wbase + 32) {
+                cur = nxt;
+                wbase += 32;
+                nxt = resolve(wbase + 32);
+                scales(nxt);
+            }
+            // items k and k + 1 (both in this segment)
+            const int n2 = k + 1 < k1 ? 2 : 1;
+            const uint32_t wa = __shfl_sync(0xffffffffu, cur.what, k & 31);
+            const bool c2 = k + 1 < wbase + 32;
+            uint32_t wb = __shfl_sync(0xffffffffu, c2 ? cur.what : nxt.what, (k + 1) & 31);
+            const uint32_t ma = wa & 0xffffu, mb = n2 == 2 ? wb & 0xffffu : 0u;
+            float2 ca{0.f, 0.f}, cbk{0.f, 0.f};
+            if constexpr (PSC) {
+                ca = make_float2(__shfl_sync(0xffffffffu, cur.sk, k & 31), __shfl_sync(0xffffffffu, cur.sv, k & 31));
+                cbk = make_float2(__shfl_sync(0xffffffffu, c2 ? cur.sk : nxt.sk, (k + 1) & 31),
+                                  __shfl_sync(0xffffffffu, c2 ? cur.sv : nxt.sv, (k + 1) & 31));
+            }
+            float *la = nullptr, *lb = nullptr;
+            if constexpr (LOGITS) {
+                const int ja = __shfl_sync(0xffffffffu, cur.j, k & 31);
+                const int jb = __shfl_sync(0xffffffffu, c2 ? cur.j : nxt.j, (k + 1) & 31);
+                float *row = a.logits + (int64_t(cb) * Hkv + ckvh) * a.MBS * (G * BS);
+                la = row + int64_t(ja) * (G * BS);
+                lb = row + int64_t(jb) * (G * BS);
+            }
+            if (ma) wait_item(k);
+            if (mb) wait_item(k + 1);
+            if ((ma || mb) && !dead)
+                step(ring + uint32_t(k % R) * C::STAGE, ma, ca, ring + uint32_t((k + 1) % R) * C::STAGE, mb, cbk, la, lb);
+            __syncwarp();  // every lane has read the stages
+            k += n2;
+            for (; issued < kn && issued < k + R; ++issued) {
+                if (issued >= wbase + 64) break;  // not resolved yet
+                issue(issued);
+            }
+        }
+        // ---- deposit, and merge by the whole CTA
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 4);
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 8);
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 16);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 4);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 8);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 16);
+        float *my = scr + warp * C::SCR;
+        const float un = F8 ? vref : 1.f;
+#pragma unroll
+        for (int mt = 0; mt < NKK; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                my[(2 * q4 + (e & 1)) * C::ROW + 16 * mt + g + (e < 2 ? 0 : 8)] = acc[mt][e] * un;
+        if (g == 0) {
+            sm_ml[warp * 16 + 2 * q4] = m0;
+            sm_ml[warp * 16 + 2 * q4 + 1] = m1;
+            sm_ml[warp * 16 + 8 + 2 * q4] = l0;
+            sm_ml[warp * 16 + 8 + 2 * q4 + 1] = l1;
+        }
+        __syncthreads();
+        const bool whole = cs0 >= pos0 && e0 <= pos1;
+        const int c0 = int(cs0 / L), npieces = int((e0 - 1) / L) - c0 + 1;  // the segment's CTAs
+        float *slot = a.part + (2 * int64_t(blockIdx.x) + (int(blockIdx.x) == c0)) * C::PART;
+        for (int idx = tid; idx < G * (D / 4); idx += C::THREADS) {
+            const int h = idx / (D / 4), d = 4 * (idx % (D / 4));
+            float M = -INFINITY, Ls = 0.f;
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) M = fmaxf(M, sm_ml[w * 16 + h]);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float mw = sm_ml[w * 16 + h], f = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
+                const float4 v = *reinterpret_cast<const float4 *>(scr + w * C::SCR + h * C::ROW + d);
+                Ls += f * sm_ml[w * 16 + 8 + h];
+                O.x += f * v.x;
+                O.y += f * v.y;
+                O.z += f * v.z;
+                O.w += f * v.w;
+            }
+            if (whole) {
+                emit(cb, ckvh, h, d, M, Ls, O);
+            } else {
+                __stcg(reinterpret_cast<float4 *>(slot + h * D + d), O);
+                if (d == 0) {
+                    __stcg(slot + 8 * D + h, M);
+                    __stcg(slot + 8 * D + 8 + h, Ls);
+                }
+            }
+        }
+        if (!whole) {
+            __syncthreads();  // the CTA's partial, published by the release below
+            if (tid == 0) *flag = atomic_add_acq_rel_gpu(a.counters + c0, 1) == npieces - 1;
+            __syncthreads();
+            if (*flag) {
+                for (int idx = tid; idx < G * (D / 4); idx += C::THREADS) {
+                    const int h = idx / (D / 4), d = 4 * (idx % (D / 4));
+                    float M = -INFINITY, Ls = 0.f;
+                    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int i = 0; i < npieces; ++i) {
+                        const float *ps = a.part + (2 * int64_t(c0 + i) + (i == 0)) * C::PART;
+                        const float mw = __ldcg(ps + 8 * D + h), lw = __ldcg(ps + 8 * D + 8 + h);
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(ps + h * D + d));
+                        const float Mn = fmaxf(M, mw);
+                        const float f = M == -INFINITY ? 0.f : fast_exp2(M - Mn);
+                        const float w = mw == -INFINITY ? 0.f : fast_exp2(mw - Mn);
+                        M = Mn;
+                        Ls = Ls * f + lw * w;
+                        O.x = O.x * f + v.x * w;
+                        O.y = O.y * f + v.y * w;
+                        O.z = O.z * f + v.z * w;
+                        O.w = O.w * f + v.w * w;
+                    }
+                    emit(cb, ckvh, h, d, M, Ls, O);
+                }
+                if (tid == 0) a.counters[c0] = 0;
+            }
+        }
+        if (!more) break;
+        __syncthreads();  // the states may be written again
+    }
+    // after a wait that gave up: no copy may land in memory of a CTA that is gone
+    if (dead && lane == 0)
+        for (int st = 0; st < R; ++st) mbar_wait_bounded(bars + st * 8, ((armed >> st) & 1u) ^ 1u, a.wait_ns);
+}
+
+// ---- accumulated weights: p_t = 2^(z_t - lse) summed over the group, added
+// to the cache's weights. 16 lanes per block, in token order.
+constexpr int kAddThreads = 256;
+
+__global__ void __launch_bounds__(kAddThreads) weights_add_kernel(const SubsetArgs a) {
+    pdl_trigger();
+    const int seg = blockIdx.x, b = seg / a.Hkv, kvh = seg % a.Hkv;
+    const int lim = min(max(__ldg(a.ctx + b), 0), a.MBS * kBlockSize);
+    const int t0 = threadIdx.x % kBlockSize;
+    pdl_wait();
+    float ls[kMaxGroup];
+#pragma unroll
+    for (int h = 0; h < kMaxGroup; ++h) ls[h] = h < a.G ? __ldcg(a.lse + int64_t(b) * a.Hq + kvh * a.G + h) : INFINITY;
+    for (int j = blockIdx.y * (kAddThreads / kBlockSize) + threadIdx.x / kBlockSize; j * kBlockSize < lim;
+         j += gridDim.y * (kAddThreads / kBlockSize)) {
+        const int phys = __ldg(a.bt + int64_t(b) * a.MBS + j);
+        if (phys < 0 || int64_t(phys) >= a.NB || j * kBlockSize + t0 >= lim) continue;
+        const float *z = a.logits + (int64_t(seg) * a.MBS + j) * (a.G * kBlockSize) + t0;
+        float zz[kMaxGroup], w = 0.f;
+#pragma unroll
+        for (int h = 0; h < kMaxGroup; ++h) zz[h] = h < a.G ? __ldcg(z + h * kBlockSize) : 0.f;
+#pragma unroll
+        for (int h = 0; h < kMaxGroup; ++h) w += fast_exp2(zz[h] - ls[h]);  // 0 for h >= G
+        // a block of one sequence gets one addition: the same bits every time
+        atomicAdd(a.weights + (int64_t(phys) * a.Hkv + kvh) * kBlockSize + t0, w);
+    }
+}
+
+template <int D, CacheKind KIND, bool LOGITS>
+cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const SubsetArgs &a, int grid,
+                     cudaStream_t stream) {
+    using C = StreamCfg<D, KIND>;
+    const auto kernel = stream_decode_kernel<D, KIND, LOGITS>;
+    const cudaError_t e = smem_once(reinterpret_cast<const void *>(kernel), C::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3(grid), dim3(C::THREADS), C::SMEM, stream, tk, tv, a);
+}
+
+}  // namespace
+
+size_t stream_part_floats(int head_dim) { return size_t(8) * head_dim + 16; }
+
+cudaError_t launch_stream_decode(const CUtensorMap &tk, const CUtensorMap &tv, const SubsetArgs &args, int head_dim,
+                                 CacheKind kind, int sms, cudaStream_t stream) {
+    SubsetArgs a = args;
+    // one CTA per SM; a range holds at least two items per warp, so that a
+    // small call is not spread over CTAs that cost more to merge than to run
+    a.min_items = 12;
+    if (a.weights) {
+        cudaError_t e = head_dim == 128 ? launch_t<128, kCacheBf16, true>(tk, tv, a, sms, stream)
+                                        : launch_t<64, kCacheBf16, true>(tk, tv, a, sms, stream);
+        if (e != cudaSuccess) return e;
+        const int per = kAddThreads / kBlockSize;  // blocks a CTA takes per turn
+        const int x = (a.MBS + per - 1) / per;
+        return launch_pdl(weights_add_kernel, dim3(a.nseq * a.Hkv, x < 16 ? x : 16), dim3(kAddThreads), 0, stream, a);
+    }
+    if (kind == kCacheE4m3) return launch_t<128, kCacheE4m3, false>(tk, tv, a, sms, stream);
+    if (kind == kCacheE4m3Block) return launch_t<128, kCacheE4m3Block, false>(tk, tv, a, sms, stream);
+    return head_dim == 128 ? launch_t<128, kCacheBf16, false>(tk, tv, a, sms, stream)
+                           : launch_t<64, kCacheBf16, false>(tk, tv, a, sms, stream);
+}
+
+}  // namespace pa

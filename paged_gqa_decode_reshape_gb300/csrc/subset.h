@@ -3,8 +3,13 @@
 // evict.cu).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <mutex>
+#include <utility>
+#include <vector>
 
 namespace pa {
 
@@ -29,9 +34,40 @@ struct SubsetArgs {
     int MBS, PMBS, nseq, ngroups, rows, Hq, Hkv, G;
     int window, sinks;            // window: INT_MAX when everything before lim is seen
     float scale_log2;             // softmax scale * log2(e)
+    // workspace
+    int32_t *status;              // status word
+    int32_t *counters;            // [CTAs] arrivals at the segment that begins in a CTA and leaves it (zero between calls)
+    float *part;                  // [2 * CTAs] pieces of segments cut between CTAs: O, m, l
+    float *lse;                   // weights: [nseq][Hq] log2 of the normaliser
+    float *logits;                // weights: [nseq][Hkv][MBS][G][16] logits (log2 domain)
+    uint64_t wait_ns;             // limit of every bounded wait
+    int stop_item;                // failure tests: a warp's copies stop at this item (else INT_MAX)
+    int min_items;                // items of a CTA's range at least
 };
 
-cudaError_t launch_subset_decode(const SubsetArgs &a, int head_dim, CacheKind kind, cudaStream_t stream);
+// Dynamic shared memory limit of a kernel, set once per device.
+inline cudaError_t smem_once(const void *kernel, size_t bytes) {
+    static std::mutex mu;
+    static std::vector<std::pair<int, const void *>> done;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    for (const auto &d : done)
+        if (d.first == dev && d.second == kernel) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    if (e == cudaSuccess) done.emplace_back(dev, kernel);
+    return e;
+}
+
+// one query row per sequence, window and sinks, or (weights set) the dense
+// decode that adds up the attention weights; tk, tv: tensor maps of the caches
+size_t stream_part_floats(int head_dim);
+cudaError_t launch_stream_decode(const CUtensorMap &tk, const CUtensorMap &tv, const SubsetArgs &a, int head_dim,
+                                 CacheKind kind, int sms, cudaStream_t stream);
+
+// query rows of any number per sequence, or shared prefixes (bf16)
+cudaError_t launch_subset_decode(const SubsetArgs &a, int head_dim, cudaStream_t stream);
 
 struct EvictArgs {
     int32_t *kept, *new_lens;     // [B][Hkv][budget], [B]

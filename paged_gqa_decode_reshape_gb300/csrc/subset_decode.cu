@@ -1,13 +1,11 @@
-// subset_decode.cu -- decode attention over a part of the cache (window and
-// sinks), over a shared prefix and a sequence's own tokens, and with the
-// attention weights added up per cached token.
+// subset_decode.cu -- attention of several query rows per sequence over a
+// window and sinks, and over a shared prefix and a sequence's own tokens.
 //
 // For a query row of sequence b, KV head g and the query heads h of its group
 // (z in the log2 domain, z = scale * log2(e) * q_h . K_t):
 //   out_h = sum_t 2^(z_t - m) V_t / sum_t 2^(z_t - m),   m = max_t z_t
 // over the tokens the row sees. One pass with the running maximum and sum;
-// the states of a CTA's warps are merged at the end. The accumulated weights
-// take a second pass over K, with p_t = 2^(z_t - m) / l.
+// the states of a CTA's warps are merged at the end.
 //
 // The plain form: one CTA per (query row, KV head), one warp per token, a lane
 // per D / 32 dims, everything in fp32.
@@ -63,8 +61,7 @@ __device__ __forceinline__ Seen row_seen(const SubsetArgs &a, int row) {
     return s;
 }
 
-// dims [lane * V, lane * V + V) of one cached row, decoded; false: no such block
-template <int D, CacheKind KIND, int V>
+// physical block of the i-th token the row sees, or -1, and the token's offset in it
 __device__ __forceinline__ int64_t block_of(const SubsetArgs &a, const Seen &s, int i, int &off) {
     int phys;
     if (i < s.np) {
@@ -79,40 +76,15 @@ __device__ __forceinline__ int64_t block_of(const SubsetArgs &a, const Seen &s, 
     return phys >= 0 && phys < a.NB ? phys : -1;
 }
 
-__device__ __forceinline__ float e4m3_value(uint8_t c) {
-    return f16_lo(e4m3x2_to_f16x2(c));
+template <int D, int V>
+__device__ __forceinline__ void load_row(const void *cache, int Hkv, int64_t blk, int off, int kvh, int lane,
+                                         float (&x)[V]) {
+    const int64_t e = ((blk * kBlockSize + off) * Hkv + kvh) * D + lane * V;
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = __uint_as_float(uint32_t(static_cast<const uint16_t *>(cache)[e + i]) << 16);
 }
 
-template <int D, CacheKind KIND, int V>
-__device__ __forceinline__ void load_k(const SubsetArgs &a, int64_t blk, int off, int kvh, int lane, float (&x)[V]) {
-    const int64_t e = ((blk * kBlockSize + off) * a.Hkv + kvh) * D + lane * V;
-    if constexpr (KIND == kCacheBf16) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = __uint_as_float(uint32_t(static_cast<const uint16_t *>(a.kc)[e + i]) << 16);
-    } else {
-        const float sc = __ldg(a.k_scale + (KIND == kCacheE4m3 ? kvh : blk * a.Hkv + kvh));
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = e4m3_value(static_cast<const uint8_t *>(a.kc)[e + i]) * sc;
-    }
-}
-
-template <int D, CacheKind KIND, int V>
-__device__ __forceinline__ void load_v(const SubsetArgs &a, int64_t blk, int off, int kvh, int lane, float (&x)[V]) {
-    if constexpr (KIND == kCacheBf16) {
-        const int64_t e = ((blk * kBlockSize + off) * a.Hkv + kvh) * D + lane * V;
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = __uint_as_float(uint32_t(static_cast<const uint16_t *>(a.vc)[e + i]) << 16);
-    } else {
-        const float sc = __ldg(a.v_scale + (KIND == kCacheE4m3 ? kvh : blk * a.Hkv + kvh));
-        const int at = 4 * ((off % 8) / 2) + 2 * (off / 8) + off % 2;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            x[i] = e4m3_value(static_cast<const uint8_t *>(
-                       a.vc)[((blk * a.Hkv + kvh) * D + lane * V + i) * kBlockSize + at]) * sc;
-    }
-}
-
-template <int D, CacheKind KIND>
+template <int D>
 __global__ void __launch_bounds__(kWarps * 32) subset_decode_kernel(const SubsetArgs a) {
     constexpr int V = D / 32;
     __shared__ float sm_acc[kWarps][kMaxGroup][D];
@@ -136,7 +108,7 @@ __global__ void __launch_bounds__(kWarps * 32) subset_decode_kernel(const Subset
     }
     auto logits = [&](int64_t blk, int off, float (&z)[kMaxGroup]) {
         float k[V];
-        load_k<D, KIND, V>(a, blk, off, kvh, lane, k);
+        load_row<D>(a.kc, a.Hkv, blk, off, kvh, lane, k);
 #pragma unroll
         for (int h = 0; h < kMaxGroup; ++h) {
             float d = 0.f;
@@ -149,11 +121,11 @@ __global__ void __launch_bounds__(kWarps * 32) subset_decode_kernel(const Subset
     };
     for (int i = warp; i < n; i += kWarps) {
         int off;
-        const int64_t blk = block_of<D, KIND, V>(a, s, i, off);
+        const int64_t blk = block_of(a, s, i, off);
         if (blk < 0) continue;
         float z[kMaxGroup], v[V];
         logits(blk, off, z);
-        load_v<D, KIND, V>(a, blk, off, kvh, lane, v);
+        load_row<D>(a.vc, a.Hkv, blk, off, kvh, lane, v);
 #pragma unroll
         for (int h = 0; h < kMaxGroup; ++h) {
             const float mn = fmaxf(m[h], z[h]);
@@ -174,15 +146,6 @@ __global__ void __launch_bounds__(kWarps * 32) subset_decode_kernel(const Subset
         }
     }
     __syncthreads();
-    float M[kMaxGroup], Ls[kMaxGroup];
-#pragma unroll
-    for (int h = 0; h < kMaxGroup; ++h) {
-        M[h] = -INFINITY;
-        Ls[h] = 0.f;
-        for (int w = 0; w < kWarps; ++w) M[h] = fmaxf(M[h], sm_m[w][h]);
-        for (int w = 0; w < kWarps; ++w)
-            if (sm_m[w][h] != -INFINITY) Ls[h] += sm_l[w][h] * exp2f(sm_m[w][h] - M[h]);
-    }
     if (warp < a.G) {
         const int h = warp;
         float Mh = -INFINITY, Lh = 0.f;
@@ -198,29 +161,14 @@ __global__ void __launch_bounds__(kWarps * 32) subset_decode_kernel(const Subset
                 __bfloat16_as_ushort(__float2bfloat16_rn(Lh > 0.f ? o / Lh : 0.f));
         }
     }
-    if (!a.weights) return;
-    for (int i = warp; i < n; i += kWarps) {
-        int off;
-        const int64_t blk = block_of<D, KIND, V>(a, s, i, off);
-        if (blk < 0) continue;
-        float z[kMaxGroup], w = 0.f;
-        logits(blk, off, z);
-#pragma unroll
-        for (int h = 0; h < kMaxGroup; ++h)
-            if (h < a.G) w += exp2f(z[h] - M[h]) / Ls[h];
-        if (lane == 0) atomicAdd(a.weights + (blk * a.Hkv + kvh) * kBlockSize + off, w);
-    }
 }
 
 }  // namespace
 
-cudaError_t launch_subset_decode(const SubsetArgs &a, int head_dim, CacheKind kind, cudaStream_t stream) {
+cudaError_t launch_subset_decode(const SubsetArgs &a, int head_dim, cudaStream_t stream) {
     const dim3 grid(a.rows, a.Hkv), block(kWarps * 32);
-    if (kind == kCacheE4m3) return launch_pdl(subset_decode_kernel<128, kCacheE4m3>, grid, block, 0, stream, a);
-    if (kind == kCacheE4m3Block)
-        return launch_pdl(subset_decode_kernel<128, kCacheE4m3Block>, grid, block, 0, stream, a);
-    return head_dim == 128 ? launch_pdl(subset_decode_kernel<128, kCacheBf16>, grid, block, 0, stream, a)
-                           : launch_pdl(subset_decode_kernel<64, kCacheBf16>, grid, block, 0, stream, a);
+    return head_dim == 128 ? launch_pdl(subset_decode_kernel<128>, grid, block, 0, stream, a)
+                           : launch_pdl(subset_decode_kernel<64>, grid, block, 0, stream, a);
 }
 
 }  // namespace pa
