@@ -854,46 +854,69 @@ SubsetArgs subset_args(pa_bf16 *out, const pa_bf16 *query, const void *kc, const
     return a;
 }
 
-// Workspace of the streaming kernel: status word, arrival counters and two
-// piece slots per CTA, then (accumulated weights) normalisers and logits.
-struct StreamWorkspace {
-    size_t part, lse, logits, bytes;
+// What a call of this section needs: the streaming kernel (one query row per
+// sequence), the row-tile kernel (many), or one after the other (prefixes).
+struct SubsetPlan {
+    bool stream, tiles, prefix;
+    int64_t logit_blocks;  // accumulated weights: max_blocks_per_seq
 };
 
-int stream_workspace(StreamWorkspace *w, int *sms, int B, int Hq, int D, int64_t logit_blocks) {
+// The workspace's parts: status word, arrival counters, two piece slots per
+// CTA and kernel, then what the operator keeps per row.
+struct SubsetWorkspace {
+    size_t part, slots, rowres, rowml, desc, lse, logits, bytes;
+    int sms;
+};
+
+int subset_workspace(SubsetWorkspace *w, const SubsetPlan &plan, int64_t rows, int Hq, int Hkv, int D) {
     DecodeGeometry geo;
     const cudaError_t e = decode_geometry(D, &geo);
     if (e != cudaSuccess) return cuda_fail(e);
-    const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    *sms = geo.grid;
-    w->part = 256 + up(size_t(geo.grid) * 4);
-    w->lse = w->part + up(size_t(geo.grid) * 2 * stream_part_floats(D) * 4);
-    w->logits = w->lse + (logit_blocks ? up(size_t(B) * Hq * 4) : 0);
-    w->bytes = w->logits + up(size_t(B) * Hq * logit_blocks * kBlockSize * 4);
+    size_t at = 256;
+    const auto take = [&](bool want, size_t bytes) {
+        const size_t here = at;
+        if (want) at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    w->sms = geo.grid;  // one CTA per SM
+    const size_t heads = size_t(rows) * Hq;
+    take(true, size_t(geo.grid) * 2 * 4);
+    w->part = take(plan.stream, size_t(geo.grid) * 2 * stream_part_floats(D) * 4);
+    w->slots = take(plan.tiles, size_t(geo.grid) * 2 * row_tiles_slot_floats(D) * 4);
+    w->rowres = take(plan.prefix, heads * D * 4);
+    w->rowml = take(plan.prefix, heads * 8);
+    w->desc = take(plan.prefix, size_t(rows) * Hkv * sizeof(int4));
+    w->lse = take(plan.logit_blocks > 0, heads * 4);
+    w->logits = take(plan.logit_blocks > 0, heads * plan.logit_blocks * kBlockSize * 4);
+    w->bytes = at;
     return PA_OK;
 }
 
-size_t stream_workspace_bytes(int batch, int Hq, int Hkv, int D, int64_t logit_blocks) {
-    if (batch <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || batch > kMaxBatch) return 0;
+size_t subset_workspace_bytes(const SubsetPlan &plan, int64_t rows, int64_t max_rows, int Hq, int Hkv, int D) {
+    if (rows <= 0 || rows > max_rows || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
     if (!shape_supported(D, kBlockSize) || Hq / Hkv > kMaxGroup || Hkv > 65535) return 0;
-    StreamWorkspace w;
-    int sms;
-    return stream_workspace(&w, &sms, batch, Hq, D, logit_blocks) == PA_OK ? w.bytes : 0;
+    SubsetWorkspace w;
+    return subset_workspace(&w, plan, rows, Hq, Hkv, D) == PA_OK ? w.bytes : 0;
 }
 
-// the streaming kernel's launch, after the argument checks
-int run_stream(SubsetArgs a, int D, CacheKind kind, void *workspace, size_t workspace_bytes, void *stream) {
-    StreamWorkspace w;
-    int sms = 0;
-    int rc = stream_workspace(&w, &sms, a.nseq, a.Hq, D, a.weights ? a.MBS : 0);
+// the launches, after the argument checks
+int run_subset(SubsetArgs a, const SubsetPlan &plan, int D, CacheKind kind, void *workspace, size_t workspace_bytes,
+               void *stream) {
+    SubsetWorkspace w;
+    int rc = subset_workspace(&w, plan, a.rows, a.Hq, a.Hkv, D);
     if (rc != PA_OK) return rc;
     if (workspace_bytes < w.bytes) return PA_ERR_WORKSPACE;
     uint8_t *p = static_cast<uint8_t *>(workspace);
     a.status = reinterpret_cast<int32_t *>(p);
     a.counters = reinterpret_cast<int32_t *>(p + 256);
     a.part = reinterpret_cast<float *>(p + w.part);
+    a.slots = reinterpret_cast<float *>(p + w.slots);
+    a.rowres = reinterpret_cast<float *>(p + w.rowres);
+    a.rowml = reinterpret_cast<float *>(p + w.rowml);
+    a.desc = plan.prefix ? reinterpret_cast<int4 *>(p + w.desc) : nullptr;
     a.lse = reinterpret_cast<float *>(p + w.lse);
     a.logits = reinterpret_cast<float *>(p + w.logits);
+    a.pgrid = w.sms;
     a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
     a.stop_item = g_stop_item.load(std::memory_order_relaxed);
     const bool fp8 = kind != kCacheBf16;
@@ -901,14 +924,21 @@ int run_stream(SubsetArgs a, int D, CacheKind kind, void *workspace, size_t work
     if ((rc = make_cache_map(&tk, a.kc, a.Hkv, D, kBlockSize, a.NB, fp8)) != PA_OK) return rc;
     if (fp8) std::memset(&tv, 0, sizeof tv);  // an E4M3 V tile is contiguous: plain bulk copies
     else if ((rc = make_cache_map(&tv, a.vc, a.Hkv, D, kBlockSize, a.NB)) != PA_OK) return rc;
-    const cudaError_t e = launch_stream_decode(tk, tv, a, D, kind, sms, static_cast<cudaStream_t>(stream));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (plan.tiles) e = launch_row_tiles(tk, tv, a, D, w.sms, st);
+    if (e == cudaSuccess && plan.stream) e = launch_stream_decode(tk, tv, a, D, kind, w.sms, st);
     return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
+
+constexpr SubsetPlan kWindowPlan{true, false, false, 0}, kWindowMultiPlan{false, true, false, 0},
+    kPrefixPlan{true, true, true, 0};
+SubsetPlan weights_plan(int MBS) { return SubsetPlan{true, false, false, MBS}; }
 
 int run_window(pa_bf16 *out, const pa_bf16 *query, const void *kc, const void *vc, const float *k_scale,
                const float *v_scale, CacheKind kind, const int32_t *bt, int MBS, const int32_t *cu_q,
                const int32_t *ctx, int nseq, int rows, int Hq, int Hkv, int D, int BS, int64_t NB, int window,
-               int sinks, float scale, void *workspace, size_t workspace_bytes, size_t need, void *stream) {
+               int sinks, float scale, void *workspace, size_t workspace_bytes, void *stream) {
     const int rc = check_subset_args(out, query, kc, vc, bt, MBS, ctx, nseq, rows, cu_q ? kMaxWindowRows : kMaxBatch,
                                      Hq, Hkv, D, BS, NB, scale, workspace);
     if (rc != PA_OK) return rc;
@@ -923,10 +953,7 @@ int run_window(pa_bf16 *out, const pa_bf16 *query, const void *kc, const void *v
     a.cu_q = cu_q;
     a.window = window;
     a.sinks = sinks;
-    if (!cu_q) return run_stream(a, D, kind, workspace, workspace_bytes, stream);
-    if (workspace_bytes < need) return PA_ERR_WORKSPACE;
-    const cudaError_t e = launch_subset_decode(a, D, static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? PA_OK : cuda_fail(e);
+    return run_subset(a, cu_q ? kWindowMultiPlan : kWindowPlan, D, kind, workspace, workspace_bytes, stream);
 }
 
 }  // namespace
@@ -934,7 +961,7 @@ int run_window(pa_bf16 *out, const pa_bf16 *query, const void *kc, const void *v
 extern "C" {
 
 size_t pa_decode_window_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim) {
-    return stream_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, 0);
+    return subset_workspace_bytes(kWindowPlan, batch, kMaxBatch, num_q_heads, num_kv_heads, head_dim);
 }
 
 int pa_decode_window(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *key_cache, const pa_bf16 *value_cache,
@@ -944,7 +971,7 @@ int pa_decode_window(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *key_cach
     return run_window(out, query, key_cache, value_cache, nullptr, nullptr, kCacheBf16, block_tables,
                       max_blocks_per_seq, nullptr, context_lens, batch, batch, num_q_heads, num_kv_heads, head_dim,
                       block_size, num_blocks, window, sinks, scale, workspace, workspace_bytes,
-                      0, stream);
+                      stream);
 }
 
 int pa_decode_window_fp8(pa_bf16 *out, const pa_bf16 *query, const pa_e4m3 *key_cache, const pa_e4m3 *value_cache,
@@ -955,7 +982,7 @@ int pa_decode_window_fp8(pa_bf16 *out, const pa_bf16 *query, const pa_e4m3 *key_
     return run_window(out, query, key_cache, value_cache, k_scale, v_scale, kCacheE4m3, block_tables,
                       max_blocks_per_seq, nullptr, context_lens, batch, batch, num_q_heads, num_kv_heads, head_dim,
                       block_size, num_blocks, window, sinks, scale, workspace, workspace_bytes,
-                      0, stream);
+                      stream);
 }
 
 int pa_decode_window_fp8_block(pa_bf16 *out, const pa_bf16 *query, const pa_e4m3 *key_cache,
@@ -967,13 +994,13 @@ int pa_decode_window_fp8_block(pa_bf16 *out, const pa_bf16 *query, const pa_e4m3
     return run_window(out, query, key_cache, value_cache, k_bscale, v_bscale, kCacheE4m3Block, block_tables,
                       max_blocks_per_seq, nullptr, context_lens, batch, batch, num_q_heads, num_kv_heads, head_dim,
                       block_size, num_blocks, window, sinks, scale, workspace, workspace_bytes,
-                      0, stream);
+                      stream);
 }
 
 size_t pa_decode_window_multi_workspace_size(int batch, int total_q, int num_q_heads, int num_kv_heads,
                                              int head_dim) {
-    if (total_q <= 0 || total_q > kMaxWindowRows) return 0;
-    return pa_decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim);
+    if (batch <= 0 || batch > kMaxBatch) return 0;
+    return subset_workspace_bytes(kWindowMultiPlan, total_q, kMaxWindowRows, num_q_heads, num_kv_heads, head_dim);
 }
 
 int pa_decode_window_multi(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *key_cache, const pa_bf16 *value_cache,
@@ -984,14 +1011,12 @@ int pa_decode_window_multi(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *ke
     if (!cu_seqlens_q) return PA_ERR_INVALID_ARG;
     return run_window(out, query, key_cache, value_cache, nullptr, nullptr, kCacheBf16, block_tables,
                       max_blocks_per_seq, cu_seqlens_q, context_lens, batch, total_q, num_q_heads, num_kv_heads,
-                      head_dim, block_size, num_blocks, window, sinks, scale, workspace, workspace_bytes,
-                      pa_decode_window_multi_workspace_size(batch, total_q, num_q_heads, num_kv_heads, head_dim),
-                      stream);
+                      head_dim, block_size, num_blocks, window, sinks, scale, workspace, workspace_bytes, stream);
 }
 
 size_t pa_decode_prefix_workspace_size(int batch, int num_groups, int num_q_heads, int num_kv_heads, int head_dim) {
     if (num_groups <= 0 || num_groups > kMaxBatch) return 0;
-    return pa_decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim);
+    return subset_workspace_bytes(kPrefixPlan, batch, kMaxBatch, num_q_heads, num_kv_heads, head_dim);
 }
 
 int pa_decode_prefix(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *key_cache, const pa_bf16 *value_cache,
@@ -1008,8 +1033,6 @@ int pa_decode_prefix(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *key_cach
         return PA_ERR_INVALID_ARG;
     if (num_groups > kMaxBatch || int64_t(max_prefix_blocks) * block_size > int64_t(1) << 30)
         return PA_ERR_UNSUPPORTED;
-    if (workspace_bytes < pa_decode_prefix_workspace_size(batch, num_groups, num_q_heads, num_kv_heads, head_dim))
-        return PA_ERR_WORKSPACE;
     SubsetArgs a = subset_args(out, query, key_cache, value_cache, block_tables, max_blocks_per_seq, context_lens,
                                batch, batch, num_q_heads, num_kv_heads, num_blocks, scale);
     a.pt = prefix_tables;
@@ -1017,14 +1040,14 @@ int pa_decode_prefix(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *key_cach
     a.plen = prefix_lens;
     a.cu_g = cu_group;
     a.ngroups = num_groups;
-    const cudaError_t e = launch_subset_decode(a, head_dim, static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? PA_OK : cuda_fail(e);
+    return run_subset(a, kPrefixPlan, head_dim, kCacheBf16, workspace, workspace_bytes, stream);
 }
 
 size_t pa_decode_weights_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim,
                                         int max_blocks_per_seq) {
     if (max_blocks_per_seq <= 0 || int64_t(max_blocks_per_seq) * kBlockSize > int64_t(1) << 30) return 0;
-    return stream_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq);
+    return subset_workspace_bytes(weights_plan(max_blocks_per_seq), batch, kMaxBatch, num_q_heads, num_kv_heads,
+                                  head_dim);
 }
 
 int pa_decode_weights(pa_bf16 *out, float *weights, const pa_bf16 *query, const pa_bf16 *key_cache,
@@ -1040,7 +1063,7 @@ int pa_decode_weights(pa_bf16 *out, float *weights, const pa_bf16 *query, const 
     SubsetArgs a = subset_args(out, query, key_cache, value_cache, block_tables, max_blocks_per_seq, context_lens,
                                batch, batch, num_q_heads, num_kv_heads, num_blocks, scale);
     a.weights = weights;
-    return run_stream(a, head_dim, kCacheBf16, workspace, workspace_bytes, stream);
+    return run_subset(a, weights_plan(max_blocks_per_seq), head_dim, kCacheBf16, workspace, workspace_bytes, stream);
 }
 
 int pa_reset_weights(float *weights, const int64_t *slot_mapping, int64_t num_tokens, int num_kv_heads,

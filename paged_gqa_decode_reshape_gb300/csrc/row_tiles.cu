@@ -1,0 +1,733 @@
+// row_tiles.cu -- attention of many query rows over the same cached tokens on
+// the fifth-generation tensor cores (sm_103a): query rows of one sequence over
+// its window and sinks (speculative tokens, prefill chunks), and the rows of a
+// group of sequences over their shared prefix.
+//
+// With rows r = (query row, head of the KV head's group), tokens t, z = scale *
+// log2(e) * Q K^T:  O_r = sum_t 2^(z_rt - m_r) V_t,  l_r = sum_t 2^(z_rt - m_r),
+// out = O / l, one pass with a running m.
+//
+// Bound: 4 D flops per (row, token) against 4 D bytes per token and KV head:
+// with R rows sharing the tokens R flops per byte, so a call is bound by HBM
+// below a few hundred rows and by the products and the exponentials (one per
+// 4 D flops) above.
+//
+//  * A unit is up to 2 x 128 rows of one KV head: two row tiles of RQ =
+//    128 / G query rows x G heads, over the union of the blocks they see, in
+//    tiles of 128 tokens (8 blocks). Units are concatenated, tile by tile, and
+//    cut into equal ranges, one per CTA of a persistent grid: any mix of
+//    lengths loads the SMs evenly.
+//  * Roles: a producer warp copies K and V tiles by TMA (one box per block and
+//    64 dims, 128-byte swizzle) into a ring of four 128-token buffers; one
+//    thread issues the matrix products; each row tile has four softmax warps,
+//    one thread per row, with its logits S (128 columns, overwritten by the
+//    bf16 probabilities P) and its output O (D columns) in tensor memory: 2 x
+//    256 of 512 columns. While one row tile's warps work on their softmax the
+//    tensor core runs P V and the next Q K^T of the other.
+//  * O is rescaled in tensor memory only when a row's maximum has grown by more
+//    than 2^8 since the last time: until then probabilities up to 2^8 are exact
+//    multiples, bf16 keeps its 8 bits at any magnitude, and l is fp32.
+//  * Masks: a 16-bit mask per block and row on the tiles at an edge, none
+//    inside. V rows no row of the unit sees are zeroed in shared memory. A
+//    token that only other rows of the tile see meets them as 0 * V, which
+//    is not 0 if V is not finite: a row whose result is not finite is computed
+//    again, over its own tokens only, by its warp.
+//  * Units cut between CTAs leave (O, m, l) per row and piece in the workspace;
+//    the CTA that completes the count merges them in piece order (for prefixes
+//    the own-token kernel does).
+#include <climits>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "subset.h"
+#include "tcgen05.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kPreCap = 512;     // entries of the work prefix in shared memory
+constexpr int kTileTok = 128;    // tokens per tile
+constexpr int kTileBlk = kTileTok / kBlockSize;
+constexpr int kStages = 4;       // K / V tiles in the ring
+constexpr int kInfo = 8;         // tile descriptions in flight
+constexpr int kWarpsRT = 12;     // 2 x 4 softmax, producer, products, two that only make up a warpgroup
+constexpr float kGrow = 8.f;     // log2 growth of a maximum that rescales O
+
+__device__ __forceinline__ uint64_t l2_policy_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+template <int D>
+struct RowCfg {
+    static constexpr int HV = D / 64;                      // 64-dim halves
+    static constexpr int HALF = kTileTok * 128;            // bytes of a half tile
+    static constexpr int TILE = HV * HALF;                 // a K, V or Q tile
+    static constexpr int BLK = kBlockSize * 128;           // a block's 64 dims
+    static constexpr size_t off_ring = 2 * size_t(TILE);   // after the two Q tiles
+    static constexpr size_t off_bars = off_ring + size_t(kStages) * TILE;
+    static constexpr size_t off_info = off_bars + 160;
+    static constexpr size_t off_misc = off_info + kInfo * 4;
+    static constexpr size_t off_pre = off_misc + 32;
+    static constexpr size_t SMEM = 1024 + off_pre + (kPreCap + 1) * 8;
+    static constexpr int SLOT = 2 * 128 * (D + 2);         // floats of a piece: per row tile O[128][D], m[128], l[128]
+};
+
+// One unit of work, the same in every role.
+struct Unit {
+    int s, kvh, u;         // sequence (or group), KV head, index of the 2 RQ-row unit
+    int r0, nr;            // first query row, query rows (<= 2 RQ)
+    int lim0, lim1;        // tokens before which the first and the last row see
+    int nb, nb1, jw;       // blocks: nb1 sink blocks, then jw, jw + 1, ...
+    int n;                 // tiles (at least one)
+};
+
+template <bool PREFIX>
+struct Work {
+    const SubsetArgs &a;
+    const int RQ;
+    __device__ Work(const SubsetArgs &a_) : a(a_), RQ(kTileTok / a_.G) {}
+    __device__ int count() const { return PREFIX ? a.ngroups : a.nseq; }
+    __device__ void rows(int s, int &r0, int &nr) const {
+        const int32_t *cu = PREFIX ? a.cu_g : a.cu_q;
+        r0 = min(max(__ldg(cu + s), 0), a.rows);
+        nr = min(max(__ldg(cu + s + 1), r0), a.rows) - r0;
+    }
+    __device__ int units(int s) const {
+        int r0, nr;
+        rows(s, r0, nr);
+        return (nr + 2 * RQ - 1) / (2 * RQ);
+    }
+    // tokens before which row i (of n) of sequence s sees
+    __device__ int limit(int s, int i, int n) const {
+        if (PREFIX) return min(max(__ldg(a.plen + s), 0), a.PMBS * kBlockSize);
+        return max(min(max(__ldg(a.ctx + s), 0), a.MBS * kBlockSize) - (n - 1 - i), 0);
+    }
+    __device__ int sinks() const { return PREFIX ? 0 : a.sinks; }
+    __device__ int lower(int lim) const {  // first token of the window
+        return PREFIX || a.window >= lim ? 0 : lim - a.window;
+    }
+    __device__ Unit unit(int s, int kvh, int u) const {
+        Unit x;
+        int n;
+        x.s = s;
+        x.kvh = kvh;
+        x.u = u;
+        rows(s, x.r0, n);
+        const int i0 = u * 2 * RQ;
+        x.nr = max(min(n - i0, 2 * RQ), 0);
+        x.lim0 = limit(s, i0, n);
+        x.lim1 = limit(s, i0 + x.nr - 1, n);
+        x.r0 += i0;
+        x.nb1 = (min(sinks(), x.lim1) + kBlockSize - 1) / kBlockSize;
+        x.jw = max(lower(x.lim0) / kBlockSize, x.nb1);
+        x.nb = x.nb1 + max((x.lim1 + kBlockSize - 1) / kBlockSize - x.jw, 0);
+        x.n = max((x.nb + kTileBlk - 1) / kTileBlk, 1);
+        return x;
+    }
+    // tiles of one KV head of sequence s, by a whole warp
+    __device__ int64_t tiles(int s) const {
+        const int nu = units(s);
+        int64_t t = 0;
+        for (int u = threadIdx.x & 31; u < nu; u += 32) t += unit(s, 0, u).n;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        return t;
+    }
+};
+
+template <int D, bool PREFIX>
+__global__ void __launch_bounds__(kWarpsRT * 32, 1)
+    row_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const SubsetArgs a) {
+    using C = RowCfg<D>;
+    constexpr int BS = kBlockSize, HV = C::HV;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *bp = smem_raw + (base - raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int Hkv = a.Hkv, G = a.G;
+    const Work<PREFIX> work(a);
+    const int RQ = work.RQ;
+    const uint32_t ring = base + uint32_t(C::off_ring);
+    const uint32_t kv_full = base + uint32_t(C::off_bars), kv_empty = kv_full + kStages * 8;
+    const uint32_t q_ready = kv_empty + kStages * 8, s_full = q_ready + 16, p_ready = s_full + 16;
+    const uint32_t drained = p_ready + 16, piece_bar = drained + 8, last_bar = piece_bar + 16;
+    volatile int *info = reinterpret_cast<volatile int *>(bp + C::off_info);
+    volatile int *misc = reinterpret_cast<volatile int *>(bp + C::off_misc);  // [0] tensor memory, [1] gave up, [4 + w] completes the count
+    int64_t *pre = reinterpret_cast<int64_t *>(bp + C::off_pre);
+
+    pdl_trigger();
+    if (tid == 0) {
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(kv_full + 8 * i, 1);
+            mbar_init(kv_empty + 8 * i, 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(q_ready + 8 * w, 128);
+            mbar_init(s_full + 8 * w, 1);
+            mbar_init(p_ready + 8 * w, 128);
+            mbar_init(piece_bar + 8 * w, 4);
+            mbar_init(last_bar + 8 * w, 1);
+        }
+        mbar_init(drained, 1);
+        fence_barrier_init();
+        misc[1] = 0;
+        pre[0] = 0;
+    }
+    // ---- tiles per KV head of groups of `str` sequences, and their prefix sums
+    const int ns = work.count(), str = (ns + kPreCap - 1) / kPreCap, np = (ns + str - 1) / str;
+    for (int i = warp; i < np; i += kWarpsRT) {
+        int64_t t = 0;
+        for (int s = i * str; s < min((i + 1) * str, ns); ++s) t += work.tiles(s);
+        if (lane == 0) pre[i + 1] = t;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int64_t carry = 0;
+        for (int i0 = 0; i0 < np; i0 += 32) {
+            int64_t v = i0 + lane < np ? pre[i0 + lane + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            if (i0 + lane < np) pre[i0 + lane + 1] = carry + v;
+            carry += __shfl_sync(0xffffffffu, v, 31);
+        }
+    }
+    __syncthreads();
+    if (PREFIX) pdl_wait();
+    if constexpr (PREFIX) {  // sequences of no group have no prefix part
+        for (int b = blockIdx.x * (kWarpsRT * 32) + tid; b < a.rows; b += gridDim.x * (kWarpsRT * 32)) {
+            int lo = 0, hi = a.ngroups;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (__ldg(a.cu_g + mid) <= b) lo = mid; else hi = mid;
+            }
+            if (b < __ldg(a.cu_g + lo) || b >= __ldg(a.cu_g + lo + 1))
+                for (int h = 0; h < Hkv; ++h) a.desc[int64_t(b) * Hkv + h] = make_int4(0, 0, 0, 0);
+        }
+    }
+    const int64_t total = int64_t(Hkv) * pre[np];
+    const int64_t L = max((total + gridDim.x - 1) / gridDim.x, int64_t(a.min_items));
+    const int64_t pos0 = int64_t(blockIdx.x) * L, pos1 = min(total, pos0 + L);
+    if (pos0 >= pos1) return;  // whole CTA: nothing to do
+
+    if (warp == 9) tmem_alloc(smem_u32(const_cast<int *>(misc)), 512);
+    // ---- the first unit, by every warp
+    Unit x;
+    int64_t s0;  // global position of its first tile
+    int nu;      // units per KV head of its sequence
+    {
+        int lo = 0, hi = np;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (int64_t(Hkv) * pre[mid] <= pos0) lo = mid; else hi = mid;
+        }
+        int s = lo * str;
+        int64_t rem = pos0 - int64_t(Hkv) * pre[lo], t = work.tiles(s);
+        while (rem >= int64_t(Hkv) * t && s + 1 < ns) {
+            rem -= int64_t(Hkv) * t;
+            t = work.tiles(++s);
+        }
+        const int kvh = int(rem / t);
+        rem -= int64_t(kvh) * t;
+        nu = work.units(s);
+        int u = 0;
+        for (int u0 = 0; u0 < nu; u0 += 32) {  // 32 units at a time
+            const int n = u0 + lane < nu ? work.unit(s, kvh, u0 + lane).n : 0;
+            int64_t e = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, e, o);
+                if (lane >= o) e += v;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, n > 0 && e > rem);
+            if (past) {
+                const int at = __ffs(past) - 1;
+                u = u0 + at;
+                rem -= __shfl_sync(0xffffffffu, e - n, at);
+                break;
+            }
+            rem -= __shfl_sync(0xffffffffu, e, 31);
+        }
+        x = work.unit(s, kvh, u);
+        s0 = pos0 - rem;
+    }
+    auto next_unit = [&]() {
+        s0 += x.n;
+        int s = x.s, kvh = x.kvh, u = x.u + 1;
+        if (u == nu) {
+            u = 0;
+            if (++kvh == Hkv) {
+                kvh = 0;
+                do nu = work.units(++s);
+                while (nu == 0 && s + 1 < ns);  // positions are left, so there is one
+            }
+        }
+        x = work.unit(s, kvh, u);
+    };
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = uint32_t(misc[0]);
+    if (!PREFIX) pdl_wait();
+    auto give_up = [&]() {
+        if (lane == 0) {
+            misc[1] = 1;
+            atomicOr(a.status, kStatusTimeout);
+        }
+    };
+    // wait unless the CTA gave up; false: it has
+    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        const bool ok = !misc[1] && mbar_wait_bounded(bar, parity & 1u, a.wait_ns);
+        if (__all_sync(0xffffffffu, ok)) return true;
+        give_up();
+        return false;
+    };
+
+    // registers: the 168 per thread of the launch, 224 + 224 + 56 over its three warpgroups
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 8) {
+        // ============================================================ producer
+        const int32_t *table = PREFIX ? a.pt : a.bt;
+        const int mbs = PREFIX ? a.PMBS : a.MBS;
+        const uint64_t policy = l2_policy_normal();  // other units of the KV head read the same blocks
+        uint32_t fill = 0, tile_no = 0;  // ring buffers and tiles so far
+        bool ok = true;
+        for (int64_t p = pos0; ok && p < pos1;) {
+            const int t0 = int(p - s0), t1 = int(min(pos1 - s0, int64_t(x.n)));
+            // physical blocks of 32 list entries (4 tiles), one per lane
+            auto entry = [&](int e) -> int {
+                if (e >= x.nb) return -1;
+                const int j = e < x.nb1 ? e : e - x.nb1 + x.jw;
+                const int ph = __ldg(table + int64_t(x.s) * mbs + j);
+                return ph >= 0 && int64_t(ph) < a.NB ? ph : -1;
+            };
+            int cur = entry(t0 * kTileBlk + lane), nxt = entry(t0 * kTileBlk + 32 + lane), at = t0;
+            for (int t = t0; t < t1; ++t, ++tile_no) {
+                if (t == at + 4) {
+                    at = t;
+                    cur = nxt;
+                    nxt = entry(t * kTileBlk + 32 + lane);
+                }
+                const int i = lane / HV, hf = lane % HV;  // this lane's block and half
+                const int ph = __shfl_sync(0xffffffffu, cur, (t - at) * kTileBlk + (i & 7));
+                const unsigned live = __ballot_sync(0xffffffffu, lane < 8 * HV && hf == 0 && ph >= 0);
+                unsigned blocks = 0;  // bit i: block i of the tile is there
+#pragma unroll
+                for (int b = 0; b < 8; ++b) blocks |= ((live >> (b * HV)) & 1u) << b;
+                const uint32_t bytes = uint32_t(__popc(blocks)) * C::BLK * HV;
+                for (int kv = 0; ok && kv < 2; ++kv, ++fill) {
+                    const uint32_t st = fill % kStages;
+                    if (fill >= kStages) ok = wait(kv_empty + 8 * st, fill / kStages + 1);
+                    if (!ok || int(fill) >= a.stop_item) {
+                        ok = ok && int(fill) < a.stop_item;
+                        break;
+                    }
+                    if (lane == 0) {
+                        if (kv == 0) info[tile_no % kInfo] = int(blocks);
+                        if (bytes) mbar_arrive_expect_tx(kv_full + 8 * st, bytes);
+                        else mbar_arrive(kv_full + 8 * st);
+                    }
+                    __syncwarp();
+                    if (lane < 8 * HV && ph >= 0)
+                        tma_load_4d(ring + st * C::TILE + hf * C::HALF + i * C::BLK, kv ? &tm_v : &tm_k,
+                                    kv_full + 8 * st, hf * 64, x.kvh, 0, ph, policy);
+                }
+                if (!ok) break;
+            }
+            p = s0 + t1;
+            if (p < pos1) next_unit();
+        }
+        // no copy may land after the CTA is gone
+        for (uint32_t f = fill > kStages ? fill - kStages : 0; f < fill; ++f)
+            mbar_wait_bounded(kv_full + 8 * (f % kStages), (f / kStages) & 1u, a.wait_ns);
+    } else if (warp == 9) {
+        // ====================================================== matrix products
+        constexpr uint32_t id_s = tc_idesc(128, 128, false), id_o = tc_idesc(128, D, true);
+        uint32_t use = 0, tile_no = 0;          // ring buffers and tiles so far
+        uint32_t nq[2] = {0, 0}, np_[2] = {0, 0};  // phases of q_ready and p_ready
+        bool ok = true;
+        // S_w = Q_w K^T from ring buffer st
+        auto qk = [&](int w, uint32_t st) {
+            const uint32_t q = base + w * C::TILE, k = ring + st * C::TILE;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t o = (kk / 4) * C::HALF + (kk % 4) * 32;
+                tc_mma_ss(tmem + 256 * w, tc_desc(q + o, 16, 1024), tc_desc(k + o, 16, 1024), id_s, kk > 0);
+            }
+        };
+        // O_w (+)= P_w V from ring buffer st
+        auto pv = [&](int w, uint32_t st, bool first) {
+            const uint32_t v = ring + st * C::TILE;
+#pragma unroll
+            for (int kk = 0; kk < kTileTok / 16; ++kk)
+                tc_mma_ts(tmem + 256 * w + 128, tmem + 256 * w + 8 * kk, tc_desc(v + kk * 2048, C::HALF, 1024), id_o,
+                          !first || kk > 0);
+        };
+        for (int64_t p = pos0; ok && p < pos1;) {
+            const int t0 = int(p - s0), t1 = int(min(pos1 - s0, int64_t(x.n)));
+            const int nact = x.nr > RQ ? 2 : 1;
+            for (int t = t0; ok && t <= t1; ++t) {
+                const uint32_t ks = use % kStages, vs = (use - 1) % kStages;  // K of tile t, V of tile t - 1
+                if (t < t1 && !(ok = wait(kv_full + 8 * ks, use / kStages))) break;
+                if (t > t0) {
+                    if (!(ok = wait(kv_full + 8 * vs, (use - 1) / kStages))) break;
+                    // V rows nobody sees: blocks that are not there, and what lies past the last row's limit
+                    const int blocks = info[(tile_no - 1) % kInfo];
+                    const int e_last = x.nb - 1, tail = x.lim1 % BS;
+                    const int lb = e_last - (t - 1) * kTileBlk;  // the unit's last block, if in this tile
+                    const bool cut = tail && lb >= 0 && lb < kTileBlk;
+                    if (blocks != 0xff || cut) {
+                        for (int idx = lane; idx < kTileTok * HV * 8; idx += 32) {
+                            const int c = idx & 7, row = (idx >> 3) % kTileTok, hf = idx / (8 * kTileTok);
+                            const int i = row / BS;
+                            if (!((blocks >> i) & 1) || (cut && i == lb && row % BS >= tail))
+                                *reinterpret_cast<uint4 *>(bp + C::off_ring + vs * C::TILE + hf * C::HALF + row * 128 +
+                                                           c * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async();
+                        __syncwarp();
+                    }
+                }
+                for (int w = 0; w < nact; ++w) {
+                    if (t == t0) ok = wait(q_ready + 8 * w, nq[w]++);
+                    else ok = wait(p_ready + 8 * w, np_[w]++);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        if (t > t0) pv(w, vs, t == t0 + 1);
+                        if (t < t1) qk(w, ks);
+                        tc_commit(s_full + 8 * w);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (lane == 0) {
+                    if (t > t0) tc_commit(kv_empty + 8 * vs);
+                    if (t < t1) tc_commit(kv_empty + 8 * ks);
+                }
+                __syncwarp();
+                if (t < t1) {
+                    use += 2;  // this K, and the V that follows it
+                    ++tile_no;
+                }
+            }
+            p = s0 + t1;
+            if (p < pos1) next_unit();
+        }
+        if (!ok) {
+            // gave up: the products in flight end before the memory they use goes
+            if (lane == 0) tc_commit(drained);
+            __syncwarp();
+            mbar_wait_bounded(drained, 0, a.wait_ns);
+        }
+    }
+    } else {
+        // ============================================================= softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        const int w = warp >> 2, row = tid & 127;
+        const uint32_t lane_base = uint32_t(warp & 3) << 21;  // this warp's 32 of the 128 lanes
+        const uint32_t ts = tmem + lane_base + 256 * w, to = ts + 128;
+        const int i = row / G, h = row - i * G;
+        uint32_t ph = 0, tile_no = 0, cuts = 0;
+        bool ok = true;
+        for (int64_t p = pos0; ok && p < pos1;) {
+            const int t0 = int(p - s0), t1 = int(min(pos1 - s0, int64_t(x.n)));
+            const int ir = w * RQ + i;  // query row of the unit
+            const bool act = i < RQ && ir < x.nr;
+            if (w == 0 || x.nr > RQ) {
+                // ---- the row's query into shared memory
+                {
+                    const uint4 *src = reinterpret_cast<const uint4 *>(
+                        a.q + (int64_t(x.r0 + ir) * a.Hq + x.kvh * G + h) * D);
+                    uint8_t *dst = bp + w * C::TILE + row * 128;
+                    uint4 v[D / 8];
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) v[c] = act ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c)
+                        *reinterpret_cast<uint4 *>(dst + (c / 8) * C::HALF + (((c % 8) ^ (row & 7)) << 4)) = v[c];
+                    fence_proxy_async();
+                    tc_fence_before();  // and the previous unit's reads of O
+                    mbar_arrive(q_ready + 8 * w);
+                }
+                int lim = 0;
+                if (act) {
+                    if (PREFIX) {
+                        lim = x.lim1;
+                    } else {  // lim1 belongs to the unit's last row
+                        const int c = min(max(__ldg(a.ctx + x.s), 0), a.MBS * BS);
+                        int rr, nn;
+                        work.rows(x.s, rr, nn);
+                        lim = max(c - (nn - 1 - (x.r0 - rr + ir)), 0);
+                    }
+                }
+                const int S1 = min(work.sinks(), lim), lo = max(S1, work.lower(lim));
+                float m = -INFINITY, l = 0.f;
+                for (int t = t0; t < t1; ++t) {
+                    if (!(ok = wait(s_full + 8 * w, ph++))) break;
+                    tc_fence_after();
+                    const int blocks = info[(tile_no + (t - t0)) % kInfo];
+                    const int e0 = t * kTileBlk;
+                    auto tok = [&](int e) { return (e < x.nb1 ? e : e - x.nb1 + x.jw) * BS; };
+                    const int ta = tok(e0);
+                    const bool joined = e0 >= x.nb1 || e0 + kTileBlk <= x.nb1 || x.jw == x.nb1;
+                    const bool inside = blocks == 0xff && joined &&
+                                        (ta + kTileTok <= S1 || (ta >= lo && ta + kTileTok <= lim));
+                    const bool masked = !__all_sync(0xffffffffu, inside || !act);
+                    float s[kTileTok];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, reinterpret_cast<uint32_t(&)[32]>(s[32 * c]));
+                    tc_wait_ld();
+                    if (masked) {
+#pragma unroll
+                        for (int b = 0; b < kTileBlk; ++b) {
+                            const int tb = tok(e0 + b);
+                            auto bits = [&](int from, int to) -> uint32_t {
+                                const int y0 = min(max(from - tb, 0), 16), y1 = min(max(to - tb, 0), 16);
+                                return y1 > y0 ? ((1u << y1) - 1u) & ~((1u << y0) - 1u) : 0u;
+                            };
+                            const uint32_t mk = (blocks >> b) & 1 ? bits(0, S1) | bits(lo, lim) : 0u;
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                if (!((mk >> c) & 1u)) s[16 * b + c] = -INFINITY;
+                        }
+                    }
+                    float mx = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
+#pragma unroll
+                    for (int c = 4; c < kTileTok; c += 4) {
+                        mx = fmaxf(mx, s[c]);
+                        mx1 = fmaxf(mx1, s[c + 1]);
+                        mx2 = fmaxf(mx2, s[c + 2]);
+                        mx3 = fmaxf(mx3, s[c + 3]);
+                    }
+                    mx = fmaxf(fmaxf(mx, mx1), fmaxf(mx2, mx3)) * a.scale_log2;
+                    const bool grow = mx > m + kGrow || (m == -INFINITY && mx > m);
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float f = grow ? (m == -INFINITY ? 0.f : fast_exp2(m - mx)) : 1.f;
+                        if (grow) m = mx;
+                        l *= f;
+                        if (t > t0) {  // P V of the tile before is complete: S of this one was issued after it
+#pragma unroll
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                tmem_ld32(to + 32 * c, o);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st32(to + 32 * c, o);
+                            }
+                        }
+                    }
+                    const float mr = m == -INFINITY ? 0.f : m;
+                    float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const int k = 64 * c + 2 * e;
+                            const float p0 = fast_exp2(fmaf(s[k], a.scale_log2, -mr));
+                            const float p1 = fast_exp2(fmaf(s[k + 1], a.scale_log2, -mr));
+                            const float p2 = fast_exp2(fmaf(s[k + 2], a.scale_log2, -mr));
+                            const float p3 = fast_exp2(fmaf(s[k + 3], a.scale_log2, -mr));
+                            l0 += p0;
+                            l1 += p1;
+                            l2 += p2;
+                            l3 += p3;
+                            pk[e] = pack_bf16x2(p0, p1);
+                            pk[e + 1] = pack_bf16x2(p2, p3);
+                        }
+                        tmem_st32(ts + 32 * c, pk);
+                    }
+                    l += (l0 + l1) + (l2 + l3);
+                    tc_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(p_ready + 8 * w);
+                }
+                // ---- the end of the unit, or of this CTA's piece of it
+                if (ok) ok = wait(s_full + 8 * w, ph++);
+                if (!ok) break;
+                tc_fence_after();
+                const bool whole = t0 == 0 && t1 == x.n;
+                const int64_t orow = int64_t(x.r0 + ir) * a.Hq + x.kvh * G + h;
+                const int c0 = int(s0 / L);
+                float *slot = a.slots + (2 * int64_t(blockIdx.x) + (int(blockIdx.x) == c0)) * C::SLOT + w * (C::SLOT / 2);
+                const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
+                bool bad = false;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    __syncwarp();
+                    tmem_ld32(to + 32 * c, o);
+                    tc_wait_ld();
+                    if (m == -INFINITY && l == 0.f) {  // no token seen: 0, whatever the products held
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0u;
+                    }
+                    if (!act) {
+                    } else if (!PREFIX && whole) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * D + 32 * c);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            float v[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                v[k] = __uint_as_float(o[e + k]) * inv;
+                                bad |= !(fabsf(v[k]) <= 3.4028234e38f);
+                            }
+                            dst[e / 8] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                    pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+                        }
+                    } else {
+                        uint4 *dst = reinterpret_cast<uint4 *>((PREFIX && whole ? a.rowres + orow * D
+                                                                               : slot + row * D) + 32 * c);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) __stcg(dst + e / 4, make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+                    }
+                }
+                if (act && (PREFIX || !whole)) {
+                    if (PREFIX && whole) {
+                        __stcg(reinterpret_cast<float2 *>(a.rowml) + orow, make_float2(m, l));
+                    } else {
+                        __stcg(slot + 128 * D + row, m);
+                        __stcg(slot + 128 * (D + 1) + row, l);
+                    }
+                }
+                const int npieces = int((s0 + x.n - 1) / L) - c0 + 1;
+                if (PREFIX && act && h == 0 && t0 == 0)  // where this row's parts are
+                    a.desc[int64_t(x.r0 + ir) * Hkv + x.kvh] = make_int4(c0, npieces, w, row);
+                if constexpr (!PREFIX) {
+                    if (!whole) {
+                        // the row tile's four warps publish their part; the piece that completes the count merges
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(piece_bar + 8 * w);
+                        if ((warp & 3) == 0) {
+                            if (!(ok = wait(piece_bar + 8 * w, cuts))) break;
+                            if (lane == 0) {
+                                misc[4 + w] = atomic_add_acq_rel_gpu(a.counters + 2 * c0 + w, 1) == npieces - 1;
+                                mbar_arrive(last_bar + 8 * w);
+                            }
+                        }
+                        if (!(ok = wait(last_bar + 8 * w, cuts))) break;
+                        ++cuts;
+                        if (misc[4 + w]) {
+                            if (act) {
+                                float M = -INFINITY, Ls = 0.f;
+                                for (int k = 0; k < npieces; ++k) {
+                                    const float *ps = a.slots + (2 * int64_t(c0 + k) + (k == 0)) * C::SLOT + w * (C::SLOT / 2);
+                                    M = fmaxf(M, __ldcg(ps + 128 * D + row));
+                                }
+                                const float Mr = M == -INFINITY ? 0.f : M;
+                                for (int k = 0; k < npieces; ++k) {
+                                    const float *ps = a.slots + (2 * int64_t(c0 + k) + (k == 0)) * C::SLOT + w * (C::SLOT / 2);
+                                    Ls += fast_exp2(__ldcg(ps + 128 * D + row) - Mr) * __ldcg(ps + 128 * (D + 1) + row);
+                                }
+                                const float iv = Ls == 0.f ? 0.f : 1.f / Ls;
+                                for (int d = 0; d < D; d += 8) {
+                                    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                                    for (int k = 0; k < npieces; ++k) {
+                                        const float *ps = a.slots + (2 * int64_t(c0 + k) + (k == 0)) * C::SLOT + w * (C::SLOT / 2);
+                                        const float f = fast_exp2(__ldcg(ps + 128 * D + row) - Mr) * iv;
+                                        const float4 y0 = __ldcg(reinterpret_cast<const float4 *>(ps + row * D + d));
+                                        const float4 y1 = __ldcg(reinterpret_cast<const float4 *>(ps + row * D + d + 4));
+                                        if (f == 0.f) continue;  // a piece in which the row saw nothing
+                                        v[0] += f * y0.x, v[1] += f * y0.y, v[2] += f * y0.z, v[3] += f * y0.w;
+                                        v[4] += f * y1.x, v[5] += f * y1.y, v[6] += f * y1.z, v[7] += f * y1.w;
+                                    }
+#pragma unroll
+                                    for (int k = 0; k < 8; ++k) bad |= !(fabsf(v[k]) <= 3.4028234e38f);
+                                    *reinterpret_cast<uint4 *>(a.out + orow * D + d) =
+                                        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                   pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+                                }
+                            }
+                            if (row == 0) a.counters[2 * c0 + w] = 0;
+                        }
+                    }
+                    // ---- rows that are not finite, again over their own tokens only (in fp32, a row per warp)
+                    unsigned again = __ballot_sync(0xffffffffu, bad);
+                    while (again) {
+                        const int src = __ffs(again) - 1;
+                        again &= again - 1;
+                        const int rs1 = __shfl_sync(0xffffffffu, S1, src), rlo = __shfl_sync(0xffffffffu, lo, src);
+                        const int rlim = __shfl_sync(0xffffffffu, lim, src);
+                        const int64_t ro = __shfl_sync(0xffffffffu, orow, src);
+                        constexpr int V = D / 32;
+                        float q[V], acc[V], M = -INFINITY, Ls = 0.f;
+#pragma unroll
+                        for (int k = 0; k < V; ++k) {
+                            q[k] = __uint_as_float(uint32_t(a.q[ro * D + lane * V + k]) << 16);
+                            acc[k] = 0.f;
+                        }
+                        const int cnt = rs1 + max(rlim - rlo, 0);
+                        for (int k = 0; k < cnt; ++k) {
+                            const int tk = k < rs1 ? k : k - rs1 + rlo;
+                            const int phb = __ldg(a.bt + int64_t(x.s) * a.MBS + tk / BS);
+                            if (phb < 0 || int64_t(phb) >= a.NB) continue;
+                            const int64_t off = ((int64_t(phb) * BS + tk % BS) * Hkv + x.kvh) * D + lane * V;
+                            float z = 0.f;
+#pragma unroll
+                            for (int e = 0; e < V; ++e)
+                                z = fmaf(q[e], __uint_as_float(uint32_t(static_cast<const uint16_t *>(a.kc)[off + e]) << 16), z);
+#pragma unroll
+                            for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+                            z *= a.scale_log2;
+                            const float Mn = fmaxf(M, z);
+                            const float f = M == -INFINITY ? 0.f : fast_exp2(M - Mn), pp = fast_exp2(z - Mn);
+                            M = Mn;
+                            Ls = Ls * f + pp;
+#pragma unroll
+                            for (int e = 0; e < V; ++e)
+                                acc[e] = acc[e] * f + pp * __uint_as_float(uint32_t(static_cast<const uint16_t *>(a.vc)[off + e]) << 16);
+                        }
+#pragma unroll
+                        for (int e = 0; e < V; ++e)
+                            a.out[ro * D + lane * V + e] = __bfloat16_as_ushort(__float2bfloat16_rn(Ls > 0.f ? acc[e] / Ls : Ls != Ls ? Ls : 0.f));
+                    }
+                }
+            }
+            tile_no += uint32_t(t1 - t0);
+            p = s0 + t1;
+            if (p < pos1) next_unit();
+        }
+    }
+    // ---- every role is done: the tensor memory goes back
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_free(tmem, 512);
+    }
+}
+
+template <int D, bool PREFIX>
+cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const SubsetArgs &a, int grid,
+                     cudaStream_t stream) {
+    const auto kernel = row_tiles_kernel<D, PREFIX>;
+    const cudaError_t e = smem_once(reinterpret_cast<const void *>(kernel), RowCfg<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3(grid), dim3(kWarpsRT * 32), RowCfg<D>::SMEM, stream, tk, tv, a);
+}
+
+}  // namespace
+
+size_t row_tiles_slot_floats(int head_dim) { return size_t(2) * 128 * (head_dim + 2); }
+
+cudaError_t launch_row_tiles(const CUtensorMap &tk, const CUtensorMap &tv, const SubsetArgs &args, int head_dim,
+                             int sms, cudaStream_t stream) {
+    SubsetArgs a = args;
+    a.min_items = 2;
+    if (a.pt) return head_dim == 128 ? launch_t<128, true>(tk, tv, a, sms, stream) : launch_t<64, true>(tk, tv, a, sms, stream);
+    return head_dim == 128 ? launch_t<128, false>(tk, tv, a, sms, stream) : launch_t<64, false>(tk, tv, a, sms, stream);
+}
+
+}  // namespace pa

@@ -40,7 +40,7 @@
 namespace pa {
 namespace {
 
-constexpr int kPreCap = 1024;  // entries of the items-per-sequence prefix in shared memory
+constexpr int kPreCap = 512;  // entries of the items-per-sequence prefix in shared memory
 
 template <int D, CacheKind KIND>
 struct StreamCfg {
@@ -62,7 +62,7 @@ struct StreamCfg {
     static constexpr size_t off_ml = off_scr + size_t(NW) * SCR * 4;
     static constexpr size_t off_flag = off_ml + size_t(NW) * 16 * 4;
     static constexpr size_t off_pre = off_flag + 16;
-    static constexpr size_t SMEM = 1024 + off_pre + (kPreCap + 1) * 4 + 12;
+    static constexpr size_t SMEM = 1024 + off_pre + (kPreCap + 1) * 8;
 };
 
 // a sequence's visible tokens [0, s1) and [lo, lim), as items
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
     float *scr = reinterpret_cast<float *>(bp + C::off_scr);
     float *sm_ml = reinterpret_cast<float *>(bp + C::off_ml);  // [NW][16]: m[8], l[8]
     volatile int *flag = reinterpret_cast<volatile int *>(bp + C::off_flag);
-    int *pre = reinterpret_cast<int *>(bp + C::off_pre);
+    int64_t *pre = reinterpret_cast<int64_t *>(bp + C::off_pre);
     const uint32_t ring = base + uint32_t(warp) * C::RING;
     const uint32_t bars = base + uint32_t(C::off_bars) + uint32_t(warp) * R * 8;
 
@@ -119,19 +119,19 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
     // ---- items of groups of `str` sequences and their prefix sums
     const int str = (a.nseq + kPreCap - 1) / kPreCap, np = (a.nseq + str - 1) / str;
     for (int i = tid; i < np; i += C::THREADS) {
-        int n = 0;
+        int64_t n = 0;
         for (int b = i * str; b < min((i + 1) * str, a.nseq); ++b) n += span_of(a, b).n;
         pre[i + 1] = n;
     }
     if (tid == 0) pre[0] = 0;
     __syncthreads();
     if (warp == 0) {
-        int carry = 0;
+        int64_t carry = 0;
         for (int i0 = 0; i0 < np; i0 += 32) {
-            int v = i0 + lane < np ? pre[i0 + lane + 1] : 0;
+            int64_t v = i0 + lane < np ? pre[i0 + lane + 1] : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, v, o);
+                const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
                 if (lane >= o) v += u;
             }
             if (i0 + lane < np) pre[i0 + lane + 1] = carry + v;
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
         int b = lo * str;
         rem = p - int64_t(Hkv) * pre[lo];
         s = span_of(a, b);
-        while (rem >= int64_t(Hkv) * s.n) {
+        while (rem >= int64_t(Hkv) * s.n && b + 1 < a.nseq) {
             rem -= int64_t(Hkv) * s.n;
             s = span_of(a, ++b);
         }
@@ -414,6 +414,36 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
 
     // the finished row: O relative to the maximum M with normaliser Ls, head h, dims d .. d + 3
     auto emit = [&](int b, int kvh, int h, int d, float M, float Ls, float4 O) {
+        if (a.desc) {  // the parts over the group's prefix
+            const int4 at = __ldcg(a.desc + int64_t(b) * Hkv + kvh);
+            // in bounds also for row offsets that were not ascending
+            const int first = min(max(at.x, 0), a.pgrid - 1), n = min(max(at.y, 0), a.pgrid - first);
+            const int prow = min(max(at.w, 0), 128 - G) + h;
+            for (int i = 0; i < n; ++i) {
+                float2 ml;
+                const float *po;
+                if (n == 1) {
+                    const int64_t r = int64_t(b) * a.Hq + kvh * G + h;
+                    po = a.rowres + r * D;
+                    ml = __ldcg(reinterpret_cast<const float2 *>(a.rowml) + r);
+                } else {
+                    const float *ps = a.slots + (2 * int64_t(first + i) + (i == 0)) * (2 * 128 * (D + 2)) +
+                                      (at.z & 1) * (128 * (D + 2));
+                    po = ps + prow * D;
+                    ml = make_float2(__ldcg(ps + 128 * D + prow), __ldcg(ps + 128 * (D + 1) + prow));
+                }
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(po + d));
+                const float Mn = fmaxf(M, ml.x);
+                const float f = M == -INFINITY ? 0.f : fast_exp2(M - Mn);
+                const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : ml.y) : fast_exp2(ml.x - Mn);
+                M = Mn;
+                Ls = Ls * f + ml.y * w;
+                O.x = O.x * f + v.x * w;
+                O.y = O.y * f + v.y * w;
+                O.z = O.z * f + v.z * w;
+                O.w = O.w * f + v.w * w;
+            }
+        }
         const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
         const int64_t row = int64_t(b) * a.Hq + kvh * G + h;
         *reinterpret_cast<uint2 *>(a.out + row * D + d) =

@@ -36,8 +36,12 @@ struct SubsetArgs {
     float scale_log2;             // softmax scale * log2(e)
     // workspace
     int32_t *status;              // status word
-    int32_t *counters;            // [CTAs] arrivals at the segment that begins in a CTA and leaves it (zero between calls)
+    int32_t *counters;            // [2 * CTAs] arrivals at what begins in a CTA and leaves it (zero between calls)
     float *part;                  // [2 * CTAs] pieces of segments cut between CTAs: O, m, l
+    float *slots;                 // [2 * CTAs] pieces of row-tile units cut between CTAs
+    float *rowres, *rowml;        // prefixes: [rows][Hq][D] O and [rows][Hq][2] m, l of units that were not cut
+    int4 *desc;                   // prefixes: [rows][Hkv] first CTA, pieces, row tile, first row in it
+    int pgrid;                    // prefixes: CTAs of the row-tile kernel
     float *lse;                   // weights: [nseq][Hq] log2 of the normaliser
     float *logits;                // weights: [nseq][Hkv][MBS][G][16] logits (log2 domain)
     uint64_t wait_ns;             // limit of every bounded wait
@@ -66,8 +70,11 @@ size_t stream_part_floats(int head_dim);
 cudaError_t launch_stream_decode(const CUtensorMap &tk, const CUtensorMap &tv, const SubsetArgs &a, int head_dim,
                                  CacheKind kind, int sms, cudaStream_t stream);
 
-// query rows of any number per sequence, or shared prefixes (bf16)
-cudaError_t launch_subset_decode(const SubsetArgs &a, int head_dim, cudaStream_t stream);
+// query rows of any number per sequence over window and sinks, or (pt set) the
+// rows of groups of sequences over their prefixes, left in slots / rowres / desc
+size_t row_tiles_slot_floats(int head_dim);
+cudaError_t launch_row_tiles(const CUtensorMap &tk, const CUtensorMap &tv, const SubsetArgs &a, int head_dim,
+                             int sms, cudaStream_t stream);
 
 struct EvictArgs {
     int32_t *kept, *new_lens;     // [B][Hkv][budget], [B]
