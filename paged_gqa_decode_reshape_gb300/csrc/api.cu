@@ -862,9 +862,9 @@ struct SubsetPlan {
 };
 
 // The workspace's parts: status word, arrival counters, two piece slots per
-// CTA and kernel, then what the operator keeps per row.
+// worker and kernel, then what the operator keeps per row.
 struct SubsetWorkspace {
-    size_t part, slots, rowres, rowml, desc, lse, logits, bytes;
+    size_t part, slots, rowres, rowml, ownres, ownml, desc, lse, logits, bytes;
     int sms;
 };
 
@@ -880,11 +880,13 @@ int subset_workspace(SubsetWorkspace *w, const SubsetPlan &plan, int64_t rows, i
     };
     w->sms = geo.grid;  // one CTA per SM
     const size_t heads = size_t(rows) * Hq;
-    take(true, size_t(geo.grid) * 2 * 4);
-    w->part = take(plan.stream, size_t(geo.grid) * 2 * stream_part_floats(D) * 4);
+    take(true, stream_workers(geo.grid) * 4);  // counters (of either kernel)
+    w->part = take(plan.stream, stream_part_floats(geo.grid, D) * 4);
     w->slots = take(plan.tiles, size_t(geo.grid) * 2 * row_tiles_slot_floats(D) * 4);
     w->rowres = take(plan.prefix, heads * D * 4);
     w->rowml = take(plan.prefix, heads * 8);
+    w->ownres = take(plan.prefix, heads * D * 4);
+    w->ownml = take(plan.prefix, heads * 8);
     w->desc = take(plan.prefix, size_t(rows) * Hkv * sizeof(int4));
     w->lse = take(plan.logit_blocks > 0, heads * 4);
     w->logits = take(plan.logit_blocks > 0, heads * plan.logit_blocks * kBlockSize * 4);
@@ -913,7 +915,9 @@ int run_subset(SubsetArgs a, const SubsetPlan &plan, int D, CacheKind kind, void
     a.slots = reinterpret_cast<float *>(p + w.slots);
     a.rowres = reinterpret_cast<float *>(p + w.rowres);
     a.rowml = reinterpret_cast<float *>(p + w.rowml);
-    a.desc = plan.prefix ? reinterpret_cast<int4 *>(p + w.desc) : nullptr;
+    a.ownres = plan.prefix ? reinterpret_cast<float *>(p + w.ownres) : nullptr;
+    a.ownml = reinterpret_cast<float *>(p + w.ownml);
+    a.desc = reinterpret_cast<int4 *>(p + w.desc);
     a.lse = reinterpret_cast<float *>(p + w.lse);
     a.logits = reinterpret_cast<float *>(p + w.logits);
     a.pgrid = w.sms;
@@ -928,6 +932,7 @@ int run_subset(SubsetArgs a, const SubsetPlan &plan, int D, CacheKind kind, void
     cudaError_t e = cudaSuccess;
     if (plan.tiles) e = launch_row_tiles(tk, tv, a, D, w.sms, st);
     if (e == cudaSuccess && plan.stream) e = launch_stream_decode(tk, tv, a, D, kind, w.sms, st);
+    if (e == cudaSuccess && plan.prefix) e = launch_prefix_join(a, D, st);
     return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 

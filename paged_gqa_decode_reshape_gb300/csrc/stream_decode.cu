@@ -12,14 +12,17 @@
 //
 //  * Work list. A (sequence, KV head) is a segment with one item per 16-token
 //    block that holds a visible token (sink blocks, then window blocks; at
-//    least one item, so that every output row is written). The segments are
-//    concatenated and cut into equal ranges, one per CTA, so that ragged
-//    lengths load the SMs evenly.
-//  * Each warp is its own producer: item k of warp w is position
-//    pos0 + w + NW k of the range, copied by TMA (K and V in 64-dim halves,
-//    128-byte swizzle; E4M3: K box and V tile) into the warp's private ring of
-//    R stages, which only this warp fills and empties. No warp waits for
-//    another between segment ends, and copies run ahead across them.
+//    least one item, so that every output row is written).
+//    Up to one segment per SM: every CTA takes one piece of one segment, all
+//    pieces at most L items, L the smallest for which the pieces fit the
+//    grid. Its warps take the piece's items in turn and merge once.
+//    More segments: every warp is a worker of its own. The segments are laid
+//    end to end, each with kEndCost empty items after it for what its end
+//    costs, and cut into equal ranges, one per warp; no warp waits for
+//    another, so many short sequences load the SMs as evenly as a few long.
+//  * Each warp is its own producer: its items are copied by TMA (K and V in
+//    64-dim halves, 128-byte swizzle; E4M3: K box and V tile) into its private
+//    ring of R stages, which only this warp fills and empties.
 //  * Math as mma.sync m16n8k16 on S^T = K Q^T and O^T += V^T P^T: tokens (then
 //    dims) are the 16 rows, the up to 8 heads of the group the 8 columns, so
 //    a K/V byte serves the whole group. tcgen05's smallest M of 64 would be
@@ -27,11 +30,11 @@
 //    wait for them; at 2 G flops per byte the tensor pipes are nearly idle.
 //  * Two blocks (32 tokens) per softmax step; a 16-bit mask per block says
 //    which tokens are seen, masked V lanes are zeroed (they may hold NaN).
-//  * At a segment's end the warps' states are merged in shared memory by all
-//    threads. A segment cut between CTAs leaves (O, m, l) per piece in the
-//    workspace, and the CTA that completes its arrival counter merges them,
-//    in piece order: the result does not depend on who is last.
+//  * A segment cut between workers leaves (O, m, l) per piece in the workspace,
+//    and the worker that completes its arrival counter merges them, in piece
+//    order: the result does not depend on who is last.
 #include <climits>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -40,17 +43,28 @@
 namespace pa {
 namespace {
 
-constexpr int kPreCap = 512;  // entries of the items-per-sequence prefix in shared memory
+constexpr int kPreCap = 512;   // entries of the items-per-sequence prefix in shared memory
+constexpr int kEndCost = 4;    // items that the end of a segment costs a warp
+constexpr int kMinPiece = 24;  // items of a CTA's piece at least, where there are as many
+
+#ifndef PA_STREAM_WARPS_F8
+#define PA_STREAM_WARPS_F8 8
+#endif
+#ifndef PA_STREAM_STAGES_F8
+#define PA_STREAM_STAGES_F8 5
+#endif
+constexpr int kMaxStreamWarps = 12;
 
 template <int D, CacheKind KIND>
 struct StreamCfg {
     static constexpr bool F8 = KIND != kCacheBf16;
     static_assert(!F8 || D == 128, "the E4M3 cache path is for head_dim 128");
-    static constexpr int NW = 6;                          // warps
+    static constexpr int NW = F8 ? PA_STREAM_WARPS_F8 : 6;  // warps
+    static_assert(NW <= kMaxStreamWarps, "pieces and counters of the workspace");
     static constexpr int KT = kBlockSize * D * (F8 ? 1 : 2);  // bytes of a K (or V) tile of one block
     static constexpr int STAGE = 2 * KT;
-    static constexpr int RING = 32 * 1024;                // bytes in flight per warp
-    static constexpr int R = RING / STAGE;                // stages per warp
+    static constexpr int R = F8 ? PA_STREAM_STAGES_F8 : (D == 128 ? 4 : 8);  // stages per warp
+    static constexpr int RING = R * STAGE;                // bytes in flight per warp
     static constexpr int NKK = D / 16;
     static constexpr int HALF = kBlockSize * 128;         // bytes of one 64-dim half tile (bf16)
     static constexpr int ROW = D + 4;                     // floats per head row of a warp's state (conflict-free)
@@ -68,6 +82,7 @@ struct StreamCfg {
 // a sequence's visible tokens [0, s1) and [lo, lim), as items
 struct Span {
     int lim, s1, lo, nb1, jw, n;  // nb1 sink blocks, then blocks jw, jw + 1, ...; n items (at least one)
+    __device__ int block(int e) const { return e < nb1 ? e : e - nb1 + jw; }  // logical block of item e
 };
 
 __device__ __forceinline__ Span span_of(const SubsetArgs &a, int b) {
@@ -116,50 +131,130 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
         for (int s = 0; s < R; ++s) mbar_init(bars + s * 8, 1);
         fence_barrier_init();
     }
-    // ---- items of groups of `str` sequences and their prefix sums
-    const int str = (a.nseq + kPreCap - 1) / kPreCap, np = (a.nseq + str - 1) / str;
-    for (int i = tid; i < np; i += C::THREADS) {
-        int64_t n = 0;
-        for (int b = i * str; b < min((i + 1) * str, a.nseq); ++b) n += span_of(a, b).n;
-        pre[i + 1] = n;
-    }
-    if (tid == 0) pre[0] = 0;
-    __syncthreads();
-    if (warp == 0) {
-        int64_t carry = 0;
-        for (int i0 = 0; i0 < np; i0 += 32) {
-            int64_t v = i0 + lane < np ? pre[i0 + lane + 1] : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += u;
-            }
-            if (i0 + lane < np) pre[i0 + lane + 1] = carry + v;
-            carry += __shfl_sync(0xffffffffu, v, 31);
+    // ---- what this warp works on: items [first, last) in steps of `step`, of one segment
+    // (item numbers in it) or of the concatenated segments (positions)
+    const bool one = int64_t(a.nseq) * Hkv <= gridDim.x;  // a piece of one segment per CTA
+    int64_t first, last, L = 1;
+    int np = 0, str = 1;
+    int b = 0, kvh = 0, piece = 0, npieces = 1, w0 = 0;  // one: the segment, this CTA's piece, the segment's first CTA
+    Span sp;
+    if (one) {
+        int *cnt = reinterpret_cast<int *>(pre);  // items, then pieces per sequence and their prefix
+        int *found = reinterpret_cast<int *>(sm_ml);
+        int nmax = 0;
+        for (int i = tid; i < a.nseq; i += C::THREADS) cnt[i + 1] = span_of(a, i).n;
+        __syncthreads();
+        int64_t sum = 0;
+        for (int i = lane; i < a.nseq; i += 32) {
+            sum += cnt[i + 1];
+            nmax = max(nmax, cnt[i + 1]);
         }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            nmax = max(nmax, __shfl_xor_sync(0xffffffffu, nmax, o));
+        }
+        // smallest piece size for which Hkv * sum ceil(n / size) <= CTAs, by NW warps at a time
+        int lo = int(min(max((sum * Hkv + gridDim.x - 1) / gridDim.x, int64_t(kMinPiece)), int64_t(nmax)));
+        int hi = nmax;  // always fits: one piece per segment
+        while (lo < hi) {
+            const int at = min(lo + int((int64_t(hi) - lo) * warp / NW), hi);
+            int c = 0;
+            for (int i = lane; i < a.nseq; i += 32) c += (cnt[i + 1] + at - 1) / at;
+            c = __reduce_add_sync(0xffffffffu, c);
+            if (lane == 0) found[warp] = int64_t(c) * Hkv <= gridDim.x ? at : -1;
+            __syncthreads();
+            int nlo = lo + 1, nhi = hi;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const int f = found[w], fat = min(lo + int((int64_t(hi) - lo) * w / NW), hi);
+                if (f < 0) nlo = max(nlo, fat + 1);
+                else nhi = min(nhi, f);
+            }
+            __syncthreads();
+            if (nhi == lo) nlo = lo;
+            lo = min(nlo, nhi);
+            hi = nhi;
+        }
+        if (warp == 0) {
+            int carry = 0;
+            for (int i0 = 0; i0 < a.nseq; i0 += 32) {
+                int v = i0 + lane < a.nseq ? (cnt[i0 + lane + 1] + hi - 1) / hi : 0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int u = __shfl_up_sync(0xffffffffu, v, o);
+                    if (lane >= o) v += u;
+                }
+                if (i0 + lane < a.nseq) cnt[i0 + lane + 1] = carry + v;
+                carry += __shfl_sync(0xffffffffu, v, 31);
+            }
+            if (lane == 0) cnt[0] = 0;
+        }
+        __syncthreads();
+        if (int(blockIdx.x) >= Hkv * cnt[a.nseq]) return;  // whole CTA: nothing to do
+        int x = 0, y = a.nseq;
+        while (y - x > 1) {
+            const int mid = (x + y) >> 1;
+            if (Hkv * cnt[mid] <= int(blockIdx.x)) x = mid; else y = mid;
+        }
+        b = x;
+        npieces = cnt[b + 1] - cnt[b];
+        const int rem = int(blockIdx.x) - Hkv * cnt[b];
+        kvh = rem / npieces;
+        piece = rem - kvh * npieces;
+        w0 = int(blockIdx.x) - piece;
+        sp = span_of(a, b);
+        first = int64_t(sp.n) * piece / npieces + warp;
+        last = int64_t(sp.n) * (piece + 1) / npieces;
+    } else {
+        // items (and end costs) of groups of `str` sequences, and their prefix sums
+        str = (a.nseq + kPreCap - 1) / kPreCap;
+        np = (a.nseq + str - 1) / str;
+        for (int i = tid; i < np; i += C::THREADS) {
+            int64_t n = 0;
+            for (int j = i * str; j < min((i + 1) * str, a.nseq); ++j) n += span_of(a, j).n + kEndCost;
+            pre[i + 1] = n;
+        }
+        if (tid == 0) pre[0] = 0;
+        __syncthreads();
+        if (warp == 0) {
+            int64_t carry = 0;
+            for (int i0 = 0; i0 < np; i0 += 32) {
+                int64_t v = i0 + lane < np ? pre[i0 + lane + 1] : 0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+                    if (lane >= o) v += u;
+                }
+                if (i0 + lane < np) pre[i0 + lane + 1] = carry + v;
+                carry += __shfl_sync(0xffffffffu, v, 31);
+            }
+        }
+        __syncthreads();
+        const int64_t total = int64_t(Hkv) * pre[np];
+        const int workers = int(gridDim.x) * NW, me = warp * int(gridDim.x) + int(blockIdx.x);
+        L = (total + workers - 1) / workers;
+        first = me * L;
+        last = min(total, first + L);
+        if (first >= last) return;  // nothing to do (no barrier of the whole CTA follows)
     }
-    __syncthreads();
-    const int64_t total = int64_t(Hkv) * pre[np];
-    const int64_t L = max((total + gridDim.x - 1) / gridDim.x, int64_t(a.min_items));
-    const int64_t pos0 = int64_t(blockIdx.x) * L, pos1 = min(total, pos0 + L);
-    if (pos0 >= pos1) return;  // whole CTA: nothing to do
-    const int n_items = int(pos1 - pos0);
+    const int step_ = one ? NW : 1;
 
-    // the sequence of global position p, and p's offset inside its items
+    // the sequence of position p, and p's offset inside its items
     auto locate = [&](int64_t p, Span &s, int64_t &rem) -> int {
         int lo = 0, hi = np;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (int64_t(Hkv) * pre[mid] <= p) lo = mid; else hi = mid;
         }
-        int b = lo * str;
+        int q = lo * str;
         rem = p - int64_t(Hkv) * pre[lo];
-        s = span_of(a, b);
-        while (rem >= int64_t(Hkv) * s.n && b + 1 < a.nseq) {
-            rem -= int64_t(Hkv) * s.n;
-            s = span_of(a, ++b);
+        s = span_of(a, q);
+        while (rem >= int64_t(Hkv) * (s.n + kEndCost) && q + 1 < a.nseq) {
+            rem -= int64_t(Hkv) * (s.n + kEndCost);
+            s = span_of(a, ++q);
         }
-        return b;
+        return q;
     };
 
     // ---- a window of 32 of this warp's items, one per lane
@@ -169,21 +264,26 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
         int j;          // logical block (LOGITS)
         float sk, sv;   // scales of the block (per-block scales)
     };
-    const int kn = n_items > warp ? (n_items - warp + NW - 1) / NW : 0;  // this warp's items
+    const int kn = last > first ? int((last - first + step_ - 1) / step_) : 0;  // this warp's items
     auto resolve = [&](int k0) -> Win {
         Win w{-1, 0u, 0, 0.f, 0.f};
         const int k = k0 + lane;
         if (k >= kn) return w;
-        Span s;
-        int64_t rem;
-        const int b = locate(pos0 + warp + int64_t(NW) * k, s, rem);
-        const int kvh = int(rem / s.n), e = int(rem - int64_t(kvh) * s.n);
-        const int j = e < s.nb1 ? e : e - s.nb1 + s.jw;
-        const uint32_t m = bits_between(0, s.s1, j * BS) | bits_between(s.lo, s.lim, j * BS);
-        w.what = uint32_t(kvh) << 16;
+        const int64_t p = first + int64_t(step_) * k;
+        Span s = sp;
+        int q = b, head = kvh, e = int(p);
+        if (!one) {
+            int64_t rem;
+            q = locate(p, s, rem);
+            head = int(rem / (s.n + kEndCost));
+            e = int(rem - int64_t(head) * (s.n + kEndCost));
+        }
+        const int j = s.block(e);
+        const uint32_t m = e < s.n ? bits_between(0, s.s1, j * BS) | bits_between(s.lo, s.lim, j * BS) : 0u;
+        w.what = uint32_t(head) << 16;
         w.j = j;
         if (m) {
-            const int ph = __ldg(a.bt + int64_t(b) * a.MBS + j);
+            const int ph = __ldg(a.bt + int64_t(q) * a.MBS + j);
             if (ph >= 0 && int64_t(ph) < a.NB) {
                 w.phys = ph;
                 w.what |= m;
@@ -295,14 +395,14 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
         for (int e = 0; e < 4; ++e) sc[e] = sa[e] + sb[e];
     };
     // O^T += V^T P^T for a staged block; V lanes of unseen tokens zeroed
-    auto pv = [&](uint32_t vb, uint32_t p01, uint32_t p23, uint32_t mask) {
+    auto pv_masked = [&](auto masked, uint32_t vb, uint32_t p01, uint32_t p23, uint32_t mask) {
+        constexpr bool MASKED = decltype(masked)::value;
         const uint32_t pb0 = movmatrix_trans(p01), pb1 = movmatrix_trans(p23);
-        uint32_t mlo = 0xffffffffu, mhi = 0xffffffffu;
-        if (mask != 0xffffu) {
-            const uint32_t t = mask >> (2 * q4);
-            mlo = (t & 1u ? 0x0000ffffu : 0u) | (t & 2u ? 0xffff0000u : 0u);
-            mhi = (t & 0x100u ? 0x0000ffffu : 0u) | (t & 0x200u ? 0xffff0000u : 0u);
-        }
+        const uint32_t t = mask >> (2 * q4);
+        const uint32_t mlo = (t & 1u ? 0x0000ffffu : 0u) | (t & 2u ? 0xffff0000u : 0u);
+        const uint32_t mhi = (t & 0x100u ? 0x0000ffffu : 0u) | (t & 0x200u ? 0xffff0000u : 0u);
+        auto lo = [&](uint32_t v) { return MASKED ? v & mlo : v; };
+        auto hi = [&](uint32_t v) { return MASKED ? v & mhi : v; };
         if constexpr (F8) {
 #pragma unroll
             for (int c2 = 0; c2 < NKK / 2; ++c2) {
@@ -312,8 +412,8 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
                 e4m3x4_to_f16x2x2(r1, a1, a3);
                 e4m3x4_to_f16x2x2(r2, b0, b2);
                 e4m3x4_to_f16x2x2(r3, b1, b3);
-                mma_f16(acc[2 * c2], a0 & mlo, a1 & mlo, a2 & mhi, a3 & mhi, pb0, pb1);
-                mma_f16(acc[2 * c2 + 1], b0 & mlo, b1 & mlo, b2 & mhi, b3 & mhi, pb0, pb1);
+                mma_f16(acc[2 * c2], lo(a0), lo(a1), hi(a2), hi(a3), pb0, pb1);
+                mma_f16(acc[2 * c2 + 1], lo(b0), lo(b1), hi(b2), hi(b3), pb0, pb1);
             }
         } else {
             const int rv = (lane & 7) + ((lane >> 4) << 3);
@@ -322,9 +422,13 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
                 const int ch = ((mt & 3) << 1) + ((lane >> 3) & 1);
                 uint32_t a0, a1, a2, a3;
                 ldsm_x4_trans(vb + (mt >> 2) * C::HALF + rv * 128 + ((ch ^ (lane & 7)) << 4), a0, a1, a2, a3);
-                mma_bf16(acc[mt], a0 & mlo, a1 & mlo, a2 & mhi, a3 & mhi, pb0, pb1);
+                mma_bf16(acc[mt], lo(a0), lo(a1), hi(a2), hi(a3), pb0, pb1);
             }
         }
+    };
+    auto pv = [&](uint32_t vb, uint32_t p01, uint32_t p23, uint32_t mask) {
+        if (mask == 0xffffu) pv_masked(std::false_type{}, vb, p01, p23, mask);
+        else pv_masked(std::true_type{}, vb, p01, p23, mask);
     };
     // one online-softmax step over up to two staged blocks (mask 0: none);
     // ca, cb: their K and V scales (per-block scales)
@@ -414,42 +518,18 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
 
     // the finished row: O relative to the maximum M with normaliser Ls, head h, dims d .. d + 3
     auto emit = [&](int b, int kvh, int h, int d, float M, float Ls, float4 O) {
-        if (a.desc) {  // the parts over the group's prefix
-            const int4 at = __ldcg(a.desc + int64_t(b) * Hkv + kvh);
-            // in bounds also for row offsets that were not ascending
-            const int first = min(max(at.x, 0), a.pgrid - 1), n = min(max(at.y, 0), a.pgrid - first);
-            const int prow = min(max(at.w, 0), 128 - G) + h;
-            for (int i = 0; i < n; ++i) {
-                float2 ml;
-                const float *po;
-                if (n == 1) {
-                    const int64_t r = int64_t(b) * a.Hq + kvh * G + h;
-                    po = a.rowres + r * D;
-                    ml = __ldcg(reinterpret_cast<const float2 *>(a.rowml) + r);
-                } else {
-                    const float *ps = a.slots + (2 * int64_t(first + i) + (i == 0)) * (2 * 128 * (D + 2)) +
-                                      (at.z & 1) * (128 * (D + 2));
-                    po = ps + prow * D;
-                    ml = make_float2(__ldcg(ps + 128 * D + prow), __ldcg(ps + 128 * (D + 1) + prow));
-                }
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(po + d));
-                const float Mn = fmaxf(M, ml.x);
-                const float f = M == -INFINITY ? 0.f : fast_exp2(M - Mn);
-                const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : ml.y) : fast_exp2(ml.x - Mn);
-                M = Mn;
-                Ls = Ls * f + ml.y * w;
-                O.x = O.x * f + v.x * w;
-                O.y = O.y * f + v.y * w;
-                O.z = O.z * f + v.z * w;
-                O.w = O.w * f + v.w * w;
-            }
+        if (a.ownres) {  // the own part of a row with a prefix
+            const int64_t r = int64_t(b) * a.Hq + kvh * G + h;
+            __stcg(reinterpret_cast<float4 *>(a.ownres + r * D + d), O);
+            if (d == 0) __stcg(reinterpret_cast<float2 *>(a.ownml) + r, make_float2(M, Ls));
+            return;
         }
-        const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+        const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
         const int64_t row = int64_t(b) * a.Hq + kvh * G + h;
         *reinterpret_cast<uint2 *>(a.out + row * D + d) =
             make_uint2(pack_bf16x2(O.x * inv, O.y * inv), pack_bf16x2(O.z * inv, O.w * inv));
         // a row without tokens: every weight 2^(z - inf) = 0 (it has none)
-        if (LOGITS && d == 0) a.lse[row] = Ls > 0.f ? M + log2f(Ls) : INFINITY;
+        if (LOGITS && d == 0) a.lse[row] = Ls == 0.f ? INFINITY : M + log2f(Ls);
     };
 
     auto wait_item = [&](int k) {
@@ -464,32 +544,9 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
 
     int issued = min(kn, R);
     for (int i = 0; i < issued; ++i) issue(i);
-
-    // ---- the segments of this CTA's range
-    int64_t p = pos0, rem;
-    Span sp;
-    int b = locate(p, sp, rem);
-    int kvh = int(rem / sp.n);
-    int64_t s0 = p - (rem - int64_t(kvh) * sp.n);  // global position of the segment's first item
-    fetch_q(b, kvh);
     int k = 0;
-    while (true) {
-        const int64_t e0 = s0 + sp.n;
-        const int64_t pe = min(e0, pos1);
-        const int k1 = min(kn, int(max(int64_t(0), (pe - pos0 - warp + NW - 1) / NW)));  // this warp's items before pe
-        const int cb = b, ckvh = kvh;
-        const int64_t cs0 = s0;
-        begin_segment(kvh);
-        // the next segment, and its query
-        const bool more = pe < pos1;
-        if (more) {
-            s0 = e0;
-            if (++kvh == Hkv) {
-                kvh = 0;
-                sp = span_of(a, ++b);
-            }
-            fetch_q(b, kvh);
-        }
+    // the items k < k1 of segment (cb, ckvh)
+    auto stream = [&](int k1, int cb, int ckvh) {
         while (k < k1) {
             if (k >= wbase + 32) {
                 cur = nxt;
@@ -501,7 +558,7 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
             const int n2 = k + 1 < k1 ? 2 : 1;
             const uint32_t wa = __shfl_sync(0xffffffffu, cur.what, k & 31);
             const bool c2 = k + 1 < wbase + 32;
-            uint32_t wb = __shfl_sync(0xffffffffu, c2 ? cur.what : nxt.what, (k + 1) & 31);
+            const uint32_t wb = __shfl_sync(0xffffffffu, c2 ? cur.what : nxt.what, (k + 1) & 31);
             const uint32_t ma = wa & 0xffffu, mb = n2 == 2 ? wb & 0xffffu : 0u;
             float2 ca{0.f, 0.f}, cbk{0.f, 0.f};
             if constexpr (PSC) {
@@ -523,12 +580,11 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
                 step(ring + uint32_t(k % R) * C::STAGE, ma, ca, ring + uint32_t((k + 1) % R) * C::STAGE, mb, cbk, la, lb);
             __syncwarp();  // every lane has read the stages
             k += n2;
-            for (; issued < kn && issued < k + R; ++issued) {
-                if (issued >= wbase + 64) break;  // not resolved yet
-                issue(issued);
-            }
+            for (; issued < kn && issued < k + R; ++issued) issue(issued);
         }
-        // ---- deposit, and merge by the whole CTA
+    };
+    // this warp's state into its shared-memory slot
+    auto deposit = [&]() {
         l0 += __shfl_xor_sync(0xffffffffu, l0, 4);
         l0 += __shfl_xor_sync(0xffffffffu, l0, 8);
         l0 += __shfl_xor_sync(0xffffffffu, l0, 16);
@@ -548,66 +604,139 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
             sm_ml[warp * 16 + 8 + 2 * q4] = l0;
             sm_ml[warp * 16 + 8 + 2 * q4 + 1] = l1;
         }
+    };
+    // (M, Ls, O) += another part
+    auto fold = [](float &M, float &Ls, float4 &O, float m, float l, float4 v) {
+        const float Mn = fmaxf(M, m);
+        const float f = M == -INFINITY ? 0.f : fast_exp2(M - Mn), w = m == -INFINITY ? 0.f : fast_exp2(m - Mn);
+        M = Mn;
+        Ls = Ls * f + l * w;
+        O = make_float4(O.x * f + v.x * w, O.y * f + v.y * w, O.z * f + v.z * w, O.w * f + v.w * w);
+    };
+    auto put_piece = [&](float *ps, int h, int d, float M, float Ls, float4 O) {
+        __stcg(reinterpret_cast<float4 *>(ps + h * D + d), O);
+        if (d == 0) {
+            __stcg(ps + 8 * D + h, M);
+            __stcg(ps + 8 * D + 8 + h, Ls);
+        }
+    };
+    // merge n pieces, piece i at slot_of(i), for head h, dims d .. d + 3; four pieces' loads in flight
+    auto merge_pieces = [&](auto slot_of, int n, int sb, int sh, int h, int d) {
+        float M = -INFINITY, Ls = 0.f;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = 0; i0 < n; i0 += 4) {
+            float m[4], l[4];
+            float4 v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float *ps = slot_of(min(i0 + u, n - 1));
+                m[u] = __ldcg(ps + 8 * D + h);
+                l[u] = __ldcg(ps + 8 * D + 8 + h);
+                v[u] = __ldcg(reinterpret_cast<const float4 *>(ps + h * D + d));
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i0 + u < n) fold(M, Ls, O, m[u], l[u], v[u]);
+        }
+        emit(sb, sh, h, d, M, Ls, O);
+    };
+    const int tasks = G * (D / 4);
+
+    if (one) {
+        // ---- one piece per CTA: stream it, merge the warps' states once
+        fetch_q(b, kvh);
+        begin_segment(kvh);
+        stream(kn, b, kvh);
+        deposit();
         __syncthreads();
-        const bool whole = cs0 >= pos0 && e0 <= pos1;
-        const int c0 = int(cs0 / L), npieces = int((e0 - 1) / L) - c0 + 1;  // the segment's CTAs
-        float *slot = a.part + (2 * int64_t(blockIdx.x) + (int(blockIdx.x) == c0)) * C::PART;
-        for (int idx = tid; idx < G * (D / 4); idx += C::THREADS) {
+        float *slot = a.part + int64_t(blockIdx.x) * C::PART;
+        for (int idx = tid; idx < tasks; idx += C::THREADS) {
             const int h = idx / (D / 4), d = 4 * (idx % (D / 4));
             float M = -INFINITY, Ls = 0.f;
             float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < NW; ++w) M = fmaxf(M, sm_ml[w * 16 + h]);
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                const float mw = sm_ml[w * 16 + h], f = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
-                const float4 v = *reinterpret_cast<const float4 *>(scr + w * C::SCR + h * C::ROW + d);
-                Ls += f * sm_ml[w * 16 + 8 + h];
-                O.x += f * v.x;
-                O.y += f * v.y;
-                O.z += f * v.z;
-                O.w += f * v.w;
-            }
-            if (whole) {
-                emit(cb, ckvh, h, d, M, Ls, O);
-            } else {
-                __stcg(reinterpret_cast<float4 *>(slot + h * D + d), O);
-                if (d == 0) {
-                    __stcg(slot + 8 * D + h, M);
-                    __stcg(slot + 8 * D + 8 + h, Ls);
-                }
-            }
+            for (int w = 0; w < NW; ++w)
+                fold(M, Ls, O, sm_ml[w * 16 + h], sm_ml[w * 16 + 8 + h],
+                     *reinterpret_cast<const float4 *>(scr + w * C::SCR + h * C::ROW + d));
+            if (npieces == 1) emit(b, kvh, h, d, M, Ls, O);
+            else put_piece(slot, h, d, M, Ls, O);
         }
-        if (!whole) {
-            __syncthreads();  // the CTA's partial, published by the release below
-            if (tid == 0) *flag = atomic_add_acq_rel_gpu(a.counters + c0, 1) == npieces - 1;
+        if (npieces > 1) {
+            __syncthreads();  // the CTA's piece, published by the release below
+            if (tid == 0) *flag = atomic_add_acq_rel_gpu(a.counters + w0, 1) == npieces - 1;
             __syncthreads();
             if (*flag) {
-                for (int idx = tid; idx < G * (D / 4); idx += C::THREADS) {
-                    const int h = idx / (D / 4), d = 4 * (idx % (D / 4));
-                    float M = -INFINITY, Ls = 0.f;
-                    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int i = 0; i < npieces; ++i) {
-                        const float *ps = a.part + (2 * int64_t(c0 + i) + (i == 0)) * C::PART;
-                        const float mw = __ldcg(ps + 8 * D + h), lw = __ldcg(ps + 8 * D + 8 + h);
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(ps + h * D + d));
-                        const float Mn = fmaxf(M, mw);
-                        const float f = M == -INFINITY ? 0.f : fast_exp2(M - Mn);
-                        const float w = mw == -INFINITY ? 0.f : fast_exp2(mw - Mn);
-                        M = Mn;
-                        Ls = Ls * f + lw * w;
-                        O.x = O.x * f + v.x * w;
-                        O.y = O.y * f + v.y * w;
-                        O.z = O.z * f + v.z * w;
-                        O.w = O.w * f + v.w * w;
-                    }
-                    emit(cb, ckvh, h, d, M, Ls, O);
-                }
-                if (tid == 0) a.counters[c0] = 0;
+                for (int idx = tid; idx < tasks; idx += C::THREADS)
+                    merge_pieces([&](int i) { return a.part + int64_t(w0 + i) * C::PART; }, npieces, b, kvh,
+                                 idx / (D / 4), 4 * (idx % (D / 4)));
+                if (tid == 0) a.counters[w0] = 0;
             }
         }
-        if (!more) break;
-        __syncthreads();  // the states may be written again
+    } else {
+        // ---- the segments of this warp's range
+        int64_t rem;
+        b = locate(first, sp, rem);
+        kvh = int(rem / (sp.n + kEndCost));
+        int64_t s0 = first - (rem - int64_t(kvh) * (sp.n + kEndCost));  // position of the segment's first item
+        fetch_q(b, kvh);
+        const int64_t me = first / L;
+        while (true) {
+            const int64_t e0 = s0 + sp.n, end = e0 + kEndCost;
+            const int k1 = int(min(e0, last) - first);  // items before the segment's end; none: only its end cost is here
+            const int cb = b, ckvh = kvh;
+            const int64_t cs0 = s0;
+            begin_segment(kvh);
+            const bool more = end < last;
+            if (more) {  // the next segment, and its query
+                s0 = end;
+                if (++kvh == Hkv) {
+                    kvh = 0;
+                    sp = span_of(a, ++b);
+                }
+                fetch_q(b, kvh);
+            }
+            if (k1 > 0) {
+                stream(k1, cb, ckvh);
+                deposit();
+                __syncwarp();
+                const int64_t c0 = cs0 / L;
+                const int n = int((e0 - 1) / L - c0) + 1;  // the workers that hold a piece
+                // worker c's slot: 2 c + 1 for the segment that begins in its range, 2 c for one that began before
+                auto slot_of = [&](int i) { return a.part + (2 * (c0 + i) + (i == 0)) * C::PART; };
+                float *slot = slot_of(int(me - c0));
+                const float *my = scr + warp * C::SCR;
+                for (int idx = lane; idx < tasks; idx += 32) {
+                    const int h = idx / (D / 4), d = 4 * (idx % (D / 4));
+                    const float M = sm_ml[warp * 16 + h], Ls = sm_ml[warp * 16 + 8 + h];
+                    const float4 O = *reinterpret_cast<const float4 *>(my + h * C::ROW + d);
+                    if (n == 1) emit(cb, ckvh, h, d, M, Ls, O);
+                    else put_piece(slot, h, d, M, Ls, O);
+                }
+                __syncwarp();
+                if (n > 1) {
+                    int done = 0;
+                    if (lane == 0) done = atomic_add_acq_rel_gpu(a.counters + c0, 1) == n - 1;
+                    done = __shfl_sync(0xffffffffu, done, 0);
+                    __syncwarp();  // every lane's reads of the pieces follow lane 0's acquire
+                    if (done) {
+                        for (int idx = lane; idx < tasks; idx += 32)
+                            merge_pieces(slot_of, n, cb, ckvh, idx / (D / 4), 4 * (idx % (D / 4)));
+                        if (lane == 0) a.counters[c0] = 0;
+                    }
+                }
+            }
+            // the end cost's empty items
+            for (; k < kn && first + k < min(end, last); ++k) {
+                if (k >= wbase + 32) {
+                    cur = nxt;
+                    wbase += 32;
+                    nxt = resolve(wbase + 32);
+                    scales(nxt);
+                }
+            }
+            for (; issued < kn && issued < k + R; ++issued) issue(issued);
+            if (!more) break;
+        }
     }
     // after a wait that gave up: no copy may land in memory of a CTA that is gone
     if (dead && lane == 0)
@@ -654,14 +783,80 @@ cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const SubsetA
 
 }  // namespace
 
-size_t stream_part_floats(int head_dim) { return size_t(8) * head_dim + 16; }
+size_t stream_workers(int sms) { return size_t(sms) * kMaxStreamWarps; }
+size_t stream_part_floats(int sms, int head_dim) { return 2 * stream_workers(sms) * (size_t(8) * head_dim + 16); }
 
-cudaError_t launch_stream_decode(const CUtensorMap &tk, const CUtensorMap &tv, const SubsetArgs &args, int head_dim,
+// ---- rows with a prefix: the own part and the prefix's parts, a warp per row
+template <int D>
+__global__ void __launch_bounds__(256) prefix_join_kernel(const SubsetArgs a) {
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    pdl_wait();
+    if (r >= int64_t(a.rows) * a.Hq) return;
+    constexpr int V = D / 32;  // dims per lane
+    const int b = int(r / a.Hq), hq = int(r - int64_t(b) * a.Hq), kvh = hq / a.G, h = hq - kvh * a.G;
+    auto load = [&](const float *p, float (&v)[V]) {
+        if constexpr (V == 4) {
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(p) + lane);
+            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+        } else {
+            const float2 x = __ldcg(reinterpret_cast<const float2 *>(p) + lane);
+            v[0] = x.x, v[1] = x.y;
+        }
+    };
+    const int4 at = __ldcg(a.desc + int64_t(b) * a.Hkv + kvh);
+    const float2 own = __ldcg(reinterpret_cast<const float2 *>(a.ownml) + r);
+    float O[V], M = own.x, Ls = own.y;
+    load(a.ownres + r * D, O);
+    // in bounds also for row offsets that were not ascending
+    const int first = min(max(at.x, 0), a.pgrid - 1), n = min(max(at.y, 0), a.pgrid - first);
+    const int prow = min(max(at.w, 0), 128 - a.G) + h;
+    auto fold = [&](float m, float l, const float (&v)[V]) {
+        const float Mn = fmaxf(M, m);
+        const float f = M == -INFINITY ? 0.f : fast_exp2(M - Mn), w = m == -INFINITY ? 0.f : fast_exp2(m - Mn);
+        M = Mn;
+        Ls = Ls * f + l * w;
+#pragma unroll
+        for (int i = 0; i < V; ++i) O[i] = O[i] * f + v[i] * w;
+    };
+    if (n == 1) {
+        float v[V];
+        load(a.rowres + r * D, v);
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.rowml) + r);
+        fold(ml.x, ml.y, v);
+    } else {
+        constexpr int U = 8;  // pieces in flight
+        for (int i0 = 0; i0 < n; i0 += U) {
+            float v[U][V], m[U], l[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = min(i0 + u, n - 1);
+                const float *ps = a.slots + (2 * int64_t(first + i) + (i == 0)) * (2 * 128 * (D + 2)) +
+                                  (at.z & 1) * (128 * (D + 2));
+                load(ps + prow * D, v[u]);
+                m[u] = __ldcg(ps + 128 * D + prow);
+                l[u] = __ldcg(ps + 128 * (D + 1) + prow);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i0 + u < n) fold(m[u], l[u], v[u]);
+        }
+    }
+    const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
+    uint32_t *out = reinterpret_cast<uint32_t *>(a.out + r * D) + lane * (V / 2);
+#pragma unroll
+    for (int i = 0; i < V; i += 2) out[i / 2] = pack_bf16x2(O[i] * inv, O[i + 1] * inv);
+}
+
+cudaError_t launch_prefix_join(const SubsetArgs &a, int head_dim, cudaStream_t stream) {
+    const dim3 grid(unsigned((int64_t(a.rows) * a.Hq + 7) / 8));
+    return head_dim == 128 ? launch_pdl(prefix_join_kernel<128>, grid, dim3(256), 0, stream, a)
+                           : launch_pdl(prefix_join_kernel<64>, grid, dim3(256), 0, stream, a);
+}
+
+cudaError_t launch_stream_decode(const CUtensorMap &tk, const CUtensorMap &tv, const SubsetArgs &a, int head_dim,
                                  CacheKind kind, int sms, cudaStream_t stream) {
-    SubsetArgs a = args;
-    // one CTA per SM; a range holds at least two items per warp, so that a
-    // small call is not spread over CTAs that cost more to merge than to run
-    a.min_items = 12;
     if (a.weights) {
         cudaError_t e = head_dim == 128 ? launch_t<128, kCacheBf16, true>(tk, tv, a, sms, stream)
                                         : launch_t<64, kCacheBf16, true>(tk, tv, a, sms, stream);

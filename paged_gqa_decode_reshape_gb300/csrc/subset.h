@@ -36,17 +36,18 @@ struct SubsetArgs {
     float scale_log2;             // softmax scale * log2(e)
     // workspace
     int32_t *status;              // status word
-    int32_t *counters;            // [2 * CTAs] arrivals at what begins in a CTA and leaves it (zero between calls)
-    float *part;                  // [2 * CTAs] pieces of segments cut between CTAs: O, m, l
+    int32_t *counters;            // [workers] arrivals at what begins in a worker's range and leaves it (zero between calls)
+    float *part;                  // [2 * workers] pieces of segments cut between workers: O, m, l
     float *slots;                 // [2 * CTAs] pieces of row-tile units cut between CTAs
     float *rowres, *rowml;        // prefixes: [rows][Hq][D] O and [rows][Hq][2] m, l of units that were not cut
     int4 *desc;                   // prefixes: [rows][Hkv] first CTA, pieces, row tile, first row in it
     int pgrid;                    // prefixes: CTAs of the row-tile kernel
+    float *ownres, *ownml;        // prefixes: [rows][Hq][D] O and [rows][Hq][2] m, l of the own tokens (else null)
     float *lse;                   // weights: [nseq][Hq] log2 of the normaliser
     float *logits;                // weights: [nseq][Hkv][MBS][G][16] logits (log2 domain)
     uint64_t wait_ns;             // limit of every bounded wait
     int stop_item;                // failure tests: a warp's copies stop at this item (else INT_MAX)
-    int min_items;                // items of a CTA's range at least
+    int min_items;                // row tiles: tiles of a CTA's range at least
 };
 
 // Dynamic shared memory limit of a kernel, set once per device.
@@ -66,7 +67,8 @@ inline cudaError_t smem_once(const void *kernel, size_t bytes) {
 
 // one query row per sequence, window and sinks, or (weights set) the dense
 // decode that adds up the attention weights; tk, tv: tensor maps of the caches
-size_t stream_part_floats(int head_dim);
+size_t stream_workers(int sms);
+size_t stream_part_floats(int sms, int head_dim);
 cudaError_t launch_stream_decode(const CUtensorMap &tk, const CUtensorMap &tv, const SubsetArgs &a, int head_dim,
                                  CacheKind kind, int sms, cudaStream_t stream);
 
@@ -75,6 +77,9 @@ cudaError_t launch_stream_decode(const CUtensorMap &tk, const CUtensorMap &tv, c
 size_t row_tiles_slot_floats(int head_dim);
 cudaError_t launch_row_tiles(const CUtensorMap &tk, const CUtensorMap &tv, const SubsetArgs &a, int head_dim,
                              int sms, cudaStream_t stream);
+
+// rows of own part and prefix parts joined, written out
+cudaError_t launch_prefix_join(const SubsetArgs &a, int head_dim, cudaStream_t stream);
 
 struct EvictArgs {
     int32_t *kept, *new_lens;     // [B][Hkv][budget], [B]
