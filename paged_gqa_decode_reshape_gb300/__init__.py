@@ -1101,7 +1101,29 @@ def _scratch(workspace: Optional[torch.Tensor], dev: torch.device, nbytes: int):
             raise TypeError("workspace must be a torch.Tensor")
         if workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    return _ptr(workspace), workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+_sizes = {}  # workspace bytes per (query, device, shape): they depend on nothing else
+
+
+def _run(name: str, dev: torch.device, args, workspace: Optional[torch.Tensor] = None, shape=None) -> None:
+    """Call an entry point on dev's current stream; with a shape, its workspace (sized by
+    <name>_workspace_size(*shape)) goes before the stream."""
+    if torch._C._cuda_getDevice() != dev.index:
+        with torch.cuda.device(dev):
+            return _run(name, dev, args, workspace, shape)
+    L = load_library()
+    if shape is not None:
+        key = (name, dev.index, shape)
+        nbytes = _sizes.get(key)
+        if nbytes is None:
+            size = name[:-len("_fp8_block")] if name.endswith("_fp8_block") else name.removesuffix("_fp8")
+            nbytes = _sizes[key] = getattr(L, size + "_workspace_size")(*shape)
+        args += _scratch(workspace, dev, nbytes)
+    status = getattr(L, name)(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if status != PA_OK:
+        raise PagedDecodeError(name, status)
 
 
 def pa_decode_window_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
@@ -1129,30 +1151,24 @@ def pa_decode_window(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Te
                      block_tables: torch.Tensor, context_lens: torch.Tensor, window: int, sinks: int, scale: float,
                      workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Decode attention over each sequence's first `sinks` and last `window` tokens; writes out [B, Hq, D] (bf16)."""
-    L = load_library()
     dev, B, Hq, Hkv, D, BS, NB, MBS = _attention_checks(out, query, key_cache, value_cache, block_tables,
                                                         context_lens)
     window, sinks = _tokens(window, "window"), _tokens(sinks, "sinks")
-    with torch.cuda.device(dev):
-        ws, nbytes = _scratch(workspace, dev, L.pa_decode_window_workspace_size(B, Hq, Hkv, D))
-        _check("pa_decode_window",
-               L.pa_decode_window(_ptr(out), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(block_tables), MBS,
-                                  _ptr(context_lens), B, Hq, Hkv, D, BS, NB, window, sinks, float(scale),
-                                  ws, nbytes, _stream(dev)))
+    _run("pa_decode_window", dev,
+         (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(), MBS,
+          context_lens.data_ptr(), B, Hq, Hkv, D, BS, NB, window, sinks, float(scale)), workspace, (B, Hq, Hkv, D))
     return out
 
 
 def _window_fp8(name, per_block, out, query, key_cache, value_cache, k_scale, v_scale, block_tables, context_lens,
                 window, sinks, scale, workspace):
-    L = load_library()
     dev, B, Hq, Hkv, D, BS, NB, MBS = _attention_checks_fp8(out, query, key_cache, value_cache, block_tables,
                                                             context_lens, k_scale, v_scale, per_block)
     window, sinks = _tokens(window, "window"), _tokens(sinks, "sinks")
-    with torch.cuda.device(dev):
-        ws, nbytes = _scratch(workspace, dev, L.pa_decode_window_workspace_size(B, Hq, Hkv, D))
-        _check(name, getattr(L, name)(_ptr(out), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(k_scale),
-                                      _ptr(v_scale), _ptr(block_tables), MBS, _ptr(context_lens), B, Hq, Hkv, D, BS,
-                                      NB, window, sinks, float(scale), ws, nbytes, _stream(dev)))
+    _run(name, dev,
+         (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), k_scale.data_ptr(),
+          v_scale.data_ptr(), block_tables.data_ptr(), MBS, context_lens.data_ptr(), B, Hq, Hkv, D, BS, NB, window,
+          sinks, float(scale)), workspace, (B, Hq, Hkv, D))
     return out
 
 
@@ -1180,7 +1196,6 @@ def pa_decode_window_multi(out: torch.Tensor, query: torch.Tensor, key_cache: to
                            workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Windowed attention of several query rows per sequence: query / out [total_q, Hq, D], rows of sequence b
     cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1, right-aligned causal masks."""
-    L = load_library()
     _need(key_cache, "key_cache", torch.bfloat16, 4)
     dev = key_cache.device
     _need(value_cache, "value_cache", torch.bfloat16, 4, dev)
@@ -1197,13 +1212,10 @@ def pa_decode_window_multi(out: torch.Tensor, query: torch.Tensor, key_cache: to
     if context_lens.shape[0] != B or cu_seqlens_q.shape[0] != B + 1:
         raise ValueError("block_tables / context_lens / cu_seqlens_q batch mismatch")
     window, sinks = _tokens(window, "window"), _tokens(sinks, "sinks")
-    with torch.cuda.device(dev):
-        ws, nbytes = _scratch(workspace, dev, L.pa_decode_window_multi_workspace_size(B, T, Hq, Hkv, D))
-        _check("pa_decode_window_multi",
-               L.pa_decode_window_multi(_ptr(out), _ptr(query), _ptr(key_cache), _ptr(value_cache),
-                                        _ptr(block_tables), MBS, _ptr(cu_seqlens_q), _ptr(context_lens), B, T, Hq,
-                                        Hkv, D, BS, NB, window, sinks, float(scale), ws, nbytes,
-                                        _stream(dev)))
+    _run("pa_decode_window_multi", dev,
+         (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(), MBS,
+          cu_seqlens_q.data_ptr(), context_lens.data_ptr(), B, T, Hq, Hkv, D, BS, NB, window, sinks, float(scale)),
+         workspace, (B, T, Hq, Hkv, D))
     return out
 
 
@@ -1213,7 +1225,6 @@ def pa_decode_prefix(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Te
                      workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Decode attention of a batch with shared prefixes: sequences cu_group[g] .. cu_group[g + 1] - 1 see the
     prefix_lens[g] tokens of prefix_tables[g], then their own context_lens[b] tokens of block_tables[b]."""
-    L = load_library()
     dev, B, Hq, Hkv, D, BS, NB, MBS = _attention_checks(out, query, key_cache, value_cache, block_tables,
                                                         context_lens)
     _need(prefix_tables, "prefix_tables", torch.int32, 2, dev)
@@ -1222,12 +1233,10 @@ def pa_decode_prefix(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Te
     NG, PMBS = prefix_tables.shape
     if prefix_lens.shape[0] != NG or cu_group.shape[0] != NG + 1:
         raise ValueError("prefix_tables / prefix_lens / cu_group mismatch")
-    with torch.cuda.device(dev):
-        ws, nbytes = _scratch(workspace, dev, L.pa_decode_prefix_workspace_size(B, NG, Hq, Hkv, D))
-        _check("pa_decode_prefix",
-               L.pa_decode_prefix(_ptr(out), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(prefix_tables),
-                                  PMBS, _ptr(prefix_lens), _ptr(cu_group), NG, _ptr(block_tables), MBS,
-                                  _ptr(context_lens), B, Hq, Hkv, D, BS, NB, float(scale), ws, nbytes, _stream(dev)))
+    _run("pa_decode_prefix", dev,
+         (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), prefix_tables.data_ptr(),
+          PMBS, prefix_lens.data_ptr(), cu_group.data_ptr(), NG, block_tables.data_ptr(), MBS,
+          context_lens.data_ptr(), B, Hq, Hkv, D, BS, NB, float(scale)), workspace, (B, NG, Hq, Hkv, D))
     return out
 
 
@@ -1242,30 +1251,23 @@ def pa_decode_weights(out: torch.Tensor, weights: torch.Tensor, query: torch.Ten
                       scale: float, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """pa_decode that also adds each cached token's attention weight, summed over its KV head's query heads, to
     weights [NB, Hkv, BS] (fp32)."""
-    L = load_library()
     dev, B, Hq, Hkv, D, BS, NB, MBS = _attention_checks(out, query, key_cache, value_cache, block_tables,
                                                         context_lens)
     _need_weights(weights, NB, Hkv, BS, dev)
-    with torch.cuda.device(dev):
-        ws, nbytes = _scratch(workspace, dev, L.pa_decode_weights_workspace_size(B, Hq, Hkv, D, MBS))
-        _check("pa_decode_weights",
-               L.pa_decode_weights(_ptr(out), _ptr(weights), _ptr(query), _ptr(key_cache), _ptr(value_cache),
-                                   _ptr(block_tables), MBS, _ptr(context_lens), B, Hq, Hkv, D, BS, NB, float(scale),
-                                   ws, nbytes, _stream(dev)))
+    _run("pa_decode_weights", dev,
+         (out.data_ptr(), weights.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+          block_tables.data_ptr(), MBS, context_lens.data_ptr(), B, Hq, Hkv, D, BS, NB, float(scale)), workspace,
+         (B, Hq, Hkv, D, MBS))
     return out
 
 
 def pa_reset_weights(weights: torch.Tensor, slot_mapping: torch.Tensor) -> None:
     """Zero the accumulated weights [NB, Hkv, BS] of a write's slots."""
-    L = load_library()
     _need(weights, "weights", torch.float32, 3)
     dev = weights.device
     _need(slot_mapping, "slot_mapping", torch.int64, 1, dev)
     NB, Hkv, BS = weights.shape
-    with torch.cuda.device(dev):
-        _check("pa_reset_weights",
-               L.pa_reset_weights(_ptr(weights), _ptr(slot_mapping), slot_mapping.shape[0], Hkv, BS, NB,
-                                  _stream(dev)))
+    _run("pa_reset_weights", dev, (weights.data_ptr(), slot_mapping.data_ptr(), slot_mapping.shape[0], Hkv, BS, NB))
 
 
 def pa_evict(kept: torch.Tensor, new_lens: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Tensor,
@@ -1273,7 +1275,6 @@ def pa_evict(kept: torch.Tensor, new_lens: torch.Tensor, key_cache: torch.Tensor
              dst_tables: torch.Tensor, recent: int) -> None:
     """Keep at most kept.shape[2] tokens per (sequence, KV head), the `recent` newest and the largest weights of the
     rest, and copy them to the blocks of dst_tables; writes kept [B, Hkv, budget] and new_lens [B]."""
-    L = load_library()
     _need(key_cache, "key_cache", torch.bfloat16, 4)
     dev = key_cache.device
     _need(value_cache, "value_cache", torch.bfloat16, 4, dev)
@@ -1291,8 +1292,7 @@ def pa_evict(kept: torch.Tensor, new_lens: torch.Tensor, key_cache: torch.Tensor
         raise ValueError("block_tables / context_lens / dst_tables / kept / new_lens mismatch")
     if new_lens.data_ptr() == context_lens.data_ptr():
         raise ValueError("new_lens must not be context_lens")
-    with torch.cuda.device(dev):
-        _check("pa_evict",
-               L.pa_evict(_ptr(kept), _ptr(new_lens), _ptr(key_cache), _ptr(value_cache), _ptr(weights),
-                          _ptr(block_tables), MBS, _ptr(context_lens), _ptr(dst_tables), dst_tables.shape[1], B, Hkv,
-                          D, BS, NB, kept.shape[2], _tokens(recent, "recent"), _stream(dev)))
+    _run("pa_evict", dev,
+         (kept.data_ptr(), new_lens.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), weights.data_ptr(),
+          block_tables.data_ptr(), MBS, context_lens.data_ptr(), dst_tables.data_ptr(), dst_tables.shape[1], B, Hkv,
+          D, BS, NB, kept.shape[2], _tokens(recent, "recent")))
