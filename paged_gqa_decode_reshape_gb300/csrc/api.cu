@@ -901,6 +901,21 @@ size_t subset_workspace_bytes(const SubsetPlan &plan, int64_t rows, int64_t max_
     return subset_workspace(&w, plan, rows, Hq, Hkv, D) == PA_OK ? w.bytes : 0;
 }
 
+// Tensor map over the queries [rows][Hq][D], boxes of [query rows of a row
+// tile][heads of a group][64 dims] with 128-byte swizzle.
+int make_query_map(CUtensorMap *map, const void *q, int rows, int Hq, int G, int D) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return cuda_fail(cudaErrorNotSupported);
+    const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(Hq), cuuint64_t(rows)};
+    const cuuint64_t strides[2] = {cuuint64_t(D) * 2, cuuint64_t(Hq) * D * 2};
+    const cuuint32_t box[3] = {64u, cuuint32_t(G), cuuint32_t(kRowTile / G)};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PA_OK : cuda_fail(cudaErrorInvalidValue);
+}
+
 // the launches, after the argument checks
 int run_subset(SubsetArgs a, const SubsetPlan &plan, int D, CacheKind kind, void *workspace, size_t workspace_bytes,
                void *stream) {
@@ -930,7 +945,11 @@ int run_subset(SubsetArgs a, const SubsetPlan &plan, int D, CacheKind kind, void
     else if ((rc = make_cache_map(&tv, a.vc, a.Hkv, D, kBlockSize, a.NB)) != PA_OK) return rc;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
-    if (plan.tiles) e = launch_row_tiles(tk, tv, a, D, w.sms, st);
+    if (plan.tiles) {
+        CUtensorMap tq;
+        if ((rc = make_query_map(&tq, a.q, a.rows, a.Hq, a.G, D)) != PA_OK) return rc;
+        e = launch_row_tiles(tk, tv, tq, a, D, w.sms, st);
+    }
     if (e == cudaSuccess && plan.stream) e = launch_stream_decode(tk, tv, a, D, kind, w.sms, st);
     if (e == cudaSuccess && plan.prefix) e = launch_prefix_join(a, D, st);
     return e == cudaSuccess ? PA_OK : cuda_fail(e);

@@ -18,7 +18,8 @@
 //    cut into equal ranges, one per CTA of a persistent grid: any mix of
 //    lengths loads the SMs evenly.
 //  * Roles: a producer warp copies K and V tiles by TMA (one box per block and
-//    64 dims, 128-byte swizzle) into a ring of four 128-token buffers; one
+//    64 dims, 128-byte swizzle) into a ring of four 128-token buffers, and each
+//    unit's queries (one box per row tile and 64 dims: RQ rows of G heads); one
 //    thread issues the matrix products; each row tile has four softmax warps,
 //    one thread per row, with its logits S (128 columns, overwritten by the
 //    bf16 probabilities P) and its output O (D columns) in tensor memory: 2 x
@@ -53,6 +54,16 @@ constexpr int kInfo = 8;         // tile descriptions in flight
 constexpr int kWarpsRT = 12;     // 2 x 4 softmax, producer, products, two that only make up a warpgroup
 constexpr float kGrow = 8.f;     // log2 growth of a maximum that rescales O
 
+// 3-D tiled TMA load into shared memory, completion counted on `bar`.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2,
+                                            uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+        : "memory");
+}
+
 __device__ __forceinline__ uint64_t l2_policy_normal() {
     uint64_t p;
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
@@ -67,7 +78,7 @@ struct RowCfg {
     static constexpr int BLK = kBlockSize * 128;           // a block's 64 dims
     static constexpr size_t off_ring = 2 * size_t(TILE);   // after the two Q tiles
     static constexpr size_t off_bars = off_ring + size_t(kStages) * TILE;
-    static constexpr size_t off_info = off_bars + 160;
+    static constexpr size_t off_info = off_bars + 192;
     static constexpr size_t off_misc = off_info + kInfo * 4;
     static constexpr size_t off_pre = off_misc + 32;
     static constexpr size_t SMEM = 1024 + off_pre + (kPreCap + 1) * 8;
@@ -140,21 +151,21 @@ struct Work {
 template <int D, bool PREFIX>
 __global__ void __launch_bounds__(kWarpsRT * 32, 1)
     row_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                     const SubsetArgs a) {
+                     const __grid_constant__ CUtensorMap tm_q, const SubsetArgs a) {
     using C = RowCfg<D>;
     constexpr int BS = kBlockSize, HV = C::HV;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *bp = smem_raw + (base - raw);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int Hkv = a.Hkv, G = a.G;
     const Work<PREFIX> work(a);
     const int RQ = work.RQ;
     const uint32_t ring = base + uint32_t(C::off_ring);
     const uint32_t kv_full = base + uint32_t(C::off_bars), kv_empty = kv_full + kStages * 8;
-    const uint32_t q_ready = kv_empty + kStages * 8, s_full = q_ready + 16, p_ready = s_full + 16;
-    const uint32_t drained = p_ready + 16, piece_bar = drained + 8, last_bar = piece_bar + 16;
+    const uint32_t q_full = kv_empty + kStages * 8, q_empty = q_full + 16, s_full = q_empty + 16;
+    const uint32_t p_ready = s_full + 16, o_full = p_ready + 16, drained = o_full + 16, piece_bar = drained + 8, last_bar = piece_bar + 16;
     volatile int *info = reinterpret_cast<volatile int *>(bp + C::off_info);
     volatile int *misc = reinterpret_cast<volatile int *>(bp + C::off_misc);  // [0] tensor memory, [1] gave up, [4 + w] completes the count
     int64_t *pre = reinterpret_cast<int64_t *>(bp + C::off_pre);
@@ -163,14 +174,17 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
     if (tid == 0) {
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
+        prefetch_tensormap(&tm_q);
         for (int i = 0; i < kStages; ++i) {
             mbar_init(kv_full + 8 * i, 1);
             mbar_init(kv_empty + 8 * i, 1);
         }
         for (int w = 0; w < 2; ++w) {
-            mbar_init(q_ready + 8 * w, 128);
+            mbar_init(q_full + 8 * w, 1);
+            mbar_init(q_empty + 8 * w, 1);
             mbar_init(s_full + 8 * w, 1);
             mbar_init(p_ready + 8 * w, 128);
+            mbar_init(o_full + 8 * w, 1);
             mbar_init(piece_bar + 8 * w, 4);
             mbar_init(last_bar + 8 * w, 1);
         }
@@ -300,6 +314,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
         const int mbs = PREFIX ? a.PMBS : a.MBS;
         const uint64_t policy = l2_policy_normal();  // other units of the KV head read the same blocks
         uint32_t fill = 0, tile_no = 0;  // ring buffers and tiles so far
+        uint32_t nq[2] = {0, 0};         // query tiles so far
         bool ok = true;
         for (int64_t p = pos0; ok && p < pos1;) {
             const int t0 = int(p - s0), t1 = int(min(pos1 - s0, int64_t(x.n)));
@@ -340,6 +355,22 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                     if (lane < 8 * HV && ph >= 0)
                         tma_load_4d(ring + st * C::TILE + hf * C::HALF + i * C::BLK, kv ? &tm_v : &tm_k,
                                     kv_full + 8 * st, hf * 64, x.kvh, 0, ph, policy);
+                    if (kv == 0 && t == t0) {
+                        // the unit's queries: rows (query row, head) are consecutive; rows past the
+                        // unit's are read too and dropped at the end
+                        for (int w = 0; ok && w < (x.nr > RQ ? 2 : 1); ++w) {
+                            if (nq[w] > 0) ok = wait(q_empty + 8 * w, nq[w] + 1);
+                            if (!ok) break;
+                            ++nq[w];
+                            if (lane == 0) {
+                                mbar_arrive_expect_tx(q_full + 8 * w, uint32_t(RQ * G * D * 2));
+                                for (int f = 0; f < HV; ++f)
+                                    tma_load_3d(base + w * C::TILE + f * C::HALF, &tm_q, q_full + 8 * w, f * 64,
+                                                x.kvh * G, x.r0 + w * RQ, policy);
+                            }
+                            __syncwarp();
+                        }
+                    }
                 }
                 if (!ok) break;
             }
@@ -349,28 +380,37 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
         // no copy may land after the CTA is gone
         for (uint32_t f = fill > kStages ? fill - kStages : 0; f < fill; ++f)
             mbar_wait_bounded(kv_full + 8 * (f % kStages), (f / kStages) & 1u, a.wait_ns);
+        for (int w = 0; w < 2; ++w)
+            if (nq[w] > 0) mbar_wait_bounded(q_full + 8 * w, (nq[w] - 1) & 1u, a.wait_ns);
     } else if (warp == 9) {
         // ====================================================== matrix products
         constexpr uint32_t id_s = tc_idesc(128, 128, false), id_o = tc_idesc(128, D, true);
         uint32_t use = 0, tile_no = 0;          // ring buffers and tiles so far
-        uint32_t nq[2] = {0, 0}, np_[2] = {0, 0};  // phases of q_ready and p_ready
+        uint32_t nq[2] = {0, 0}, np_[2] = {0, 0};  // phases of q_full and p_ready
         bool ok = true;
+        // the same value in every lane, known as such: the products take uniform operands
+        auto uniform = [](uint32_t v) -> uint32_t { return __shfl_sync(0xffffffffu, v, 0); };
         // S_w = Q_w K^T from ring buffer st
         auto qk = [&](int w, uint32_t st) {
-            const uint32_t q = base + w * C::TILE, k = ring + st * C::TILE;
+            const uint32_t q = uniform(tc_desc_lo(base + w * C::TILE, 16));
+            const uint32_t k = uniform(tc_desc_lo(ring + st * C::TILE, 16)), d = uniform(tmem + 256 * w);
+            if (tc_elect()) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t o = (kk / 4) * C::HALF + (kk % 4) * 32;
-                tc_mma_ss(tmem + 256 * w, tc_desc(q + o, 16, 1024), tc_desc(k + o, 16, 1024), id_s, kk > 0);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t o = ((kk / 4) * C::HALF + (kk % 4) * 32) >> 4;
+                    tc_mma_ss(d, q + o, kTcDescHi, k + o, kTcDescHi, id_s, kk > 0);
+                }
             }
         };
         // O_w (+)= P_w V from ring buffer st
         auto pv = [&](int w, uint32_t st, bool first) {
-            const uint32_t v = ring + st * C::TILE;
+            const uint32_t v = uniform(tc_desc_lo(ring + st * C::TILE, C::HALF)), t = uniform(tmem + 256 * w);
+            const bool more = uniform(!first);
+            if (tc_elect()) {
 #pragma unroll
-            for (int kk = 0; kk < kTileTok / 16; ++kk)
-                tc_mma_ts(tmem + 256 * w + 128, tmem + 256 * w + 8 * kk, tc_desc(v + kk * 2048, C::HALF, 1024), id_o,
-                          !first || kk > 0);
+                for (int kk = 0; kk < kTileTok / 16; ++kk)
+                    tc_mma_ts(t + 128, t + 8 * kk, v + (kk * 2048 >> 4), kTcDescHi, id_o, more || kk > 0);
+            }
         };
         for (int64_t p = pos0; ok && p < pos1;) {
             const int t0 = int(p - s0), t1 = int(min(pos1 - s0, int64_t(x.n)));
@@ -398,19 +438,20 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                     }
                 }
                 for (int w = 0; w < nact; ++w) {
-                    if (t == t0) ok = wait(q_ready + 8 * w, nq[w]++);
+                    if (t == t0) ok = wait(q_full + 8 * w, nq[w]++);
                     else ok = wait(p_ready + 8 * w, np_[w]++);
                     if (!ok) break;
                     tc_fence_after();
-                    if (lane == 0) {
-                        if (t > t0) pv(w, vs, t == t0 + 1);
-                        if (t < t1) qk(w, ks);
-                        tc_commit(s_full + 8 * w);
+                    if (t > t0) pv(w, vs, t == t0 + 1);
+                    if (t < t1) qk(w, ks);
+                    if (tc_elect()) {
+                        tc_commit((t < t1 ? s_full : o_full) + 8 * w);
+                        if (t == t1 - 1) tc_commit(q_empty + 8 * w);
                     }
                     __syncwarp();
                 }
                 if (!ok) break;
-                if (lane == 0) {
+                if (tc_elect()) {
                     if (t > t0) tc_commit(kv_empty + 8 * vs);
                     if (t < t1) tc_commit(kv_empty + 8 * ks);
                 }
@@ -425,7 +466,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
         }
         if (!ok) {
             // gave up: the products in flight end before the memory they use goes
-            if (lane == 0) tc_commit(drained);
+            if (tc_elect()) tc_commit(drained);
             __syncwarp();
             mbar_wait_bounded(drained, 0, a.wait_ns);
         }
@@ -437,28 +478,13 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
         const uint32_t lane_base = uint32_t(warp & 3) << 21;  // this warp's 32 of the 128 lanes
         const uint32_t ts = tmem + lane_base + 256 * w, to = ts + 128;
         const int i = row / G, h = row - i * G;
-        uint32_t ph = 0, tile_no = 0, cuts = 0;
+        uint32_t ph = 0, tile_no = 0, units = 0, cuts = 0;
         bool ok = true;
         for (int64_t p = pos0; ok && p < pos1;) {
             const int t0 = int(p - s0), t1 = int(min(pos1 - s0, int64_t(x.n)));
             const int ir = w * RQ + i;  // query row of the unit
             const bool act = i < RQ && ir < x.nr;
             if (w == 0 || x.nr > RQ) {
-                // ---- the row's query into shared memory
-                {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(
-                        a.q + (int64_t(x.r0 + ir) * a.Hq + x.kvh * G + h) * D);
-                    uint8_t *dst = bp + w * C::TILE + row * 128;
-                    uint4 v[D / 8];
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c) v[c] = act ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c)
-                        *reinterpret_cast<uint4 *>(dst + (c / 8) * C::HALF + (((c % 8) ^ (row & 7)) << 4)) = v[c];
-                    fence_proxy_async();
-                    tc_fence_before();  // and the previous unit's reads of O
-                    mbar_arrive(q_ready + 8 * w);
-                }
                 int lim = 0;
                 if (act) {
                     if (PREFIX) {
@@ -554,7 +580,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                     mbar_arrive(p_ready + 8 * w);
                 }
                 // ---- the end of the unit, or of this CTA's piece of it
-                if (ok) ok = wait(s_full + 8 * w, ph++);
+                if (ok) ok = wait(o_full + 8 * w, units++);
                 if (!ok) break;
                 tc_fence_after();
                 const bool whole = t0 == 0 && t1 == x.n;
@@ -622,32 +648,43 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                         if (misc[4 + w]) {
                             if (act) {
                                 float M = -INFINITY, Ls = 0.f;
-                                for (int k = 0; k < npieces; ++k) {
-                                    const float *ps = a.slots + (2 * int64_t(c0 + k) + (k == 0)) * C::SLOT + w * (C::SLOT / 2);
-                                    M = fmaxf(M, __ldcg(ps + 128 * D + row));
-                                }
+                                auto piece_of = [&](int k) {
+                                    return a.slots + (2 * int64_t(c0 + k) + (k == 0)) * C::SLOT + w * (C::SLOT / 2);
+                                };
+                                for (int k = 0; k < npieces; ++k) M = fmaxf(M, __ldcg(piece_of(k) + 128 * D + row));
                                 const float Mr = M == -INFINITY ? 0.f : M;
                                 for (int k = 0; k < npieces; ++k) {
-                                    const float *ps = a.slots + (2 * int64_t(c0 + k) + (k == 0)) * C::SLOT + w * (C::SLOT / 2);
+                                    const float *ps = piece_of(k);
                                     Ls += fast_exp2(__ldcg(ps + 128 * D + row) - Mr) * __ldcg(ps + 128 * (D + 1) + row);
                                 }
                                 const float iv = Ls == 0.f ? 0.f : 1.f / Ls;
-                                for (int d = 0; d < D; d += 8) {
-                                    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                                for (int d = 0; d < D; d += 32) {
+                                    float v[32];
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) v[e] = 0.f;
                                     for (int k = 0; k < npieces; ++k) {
-                                        const float *ps = a.slots + (2 * int64_t(c0 + k) + (k == 0)) * C::SLOT + w * (C::SLOT / 2);
+                                        const float *ps = piece_of(k);
+                                        float4 y[8];
                                         const float f = fast_exp2(__ldcg(ps + 128 * D + row) - Mr) * iv;
-                                        const float4 y0 = __ldcg(reinterpret_cast<const float4 *>(ps + row * D + d));
-                                        const float4 y1 = __ldcg(reinterpret_cast<const float4 *>(ps + row * D + d + 4));
+#pragma unroll
+                                        for (int e = 0; e < 8; ++e)
+                                            y[e] = __ldcg(reinterpret_cast<const float4 *>(ps + row * D + d) + e);
                                         if (f == 0.f) continue;  // a piece in which the row saw nothing
-                                        v[0] += f * y0.x, v[1] += f * y0.y, v[2] += f * y0.z, v[3] += f * y0.w;
-                                        v[4] += f * y1.x, v[5] += f * y1.y, v[6] += f * y1.z, v[7] += f * y1.w;
+#pragma unroll
+                                        for (int e = 0; e < 8; ++e) {
+                                            v[4 * e] += f * y[e].x;
+                                            v[4 * e + 1] += f * y[e].y;
+                                            v[4 * e + 2] += f * y[e].z;
+                                            v[4 * e + 3] += f * y[e].w;
+                                        }
                                     }
 #pragma unroll
-                                    for (int k = 0; k < 8; ++k) bad |= !(fabsf(v[k]) <= 3.4028234e38f);
-                                    *reinterpret_cast<uint4 *>(a.out + orow * D + d) =
-                                        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                   pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+                                    for (int e = 0; e < 32; ++e) bad |= !(fabsf(v[e]) <= 3.4028234e38f);
+#pragma unroll
+                                    for (int e = 0; e < 32; e += 8)
+                                        *reinterpret_cast<uint4 *>(a.out + orow * D + d + e) =
+                                            make_uint4(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]),
+                                                       pack_bf16x2(v[e + 4], v[e + 5]), pack_bf16x2(v[e + 6], v[e + 7]));
                                 }
                             }
                             if (row == 0) a.counters[2 * c0 + w] = 0;
@@ -710,24 +747,24 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
 }
 
 template <int D, bool PREFIX>
-cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const SubsetArgs &a, int grid,
-                     cudaStream_t stream) {
+cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tq, const SubsetArgs &a,
+                     int grid, cudaStream_t stream) {
     const auto kernel = row_tiles_kernel<D, PREFIX>;
     const cudaError_t e = smem_once(reinterpret_cast<const void *>(kernel), RowCfg<D>::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3(grid), dim3(kWarpsRT * 32), RowCfg<D>::SMEM, stream, tk, tv, a);
+    return launch_pdl(kernel, dim3(grid), dim3(kWarpsRT * 32), RowCfg<D>::SMEM, stream, tk, tv, tq, a);
 }
 
 }  // namespace
 
 size_t row_tiles_slot_floats(int head_dim) { return size_t(2) * 128 * (head_dim + 2); }
 
-cudaError_t launch_row_tiles(const CUtensorMap &tk, const CUtensorMap &tv, const SubsetArgs &args, int head_dim,
-                             int sms, cudaStream_t stream) {
+cudaError_t launch_row_tiles(const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tq,
+                             const SubsetArgs &args, int head_dim, int sms, cudaStream_t stream) {
     SubsetArgs a = args;
     a.min_items = 2;
-    if (a.pt) return head_dim == 128 ? launch_t<128, true>(tk, tv, a, sms, stream) : launch_t<64, true>(tk, tv, a, sms, stream);
-    return head_dim == 128 ? launch_t<128, false>(tk, tv, a, sms, stream) : launch_t<64, false>(tk, tv, a, sms, stream);
+    if (a.pt) return head_dim == 128 ? launch_t<128, true>(tk, tv, tq, a, sms, stream) : launch_t<64, true>(tk, tv, tq, a, sms, stream);
+    return head_dim == 128 ? launch_t<128, false>(tk, tv, tq, a, sms, stream) : launch_t<64, false>(tk, tv, tq, a, sms, stream);
 }
 
 }  // namespace pa
