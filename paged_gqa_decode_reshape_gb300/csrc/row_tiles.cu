@@ -46,7 +46,7 @@
 namespace pa {
 namespace {
 
-constexpr int kPreCap = 512;     // entries of the work prefix in shared memory
+constexpr int kPreCap = 128;     // entries of the work prefix in shared memory
 constexpr int kTileTok = 128;    // tokens per tile
 constexpr int kTileBlk = kTileTok / kBlockSize;
 constexpr int kStages = 4;       // K / V tiles in the ring
@@ -77,7 +77,8 @@ struct RowCfg {
     static constexpr int TILE = HV * HALF;                 // a K, V or Q tile
     static constexpr int BLK = kBlockSize * 128;           // a block's 64 dims
     static constexpr size_t off_ring = 2 * size_t(TILE);   // after the two Q tiles
-    static constexpr size_t off_bars = off_ring + size_t(kStages) * TILE;
+    static constexpr size_t off_stage = off_ring + size_t(kStages) * TILE;  // 32 rows of 128 bytes per softmax warp
+    static constexpr size_t off_bars = off_stage + 8 * 4096;
     static constexpr size_t off_info = off_bars + 192;
     static constexpr size_t off_misc = off_info + kInfo * 4;
     static constexpr size_t off_pre = off_misc + 32;
@@ -299,6 +300,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
     };
     // wait unless the CTA gave up; false: it has
     auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u))) return true;
         const bool ok = !misc[1] && mbar_wait_bounded(bar, parity & 1u, a.wait_ns);
         if (__all_sync(0xffffffffu, ok)) return true;
         give_up();
@@ -426,12 +428,14 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                     const int lb = e_last - (t - 1) * kTileBlk;  // the unit's last block, if in this tile
                     const bool cut = tail && lb >= 0 && lb < kTileBlk;
                     if (blocks != 0xff || cut) {
-                        for (int idx = lane; idx < kTileTok * HV * 8; idx += 32) {
-                            const int c = idx & 7, row = (idx >> 3) % kTileTok, hf = idx / (8 * kTileTok);
-                            const int i = row / BS;
-                            if (!((blocks >> i) & 1) || (cut && i == lb && row % BS >= tail))
-                                *reinterpret_cast<uint4 *>(bp + C::off_ring + vs * C::TILE + hf * C::HALF + row * 128 +
-                                                           c * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        uint8_t *v = bp + C::off_ring + vs * C::TILE;
+                        for (int i = 0; i < kTileBlk; ++i) {
+                            const int from = !((blocks >> i) & 1) ? 0 : cut && i == lb ? tail : BS;  // first row to zero
+                            for (int idx = from * 8 + lane; idx < BS * 8; idx += 32)
+#pragma unroll
+                                for (int hf = 0; hf < HV; ++hf)
+                                    *reinterpret_cast<uint4 *>(v + hf * C::HALF + i * C::BLK + idx * 16) =
+                                        make_uint4(0u, 0u, 0u, 0u);
                         }
                         fence_proxy_async();
                         __syncwarp();
@@ -442,7 +446,10 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                     else ok = wait(p_ready + 8 * w, np_[w]++);
                     if (!ok) break;
                     tc_fence_after();
-                    if (t > t0) pv(w, vs, t == t0 + 1);
+                    if (t > t0) {
+                        pv(w, vs, t == t0 + 1);
+                        if (w == nact - 1 && tc_elect()) tc_commit(kv_empty + 8 * vs);
+                    }
                     if (t < t1) qk(w, ks);
                     if (tc_elect()) {
                         tc_commit((t < t1 ? s_full : o_full) + 8 * w);
@@ -451,10 +458,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                     __syncwarp();
                 }
                 if (!ok) break;
-                if (tc_elect()) {
-                    if (t > t0) tc_commit(kv_empty + 8 * vs);
-                    if (t < t1) tc_commit(kv_empty + 8 * ks);
-                }
+                if (t < t1 && tc_elect()) tc_commit(kv_empty + 8 * ks);
                 __syncwarp();
                 if (t < t1) {
                     use += 2;  // this K, and the V that follows it
@@ -588,36 +592,66 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                 const int c0 = int(s0 / L);
                 float *slot = a.slots + (2 * int64_t(blockIdx.x) + (int(blockIdx.x) == c0)) * C::SLOT + w * (C::SLOT / 2);
                 const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
-                bool bad = false;
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t o[32];
+                const unsigned acts = __ballot_sync(0xffffffffu, act);
+                uint8_t *stage = bp + C::off_stage + warp * 4096;
+                const int sj = lane & 7, sr = lane >> 3;
+                // 32 rows of 128 bytes, one per lane, to global memory: eight lanes per row
+                auto store_rows = [&](const uint4 (&v)[8], auto row_at) {
                     __syncwarp();
-                    tmem_ld32(to + 32 * c, o);
-                    tc_wait_ld();
-                    if (m == -INFINITY && l == 0.f) {  // no token seen: 0, whatever the products held
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0u;
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<uint4 *>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = v[j];
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int r = 4 * k + sr;
+                        const uint4 y = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((sj ^ (r & 7)) << 4));
+                        const int64_t ro = __shfl_sync(0xffffffffu, orow, r);
+                        if ((acts >> r) & 1u) __stcg(reinterpret_cast<uint4 *>(row_at(r, ro)) + sj, y);
                     }
-                    if (!act) {
-                    } else if (!PREFIX && whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * D + 32 * c);
+                };
+                unsigned bad = 0;  // rows of this warp whose result is not finite
+                auto finite = [](float v) { return fabsf(v) <= 3.4028234e38f; };
+                if (!PREFIX && whole) {
+                    bool mine = true;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            float v[8];
+                    for (int c = 0; c < HV; ++c) {
+                        uint4 v[8];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                v[k] = __uint_as_float(o[e + k]) * inv;
-                                bad |= !(fabsf(v[k]) <= 3.4028234e38f);
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t o[32];
+                            tmem_ld32(to + 64 * c + 32 * q, o);
+                            tc_wait_ld();
+                            uint32_t y[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                // no token seen: 0, whatever the products held
+                                const float x0 = l == 0.f ? 0.f : __uint_as_float(o[2 * e]) * inv;
+                                const float x1 = l == 0.f ? 0.f : __uint_as_float(o[2 * e + 1]) * inv;
+                                mine = mine && finite(x0) && finite(x1);
+                                y[e] = pack_bf16x2(x0, x1);
                             }
-                            dst[e / 8] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                    pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-                        }
-                    } else {
-                        uint4 *dst = reinterpret_cast<uint4 *>((PREFIX && whole ? a.rowres + orow * D
-                                                                               : slot + row * D) + 32 * c);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) __stcg(dst + e / 4, make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+                            for (int e = 0; e < 4; ++e)
+                                v[4 * q + e] = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+                        }
+                        store_rows(v, [&](int, int64_t ro) { return a.out + ro * D + 64 * c; });
+                    }
+                    bad = __ballot_sync(0xffffffffu, act && !mine);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        uint4 v[8];
+                        tmem_ld32(to + 32 * c, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            v[e] = l == 0.f ? make_uint4(0u, 0u, 0u, 0u)
+                                            : make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        store_rows(v, [&](int r, int64_t ro) {
+                            return (PREFIX && whole ? a.rowres + ro * D : slot + ((warp & 3) * 32 + r) * D) + 32 * c;
+                        });
                     }
                 }
                 if (act && (PREFIX || !whole)) {
@@ -646,53 +680,73 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                         if (!(ok = wait(last_bar + 8 * w, cuts))) break;
                         ++cuts;
                         if (misc[4 + w]) {
-                            if (act) {
-                                float M = -INFINITY, Ls = 0.f;
-                                auto piece_of = [&](int k) {
-                                    return a.slots + (2 * int64_t(c0 + k) + (k == 0)) * C::SLOT + w * (C::SLOT / 2);
-                                };
-                                for (int k = 0; k < npieces; ++k) M = fmaxf(M, __ldcg(piece_of(k) + 128 * D + row));
-                                const float Mr = M == -INFINITY ? 0.f : M;
+                            auto piece_of = [&](int k) {
+                                return a.slots + (2 * int64_t(c0 + k) + (k == 0)) * C::SLOT + w * (C::SLOT / 2);
+                            };
+                            // weights of the pieces: lane = row; values: a row per load, all lanes
+                            float M = -INFINITY, Ls = 0.f;
+                            for (int k = 0; k < npieces; ++k)
+                                if (act) M = fmaxf(M, __ldcg(piece_of(k) + 128 * D + row));
+                            const float Mr = M == -INFINITY ? 0.f : M;
+                            for (int k = 0; k < npieces; ++k)
+                                if (act)
+                                    Ls += fast_exp2(__ldcg(piece_of(k) + 128 * D + row) - Mr) *
+                                          __ldcg(piece_of(k) + 128 * (D + 1) + row);
+                            const float iv = Ls == 0.f ? 0.f : 1.f / Ls;
+                            constexpr int V = D / 32, RB = 16;  // values per lane and row, rows at once
+                            for (int rb = 0; rb < 32; rb += RB) {
+                                if (!((acts >> rb) & ((1u << RB) - 1u))) continue;
+                                float v[RB][V];
+#pragma unroll
+                                for (int r = 0; r < RB; ++r)
+#pragma unroll
+                                    for (int e = 0; e < V; ++e) v[r][e] = 0.f;
                                 for (int k = 0; k < npieces; ++k) {
                                     const float *ps = piece_of(k);
-                                    Ls += fast_exp2(__ldcg(ps + 128 * D + row) - Mr) * __ldcg(ps + 128 * (D + 1) + row);
-                                }
-                                const float iv = Ls == 0.f ? 0.f : 1.f / Ls;
-                                for (int d = 0; d < D; d += 32) {
-                                    float v[32];
+                                    const float f = act ? fast_exp2(__ldcg(ps + 128 * D + row) - Mr) * iv : 0.f;
+                                    const float *src = ps + ((warp & 3) * 32 + rb) * D + lane * V;
+                                    float y[RB][V];
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e) v[e] = 0.f;
-                                    for (int k = 0; k < npieces; ++k) {
-                                        const float *ps = piece_of(k);
-                                        float4 y[8];
-                                        const float f = fast_exp2(__ldcg(ps + 128 * D + row) - Mr) * iv;
+                                    for (int r = 0; r < RB; ++r) {
+                                        if (!((acts >> (rb + r)) & 1u)) {
 #pragma unroll
-                                        for (int e = 0; e < 8; ++e)
-                                            y[e] = __ldcg(reinterpret_cast<const float4 *>(ps + row * D + d) + e);
-                                        if (f == 0.f) continue;  // a piece in which the row saw nothing
-#pragma unroll
-                                        for (int e = 0; e < 8; ++e) {
-                                            v[4 * e] += f * y[e].x;
-                                            v[4 * e + 1] += f * y[e].y;
-                                            v[4 * e + 2] += f * y[e].z;
-                                            v[4 * e + 3] += f * y[e].w;
+                                            for (int e = 0; e < V; ++e) y[r][e] = 0.f;
+                                        } else if constexpr (V == 4) {
+                                            const float4 t = __ldcg(reinterpret_cast<const float4 *>(src + r * D));
+                                            y[r][0] = t.x, y[r][1] = t.y, y[r][2] = t.z, y[r][3] = t.w;
+                                        } else {
+                                            const float2 t = __ldcg(reinterpret_cast<const float2 *>(src + r * D));
+                                            y[r][0] = t.x, y[r][1] = t.y;
                                         }
                                     }
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e) bad |= !(fabsf(v[e]) <= 3.4028234e38f);
+                                    for (int r = 0; r < RB; ++r) {
+                                        const float fr = __shfl_sync(0xffffffffu, f, rb + r);
 #pragma unroll
-                                    for (int e = 0; e < 32; e += 8)
-                                        *reinterpret_cast<uint4 *>(a.out + orow * D + d + e) =
-                                            make_uint4(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]),
-                                                       pack_bf16x2(v[e + 4], v[e + 5]), pack_bf16x2(v[e + 6], v[e + 7]));
+                                        for (int e = 0; e < V; ++e) v[r][e] += fr * y[r][e];
+                                    }
+                                }
+#pragma unroll
+                                for (int r = 0; r < RB; ++r) {
+                                    const int64_t ro = __shfl_sync(0xffffffffu, orow, rb + r);
+                                    bool fine = true;
+#pragma unroll
+                                    for (int e = 0; e < V; ++e) fine = fine && finite(v[r][e]);
+                                    if (!__all_sync(0xffffffffu, fine)) bad |= 1u << (rb + r);
+                                    if ((acts >> (rb + r)) & 1u) {
+                                        uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + ro * D) + lane * (V / 2);
+#pragma unroll
+                                        for (int e = 0; e < V; e += 2) dst[e / 2] = pack_bf16x2(v[r][e], v[r][e + 1]);
+                                    }
                                 }
                             }
+                            bad &= acts;
                             if (row == 0) a.counters[2 * c0 + w] = 0;
                         }
                     }
                     // ---- rows that are not finite, again over their own tokens only (in fp32, a row per warp)
-                    unsigned again = __ballot_sync(0xffffffffu, bad);
-                    while (again) {
+                    __syncwarp();
+                    for (unsigned again = bad; again;) {
                         const int src = __ffs(again) - 1;
                         again &= again - 1;
                         const int rs1 = __shfl_sync(0xffffffffu, S1, src), rlo = __shfl_sync(0xffffffffu, lo, src);
