@@ -901,6 +901,22 @@ size_t subset_workspace_bytes(const SubsetPlan &plan, int64_t rows, int64_t max_
     return subset_workspace(&w, plan, rows, Hq, Hkv, D) == PA_OK ? w.bytes : 0;
 }
 
+// Tensor map over the V cache [NB][BS][Hkv][D] for boxes of a block's tokens
+// of one head, 64 dims (128 swizzled bytes) after 64 dims.
+int make_v_map(CUtensorMap *map, const void *cache, int Hkv, int D, int64_t NB) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return cuda_fail(cudaErrorNotSupported);
+    const cuuint64_t tok = cuuint64_t(Hkv) * D * 2;
+    const cuuint64_t dims[5] = {64, cuuint64_t(kBlockSize), cuuint64_t(D / 64), cuuint64_t(Hkv), cuuint64_t(NB)};
+    const cuuint64_t strides[4] = {tok, 128, cuuint64_t(D) * 2, tok * kBlockSize};
+    const cuuint32_t box[5] = {64u, cuuint32_t(kBlockSize), cuuint32_t(D / 64), 1u, 1u};
+    const cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(cache), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PA_OK : cuda_fail(cudaErrorInvalidValue);
+}
+
 // Tensor map over the queries [rows][Hq][D], boxes of [query rows of a row
 // tile][heads of a group][64 dims] with 128-byte swizzle.
 int make_query_map(CUtensorMap *map, const void *q, int rows, int Hq, int G, int D) {
@@ -942,13 +958,14 @@ int run_subset(SubsetArgs a, const SubsetPlan &plan, int D, CacheKind kind, void
     CUtensorMap tk, tv;
     if ((rc = make_cache_map(&tk, a.kc, a.Hkv, D, kBlockSize, a.NB, fp8)) != PA_OK) return rc;
     if (fp8) std::memset(&tv, 0, sizeof tv);  // an E4M3 V tile is contiguous: plain bulk copies
-    else if ((rc = make_cache_map(&tv, a.vc, a.Hkv, D, kBlockSize, a.NB)) != PA_OK) return rc;
+    else if (plan.stream && (rc = make_cache_map(&tv, a.vc, a.Hkv, D, kBlockSize, a.NB)) != PA_OK) return rc;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
     if (plan.tiles) {
-        CUtensorMap tq;
+        CUtensorMap tq, tv5;
         if ((rc = make_query_map(&tq, a.q, a.rows, a.Hq, a.G, D)) != PA_OK) return rc;
-        e = launch_row_tiles(tk, tv, tq, a, D, w.sms, st);
+        if ((rc = make_v_map(&tv5, a.vc, a.Hkv, D, a.NB)) != PA_OK) return rc;
+        e = launch_row_tiles(tk, tv5, tq, a, D, w.sms, st);
     }
     if (e == cudaSuccess && plan.stream) e = launch_stream_decode(tk, tv, a, D, kind, w.sms, st);
     if (e == cudaSuccess && plan.prefix) e = launch_prefix_join(a, D, st);

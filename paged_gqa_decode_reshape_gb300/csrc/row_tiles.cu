@@ -17,9 +17,10 @@
 //    tiles of 128 tokens (8 blocks). Units are concatenated, tile by tile, and
 //    cut into equal ranges, one per CTA of a persistent grid: any mix of
 //    lengths loads the SMs evenly.
-//  * Roles: a producer warp copies K and V tiles by TMA (one box per block and
-//    64 dims, 128-byte swizzle) into a ring of four 128-token buffers, and each
-//    unit's queries (one box per row tile and 64 dims: RQ rows of G heads); one
+//  * Roles: two producer warps copy K and V tiles by TMA (128-byte swizzle; a K
+//    box is 16 tokens of 64 dims, a V box 16 tokens of all dims) into two
+//    128-token buffers each, and each unit's queries (a box per row tile and 64
+//    dims: RQ rows of G heads); one
 //    thread issues the matrix products; each row tile has four softmax warps,
 //    one thread per row, with its logits S (128 columns, overwritten by the
 //    bf16 probabilities P) and its output O (D columns) in tensor memory: 2 x
@@ -49,12 +50,21 @@ namespace {
 constexpr int kPreCap = 128;     // entries of the work prefix in shared memory
 constexpr int kTileTok = 128;    // tokens per tile
 constexpr int kTileBlk = kTileTok / kBlockSize;
-constexpr int kStages = 4;       // K / V tiles in the ring
+constexpr int kStages = 2;       // K tiles, and V tiles, in flight
 constexpr int kInfo = 8;         // tile descriptions in flight
-constexpr int kWarpsRT = 12;     // 2 x 4 softmax, producer, products, two that only make up a warpgroup
+constexpr int kWarpsRT = 12;     // 2 x 4 softmax, K producer, products, V producer, one that fills the warpgroup
 constexpr float kGrow = 8.f;     // log2 growth of a maximum that rescales O
 
-// 3-D tiled TMA load into shared memory, completion counted on `bar`.
+// 3-D and 5-D tiled TMA loads into shared memory, completion counted on `bar`.
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2,
+                                            int c3, int c4, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "l"(policy)
+        : "memory");
+}
+
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2,
                                             uint64_t policy) {
     asm volatile(
@@ -77,7 +87,7 @@ struct RowCfg {
     static constexpr int TILE = HV * HALF;                 // a K, V or Q tile
     static constexpr int BLK = kBlockSize * 128;           // a block's 64 dims
     static constexpr size_t off_ring = 2 * size_t(TILE);   // after the two Q tiles
-    static constexpr size_t off_stage = off_ring + size_t(kStages) * TILE;  // 32 rows of 128 bytes per softmax warp
+    static constexpr size_t off_stage = off_ring + 2 * size_t(kStages) * TILE;  // 32 rows of 128 bytes per softmax warp
     static constexpr size_t off_bars = off_stage + 8 * 4096;
     static constexpr size_t off_info = off_bars + 192;
     static constexpr size_t off_misc = off_info + kInfo * 4;
@@ -164,8 +174,9 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
     const Work<PREFIX> work(a);
     const int RQ = work.RQ;
     const uint32_t ring = base + uint32_t(C::off_ring);
-    const uint32_t kv_full = base + uint32_t(C::off_bars), kv_empty = kv_full + kStages * 8;
-    const uint32_t q_full = kv_empty + kStages * 8, q_empty = q_full + 16, s_full = q_empty + 16;
+    const uint32_t k_full = base + uint32_t(C::off_bars), k_empty = k_full + kStages * 8;
+    const uint32_t v_full = k_empty + kStages * 8, v_empty = v_full + kStages * 8;
+    const uint32_t q_full = v_empty + kStages * 8, q_empty = q_full + 16, s_full = q_empty + 16;
     const uint32_t p_ready = s_full + 16, o_full = p_ready + 16, drained = o_full + 16, piece_bar = drained + 8, last_bar = piece_bar + 16;
     volatile int *info = reinterpret_cast<volatile int *>(bp + C::off_info);
     volatile int *misc = reinterpret_cast<volatile int *>(bp + C::off_misc);  // [0] tensor memory, [1] gave up, [4 + w] completes the count
@@ -177,8 +188,10 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
         prefetch_tensormap(&tm_v);
         prefetch_tensormap(&tm_q);
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(kv_full + 8 * i, 1);
-            mbar_init(kv_empty + 8 * i, 1);
+            mbar_init(k_full + 8 * i, 1);
+            mbar_init(k_empty + 8 * i, 1);
+            mbar_init(v_full + 8 * i, 1);
+            mbar_init(v_empty + 8 * i, 1);
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(q_full + 8 * w, 1);
@@ -310,22 +323,23 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
     // registers: the 168 per thread of the launch, 224 + 224 + 56 over its three warpgroups
     if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 8) {
-        // ============================================================ producer
+    if (warp == 8 || warp == 10) {
+        // =========================================== producers: K and queries, V
+        const bool is_k = warp == 8;
         const int32_t *table = PREFIX ? a.pt : a.bt;
         const int mbs = PREFIX ? a.PMBS : a.MBS;
         const uint64_t policy = l2_policy_normal();  // other units of the KV head read the same blocks
-        uint32_t fill = 0, tile_no = 0;  // ring buffers and tiles so far
-        uint32_t nq[2] = {0, 0};         // query tiles so far
+        const uint32_t buf = ring + (is_k ? 0 : kStages * C::TILE);
+        const uint32_t full = is_k ? k_full : v_full, empty = is_k ? k_empty : v_empty;
+        uint32_t tile_no = 0;     // tiles so far
+        uint32_t nq[2] = {0, 0};  // query tiles so far
         bool ok = true;
         for (int64_t p = pos0; ok && p < pos1;) {
             const int t0 = int(p - s0), t1 = int(min(pos1 - s0, int64_t(x.n)));
-            // physical blocks of 32 list entries (4 tiles), one per lane
+            // table entries of 32 list entries (4 tiles), one per lane, one window ahead
             auto entry = [&](int e) -> int {
                 if (e >= x.nb) return -1;
-                const int j = e < x.nb1 ? e : e - x.nb1 + x.jw;
-                const int ph = __ldg(table + int64_t(x.s) * mbs + j);
-                return ph >= 0 && int64_t(ph) < a.NB ? ph : -1;
+                return __ldg(table + int64_t(x.s) * mbs + (e < x.nb1 ? e : e - x.nb1 + x.jw));
             };
             int cur = entry(t0 * kTileBlk + lane), nxt = entry(t0 * kTileBlk + 32 + lane), at = t0;
             for (int t = t0; t < t1; ++t, ++tile_no) {
@@ -334,60 +348,65 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                     cur = nxt;
                     nxt = entry(t * kTileBlk + 32 + lane);
                 }
-                const int i = lane / HV, hf = lane % HV;  // this lane's block and half
-                const int ph = __shfl_sync(0xffffffffu, cur, (t - at) * kTileBlk + (i & 7));
-                const unsigned live = __ballot_sync(0xffffffffu, lane < 8 * HV && hf == 0 && ph >= 0);
-                unsigned blocks = 0;  // bit i: block i of the tile is there
+                const uint32_t st = tile_no % kStages;
+                // bit i: block i of the tile is in the pool
+                const unsigned blocks = (__ballot_sync(0xffffffffu, cur >= 0 && int64_t(cur) < a.NB) >>
+                                         ((t - at) * kTileBlk)) & 0xffu;
+                if (tile_no >= kStages) ok = wait(empty + 8 * st, tile_no / kStages + 1);
+                if (!ok || int(tile_no) >= a.stop_item) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    const uint32_t bytes = uint32_t(__popc(blocks)) * C::BLK * HV;
+                    if (is_k) info[tile_no % kInfo] = int(blocks);
+                    if (bytes) mbar_arrive_expect_tx(full + 8 * st, bytes);
+                    else mbar_arrive(full + 8 * st);
+                }
+                __syncwarp();
+                for (int i = 0; i < kTileBlk; ++i) {
+                    const int ph = __shfl_sync(0xffffffffu, cur, (t - at) * kTileBlk + i);
+                    if (!((blocks >> i) & 1u) || !tc_elect()) continue;
+                    if (is_k) {
 #pragma unroll
-                for (int b = 0; b < 8; ++b) blocks |= ((live >> (b * HV)) & 1u) << b;
-                const uint32_t bytes = uint32_t(__popc(blocks)) * C::BLK * HV;
-                for (int kv = 0; ok && kv < 2; ++kv, ++fill) {
-                    const uint32_t st = fill % kStages;
-                    if (fill >= kStages) ok = wait(kv_empty + 8 * st, fill / kStages + 1);
-                    if (!ok || int(fill) >= a.stop_item) {
-                        ok = ok && int(fill) < a.stop_item;
-                        break;
-                    }
-                    if (lane == 0) {
-                        if (kv == 0) info[tile_no % kInfo] = int(blocks);
-                        if (bytes) mbar_arrive_expect_tx(kv_full + 8 * st, bytes);
-                        else mbar_arrive(kv_full + 8 * st);
-                    }
-                    __syncwarp();
-                    if (lane < 8 * HV && ph >= 0)
-                        tma_load_4d(ring + st * C::TILE + hf * C::HALF + i * C::BLK, kv ? &tm_v : &tm_k,
-                                    kv_full + 8 * st, hf * 64, x.kvh, 0, ph, policy);
-                    if (kv == 0 && t == t0) {
-                        // the unit's queries: rows (query row, head) are consecutive; rows past the
-                        // unit's are read too and dropped at the end
-                        for (int w = 0; ok && w < (x.nr > RQ ? 2 : 1); ++w) {
-                            if (nq[w] > 0) ok = wait(q_empty + 8 * w, nq[w] + 1);
-                            if (!ok) break;
-                            ++nq[w];
-                            if (lane == 0) {
-                                mbar_arrive_expect_tx(q_full + 8 * w, uint32_t(RQ * G * D * 2));
-                                for (int f = 0; f < HV; ++f)
-                                    tma_load_3d(base + w * C::TILE + f * C::HALF, &tm_q, q_full + 8 * w, f * 64,
-                                                x.kvh * G, x.r0 + w * RQ, policy);
-                            }
-                            __syncwarp();
-                        }
+                        for (int hf = 0; hf < HV; ++hf)
+                            tma_load_4d(buf + st * C::TILE + hf * C::HALF + i * C::BLK, &tm_k, full + 8 * st, hf * 64,
+                                        x.kvh, 0, ph, policy);
+                    } else {
+                        tma_load_5d(buf + st * C::TILE + i * C::BLK * HV, &tm_v, full + 8 * st, 0, 0, 0, x.kvh, ph,
+                                    policy);
                     }
                 }
-                if (!ok) break;
+                __syncwarp();
+                if (is_k && t == t0) {
+                    // the unit's queries: rows (query row, head) are consecutive; rows past the
+                    // unit's are read too and dropped at the end
+                    for (int w = 0; ok && w < (x.nr > RQ ? 2 : 1); ++w) {
+                        if (nq[w] > 0) ok = wait(q_empty + 8 * w, nq[w] + 1);
+                        if (!ok) break;
+                        ++nq[w];
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(q_full + 8 * w, uint32_t(RQ * G * D * 2));
+                            for (int f = 0; f < HV; ++f)
+                                tma_load_3d(base + w * C::TILE + f * C::HALF, &tm_q, q_full + 8 * w, f * 64,
+                                            x.kvh * G, x.r0 + w * RQ, policy);
+                        }
+                        __syncwarp();
+                    }
+                }
             }
             p = s0 + t1;
-            if (p < pos1) next_unit();
+            if (ok && p < pos1) next_unit();
         }
         // no copy may land after the CTA is gone
-        for (uint32_t f = fill > kStages ? fill - kStages : 0; f < fill; ++f)
-            mbar_wait_bounded(kv_full + 8 * (f % kStages), (f / kStages) & 1u, a.wait_ns);
+        for (uint32_t f = tile_no > kStages ? tile_no - kStages : 0; f < tile_no; ++f)
+            mbar_wait_bounded(full + 8 * (f % kStages), (f / kStages) & 1u, a.wait_ns);
         for (int w = 0; w < 2; ++w)
             if (nq[w] > 0) mbar_wait_bounded(q_full + 8 * w, (nq[w] - 1) & 1u, a.wait_ns);
     } else if (warp == 9) {
         // ====================================================== matrix products
         constexpr uint32_t id_s = tc_idesc(128, 128, false), id_o = tc_idesc(128, D, true);
-        uint32_t use = 0, tile_no = 0;          // ring buffers and tiles so far
+        uint32_t tile_no = 0;                   // tiles so far
         uint32_t nq[2] = {0, 0}, np_[2] = {0, 0};  // phases of q_full and p_ready
         bool ok = true;
         // the same value in every lane, known as such: the products take uniform operands
@@ -406,35 +425,37 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
         };
         // O_w (+)= P_w V from ring buffer st
         auto pv = [&](int w, uint32_t st, bool first) {
-            const uint32_t v = uniform(tc_desc_lo(ring + st * C::TILE, C::HALF)), t = uniform(tmem + 256 * w);
+            // block-major: 16 tokens of 64 dims, then the next 64
+            const uint32_t v = uniform(tc_desc_lo(ring + (kStages + st) * C::TILE, C::BLK));
+            const uint32_t t = uniform(tmem + 256 * w);
             const bool more = uniform(!first);
             if (tc_elect()) {
 #pragma unroll
                 for (int kk = 0; kk < kTileTok / 16; ++kk)
-                    tc_mma_ts(t + 128, t + 8 * kk, v + (kk * 2048 >> 4), kTcDescHi, id_o, more || kk > 0);
+                    tc_mma_ts(t + 128, t + 8 * kk, v + (kk * C::BLK * HV >> 4), kTcDescHi, id_o, more || kk > 0);
             }
         };
         for (int64_t p = pos0; ok && p < pos1;) {
             const int t0 = int(p - s0), t1 = int(min(pos1 - s0, int64_t(x.n)));
             const int nact = x.nr > RQ ? 2 : 1;
             for (int t = t0; ok && t <= t1; ++t) {
-                const uint32_t ks = use % kStages, vs = (use - 1) % kStages;  // K of tile t, V of tile t - 1
-                if (t < t1 && !(ok = wait(kv_full + 8 * ks, use / kStages))) break;
+                const uint32_t ks = tile_no % kStages, vs = (tile_no - 1) % kStages;  // K of tile t, V of tile t - 1
+                if (t < t1 && !(ok = wait(k_full + 8 * ks, tile_no / kStages))) break;
                 if (t > t0) {
-                    if (!(ok = wait(kv_full + 8 * vs, (use - 1) / kStages))) break;
+                    if (!(ok = wait(v_full + 8 * vs, (tile_no - 1) / kStages))) break;
                     // V rows nobody sees: blocks that are not there, and what lies past the last row's limit
                     const int blocks = info[(tile_no - 1) % kInfo];
                     const int e_last = x.nb - 1, tail = x.lim1 % BS;
                     const int lb = e_last - (t - 1) * kTileBlk;  // the unit's last block, if in this tile
                     const bool cut = tail && lb >= 0 && lb < kTileBlk;
                     if (blocks != 0xff || cut) {
-                        uint8_t *v = bp + C::off_ring + vs * C::TILE;
+                        uint8_t *v = bp + C::off_ring + (kStages + vs) * C::TILE;
                         for (int i = 0; i < kTileBlk; ++i) {
                             const int from = !((blocks >> i) & 1) ? 0 : cut && i == lb ? tail : BS;  // first row to zero
                             for (int idx = from * 8 + lane; idx < BS * 8; idx += 32)
 #pragma unroll
                                 for (int hf = 0; hf < HV; ++hf)
-                                    *reinterpret_cast<uint4 *>(v + hf * C::HALF + i * C::BLK + idx * 16) =
+                                    *reinterpret_cast<uint4 *>(v + (i * HV + hf) * C::BLK + idx * 16) =
                                         make_uint4(0u, 0u, 0u, 0u);
                         }
                         fence_proxy_async();
@@ -448,7 +469,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                     tc_fence_after();
                     if (t > t0) {
                         pv(w, vs, t == t0 + 1);
-                        if (w == nact - 1 && tc_elect()) tc_commit(kv_empty + 8 * vs);
+                        if (w == nact - 1 && tc_elect()) tc_commit(v_empty + 8 * vs);
                     }
                     if (t < t1) qk(w, ks);
                     if (tc_elect()) {
@@ -458,12 +479,9 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                     __syncwarp();
                 }
                 if (!ok) break;
-                if (t < t1 && tc_elect()) tc_commit(kv_empty + 8 * ks);
+                if (t < t1 && tc_elect()) tc_commit(k_empty + 8 * ks);
                 __syncwarp();
-                if (t < t1) {
-                    use += 2;  // this K, and the V that follows it
-                    ++tile_no;
-                }
+                if (t < t1) ++tile_no;
             }
             p = s0 + t1;
             if (p < pos1) next_unit();
@@ -614,7 +632,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                 auto finite = [](float v) { return fabsf(v) <= 3.4028234e38f; };
                 if (!PREFIX && whole) {
                     bool mine = true;
-#pragma unroll
+#pragma unroll 1  // this runs once per unit: code that has to be fetched first costs more than the loop
                     for (int c = 0; c < HV; ++c) {
                         uint4 v[8];
 #pragma unroll
@@ -639,7 +657,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                     }
                     bad = __ballot_sync(0xffffffffu, act && !mine);
                 } else {
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t o[32];
                         uint4 v[8];
@@ -693,7 +711,8 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                                     Ls += fast_exp2(__ldcg(piece_of(k) + 128 * D + row) - Mr) *
                                           __ldcg(piece_of(k) + 128 * (D + 1) + row);
                             const float iv = Ls == 0.f ? 0.f : 1.f / Ls;
-                            constexpr int V = D / 32, RB = 16;  // values per lane and row, rows at once
+                            constexpr int V = D / 32, RB = 8;  // values per lane and row, rows at once
+#pragma unroll 1
                             for (int rb = 0; rb < 32; rb += RB) {
                                 if (!((acts >> rb) & ((1u << RB) - 1u))) continue;
                                 float v[RB][V];
