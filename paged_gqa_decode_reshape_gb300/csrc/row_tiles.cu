@@ -89,7 +89,7 @@ struct RowCfg {
     static constexpr size_t off_ring = 2 * size_t(TILE);   // after the two Q tiles
     static constexpr size_t off_stage = off_ring + 2 * size_t(kStages) * TILE;  // 32 rows of 128 bytes per softmax warp
     static constexpr size_t off_bars = off_stage + 8 * 4096;
-    static constexpr size_t off_info = off_bars + 192;
+    static constexpr size_t off_info = off_bars + 208;
     static constexpr size_t off_misc = off_info + kInfo * 4;
     static constexpr size_t off_pre = off_misc + 32;
     static constexpr size_t SMEM = 1024 + off_pre + (kPreCap + 1) * 8;
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
     const uint32_t k_full = base + uint32_t(C::off_bars), k_empty = k_full + kStages * 8;
     const uint32_t v_full = k_empty + kStages * 8, v_empty = v_full + kStages * 8;
     const uint32_t q_full = v_empty + kStages * 8, q_empty = q_full + 16, s_full = q_empty + 16;
-    const uint32_t p_ready = s_full + 16, o_full = p_ready + 16, drained = o_full + 16, piece_bar = drained + 8, last_bar = piece_bar + 16;
+    const uint32_t p_ready = s_full + 16, o_full = p_ready + 32, drained = o_full + 16, piece_bar = drained + 8, last_bar = piece_bar + 16;
     volatile int *info = reinterpret_cast<volatile int *>(bp + C::off_info);
     volatile int *misc = reinterpret_cast<volatile int *>(bp + C::off_misc);  // [0] tensor memory, [1] gave up, [4 + w] completes the count
     int64_t *pre = reinterpret_cast<int64_t *>(bp + C::off_pre);
@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
             mbar_init(q_full + 8 * w, 1);
             mbar_init(q_empty + 8 * w, 1);
             mbar_init(s_full + 8 * w, 1);
-            mbar_init(p_ready + 8 * w, 128);
+            mbar_init(p_ready + 16 * w, 128);
+            mbar_init(p_ready + 16 * w + 8, 128);
             mbar_init(o_full + 8 * w, 1);
             mbar_init(piece_bar + 8 * w, 4);
             mbar_init(last_bar + 8 * w, 1);
@@ -423,16 +424,18 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                 }
             }
         };
-        // O_w (+)= P_w V from ring buffer st
-        auto pv = [&](int w, uint32_t st, bool first) {
+        // O_w (+)= P_w V from ring buffer st, half hf of the tokens
+        auto pv = [&](int w, uint32_t st, bool first, int hf) {
             // block-major: 16 tokens of 64 dims, then the next 64
             const uint32_t v = uniform(tc_desc_lo(ring + (kStages + st) * C::TILE, C::BLK));
             const uint32_t t = uniform(tmem + 256 * w);
             const bool more = uniform(!first);
             if (tc_elect()) {
 #pragma unroll
-                for (int kk = 0; kk < kTileTok / 16; ++kk)
+                for (int k = 0; k < kTileTok / 32; ++k) {
+                    const int kk = hf * (kTileTok / 32) + k;
                     tc_mma_ts(t + 128, t + 8 * kk, v + (kk * C::BLK * HV >> 4), kTcDescHi, id_o, more || kk > 0);
+                }
             }
         };
         for (int64_t p = pos0; ok && p < pos1;) {
@@ -464,11 +467,14 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                 }
                 for (int w = 0; w < nact; ++w) {
                     if (t == t0) ok = wait(q_full + 8 * w, nq[w]++);
-                    else ok = wait(p_ready + 8 * w, np_[w]++);
+                    else ok = wait(p_ready + 16 * w, np_[w]);
                     if (!ok) break;
                     tc_fence_after();
                     if (t > t0) {
-                        pv(w, vs, t == t0 + 1);
+                        pv(w, vs, t == t0 + 1, 0);
+                        if (!(ok = wait(p_ready + 16 * w + 8, np_[w]++))) break;
+                        tc_fence_after();
+                        pv(w, vs, t == t0 + 1, 1);
                         if (w == nact - 1 && tc_elect()) tc_commit(v_empty + 8 * vs);
                     }
                     if (t < t1) qk(w, ks);
@@ -532,74 +538,80 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                                         (ta + kTileTok <= S1 || (ta >= lo && ta + kTileTok <= lim));
                     const bool masked = !__all_sync(0xffffffffu, inside || !act);
                     float s[kTileTok];
+                    auto load = [&](int c) { tmem_ld32(ts + 32 * c, reinterpret_cast<uint32_t(&)[32]>(s[32 * c])); };
+                    auto mask = [&](int b) {  // unseen tokens of block b
+                        const int tb = tok(e0 + b);
+                        auto bits = [&](int from, int to) -> uint32_t {
+                            const int y0 = min(max(from - tb, 0), 16), y1 = min(max(to - tb, 0), 16);
+                            return y1 > y0 ? ((1u << y1) - 1u) & ~((1u << y0) - 1u) : 0u;
+                        };
+                        const uint32_t mk = (blocks >> b) & 1 ? bits(0, S1) | bits(lo, lim) : 0u;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, reinterpret_cast<uint32_t(&)[32]>(s[32 * c]));
+                        for (int c = 0; c < 16; ++c)
+                            if (!((mk >> c) & 1u)) s[16 * b + c] = -INFINITY;
+                    };
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    // the maximum of one half while the other is on its way
+                    load(0);
+                    load(1);
                     tc_wait_ld();
-                    if (masked) {
+                    load(2);
+                    load(3);
 #pragma unroll
-                        for (int b = 0; b < kTileBlk; ++b) {
-                            const int tb = tok(e0 + b);
-                            auto bits = [&](int from, int to) -> uint32_t {
-                                const int y0 = min(max(from - tb, 0), 16), y1 = min(max(to - tb, 0), 16);
-                                return y1 > y0 ? ((1u << y1) - 1u) & ~((1u << y0) - 1u) : 0u;
-                            };
-                            const uint32_t mk = (blocks >> b) & 1 ? bits(0, S1) | bits(lo, lim) : 0u;
+                    for (int hf = 0; hf < 2; ++hf) {
+                        if (hf == 1) tc_wait_ld();
+                        if (masked) {
 #pragma unroll
-                            for (int c = 0; c < 16; ++c)
-                                if (!((mk >> c) & 1u)) s[16 * b + c] = -INFINITY;
+                            for (int b = 0; b < kTileBlk / 2; ++b) mask(hf * (kTileBlk / 2) + b);
                         }
-                    }
-                    float mx = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
 #pragma unroll
-                    for (int c = 4; c < kTileTok; c += 4) {
-                        mx = fmaxf(mx, s[c]);
-                        mx1 = fmaxf(mx1, s[c + 1]);
-                        mx2 = fmaxf(mx2, s[c + 2]);
-                        mx3 = fmaxf(mx3, s[c + 3]);
+                        for (int c = 64 * hf; c < 64 * hf + 64; c += 8)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[c + 2 * e], s[c + 2 * e + 1]);
                     }
-                    mx = fmaxf(fmaxf(mx, mx1), fmaxf(mx2, mx3)) * a.scale_log2;
-                    const bool grow = mx > m + kGrow || (m == -INFINITY && mx > m);
+                    const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale_log2;
+                    const bool grow = mt > m + kGrow || (m == -INFINITY && mt > m);
                     if (__any_sync(0xffffffffu, grow)) {
-                        const float f = grow ? (m == -INFINITY ? 0.f : fast_exp2(m - mx)) : 1.f;
-                        if (grow) m = mx;
+                        const float f = grow ? (m == -INFINITY ? 0.f : fast_exp2(m - mt)) : 1.f;
+                        if (grow) m = mt;
                         l *= f;
                         if (t > t0) {  // P V of the tile before is complete: S of this one was issued after it
-#pragma unroll
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t o[32];
-                                tmem_ld32(to + 32 * c, o);
+#pragma unroll 1
+                            for (int c = 0; c < D / 16; ++c) {
+                                uint32_t o[16];
+                                tmem_ld16(to + 16 * c, o);
                                 tc_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tmem_st32(to + 32 * c, o);
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st16(to + 16 * c, o);
                             }
                         }
                     }
                     const float mr = m == -INFINITY ? 0.f : m;
-                    float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+                    const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), mr2 = make_float2(-mr, -mr);
+                    float2 la = make_float2(0.f, 0.f), lb = la;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
+                    for (int hf = 0; hf < 2; ++hf) {
                         uint32_t pk[32];
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            const int k = 64 * c + 2 * e;
-                            const float p0 = fast_exp2(fmaf(s[k], a.scale_log2, -mr));
-                            const float p1 = fast_exp2(fmaf(s[k + 1], a.scale_log2, -mr));
-                            const float p2 = fast_exp2(fmaf(s[k + 2], a.scale_log2, -mr));
-                            const float p3 = fast_exp2(fmaf(s[k + 3], a.scale_log2, -mr));
-                            l0 += p0;
-                            l1 += p1;
-                            l2 += p2;
-                            l3 += p3;
-                            pk[e] = pack_bf16x2(p0, p1);
-                            pk[e + 1] = pack_bf16x2(p2, p3);
+                            const int k = 64 * hf + 2 * e;
+                            const float2 za = fma2(make_float2(s[k], s[k + 1]), sc2, mr2);
+                            const float2 zb = fma2(make_float2(s[k + 2], s[k + 3]), sc2, mr2);
+                            const float2 pa = make_float2(fast_exp2(za.x), fast_exp2(za.y));
+                            const float2 pb = make_float2(fast_exp2(zb.x), fast_exp2(zb.y));
+                            la = add2(la, pa);
+                            lb = add2(lb, pb);
+                            pk[e] = pack_bf16x2(pa.x, pa.y);
+                            pk[e + 1] = pack_bf16x2(pb.x, pb.y);
                         }
-                        tmem_st32(ts + 32 * c, pk);
+                        // P V begins with the first half's tokens
+                        tmem_st32(ts + 32 * hf, pk);
+                        tc_wait_st();
+                        tc_fence_before();
+                        mbar_arrive(p_ready + 16 * w + 8 * hf);
                     }
-                    l += (l0 + l1) + (l2 + l3);
-                    tc_wait_st();
-                    tc_fence_before();
-                    mbar_arrive(p_ready + 8 * w);
+                    l += (la.x + la.y) + (lb.x + lb.y);
                 }
                 // ---- the end of the unit, or of this CTA's piece of it
                 if (ok) ok = wait(o_full + 8 * w, units++);
