@@ -90,7 +90,7 @@ struct RowCfg {
     static constexpr size_t off_stage = off_ring + 2 * size_t(kStages) * TILE;  // 32 rows of 128 bytes per softmax warp
     static constexpr size_t off_bars = off_stage + 8 * 4096;
     static constexpr size_t off_info = off_bars + 208;
-    static constexpr size_t off_misc = off_info + kInfo * 4;
+    static constexpr size_t off_misc = off_info + 2 * kInfo * 4;
     static constexpr size_t off_pre = off_misc + 32;
     static constexpr size_t SMEM = 1024 + off_pre + (kPreCap + 1) * 8;
     static constexpr int SLOT = 2 * 128 * (D + 2);         // floats of a piece: per row tile O[128][D], m[128], l[128]
@@ -174,11 +174,11 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
     const Work<PREFIX> work(a);
     const int RQ = work.RQ;
     const uint32_t ring = base + uint32_t(C::off_ring);
-    const uint32_t k_full = base + uint32_t(C::off_bars), k_empty = k_full + kStages * 8;
-    const uint32_t v_full = k_empty + kStages * 8, v_empty = v_full + kStages * 8;
-    const uint32_t q_full = v_empty + kStages * 8, q_empty = q_full + 16, s_full = q_empty + 16;
+    const uint32_t full = base + uint32_t(C::off_bars), empty = full + kStages * 8;
+    const uint32_t q_full = empty + kStages * 8, q_empty = q_full + 16, s_full = q_empty + 16;
     const uint32_t p_ready = s_full + 16, o_full = p_ready + 32, drained = o_full + 16, piece_bar = drained + 8, last_bar = piece_bar + 16;
     volatile int *info = reinterpret_cast<volatile int *>(bp + C::off_info);
+    volatile int *vfix = info + kInfo;  // V rows to zero: see the producers
     volatile int *misc = reinterpret_cast<volatile int *>(bp + C::off_misc);  // [0] tensor memory, [1] gave up, [4 + w] completes the count
     int64_t *pre = reinterpret_cast<int64_t *>(bp + C::off_pre);
 
@@ -188,10 +188,8 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
         prefetch_tensormap(&tm_v);
         prefetch_tensormap(&tm_q);
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(k_full + 8 * i, 1);
-            mbar_init(k_empty + 8 * i, 1);
-            mbar_init(v_full + 8 * i, 1);
-            mbar_init(v_empty + 8 * i, 1);
+            mbar_init(full + 8 * i, 2);  // K's producer and V's
+            mbar_init(empty + 8 * i, 1);
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(q_full + 8 * w, 1);
@@ -326,15 +324,22 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 8 || warp == 10) {
         // =========================================== producers: K and queries, V
+        // step i of the CTA reads K of its tile i and V of its tile i - 1, in buffer pair i % 2
         const bool is_k = warp == 8;
         const int32_t *table = PREFIX ? a.pt : a.bt;
         const int mbs = PREFIX ? a.PMBS : a.MBS;
         const uint64_t policy = l2_policy_normal();  // other units of the KV head read the same blocks
         const uint32_t buf = ring + (is_k ? 0 : kStages * C::TILE);
-        const uint32_t full = is_k ? k_full : v_full, empty = is_k ? k_empty : v_empty;
-        uint32_t tile_no = 0;     // tiles so far
+        uint32_t i = 0;           // the next step
         uint32_t nq[2] = {0, 0};  // query tiles so far
         bool ok = true;
+        auto next_step = [&]() -> bool {  // step i's buffers are free
+            return (i < kStages || wait(empty + 8 * (i % kStages), i / kStages + 1)) && int(i) < a.stop_item;
+        };
+        if (!is_k) {  // no V in the first step
+            if (lane == 0) mbar_arrive(full);
+            i = 1;
+        }
         for (int64_t p = pos0; ok && p < pos1;) {
             const int t0 = int(p - s0), t1 = int(min(pos1 - s0, int64_t(x.n)));
             // table entries of 32 list entries (4 tiles), one per lane, one window ahead
@@ -343,39 +348,41 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                 return __ldg(table + int64_t(x.s) * mbs + (e < x.nb1 ? e : e - x.nb1 + x.jw));
             };
             int cur = entry(t0 * kTileBlk + lane), nxt = entry(t0 * kTileBlk + 32 + lane), at = t0;
-            for (int t = t0; t < t1; ++t, ++tile_no) {
+            for (int t = t0; t < t1; ++t, ++i) {
                 if (t == at + 4) {
                     at = t;
                     cur = nxt;
                     nxt = entry(t * kTileBlk + 32 + lane);
                 }
-                const uint32_t st = tile_no % kStages;
-                // bit i: block i of the tile is in the pool
+                // bit b: block b of the tile is in the pool
                 const unsigned blocks = (__ballot_sync(0xffffffffu, cur >= 0 && int64_t(cur) < a.NB) >>
                                          ((t - at) * kTileBlk)) & 0xffu;
-                if (tile_no >= kStages) ok = wait(empty + 8 * st, tile_no / kStages + 1);
-                if (!ok || int(tile_no) >= a.stop_item) {
-                    ok = false;
-                    break;
-                }
+                if (!(ok = next_step())) break;
+                const uint32_t st = i % kStages, bar = full + 8 * st;
                 if (lane == 0) {
+                    if (is_k) {
+                        info[i % kInfo] = int(blocks);
+                    } else {
+                        // V rows nobody sees: absent blocks, and what lies past the last row's limit
+                        const int tail = x.lim1 % BS, lb = x.nb - 1 - t * kTileBlk;  // lb: the unit's last block
+                        const bool cut = tail && lb >= 0 && lb < kTileBlk;
+                        vfix[i % kInfo] = blocks == 0xffu && !cut ? 0 : int(blocks | 0x100u | (cut ? (lb << 12 | tail << 16) : 0));
+                    }
                     const uint32_t bytes = uint32_t(__popc(blocks)) * C::BLK * HV;
-                    if (is_k) info[tile_no % kInfo] = int(blocks);
-                    if (bytes) mbar_arrive_expect_tx(full + 8 * st, bytes);
-                    else mbar_arrive(full + 8 * st);
+                    if (bytes) mbar_arrive_expect_tx(bar, bytes);
+                    else mbar_arrive(bar);
                 }
                 __syncwarp();
-                for (int i = 0; i < kTileBlk; ++i) {
-                    const int ph = __shfl_sync(0xffffffffu, cur, (t - at) * kTileBlk + i);
-                    if (!((blocks >> i) & 1u) || !tc_elect()) continue;
+                for (int b = 0; b < kTileBlk; ++b) {
+                    const int ph = __shfl_sync(0xffffffffu, cur, (t - at) * kTileBlk + b);
+                    if (!((blocks >> b) & 1u) || !tc_elect()) continue;
                     if (is_k) {
 #pragma unroll
                         for (int hf = 0; hf < HV; ++hf)
-                            tma_load_4d(buf + st * C::TILE + hf * C::HALF + i * C::BLK, &tm_k, full + 8 * st, hf * 64,
-                                        x.kvh, 0, ph, policy);
+                            tma_load_4d(buf + st * C::TILE + hf * C::HALF + b * C::BLK, &tm_k, bar, hf * 64, x.kvh, 0, ph,
+                                        policy);
                     } else {
-                        tma_load_5d(buf + st * C::TILE + i * C::BLK * HV, &tm_v, full + 8 * st, 0, 0, 0, x.kvh, ph,
-                                    policy);
+                        tma_load_5d(buf + st * C::TILE + b * C::BLK * HV, &tm_v, bar, 0, 0, 0, x.kvh, ph, policy);
                     }
                 }
                 __syncwarp();
@@ -399,99 +406,102 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
             p = s0 + t1;
             if (ok && p < pos1) next_unit();
         }
-        // no copy may land after the CTA is gone
-        for (uint32_t f = tile_no > kStages ? tile_no - kStages : 0; f < tile_no; ++f)
-            mbar_wait_bounded(full + 8 * (f % kStages), (f / kStages) & 1u, a.wait_ns);
-        for (int w = 0; w < 2; ++w)
-            if (nq[w] > 0) mbar_wait_bounded(q_full + 8 * w, (nq[w] - 1) & 1u, a.wait_ns);
+        if (ok && is_k) {  // no K in the last step
+            if (next_step() && lane == 0) mbar_arrive(full + 8 * (i % kStages));
+        }
     } else if (warp == 9) {
         // ====================================================== matrix products
         constexpr uint32_t id_s = tc_idesc(128, 128, false), id_o = tc_idesc(128, D, true);
-        uint32_t tile_no = 0;                   // tiles so far
-        uint32_t nq[2] = {0, 0}, np_[2] = {0, 0};  // phases of q_full and p_ready
-        bool ok = true;
         // the same value in every lane, known as such: the products take uniform operands
         auto uniform = [](uint32_t v) -> uint32_t { return __shfl_sync(0xffffffffu, v, 0); };
-        // S_w = Q_w K^T from ring buffer st
+        const uint32_t td = uniform(tmem), qd = uniform(tc_desc_lo(base, 16)), kd = uniform(tc_desc_lo(ring, 16));
+        // V block-major: 16 tokens of 64 dims, then the next 64
+        const uint32_t vd = uniform(tc_desc_lo(ring + kStages * C::TILE, C::BLK));
+        // S_w = Q_w K^T
         auto qk = [&](int w, uint32_t st) {
-            const uint32_t q = uniform(tc_desc_lo(base + w * C::TILE, 16));
-            const uint32_t k = uniform(tc_desc_lo(ring + st * C::TILE, 16)), d = uniform(tmem + 256 * w);
+            const uint32_t q = qd + w * (C::TILE >> 4), k = uniform(kd + st * (C::TILE >> 4));
             if (tc_elect()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t o = ((kk / 4) * C::HALF + (kk % 4) * 32) >> 4;
-                    tc_mma_ss(d, q + o, kTcDescHi, k + o, kTcDescHi, id_s, kk > 0);
+                    tc_mma_ss(td + 256 * w, q + o, kTcDescHi, k + o, kTcDescHi, id_s, kk > 0);
                 }
+                tc_commit(s_full + 8 * w);
             }
         };
-        // O_w (+)= P_w V from ring buffer st, half hf of the tokens
-        auto pv = [&](int w, uint32_t st, bool first, int hf) {
-            // block-major: 16 tokens of 64 dims, then the next 64
-            const uint32_t v = uniform(tc_desc_lo(ring + (kStages + st) * C::TILE, C::BLK));
-            const uint32_t t = uniform(tmem + 256 * w);
-            const bool more = uniform(!first);
+        // O_w (+)= P_w V, half hf of the tokens
+        auto pv = [&](int w, uint32_t st, bool more, int hf) {
+            const uint32_t v = uniform(vd + st * (C::TILE >> 4));
+            more = uniform(more);
             if (tc_elect()) {
 #pragma unroll
                 for (int k = 0; k < kTileTok / 32; ++k) {
                     const int kk = hf * (kTileTok / 32) + k;
-                    tc_mma_ts(t + 128, t + 8 * kk, v + (kk * C::BLK * HV >> 4), kTcDescHi, id_o, more || kk > 0);
+                    tc_mma_ts(td + 256 * w + 128, td + 256 * w + 8 * kk, v + (kk * C::BLK * HV >> 4), kTcDescHi, id_o,
+                              more || kk > 0);
                 }
             }
         };
-        for (int64_t p = pos0; ok && p < pos1;) {
-            const int t0 = int(p - s0), t1 = int(min(pos1 - s0, int64_t(x.n)));
-            const int nact = x.nr > RQ ? 2 : 1;
-            for (int t = t0; ok && t <= t1; ++t) {
-                const uint32_t ks = tile_no % kStages, vs = (tile_no - 1) % kStages;  // K of tile t, V of tile t - 1
-                if (t < t1 && !(ok = wait(k_full + 8 * ks, tile_no / kStages))) break;
-                if (t > t0) {
-                    if (!(ok = wait(v_full + 8 * vs, (tile_no - 1) / kStages))) break;
-                    // V rows nobody sees: blocks that are not there, and what lies past the last row's limit
-                    const int blocks = info[(tile_no - 1) % kInfo];
-                    const int e_last = x.nb - 1, tail = x.lim1 % BS;
-                    const int lb = e_last - (t - 1) * kTileBlk;  // the unit's last block, if in this tile
-                    const bool cut = tail && lb >= 0 && lb < kTileBlk;
-                    if (blocks != 0xff || cut) {
-                        uint8_t *v = bp + C::off_ring + (kStages + vs) * C::TILE;
-                        for (int i = 0; i < kTileBlk; ++i) {
-                            const int from = !((blocks >> i) & 1) ? 0 : cut && i == lb ? tail : BS;  // first row to zero
-                            for (int idx = from * 8 + lane; idx < BS * 8; idx += 32)
+        uint32_t i = 0, nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;  // step; phases of q_full and p_ready
+        bool two = false, more = false;  // the tile before: two row tiles; not the first of its piece
+        // one step: P V of the tile before, Q K^T of this one; q0: the first tile of a piece, cur:
+        // there is a tile, cur2: with two row tiles, qlast: the last of its piece
+        auto step = [&](bool q0, bool cur, bool cur2, bool qlast) -> bool {
+            const uint32_t st = i % kStages;
+            if (!wait(full + 8 * st, i / kStages)) return false;
+            if (i > 0) {
+                const int fix = vfix[i % kInfo];
+                if (fix) {
+                    uint8_t *v = bp + C::off_ring + (kStages + st) * C::TILE;
+                    const int lb = (fix >> 12) & 15, tail = fix >> 16;
+                    for (int b = 0; b < kTileBlk; ++b) {
+                        const int from = !((fix >> b) & 1) ? 0 : tail && b == lb ? tail : BS;  // first row to zero
+                        for (int idx = from * 8 + lane; idx < BS * 8; idx += 32)
 #pragma unroll
-                                for (int hf = 0; hf < HV; ++hf)
-                                    *reinterpret_cast<uint4 *>(v + (i * HV + hf) * C::BLK + idx * 16) =
-                                        make_uint4(0u, 0u, 0u, 0u);
-                        }
-                        fence_proxy_async();
-                        __syncwarp();
+                            for (int hf = 0; hf < HV; ++hf)
+                                *reinterpret_cast<uint4 *>(v + (b * HV + hf) * C::BLK + idx * 16) =
+                                    make_uint4(0u, 0u, 0u, 0u);
                     }
-                }
-                for (int w = 0; w < nact; ++w) {
-                    if (t == t0) ok = wait(q_full + 8 * w, nq[w]++);
-                    else ok = wait(p_ready + 16 * w, np_[w]);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (t > t0) {
-                        pv(w, vs, t == t0 + 1, 0);
-                        if (!(ok = wait(p_ready + 16 * w + 8, np_[w]++))) break;
-                        tc_fence_after();
-                        pv(w, vs, t == t0 + 1, 1);
-                        if (w == nact - 1 && tc_elect()) tc_commit(v_empty + 8 * vs);
-                    }
-                    if (t < t1) qk(w, ks);
-                    if (tc_elect()) {
-                        tc_commit((t < t1 ? s_full : o_full) + 8 * w);
-                        if (t == t1 - 1) tc_commit(q_empty + 8 * w);
-                    }
+                    fence_proxy_async();
                     __syncwarp();
                 }
-                if (!ok) break;
-                if (t < t1 && tc_elect()) tc_commit(k_empty + 8 * ks);
-                __syncwarp();
-                if (t < t1) ++tile_no;
+            }
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                if (i > 0 && (w == 0 || two)) {
+                    uint32_t &n = w ? np1 : np0;
+                    if (!wait(p_ready + 16 * w, n)) return false;
+                    tc_fence_after();
+                    pv(w, st, more, 0);
+                    if (!wait(p_ready + 16 * w + 8, n++)) return false;
+                    tc_fence_after();
+                    pv(w, st, true, 1);
+                    if (q0 && tc_elect()) tc_commit(o_full + 8 * w);
+                }
+                if (cur && (w == 0 || cur2)) {
+                    if (q0 && !wait(q_full + 8 * w, w ? nq1++ : nq0++)) return false;
+                    tc_fence_after();
+                    qk(w, st);
+                    if (qlast && tc_elect()) tc_commit(q_empty + 8 * w);
+                }
+            }
+            if (tc_elect()) tc_commit(empty + 8 * st);
+            ++i;
+            return true;
+        };
+        bool ok = true;
+        for (int64_t p = pos0; ok && p < pos1;) {
+            const int t0 = int(p - s0), t1 = int(min(pos1 - s0, int64_t(x.n)));
+            const bool cur2 = x.nr > RQ;
+            for (int t = t0; t < t1; ++t) {
+                if (!(ok = step(t == t0, true, cur2, t == t1 - 1))) break;
+                two = cur2;
+                more = t > t0;
             }
             p = s0 + t1;
-            if (p < pos1) next_unit();
+            if (ok && p < pos1) next_unit();
         }
+        if (ok) ok = step(true, false, false, false);
         if (!ok) {
             // gave up: the products in flight end before the memory they use goes
             if (tc_elect()) tc_commit(drained);
@@ -829,6 +839,14 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
         tc_fence_after();
         tmem_free(tmem, 512);
     }
+    if (misc[1] && warp == 8)
+        // the CTA gave up: nothing it started may land after it is gone. Of a barrier's two parities one is
+        // complete and the other in flight (the products have waited for every copy otherwise)
+        for (int k = 0; k < 2; ++k)
+            for (uint32_t parity = 0; parity < 2; ++parity) {
+                mbar_wait_bounded(full + 8 * k, parity, a.wait_ns);
+                mbar_wait_bounded(q_full + 8 * k, parity, a.wait_ns);
+            }
 }
 
 template <int D, bool PREFIX>
