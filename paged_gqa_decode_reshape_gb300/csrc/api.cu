@@ -932,6 +932,22 @@ int make_query_map(CUtensorMap *map, const void *q, int rows, int Hq, int G, int
     return r == CUDA_SUCCESS ? PA_OK : cuda_fail(cudaErrorInvalidValue);
 }
 
+// SMs for the row-tile kernel over the prefixes; the kernel for the own tokens
+// runs beside it on the rest. Between the two kernels' one-after-the-other and
+// an even split: prefix_8k 47.7 -> 35.6 us, prefix_tenants 43.9 -> 36.1 (91 of
+// 152 SMs: 33.9 and 34.2). The lengths are not known here: by what the tables
+// hold at most, the own tokens at half of it; a step of two row tiles over 128
+// tokens takes about 2.5 us of an SM at head_dim 128, an own block 0.13 us. At
+// least half, as tables may be much longer than what is in them.
+int prefix_ctas(const SubsetArgs &a, int D, int sms) {
+    const int per_unit = 2 * (kRowTile / a.G);
+    const double tiles = double(a.Hkv) * (double(a.rows) / per_unit + a.ngroups) * ((a.PMBS + 7) / 8);
+    const double steps = tiles * 2.5 * D / 128, own = 0.5 * a.rows * double(a.Hkv) * a.MBS * 0.13 * D / 128;
+    const double share = steps / (steps + own);
+    const int n = int(sms * (share < 0.5 ? 0.5 : share > 0.75 ? 0.75 : share));
+    return n < 1 ? 1 : n > sms - 1 ? (sms > 1 ? sms - 1 : 1) : n;
+}
+
 // the launches, after the argument checks
 int run_subset(SubsetArgs a, const SubsetPlan &plan, int D, CacheKind kind, void *workspace, size_t workspace_bytes,
                void *stream) {
@@ -951,7 +967,7 @@ int run_subset(SubsetArgs a, const SubsetPlan &plan, int D, CacheKind kind, void
     a.desc = reinterpret_cast<int4 *>(p + w.desc);
     a.lse = reinterpret_cast<float *>(p + w.lse);
     a.logits = reinterpret_cast<float *>(p + w.logits);
-    a.pgrid = w.sms;
+    if (plan.prefix) a.pgrid = prefix_ctas(a, D, w.sms);
     a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
     a.stop_item = g_stop_item.load(std::memory_order_relaxed);
     const bool fp8 = kind != kCacheBf16;
@@ -967,7 +983,7 @@ int run_subset(SubsetArgs a, const SubsetPlan &plan, int D, CacheKind kind, void
         if ((rc = make_v_map(&tv5, a.vc, a.Hkv, D, a.NB)) != PA_OK) return rc;
         e = launch_row_tiles(tk, tv5, tq, a, D, w.sms, st);
     }
-    if (e == cudaSuccess && plan.stream) e = launch_stream_decode(tk, tv, a, D, kind, w.sms, st);
+    if (e == cudaSuccess && plan.stream) e = launch_stream_decode(tk, tv, a, D, kind, plan.prefix ? w.sms - a.pgrid : w.sms, st);
     if (e == cudaSuccess && plan.prefix) e = launch_prefix_join(a, D, st);
     return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }

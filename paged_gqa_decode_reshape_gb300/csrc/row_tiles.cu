@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
     volatile int *misc = reinterpret_cast<volatile int *>(bp + C::off_misc);  // [0] tensor memory, [1] gave up, [4 + w] completes the count
     int64_t *pre = reinterpret_cast<int64_t *>(bp + C::off_pre);
 
-    pdl_trigger();
+    if (!PREFIX) pdl_trigger();
     if (tid == 0) {
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
@@ -228,7 +228,12 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
         }
     }
     __syncthreads();
-    if (PREFIX) pdl_wait();
+    if (PREFIX) {
+        // the kernel for the own tokens runs beside this one: it may start once
+        // what came before this kernel is complete
+        pdl_wait();
+        pdl_trigger();
+    }
     if constexpr (PREFIX) {  // sequences of no group have no prefix part
         for (int b = blockIdx.x * (kWarpsRT * 32) + tid; b < a.rows; b += gridDim.x * (kWarpsRT * 32)) {
             int lo = 0, hi = a.ngroups;
@@ -866,8 +871,9 @@ cudaError_t launch_row_tiles(const CUtensorMap &tk, const CUtensorMap &tv, const
                              const SubsetArgs &args, int head_dim, int sms, cudaStream_t stream) {
     SubsetArgs a = args;
     a.min_items = 2;
-    if (a.pt) return head_dim == 128 ? launch_t<128, true>(tk, tv, tq, a, sms, stream) : launch_t<64, true>(tk, tv, tq, a, sms, stream);
-    return head_dim == 128 ? launch_t<128, false>(tk, tv, tq, a, sms, stream) : launch_t<64, false>(tk, tv, tq, a, sms, stream);
+    const int grid = a.pt ? a.pgrid : sms;
+    if (a.pt) return head_dim == 128 ? launch_t<128, true>(tk, tv, tq, a, grid, stream) : launch_t<64, true>(tk, tv, tq, a, grid, stream);
+    return head_dim == 128 ? launch_t<128, false>(tk, tv, tq, a, grid, stream) : launch_t<64, false>(tk, tv, tq, a, grid, stream);
 }
 
 }  // namespace pa

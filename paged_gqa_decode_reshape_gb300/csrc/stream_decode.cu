@@ -298,7 +298,9 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
             w.sv = __ldg(a.v_scale + i);
         }
     };
-    pdl_wait();
+    // with a prefix: what came before the row-tile kernel is complete already, and nothing of
+    // that kernel's is read here
+    if (!a.ownres) pdl_wait();
     Win cur = resolve(0), nxt = resolve(32);
     scales(cur);
     scales(nxt);
@@ -741,6 +743,8 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
     // after a wait that gave up: no copy may land in memory of a CTA that is gone
     if (dead && lane == 0)
         for (int st = 0; st < R; ++st) mbar_wait_bounded(bars + st * 8, ((armed >> st) & 1u) ^ 1u, a.wait_ns);
+    // with a prefix: this kernel is complete when the row-tile kernel is, so that the next need wait for one only
+    if (a.ownres && blockIdx.x == 0) pdl_wait();
 }
 
 // ---- accumulated weights: p_t = 2^(z_t - lse) summed over the group, added
