@@ -10,8 +10,8 @@
 // Bound: every visible K/V byte is read once, at about 2 G flops per byte, so
 // HBM bandwidth bounds long calls and latency short ones.
 //
-//  * Work list. A (sequence, KV head) is a segment with one item per 16-token
-//    block that holds a visible token (sink blocks, then window blocks; at
+//  * Work list. A (sequence, KV head) is a segment with one item per two 16-token
+//    blocks that hold a visible token (sink blocks, then window blocks; at
 //    least one item, so that every output row is written).
 //    Up to one segment per SM: every CTA takes one piece of one segment, all
 //    pieces at most L items, L the smallest for which the pieces fit the
@@ -28,13 +28,13 @@
 //    a K/V byte serves the whole group. tcgen05's smallest M of 64 would be
 //    filled, but its results come back through TMEM to warps that would
 //    wait for them; at 2 G flops per byte the tensor pipes are nearly idle.
-//  * Two blocks (32 tokens) per softmax step; a 16-bit mask per block says
-//    which tokens are seen, masked V lanes are zeroed (they may hold NaN).
+//  * An item (32 tokens) is one copy, one wait and one softmax step. A 16-bit
+//    mask per block says which tokens are seen; the V rows of the others (they
+//    may hold NaN) are zeroed in the stage, which only edge blocks need.
 //  * A segment cut between workers leaves (O, m, l) per piece in the workspace,
 //    and the worker that completes its arrival counter merges them, in piece
 //    order: the result does not depend on who is last.
 #include <climits>
-#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -44,14 +44,14 @@ namespace pa {
 namespace {
 
 constexpr int kPreCap = 512;   // entries of the items-per-sequence prefix in shared memory
-constexpr int kEndCost = 4;    // items that the end of a segment costs a warp
-constexpr int kMinPiece = 24;  // items of a CTA's piece at least, where there are as many
+constexpr int kEndCost = 2;    // items that the end of a segment costs a warp
+constexpr int kMinPiece = 12;  // items of a CTA's piece at least, where there are as many
 
 #ifndef PA_STREAM_WARPS_F8
-#define PA_STREAM_WARPS_F8 8
+#define PA_STREAM_WARPS_F8 10
 #endif
 #ifndef PA_STREAM_STAGES_F8
-#define PA_STREAM_STAGES_F8 5
+#define PA_STREAM_STAGES_F8 2
 #endif
 constexpr int kMaxStreamWarps = 12;
 
@@ -62,8 +62,9 @@ struct StreamCfg {
     static constexpr int NW = F8 ? PA_STREAM_WARPS_F8 : 6;  // warps
     static_assert(NW <= kMaxStreamWarps, "pieces and counters of the workspace");
     static constexpr int KT = kBlockSize * D * (F8 ? 1 : 2);  // bytes of a K (or V) tile of one block
-    static constexpr int STAGE = 2 * KT;
-    static constexpr int R = F8 ? PA_STREAM_STAGES_F8 : (D == 128 ? 4 : 8);  // stages per warp
+    static constexpr int BLK = 2 * KT;                    // K and V of a block
+    static constexpr int STAGE = 2 * BLK;                 // an item: two blocks
+    static constexpr int R = F8 ? PA_STREAM_STAGES_F8 : (D == 128 ? 2 : 4);  // stages per warp
     static constexpr int RING = R * STAGE;                // bytes in flight per warp
     static constexpr int NKK = D / 16;
     static constexpr int HALF = kBlockSize * 128;         // bytes of one 64-dim half tile (bf16)
@@ -81,8 +82,8 @@ struct StreamCfg {
 
 // a sequence's visible tokens [0, s1) and [lo, lim), as items
 struct Span {
-    int lim, s1, lo, nb1, jw, n;  // nb1 sink blocks, then blocks jw, jw + 1, ...; n items (at least one)
-    __device__ int block(int e) const { return e < nb1 ? e : e - nb1 + jw; }  // logical block of item e
+    int lim, s1, lo, nb1, jw, nb, n;  // nb1 sink blocks, then blocks jw, jw + 1, ...; nb blocks, n items (at least one)
+    __device__ int block(int e) const { return e < nb1 ? e : e - nb1 + jw; }  // logical block of list entry e
 };
 
 __device__ __forceinline__ Span span_of(const SubsetArgs &a, int b) {
@@ -92,7 +93,8 @@ __device__ __forceinline__ Span span_of(const SubsetArgs &a, int b) {
     s.lo = max(s.s1, a.window >= s.lim ? 0 : s.lim - a.window);
     s.nb1 = (s.s1 + kBlockSize - 1) / kBlockSize;
     s.jw = max(s.lo / kBlockSize, s.nb1);
-    s.n = max(s.nb1 + max((s.lim + kBlockSize - 1) / kBlockSize - s.jw, 0), 1);
+    s.nb = s.nb1 + max((s.lim + kBlockSize - 1) / kBlockSize - s.jw, 0);
+    s.n = max((s.nb + 1) / 2, 1);
     return s;
 }
 
@@ -259,43 +261,47 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
 
     // ---- a window of 32 of this warp's items, one per lane
     struct Win {
-        int phys;       // physical block, or -1: nothing to read
-        uint32_t what;  // token mask, KV head << 16
-        int j;          // logical block (LOGITS)
-        float sk, sv;   // scales of the block (per-block scales)
+        int p0, p1;       // physical blocks, or -1: nothing to read
+        uint32_t mask;    // their token masks
+        int head;         // KV head
+        int j;            // first logical block (LOGITS: the second is the next one)
+        float4 sc;        // K and V scales of the blocks (per-block scales)
     };
     const int kn = last > first ? int((last - first + step_ - 1) / step_) : 0;  // this warp's items
     auto resolve = [&](int k0) -> Win {
-        Win w{-1, 0u, 0, 0.f, 0.f};
+        Win w{-1, -1, 0u, 0, 0, make_float4(0.f, 0.f, 0.f, 0.f)};
         const int k = k0 + lane;
         if (k >= kn) return w;
         const int64_t p = first + int64_t(step_) * k;
         Span s = sp;
-        int q = b, head = kvh, e = int(p);
+        int q = b, e = 2 * int(p);
+        w.head = kvh;
         if (!one) {
             int64_t rem;
             q = locate(p, s, rem);
-            head = int(rem / (s.n + kEndCost));
-            e = int(rem - int64_t(head) * (s.n + kEndCost));
+            w.head = int(rem / (s.n + kEndCost));
+            e = 2 * int(rem - int64_t(w.head) * (s.n + kEndCost));
         }
-        const int j = s.block(e);
-        const uint32_t m = e < s.n ? bits_between(0, s.s1, j * BS) | bits_between(s.lo, s.lim, j * BS) : 0u;
-        w.what = uint32_t(head) << 16;
-        w.j = j;
-        if (m) {
-            const int ph = __ldg(a.bt + int64_t(q) * a.MBS + j);
-            if (ph >= 0 && int64_t(ph) < a.NB) {
-                w.phys = ph;
-                w.what |= m;
-            }
+        const int32_t *row = a.bt + int64_t(q) * a.MBS;
+        const int j0 = s.block(e), j1 = s.block(e + 1);
+        const int ph0 = e < s.nb ? __ldg(row + j0) : -1, ph1 = e + 1 < s.nb ? __ldg(row + j1) : -1;
+        w.j = j0;
+        const uint32_t m0 = bits_between(0, s.s1, j0 * BS) | bits_between(s.lo, s.lim, j0 * BS);
+        const uint32_t m1 = bits_between(0, s.s1, j1 * BS) | bits_between(s.lo, s.lim, j1 * BS);
+        if (ph0 >= 0 && int64_t(ph0) < a.NB) {
+            w.p0 = ph0;
+            w.mask = m0;
+        }
+        if (ph1 >= 0 && int64_t(ph1) < a.NB) {
+            w.p1 = ph1;
+            w.mask |= m1 << 16;
         }
         return w;
     };
     auto scales = [&](Win &w) {
-        if (PSC && w.phys >= 0) {
-            const int64_t i = int64_t(w.phys) * Hkv + (w.what >> 16);
-            w.sk = __ldg(a.k_scale + i);
-            w.sv = __ldg(a.v_scale + i);
+        if constexpr (PSC) {
+            const int64_t i0 = int64_t(max(w.p0, 0)) * Hkv + w.head, i1 = int64_t(max(w.p1, 0)) * Hkv + w.head;
+            w.sc = make_float4(__ldg(a.k_scale + i0), __ldg(a.v_scale + i0), __ldg(a.k_scale + i1), __ldg(a.v_scale + i1));
         }
     };
     // with a prefix: what came before the row-tile kernel is complete already, and nothing of
@@ -312,25 +318,25 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
     // start the copy of item i (i < kn, in cur or nxt) into its stage
     auto issue = [&](int i) {
         const bool c = i < wbase + 32;
-        const int phys = __shfl_sync(0xffffffffu, c ? cur.phys : nxt.phys, i & 31);
-        const uint32_t what = __shfl_sync(0xffffffffu, c ? cur.what : nxt.what, i & 31);
-        if (phys < 0 || dead || i >= a.stop_item) return;
+        const int p0 = __shfl_sync(0xffffffffu, c ? cur.p0 : nxt.p0, i & 31);
+        const int p1 = __shfl_sync(0xffffffffu, c ? cur.p1 : nxt.p1, i & 31);
+        const int head = __shfl_sync(0xffffffffu, c ? cur.head : nxt.head, i & 31);
+        if ((p0 < 0 && p1 < 0) || dead || i >= a.stop_item) return;
         const uint32_t st = uint32_t(i) % R;
         armed ^= 1u << st;
-        const uint32_t fb = bars + st * 8, dst = ring + st * C::STAGE;
-        const int kvh = int(what >> 16);
-        if (lane == 0) mbar_arrive_expect_tx(fb, C::STAGE);
+        const uint32_t fb = bars + st * 8;
+        if (lane == 0) mbar_arrive_expect_tx(fb, (p0 >= 0 ? C::BLK : 0) + (p1 >= 0 ? C::BLK : 0));
         __syncwarp();
-        if constexpr (F8) {
-            if (lane == 0) tma_load_4d(dst, &tm_k, fb, 0, kvh, 0, phys, policy);
-            if (lane == 1)
-                bulk_load_1d(dst + C::KT, static_cast<const uint8_t *>(a.vc) + (int64_t(phys) * Hkv + kvh) * C::KT,
-                             C::KT, fb, policy);
-        } else {
-            constexpr int HV = D / 64;
-            if (lane < 2 * HV)
-                tma_load_4d(dst + (lane / HV) * C::KT + (lane % HV) * C::HALF, lane / HV ? &tm_v : &tm_k, fb,
-                            (lane % HV) * 64, kvh, 0, phys, policy);
+        // one lane per copy: K then V of the first block, K then V of the second
+        constexpr int HV = F8 ? 1 : D / 64, PB = 2 * HV;
+        const int blk = lane / PB, part = lane % PB, phys = blk ? p1 : p0;
+        if (blk < 2 && phys >= 0) {
+            const uint32_t dst = ring + st * C::STAGE + blk * C::BLK + (part / HV) * C::KT + (part % HV) * C::HALF;
+            if (F8 && part == 1)
+                bulk_load_1d(dst, static_cast<const uint8_t *>(a.vc) + (int64_t(phys) * Hkv + head) * C::KT, C::KT, fb,
+                             policy);
+            else
+                tma_load_4d(dst, !F8 && part / HV ? &tm_v : &tm_k, fb, (part % HV) * 64, head, 0, phys, policy);
         }
     };
 
@@ -396,15 +402,33 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[e] = sa[e] + sb[e];
     };
-    // O^T += V^T P^T for a staged block; V lanes of unseen tokens zeroed
-    auto pv_masked = [&](auto masked, uint32_t vb, uint32_t p01, uint32_t p23, uint32_t mask) {
-        constexpr bool MASKED = decltype(masked)::value;
+    // zero the staged V rows of the tokens not in mask
+    auto hide = [&](uint32_t vb, uint32_t mask) {
+        uint8_t *v = bp + (vb - base);
+        if constexpr (F8) {  // a row of 16 tokens per dim: word w holds tokens 2w, 2w + 1, 2w + 8, 2w + 9
+            uint32_t keep[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const uint32_t t = mask >> (2 * w);
+                keep[w] = (t & 1u ? 0xffu : 0u) | (t & 2u ? 0xff00u : 0u) | (t & 0x100u ? 0xff0000u : 0u) |
+                          (t & 0x200u ? 0xff000000u : 0u);
+            }
+            for (int d = lane; d < D; d += 32) {
+                uint4 *r = reinterpret_cast<uint4 *>(v + d * 16);
+                const uint4 x = *r;
+                *r = make_uint4(x.x & keep[0], x.y & keep[1], x.z & keep[2], x.w & keep[3]);
+            }
+        } else {
+            for (int i = lane; i < BS * D / 8; i += 32)
+                if (!((mask >> (i / 8 % BS)) & 1u))
+                    *reinterpret_cast<uint4 *>(v + (i / (8 * BS)) * C::HALF + (i % (8 * BS)) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async();  // the stage is filled again by a copy
+        __syncwarp();
+    };
+    // O^T += V^T P^T for a staged block
+    auto pv = [&](uint32_t vb, uint32_t p01, uint32_t p23) {
         const uint32_t pb0 = movmatrix_trans(p01), pb1 = movmatrix_trans(p23);
-        const uint32_t t = mask >> (2 * q4);
-        const uint32_t mlo = (t & 1u ? 0x0000ffffu : 0u) | (t & 2u ? 0xffff0000u : 0u);
-        const uint32_t mhi = (t & 0x100u ? 0x0000ffffu : 0u) | (t & 0x200u ? 0xffff0000u : 0u);
-        auto lo = [&](uint32_t v) { return MASKED ? v & mlo : v; };
-        auto hi = [&](uint32_t v) { return MASKED ? v & mhi : v; };
         if constexpr (F8) {
 #pragma unroll
             for (int c2 = 0; c2 < NKK / 2; ++c2) {
@@ -414,8 +438,8 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
                 e4m3x4_to_f16x2x2(r1, a1, a3);
                 e4m3x4_to_f16x2x2(r2, b0, b2);
                 e4m3x4_to_f16x2x2(r3, b1, b3);
-                mma_f16(acc[2 * c2], lo(a0), lo(a1), hi(a2), hi(a3), pb0, pb1);
-                mma_f16(acc[2 * c2 + 1], lo(b0), lo(b1), hi(b2), hi(b3), pb0, pb1);
+                mma_f16(acc[2 * c2], a0, a1, a2, a3, pb0, pb1);
+                mma_f16(acc[2 * c2 + 1], b0, b1, b2, b3, pb0, pb1);
             }
         } else {
             const int rv = (lane & 7) + ((lane >> 4) << 3);
@@ -424,17 +448,14 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
                 const int ch = ((mt & 3) << 1) + ((lane >> 3) & 1);
                 uint32_t a0, a1, a2, a3;
                 ldsm_x4_trans(vb + (mt >> 2) * C::HALF + rv * 128 + ((ch ^ (lane & 7)) << 4), a0, a1, a2, a3);
-                mma_bf16(acc[mt], lo(a0), lo(a1), hi(a2), hi(a3), pb0, pb1);
+                mma_bf16(acc[mt], a0, a1, a2, a3, pb0, pb1);
             }
         }
     };
-    auto pv = [&](uint32_t vb, uint32_t p01, uint32_t p23, uint32_t mask) {
-        if (mask == 0xffffu) pv_masked(std::false_type{}, vb, p01, p23, mask);
-        else pv_masked(std::true_type{}, vb, p01, p23, mask);
-    };
-    // one online-softmax step over up to two staged blocks (mask 0: none);
+    // one online-softmax step over the item's two staged blocks (mask 0: none);
     // ca, cb: their K and V scales (per-block scales)
-    auto step = [&](uint32_t s0a, uint32_t ma, float2 ca, uint32_t s1a, uint32_t mb, float2 cb, float *la, float *lb) {
+    auto step = [&](uint32_t s0a, uint32_t ma, float2 ca, uint32_t mb, float2 cb, float *la, float *lb) {
+        const uint32_t s1a = s0a + C::BLK;
         float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
         if (ma) qk(s0a, s0);
         if (mb) qk(s1a, s1);
@@ -514,8 +535,14 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
                 acc[mt][3] *= al1;
             }
         }
-        if (ma) pv(s0a + C::KT, PSC ? scale_f16x2(p01, ra) : p01, PSC ? scale_f16x2(p23, ra) : p23, ma);
-        if (mb) pv(s1a + C::KT, PSC ? scale_f16x2(q01, rb) : q01, PSC ? scale_f16x2(q23, rb) : q23, mb);
+        if (ma) {
+            if (ma != 0xffffu) hide(s0a + C::KT, ma);
+            pv(s0a + C::KT, PSC ? scale_f16x2(p01, ra) : p01, PSC ? scale_f16x2(p23, ra) : p23);
+        }
+        if (mb) {
+            if (mb != 0xffffu) hide(s1a + C::KT, mb);
+            pv(s1a + C::KT, PSC ? scale_f16x2(q01, rb) : q01, PSC ? scale_f16x2(q23, rb) : q23);
+        }
     };
 
     // the finished row: O relative to the maximum M with normaliser Ls, head h, dims d .. d + 3
@@ -556,33 +583,26 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
                 nxt = resolve(wbase + 32);
                 scales(nxt);
             }
-            // items k and k + 1 (both in this segment)
-            const int n2 = k + 1 < k1 ? 2 : 1;
-            const uint32_t wa = __shfl_sync(0xffffffffu, cur.what, k & 31);
-            const bool c2 = k + 1 < wbase + 32;
-            const uint32_t wb = __shfl_sync(0xffffffffu, c2 ? cur.what : nxt.what, (k + 1) & 31);
-            const uint32_t ma = wa & 0xffffu, mb = n2 == 2 ? wb & 0xffffu : 0u;
+            const uint32_t mask = __shfl_sync(0xffffffffu, cur.mask, k & 31);
+            const uint32_t ma = mask & 0xffffu, mb = mask >> 16;
             float2 ca{0.f, 0.f}, cbk{0.f, 0.f};
             if constexpr (PSC) {
-                ca = make_float2(__shfl_sync(0xffffffffu, cur.sk, k & 31), __shfl_sync(0xffffffffu, cur.sv, k & 31));
-                cbk = make_float2(__shfl_sync(0xffffffffu, c2 ? cur.sk : nxt.sk, (k + 1) & 31),
-                                  __shfl_sync(0xffffffffu, c2 ? cur.sv : nxt.sv, (k + 1) & 31));
+                ca = make_float2(__shfl_sync(0xffffffffu, cur.sc.x, k & 31), __shfl_sync(0xffffffffu, cur.sc.y, k & 31));
+                cbk = make_float2(__shfl_sync(0xffffffffu, cur.sc.z, k & 31), __shfl_sync(0xffffffffu, cur.sc.w, k & 31));
             }
             float *la = nullptr, *lb = nullptr;
             if constexpr (LOGITS) {
-                const int ja = __shfl_sync(0xffffffffu, cur.j, k & 31);
-                const int jb = __shfl_sync(0xffffffffu, c2 ? cur.j : nxt.j, (k + 1) & 31);
-                float *row = a.logits + (int64_t(cb) * Hkv + ckvh) * a.MBS * (G * BS);
-                la = row + int64_t(ja) * (G * BS);
-                lb = row + int64_t(jb) * (G * BS);
+                const int j = __shfl_sync(0xffffffffu, cur.j, k & 31);
+                la = a.logits + ((int64_t(cb) * Hkv + ckvh) * a.MBS + j) * (G * BS);
+                lb = la + G * BS;
             }
-            if (ma) wait_item(k);
-            if (mb) wait_item(k + 1);
-            if ((ma || mb) && !dead)
-                step(ring + uint32_t(k % R) * C::STAGE, ma, ca, ring + uint32_t((k + 1) % R) * C::STAGE, mb, cbk, la, lb);
-            __syncwarp();  // every lane has read the stages
-            k += n2;
-            for (; issued < kn && issued < k + R; ++issued) issue(issued);
+            if (mask) {
+                wait_item(k);
+                if (!dead) step(ring + uint32_t(k % R) * C::STAGE, ma, ca, mb, cbk, la, lb);
+                __syncwarp();  // every lane has read the stage
+            }
+            ++k;
+            if (issued < kn && issued < k + R) issue(issued++);
         }
     };
     // this warp's state into its shared-memory slot
