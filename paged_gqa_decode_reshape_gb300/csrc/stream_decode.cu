@@ -741,8 +741,36 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
                     done = __shfl_sync(0xffffffffu, done, 0);
                     __syncwarp();  // every lane's reads of the pieces follow lane 0's acquire
                     if (done) {
-                        for (int idx = lane; idx < tasks; idx += 32)
-                            merge_pieces(slot_of, n, cb, ckvh, idx / (D / 4), 4 * (idx % (D / 4)));
+                        // the whole segment at once: every head's values of two pieces in flight
+                        constexpr int NT = 8 * (D / 4) / 32;  // (head, four dims) per lane
+                        float M[NT], Ls[NT];
+                        float4 O[NT];
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            M[t] = -INFINITY;
+                            Ls[t] = 0.f;
+                            O[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        }
+#pragma unroll 2
+                        for (int i = 0; i < n; ++i) {
+                            const float *ps = slot_of(i);
+                            float m[NT], l[NT];
+                            float4 v[NT];
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) {
+                                const int idx = lane + 32 * t, h = min(idx / (D / 4), G - 1);
+                                m[t] = __ldcg(ps + 8 * D + h);
+                                l[t] = __ldcg(ps + 8 * D + 8 + h);
+                                v[t] = __ldcg(reinterpret_cast<const float4 *>(ps + h * D) + idx % (D / 4));
+                            }
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) fold(M[t], Ls[t], O[t], m[t], l[t], v[t]);
+                        }
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            const int idx = lane + 32 * t;
+                            if (idx < tasks) emit(cb, ckvh, idx / (D / 4), 4 * (idx % (D / 4)), M[t], Ls[t], O[t]);
+                        }
                         if (lane == 0) a.counters[c0] = 0;
                     }
                 }
