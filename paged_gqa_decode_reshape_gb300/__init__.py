@@ -226,6 +226,12 @@ def _check(fn: str, status: int):
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int, device=None):
+    try:  # the usual case first: a call checks up to ten tensors
+        if (t.dtype is dtype and t.ndim == ndim and t.is_contiguous()
+                and (t.is_cuda if device is None else t.get_device() == device.index)):
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:

@@ -901,9 +901,9 @@ size_t subset_workspace_bytes(const SubsetPlan &plan, int64_t rows, int64_t max_
     return subset_workspace(&w, plan, rows, Hq, Hkv, D) == PA_OK ? w.bytes : 0;
 }
 
-// Tensor map over the V cache [NB][BS][Hkv][D] for boxes of a block's tokens
+// Tensor map over a bf16 cache [NB][BS][Hkv][D] for boxes of a block's tokens
 // of one head, 64 dims (128 swizzled bytes) after 64 dims.
-int make_v_map(CUtensorMap *map, const void *cache, int Hkv, int D, int64_t NB) {
+int make_block_map(CUtensorMap *map, const void *cache, int Hkv, int D, int64_t NB) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return cuda_fail(cudaErrorNotSupported);
     const cuuint64_t tok = cuuint64_t(Hkv) * D * 2;
@@ -971,17 +971,21 @@ int run_subset(SubsetArgs a, const SubsetPlan &plan, int D, CacheKind kind, void
     a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
     a.stop_item = g_stop_item.load(std::memory_order_relaxed);
     const bool fp8 = kind != kCacheBf16;
-    CUtensorMap tk, tv;
-    if ((rc = make_cache_map(&tk, a.kc, a.Hkv, D, kBlockSize, a.NB, fp8)) != PA_OK) return rc;
-    if (fp8) std::memset(&tv, 0, sizeof tv);  // an E4M3 V tile is contiguous: plain bulk copies
-    else if (plan.stream && (rc = make_cache_map(&tv, a.vc, a.Hkv, D, kBlockSize, a.NB)) != PA_OK) return rc;
+    // V blocks as whole boxes (an E4M3 V tile is contiguous: plain bulk copies, no map); K blocks too in the
+    // streaming kernel, in 64-dim halves in the row-tile kernel
+    CUtensorMap tv, tk, tk_half;
+    std::memset(&tv, 0, sizeof tv);
+    if (!fp8 && (rc = make_block_map(&tv, a.vc, a.Hkv, D, a.NB)) != PA_OK) return rc;
+    if (plan.stream && (rc = fp8 ? make_cache_map(&tk, a.kc, a.Hkv, D, kBlockSize, a.NB, true)
+                                 : make_block_map(&tk, a.kc, a.Hkv, D, a.NB)) != PA_OK)
+        return rc;
+    if (plan.tiles && (rc = make_cache_map(&tk_half, a.kc, a.Hkv, D, kBlockSize, a.NB)) != PA_OK) return rc;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
     if (plan.tiles) {
-        CUtensorMap tq, tv5;
+        CUtensorMap tq;
         if ((rc = make_query_map(&tq, a.q, a.rows, a.Hq, a.G, D)) != PA_OK) return rc;
-        if ((rc = make_v_map(&tv5, a.vc, a.Hkv, D, a.NB)) != PA_OK) return rc;
-        e = launch_row_tiles(tk, tv5, tq, a, D, w.sms, st);
+        e = launch_row_tiles(tk_half, tv, tq, a, D, w.sms, st);
     }
     if (e == cudaSuccess && plan.stream) e = launch_stream_decode(tk, tv, a, D, kind, plan.prefix ? w.sms - a.pgrid : w.sms, st);
     if (e == cudaSuccess && plan.prefix) e = launch_prefix_join(a, D, st);

@@ -20,9 +20,10 @@
 //    end to end, each with kEndCost empty items after it for what its end
 //    costs, and cut into equal ranges, one per warp; no warp waits for
 //    another, so many short sequences load the SMs as evenly as a few long.
-//  * Each warp is its own producer: its items are copied by TMA (K and V in
-//    64-dim halves, 128-byte swizzle; E4M3: K box and V tile) into its private
-//    ring of R stages, which only this warp fills and empties.
+//  * Each warp is its own producer: its items are copied by TMA (a box per K or V
+//    block, 64 dims after 64 dims, 128-byte swizzle; E4M3: a K box and the
+//    contiguous V tile) into its private ring of R stages, which only this warp
+//    fills and empties.
 //  * Math as mma.sync m16n8k16 on S^T = K Q^T and O^T += V^T P^T: tokens (then
 //    dims) are the 16 rows, the up to 8 heads of the group the 8 columns, so
 //    a K/V byte serves the whole group. tcgen05's smallest M of 64 would be
@@ -39,6 +40,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "subset.h"
+#include "tcgen05.cuh"
 
 namespace pa {
 namespace {
@@ -327,16 +329,17 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
         const uint32_t fb = bars + st * 8;
         if (lane == 0) mbar_arrive_expect_tx(fb, (p0 >= 0 ? C::BLK : 0) + (p1 >= 0 ? C::BLK : 0));
         __syncwarp();
-        // one lane per copy: K then V of the first block, K then V of the second
-        constexpr int HV = F8 ? 1 : D / 64, PB = 2 * HV;
-        const int blk = lane / PB, part = lane % PB, phys = blk ? p1 : p0;
-        if (blk < 2 && phys >= 0) {
-            const uint32_t dst = ring + st * C::STAGE + blk * C::BLK + (part / HV) * C::KT + (part % HV) * C::HALF;
-            if (F8 && part == 1)
+        // one lane per copy: K and V of the first block, K and V of the second
+        const int phys = lane >> 1 ? p1 : p0, part = lane & 1;
+        if (lane < 4 && phys >= 0) {
+            const uint32_t dst = ring + st * C::STAGE + (lane >> 1) * C::BLK + part * C::KT;
+            if constexpr (!F8)
+                tma_load_5d(dst, part ? &tm_v : &tm_k, fb, 0, 0, 0, head, phys, policy);
+            else if (part)
                 bulk_load_1d(dst, static_cast<const uint8_t *>(a.vc) + (int64_t(phys) * Hkv + head) * C::KT, C::KT, fb,
                              policy);
             else
-                tma_load_4d(dst, !F8 && part / HV ? &tm_v : &tm_k, fb, (part % HV) * 64, head, 0, phys, policy);
+                tma_load_4d(dst, &tm_k, fb, 0, head, 0, phys, policy);
         }
     };
 
