@@ -154,7 +154,8 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
     const uint32_t p_ready = s_full + 16, o_full = p_ready + 32, drained = o_full + 16, piece_bar = drained + 8, last_bar = piece_bar + 16;
     volatile int *info = reinterpret_cast<volatile int *>(bp + C::off_info);
     volatile int *vfix = info + kInfo;  // V rows to zero: see the producers
-    volatile int *misc = reinterpret_cast<volatile int *>(bp + C::off_misc);  // [0] tensor memory, [1] gave up, [4 + w] completes the count
+    volatile int *misc = reinterpret_cast<volatile int *>(bp + C::off_misc);  // [0] tensor memory, [1] gave up, [2 + w] queries,
+                                                                          // [4 + w] completes the count, [6], [7] steps begun
     int64_t *pre = reinterpret_cast<int64_t *>(bp + C::off_pre);
 
     if (!PREFIX) pdl_trigger();
@@ -388,6 +389,13 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
         }
         if (ok && is_k) {  // no K in the last step
             if (next_step() && lane == 0) mbar_arrive(full + 8 * (i % kStages));
+        }
+        if (lane == 0) {  // what was started, for an end after giving up
+            misc[is_k ? 6 : 7] = int(i);
+            if (is_k) {
+                misc[2] = int(nq[0]);
+                misc[3] = int(nq[1]);
+            }
         }
     } else if (warp == 9) {
         // ====================================================== matrix products
@@ -819,14 +827,15 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
         tc_fence_after();
         tmem_free(tmem, 512);
     }
-    if (misc[1] && warp == 8)
-        // the CTA gave up: nothing it started may land after it is gone. Of a barrier's two parities one is
-        // complete and the other in flight (the products have waited for every copy otherwise)
-        for (int k = 0; k < 2; ++k)
-            for (uint32_t parity = 0; parity < 2; ++parity) {
-                mbar_wait_bounded(full + 8 * k, parity, a.wait_ns);
-                mbar_wait_bounded(q_full + 8 * k, parity, a.wait_ns);
-            }
+    if (misc[1] && warp == 8) {
+        // the CTA gave up: nothing that was started may land after it is gone (otherwise the products have
+        // waited for every copy)
+        const int steps = max(misc[6], misc[7]);
+        for (int i = max(steps - kStages, 0); i < steps; ++i)
+            mbar_wait_bounded(full + 8 * (i % kStages), uint32_t(i / kStages) & 1u, a.wait_ns);
+        for (int w = 0; w < 2; ++w)
+            if (misc[2 + w] > 0) mbar_wait_bounded(q_full + 8 * w, uint32_t(misc[2 + w] - 1) & 1u, a.wait_ns);
+    }
 }
 
 template <int D, bool PREFIX>

@@ -583,3 +583,171 @@ def test_no_workspace_is_allocated_during_capture():
         mod._subset_ws = old
     graph.replay()
     torch.cuda.synchronize()
+
+
+# ----------------------------------------------- values, extents, long calls
+
+
+def test_window_multi_keeps_nan_and_inf_of_unseen_tokens_out():
+    """A token whose K or V is not finite reaches the rows that see it and no
+    other row, although rows of one tile share its matrix products."""
+    Hq, Hkv, D = 14, 2, 128
+    ctx, ql, window, sinks = [400, 300], [30, 300], 64, 3
+    g, kc, vc, bt, _, _ = pool(41, ctx, Hkv, D)
+    bad = {0: [390, 399], 1: [1, 40, 200, 299]}
+    for b, ts in bad.items():
+        for n, t in enumerate(ts):
+            blk, o = int(bt[b, t // BS]), t % BS
+            vc[blk, o, 0, 5 * n:5 * n + 3] = float("inf") if n % 2 else NAN
+            if n == 1:
+                kc[blk, o, 1, 7] = NAN
+    cu = torch.tensor([0, 30, 330], dtype=torch.int32)
+    q = bf16(g, 330, Hq, D)
+    out = torch.full((330, Hq, D), 7.0, dtype=torch.bfloat16, device=DEV)
+    pg.pa_decode_window_multi(out, *dev(q, kc, vc, bt, cu, torch.tensor(ctx, dtype=torch.int32)), window, sinks, 0.1)
+    got = out.cpu()
+    for b in range(2):
+        for i in range(ql[b]):
+            t = ref.seen(ctx[b] - ql[b] + i + 1, window, sinks)
+            k, v = ref.rows_at(kc, bt[b], t)[0], ref.rows_at(vc, bt[b], t)[0]
+            r = int(cu[b]) + i
+            want, bound, _, _ = ref.attend(q[r].double(), k, v, 0.1)
+            fine = torch.isfinite(want)
+            assert torch.equal(torch.isfinite(got[r].double()), fine), f"sequence {b} row {i}"
+            over = (got[r].double() - want).abs() - bound
+            assert (over[fine] <= 0).all(), f"sequence {b} row {i}"
+
+
+def test_window_keeps_nan_of_unseen_tokens_out():
+    """The tokens between the sinks and the window hold NaN and infinities, in blocks that are partly seen."""
+    Hq, Hkv, D = 8, 2, 128
+    ctx, window, sinks = [333, 90, 41], 37, 5
+    g, kc, vc, bt, _, _ = pool(43, ctx, Hkv, D)
+    for b, x in enumerate(ctx):
+        vis = set(ref.seen(x, window, sinks).tolist())
+        for t in set(range(x)) - vis:
+            kc[bt[b, t // BS], t % BS] = NAN
+            vc[bt[b, t // BS], t % BS] = float("inf") if t % 2 else NAN
+    q = bf16(g, 3, Hq, D)
+    out = torch.full((3, Hq, D), NAN, dtype=torch.bfloat16, device=DEV)
+    pg.pa_decode_window(out, *dev(q, kc, vc, bt, torch.tensor(ctx, dtype=torch.int32)), window, sinks, 0.1)
+    for b, x in enumerate(ctx):
+        t = ref.seen(x, window, sinks)
+        want, bound, _, _ = ref.attend(q[b].double(), ref.rows_at(kc, bt[b], t)[0], ref.rows_at(vc, bt[b], t)[0], 0.1)
+        ref.check(out[b], want, bound, f"ctx {x}")
+
+
+@pytest.mark.parametrize("scale,std", [(0.0884, 12.0), (3.0, 4.0)])
+def test_sharp_and_growing_logits(scale, std):
+    """Logits of hundreds, with the largest one late: the running maximum grows many times."""
+    Hq, Hkv, D = 7, 1, 128
+    g, kc, vc, bt, _, _ = pool(47, [1500, 1500], Hkv, D)
+    q = bf16(g, 24, Hq, D, std=std)
+    for t in range(0, 1500, 90):  # ever larger keys along the first query
+        kc[bt[0, t // BS], t % BS, 0] = (q[0, 0].float() * t / 1500 / std).to(torch.bfloat16)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32)
+    cu, ctx = i32(0, 20, 24), i32(1500, 1500)
+    out = torch.empty(24, Hq, D, dtype=torch.bfloat16, device=DEV)
+    pg.pa_decode_window_multi(out, *dev(q, kc, vc, bt, cu, ctx), 1 << 30, 0, scale)
+    pre = torch.empty(2, Hq, D, dtype=torch.bfloat16, device=DEV)
+    pg.pa_decode_prefix(pre, *dev(q[[0, 20]], kc, vc, bt[:1], ctx[:1], i32(0, 1), bt, ctx), scale)
+    one = torch.empty_like(pre)
+    pg.pa_decode_window(one, *dev(q[[0, 20]], kc, vc, bt, ctx), 1 << 30, 0, scale)
+    rows = lambda b, n: (ref.rows_at(kc, bt[b], torch.arange(n))[0], ref.rows_at(vc, bt[b], torch.arange(n))[0])
+    for b, i, r in ((0, 0, 0), (0, 19, 19), (1, 0, 20), (1, 3, 23)):
+        k, v = rows(b, 1500 - (20, 4)[b] + i + 1)
+        want, bound, _, _ = ref.attend(q[r].double(), k, v, scale)
+        ref.check(out[r], want, bound, f"row {r}")
+    for b, r in ((0, 0), (1, 20)):
+        k, v = rows(b, 1500)
+        want, bound, _, _ = ref.attend(q[r].double(), k, v, scale)
+        ref.check(one[b], want, bound, f"window {b}")
+        if b == 0:
+            k, v = torch.cat([k, k]), torch.cat([v, v])
+        want, bound, _, _ = ref.attend(q[r].double(), k, v, scale)
+        ref.check(pre[b], want, bound, f"prefix {b}")
+
+
+@pytest.mark.parametrize("T,window,sinks", [(5000, 700, 4), (2600, 1 << 30, 0)])
+def test_window_multi_whole_prompt(T, window, sinks):
+    """A prompt attended to in one call (every row new), rows sampled."""
+    Hq, Hkv, D = 28, 4, 128
+    g, kc, vc, bt, _, _ = pool(T, [T], Hkv, D)
+    q = bf16(g, T, Hq, D, std=2.0)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32)
+    out = torch.full((T, Hq, D), NAN, dtype=torch.bfloat16, device=DEV)
+    pg.pa_decode_window_multi(out, *dev(q, kc, vc, bt, i32(0, T), i32(T)), window, sinks, 0.0884)
+    assert torch.isfinite(out.float()).all()
+    for r in list(range(0, T, 131)) + [T - 1]:
+        t = ref.seen(r + 1, window, sinks)
+        want, bound, _, _ = ref.attend(q[r].double(), ref.rows_at(kc, bt[0], t)[0], ref.rows_at(vc, bt[0], t)[0], 0.0884)
+        ref.check(out[r], want, bound, f"row {r}")
+
+
+def test_blocks_past_32_bit_offsets():
+    """A pool of 4.7 GB per cache, the blocks in use at its end: offsets of elements and bytes pass 32 bits."""
+    Hq, Hkv, D = 16, 8, 128
+    NB = 145_000
+    assert NB * BS * Hkv * D > 1 << 31
+    lens, plen, n = [100, 37], 150, 30
+    g = torch.Generator().manual_seed(5)
+    ids = NB - 1 - torch.randperm(n, generator=g)
+    sk, sv = bf16(g, n, BS, Hkv, D), bf16(g, n, BS, Hkv, D)
+    kc_ = torch.zeros(NB, BS, Hkv, D, dtype=torch.bfloat16, device=DEV)
+    vc_ = torch.zeros_like(kc_)
+    kc_[ids.to(DEV)], vc_[ids.to(DEV)] = sk.to(DEV), sv.to(DEV)
+    w_ = torch.zeros(NB, Hkv, BS, device=DEV)
+    small, at = ref.tables(lens + [plen] + [48, 37], torch.arange(n))  # into sk / sv
+    big = torch.where(small >= 0, ids[small.clamp(min=0).long()], torch.tensor(-1)).int()
+    bt, pt, dst = big[:2].contiguous(), big[2:3].contiguous(), big[3:, :3].contiguous()
+    q = bf16(g, 2, Hq, D, std=2.0)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32)
+    ctx = i32(*lens)
+    q_, bt_, pt_, dst_, ctx_ = dev(q, bt, pt, dst, ctx)
+    outs = [torch.empty_like(q_) for _ in range(4)]
+    pg.pa_decode_window(outs[0], q_, kc_, vc_, bt_, ctx_, 50, 2, 0.1)
+    pg.pa_decode_window_multi(outs[1], q_, kc_, vc_, bt_, i32(0, 1, 2).to(DEV), ctx_, 50, 2, 0.1)
+    pg.pa_decode_prefix(outs[2], q_, kc_, vc_, pt_, i32(plen).to(DEV), i32(0, 2).to(DEV), bt_, ctx_, 0.1)
+    pg.pa_decode_weights(outs[3], w_, q_, kc_, vc_, bt_, ctx_, 0.1)
+    total = w_.sum().item()
+    kept = torch.empty(2, Hkv, 48, dtype=torch.int32, device=DEV)
+    new = torch.empty(2, dtype=torch.int32, device=DEV)
+    pg.pa_evict(kept, new, kc_, vc_, w_, bt_, ctx_, dst_, 48)
+    for b, x in enumerate(lens):
+        t = ref.seen(x, 50, 2)
+        rows = lambda row, pos: (ref.rows_at(sk, small[row], pos)[0], ref.rows_at(sv, small[row], pos)[0])
+        want, bound, _, _ = ref.attend(q[b].double(), *rows(b, t), 0.1)
+        ref.check(outs[0][b], want, bound, "window")
+        ref.check(outs[1][b], want, bound, "window, rows")
+        k, v = rows(b, torch.arange(x))
+        want, bound, _, _ = ref.attend(q[b].double(), k, v, 0.1)
+        ref.check(outs[3][b], want, bound, "weights")
+        pk, pv = rows(2, torch.arange(plen))
+        want, bound, _, _ = ref.attend(q[b].double(), torch.cat([pk, k]), torch.cat([pv, v]), 0.1)
+        ref.check(outs[2][b], want, bound, "prefix")
+        m = min(x, 48)  # all of them recent: the last m tokens
+        i = torch.arange(m)
+        src = small[b][(x - m + i) // BS].long(), (x - m + i) % BS
+        got = kc_[big[3 + b][i // BS].long().to(DEV), (i % BS).to(DEV)].cpu()
+        assert torch.equal(got.view(torch.int16), sk[src].view(torch.int16))
+    assert abs(total - 2 * Hq) < 1e-3  # every head's weights sum to 1
+
+
+def test_prefix_with_many_groups_and_no_own_tokens():
+    """Groups of one to three sequences, prefixes of every length, own tokens missing."""
+    Hq, Hkv, D = 6, 2, 64
+    sizes = [1 + i % 3 for i in range(150)]
+    plens = [(13 * i) % 300 for i in range(150)]
+    B = sum(sizes)
+    g, kc, vc, bt, _, _ = pool(61, plens, Hkv, D)
+    cu = torch.tensor([0] + torch.tensor(sizes).cumsum(0).tolist(), dtype=torch.int32)
+    q = bf16(g, B, Hq, D, std=2.0)
+    own, zero = torch.full((B, 1), -1, dtype=torch.int32), torch.zeros(B, dtype=torch.int32)
+    out = torch.full((B, Hq, D), NAN, dtype=torch.bfloat16, device=DEV)
+    pg.pa_decode_prefix(out, *dev(q, kc, vc, bt, torch.tensor(plens, dtype=torch.int32), cu, own, zero), 0.125)
+    for grp, p in enumerate(plens):
+        t = torch.arange(p)
+        k, v = ref.rows_at(kc, bt[grp], t)[0], ref.rows_at(vc, bt[grp], t)[0]
+        for b in range(int(cu[grp]), int(cu[grp + 1])):
+            want, bound, _, _ = ref.attend(q[b].double(), k, v, 0.125)
+            ref.check(out[b], want, bound, f"sequence {b}")
