@@ -64,7 +64,7 @@ struct RowCfg {
     static constexpr size_t off_ring = 2 * size_t(TILE);   // after the two Q tiles
     static constexpr size_t off_stage = off_ring + 2 * size_t(kStages) * TILE;  // 32 rows of 128 bytes per softmax warp
     static constexpr size_t off_bars = off_stage + 8 * 4096;
-    static constexpr size_t off_info = off_bars + 208;
+    static constexpr size_t off_info = off_bars + 224;
     static constexpr size_t off_misc = off_info + 2 * kInfo * 4;
     static constexpr size_t off_pre = off_misc + 32;
     static constexpr size_t SMEM = 1024 + off_pre + (kPreCap + 1) * 8;
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
     const uint32_t ring = base + uint32_t(C::off_ring);
     const uint32_t full = base + uint32_t(C::off_bars), empty = full + kStages * 8;
     const uint32_t q_full = empty + kStages * 8, q_empty = q_full + 16, s_full = q_empty + 16;
-    const uint32_t p_ready = s_full + 16, o_full = p_ready + 32, drained = o_full + 16, piece_bar = drained + 8, last_bar = piece_bar + 16;
+    const uint32_t p_ready = s_full + 16, o_full = p_ready + 32, drained = o_full + 16, piece_bar = drained + 8, last_bar = piece_bar + 16, seen_bar = last_bar + 16;
     volatile int *info = reinterpret_cast<volatile int *>(bp + C::off_info);
     volatile int *vfix = info + kInfo;  // V rows to zero: see the producers
     volatile int *misc = reinterpret_cast<volatile int *>(bp + C::off_misc);  // [0] tensor memory, [1] gave up, [2 + w] queries,
@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
             mbar_init(o_full + 8 * w, 1);
             mbar_init(piece_bar + 8 * w, 4);
             mbar_init(last_bar + 8 * w, 1);
+            mbar_init(seen_bar + 8 * w, 1);
         }
         mbar_init(drained, 1);
         fence_barrier_init();
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
             if (int64_t(Hkv) * pre[mid] <= pos0) lo = mid; else hi = mid;
         }
         int s = lo * str;
-        int64_t rem = pos0 - int64_t(Hkv) * pre[lo], t = work.tiles(s);
+        int64_t rem = pos0 - int64_t(Hkv) * pre[lo], t = str == 1 ? pre[lo + 1] - pre[lo] : work.tiles(s);
         while (rem >= int64_t(Hkv) * t && s + 1 < ns) {
             rem -= int64_t(Hkv) * t;
             t = work.tiles(++s);
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
         const uint32_t lane_base = uint32_t(warp & 3) << 21;  // this warp's 32 of the 128 lanes
         const uint32_t ts = tmem + lane_base + 256 * w, to = ts + 128;
         const int i = row / G, h = row - i * G;
-        uint32_t ph = 0, tile_no = 0, units = 0, cuts = 0;
+        uint32_t ph = 0, tile_no = 0, units = 0, cuts = 0, pubs = 0;
         bool ok = true;
         for (int64_t p = pos0; ok && p < pos1;) {
             const int t0 = int(p - s0), t1 = int(min(pos1 - s0, int64_t(x.n)));
@@ -612,14 +613,18 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                     l += (la.x + la.y) + (lb.x + lb.y);
                 }
                 // ---- the end of the unit, or of this CTA's piece of it
+                const bool whole = t0 == 0 && t1 == x.n;
+                const int c0 = int(s0 / L), npieces = int((s0 + x.n - 1) / L) - c0 + 1, mine = int(blockIdx.x) - c0;
+                // pieces of the row tile already counted (read while the products end)
+                int seen = 0;
+                if (!PREFIX && !whole && (warp & 3) == 0 && lane == 0) seen = ld_acquire_s32(a.counters + 2 * c0 + w);
                 if (ok) ok = wait(o_full + 8 * w, units++);
                 if (!ok) break;
                 tc_fence_after();
-                const bool whole = t0 == 0 && t1 == x.n;
                 const int64_t orow = int64_t(x.r0 + ir) * a.Hq + x.kvh * G + h;
-                const int c0 = int(s0 / L);
-                float *slot = a.slots + (2 * int64_t(blockIdx.x) + (int(blockIdx.x) == c0)) * C::SLOT + w * (C::SLOT / 2);
-                const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
+                auto piece_of = [&](int k) {
+                    return a.slots + (2 * int64_t(c0 + k) + (k == 0)) * C::SLOT + w * (C::SLOT / 2);
+                };
                 const unsigned acts = __ballot_sync(0xffffffffu, act);
                 uint8_t *stage = bp + C::off_stage + warp * 4096;
                 const int sj = lane & 7, sr = lane >> 3;
@@ -638,140 +643,163 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                         if ((acts >> r) & 1u) __stcg(reinterpret_cast<uint4 *>(row_at(r, ro)) + sj, y);
                     }
                 };
-                unsigned bad = 0;  // rows of this warp whose result is not finite
-                auto finite = [](float v) { return fabsf(v) <= 3.4028234e38f; };
-                if (!PREFIX && whole) {
-                    bool mine = true;
-#pragma unroll 1  // this runs once per unit: code that has to be fetched first costs more than the loop
-                    for (int c = 0; c < HV; ++c) {
-                        uint4 v[8];
+                // this CTA's O columns 32 c .. 32 c + 31; a row that saw no token has 0, whatever the products held
+                auto own = [&](int c, float (&v)[32]) {
+                    uint32_t o[32];
+                    __syncwarp();
+                    tmem_ld32(to + 32 * c, o);
+                    tc_wait_ld();
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            uint32_t o[32];
-                            tmem_ld32(to + 64 * c + 32 * q, o);
-                            tc_wait_ld();
-                            uint32_t y[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                // no token seen: 0, whatever the products held
-                                const float x0 = l == 0.f ? 0.f : __uint_as_float(o[2 * e]) * inv;
-                                const float x1 = l == 0.f ? 0.f : __uint_as_float(o[2 * e + 1]) * inv;
-                                mine = mine && finite(x0) && finite(x1);
-                                y[e] = pack_bf16x2(x0, x1);
-                            }
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                v[4 * q + e] = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-                        }
-                        store_rows(v, [&](int, int64_t ro) { return a.out + ro * D + 64 * c; });
-                    }
-                    bad = __ballot_sync(0xffffffffu, act && !mine);
-                } else {
-#pragma unroll 1
+                    for (int e = 0; e < 32; ++e) v[e] = l == 0.f ? 0.f : __uint_as_float(o[e]);
+                };
+                // the O of a piece, with m and l per row; PREFIX: of a whole unit too, by row
+                auto publish = [&]() {
+                    float *ps = piece_of(mine);
+#pragma unroll 1  // code that runs once per unit: what has to be fetched first costs more than a loop
                     for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        uint4 v[8];
-                        tmem_ld32(to + 32 * c, o);
-                        tc_wait_ld();
+                        float v[32];
+                        own(c, v);
+                        uint4 y[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            v[e] = l == 0.f ? make_uint4(0u, 0u, 0u, 0u)
-                                            : make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                        store_rows(v, [&](int r, int64_t ro) {
-                            return (PREFIX && whole ? a.rowres + ro * D : slot + ((warp & 3) * 32 + r) * D) + 32 * c;
+                            y[e] = make_uint4(__float_as_uint(v[4 * e]), __float_as_uint(v[4 * e + 1]),
+                                              __float_as_uint(v[4 * e + 2]), __float_as_uint(v[4 * e + 3]));
+                        store_rows(y, [&](int r, int64_t ro) {
+                            return (PREFIX && whole ? a.rowres + ro * D : ps + ((warp & 3) * 32 + r) * D) + 32 * c;
                         });
                     }
-                }
-                if (act && (PREFIX || !whole)) {
-                    if (PREFIX && whole) {
-                        __stcg(reinterpret_cast<float2 *>(a.rowml) + orow, make_float2(m, l));
-                    } else {
-                        __stcg(slot + 128 * D + row, m);
-                        __stcg(slot + 128 * (D + 1) + row, l);
+                    if (act) {
+                        if (PREFIX && whole) {
+                            __stcg(reinterpret_cast<float2 *>(a.rowml) + orow, make_float2(m, l));
+                        } else {
+                            __stcg(ps + 128 * D + row, m);
+                            __stcg(ps + 128 * (D + 1) + row, l);
+                        }
                     }
-                }
-                const int npieces = int((s0 + x.n - 1) / L) - c0 + 1;
-                if (PREFIX && act && h == 0 && t0 == 0)  // where this row's parts are
-                    a.desc[int64_t(x.r0 + ir) * Hkv + x.kvh] = make_int4(c0, npieces, w, row);
-                if constexpr (!PREFIX) {
+                };
+                if constexpr (PREFIX) {
+                    publish();
+                    if (act && h == 0 && t0 == 0)  // where this row's parts are
+                        a.desc[int64_t(x.r0 + ir) * Hkv + x.kvh] = make_int4(c0, npieces, w, row);
+                } else {
+                    bool last = whole;  // this CTA writes the rows
                     if (!whole) {
-                        // the row tile's four warps publish their part; the piece that completes the count merges
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(piece_bar + 8 * w);
-                        if ((warp & 3) == 0) {
-                            if (!(ok = wait(piece_bar + 8 * w, cuts))) break;
-                            if (lane == 0) {
-                                misc[4 + w] = atomic_add_acq_rel_gpu(a.counters + 2 * c0 + w, 1) == npieces - 1;
-                                mbar_arrive(last_bar + 8 * w);
+                        // all other pieces counted: this one need not be published
+                        if ((warp & 3) == 0 && lane == 0) {
+                            misc[4 + w] = seen == npieces - 1;
+                            mbar_arrive(seen_bar + 8 * w);
+                        }
+                        if (!(ok = wait(seen_bar + 8 * w, cuts++))) break;
+                        last = misc[4 + w];
+                        if (!last) {
+                            publish();
+                            // the row tile's four warps publish their part; the piece that completes the count merges
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(piece_bar + 8 * w);
+                            if ((warp & 3) == 0) {
+                                if (!(ok = wait(piece_bar + 8 * w, pubs))) break;
+                                if (lane == 0) {
+                                    misc[4 + w] = atomic_add_acq_rel_gpu(a.counters + 2 * c0 + w, 1) == npieces - 1;
+                                    mbar_arrive(last_bar + 8 * w);
+                                }
+                            }
+                            if (!(ok = wait(last_bar + 8 * w, pubs++))) break;
+                            last = misc[4 + w];
+                        }
+                        if (last && row == 0) a.counters[2 * c0 + w] = 0;
+                    }
+                    unsigned bad = 0;  // rows of this warp whose result is not finite
+                    if (last) {
+                        // weights of the pieces, in their order (one, if whole)
+                        constexpr int KW = 4;  // kept in registers
+                        float M = m, Ls = l, mk[KW];
+                        if (!whole) {
+                            M = -INFINITY;
+                            Ls = 0.f;
+                            for (int k = 0; k < npieces; k += KW) {
+                                float lk[KW];
+#pragma unroll
+                                for (int e = 0; e < KW; ++e) {
+                                    const float *ps = piece_of(min(k + e, npieces - 1)) + 128 * D + row;
+                                    const bool me = k + e == mine;
+                                    mk[e] = me ? m : act ? __ldcg(ps) : -INFINITY;
+                                    lk[e] = me ? l : act ? __ldcg(ps + 128) : 0.f;
+                                }
+#pragma unroll
+                                for (int e = 0; e < KW; ++e) {
+                                    if (k + e >= npieces) break;
+                                    const float Mn = fmaxf(M, mk[e]);
+                                    const float f = M == -INFINITY ? 0.f : fast_exp2(M - Mn);
+                                    Ls = Ls * f + (mk[e] == -INFINITY ? lk[e] : lk[e] * fast_exp2(mk[e] - Mn));
+                                    M = Mn;
+                                }
                             }
                         }
-                        if (!(ok = wait(last_bar + 8 * w, cuts))) break;
-                        ++cuts;
-                        if (misc[4 + w]) {
-                            auto piece_of = [&](int k) {
-                                return a.slots + (2 * int64_t(c0 + k) + (k == 0)) * C::SLOT + w * (C::SLOT / 2);
-                            };
-                            // weights of the pieces: lane = row; values: a row per load, all lanes
-                            float M = -INFINITY, Ls = 0.f;
-                            for (int k = 0; k < npieces; ++k)
-                                if (act) M = fmaxf(M, __ldcg(piece_of(k) + 128 * D + row));
-                            const float Mr = M == -INFINITY ? 0.f : M;
-                            for (int k = 0; k < npieces; ++k)
-                                if (act)
-                                    Ls += fast_exp2(__ldcg(piece_of(k) + 128 * D + row) - Mr) *
-                                          __ldcg(piece_of(k) + 128 * (D + 1) + row);
-                            const float iv = Ls == 0.f ? 0.f : 1.f / Ls;
-                            constexpr int V = D / 32, RB = 8;  // values per lane and row, rows at once
+                        const float Mr = M == -INFINITY ? 0.f : M, iv = Ls == 0.f ? 0.f : 1.f / Ls;  // NaN stays NaN
+                        bool fine = true;
 #pragma unroll 1
-                            for (int rb = 0; rb < 32; rb += RB) {
-                                if (!((acts >> rb) & ((1u << RB) - 1u))) continue;
-                                float v[RB][V];
+                        for (int c2 = 0; c2 < HV; ++c2) {
+                            uint4 y[8];
 #pragma unroll
-                                for (int r = 0; r < RB; ++r)
+                            for (int q = 0; q < 2; ++q) {
+                                const int c = 2 * c2 + q;
+                                float v[32];
+                                if (whole) {
+                                    own(c, v);
 #pragma unroll
-                                    for (int e = 0; e < V; ++e) v[r][e] = 0.f;
-                                for (int k = 0; k < npieces; ++k) {
-                                    const float *ps = piece_of(k);
-                                    const float f = act ? fast_exp2(__ldcg(ps + 128 * D + row) - Mr) * iv : 0.f;
-                                    const float *src = ps + ((warp & 3) * 32 + rb) * D + lane * V;
-                                    float y[RB][V];
+                                    for (int e = 0; e < 32; ++e) v[e] *= iv;
+                                } else {
 #pragma unroll
-                                    for (int r = 0; r < RB; ++r) {
-                                        if (!((acts >> (rb + r)) & 1u)) {
-#pragma unroll
-                                            for (int e = 0; e < V; ++e) y[r][e] = 0.f;
-                                        } else if constexpr (V == 4) {
-                                            const float4 t = __ldcg(reinterpret_cast<const float4 *>(src + r * D));
-                                            y[r][0] = t.x, y[r][1] = t.y, y[r][2] = t.z, y[r][3] = t.w;
+                                    for (int e = 0; e < 32; ++e) v[e] = 0.f;
+#pragma unroll 1
+                                    for (int k = 0; k < npieces; ++k) {
+                                        const float *ps = piece_of(k);
+                                        float o[32], mw = m;
+                                        if (k == mine) {
+                                            own(c, o);
                                         } else {
-                                            const float2 t = __ldcg(reinterpret_cast<const float2 *>(src + r * D));
-                                            y[r][0] = t.x, y[r][1] = t.y;
+                                            // rows by eight lanes each, to one per lane
+                                            mw = act ? __ldcg(ps + 128 * D + row) : -INFINITY;
+                                            uint4 in[8];
+#pragma unroll
+                                            for (int j = 0; j < 8; ++j) {
+                                                const int r = 4 * j + sr;
+                                                in[j] = (acts >> r) & 1u
+                                                            ? __ldcg(reinterpret_cast<const uint4 *>(
+                                                                         ps + ((warp & 3) * 32 + r) * D + 32 * c) + sj)
+                                                            : make_uint4(0u, 0u, 0u, 0u);
+                                            }
+                                            __syncwarp();
+#pragma unroll
+                                            for (int j = 0; j < 8; ++j) {
+                                                const int r = 4 * j + sr;
+                                                *reinterpret_cast<uint4 *>(stage + r * 128 + ((sj ^ (r & 7)) << 4)) = in[j];
+                                            }
+                                            __syncwarp();
+#pragma unroll
+                                            for (int j = 0; j < 8; ++j) {
+                                                const float4 z = *reinterpret_cast<const float4 *>(
+                                                    stage + lane * 128 + ((j ^ (lane & 7)) << 4));
+                                                o[4 * j] = z.x, o[4 * j + 1] = z.y, o[4 * j + 2] = z.z, o[4 * j + 3] = z.w;
+                                            }
                                         }
-                                    }
+                                        const float f = fast_exp2(mw - Mr) * iv;
 #pragma unroll
-                                    for (int r = 0; r < RB; ++r) {
-                                        const float fr = __shfl_sync(0xffffffffu, f, rb + r);
-#pragma unroll
-                                        for (int e = 0; e < V; ++e) v[r][e] += fr * y[r][e];
+                                        for (int e = 0; e < 32; ++e) v[e] += f * o[e];
                                     }
                                 }
 #pragma unroll
-                                for (int r = 0; r < RB; ++r) {
-                                    const int64_t ro = __shfl_sync(0xffffffffu, orow, rb + r);
-                                    bool fine = true;
+                                for (int e = 0; e < 32; ++e) fine = fine && fabsf(v[e]) <= 3.4028234e38f;
 #pragma unroll
-                                    for (int e = 0; e < V; ++e) fine = fine && finite(v[r][e]);
-                                    if (!__all_sync(0xffffffffu, fine)) bad |= 1u << (rb + r);
-                                    if ((acts >> (rb + r)) & 1u) {
-                                        uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + ro * D) + lane * (V / 2);
-#pragma unroll
-                                        for (int e = 0; e < V; e += 2) dst[e / 2] = pack_bf16x2(v[r][e], v[r][e + 1]);
-                                    }
-                                }
+                                for (int e = 0; e < 4; ++e)
+                                    y[4 * q + e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]),
+                                                              pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
+                                                              pack_bf16x2(v[8 * e + 4], v[8 * e + 5]),
+                                                              pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
                             }
-                            bad &= acts;
-                            if (row == 0) a.counters[2 * c0 + w] = 0;
+                            store_rows(y, [&](int, int64_t ro) { return a.out + ro * D + 64 * c2; });
                         }
+                        bad = __ballot_sync(0xffffffffu, act && !fine);
                     }
                     // ---- rows that are not finite, again over their own tokens only (in fp32, a row per warp)
                     __syncwarp();
