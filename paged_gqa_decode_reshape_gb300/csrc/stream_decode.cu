@@ -799,30 +799,47 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
 }
 
 // ---- accumulated weights: p_t = 2^(z_t - lse) summed over the group, added
-// to the cache's weights. 16 lanes per block, in token order.
+// to the cache's weights. A thread per four tokens of a block, the logits of
+// every head in flight; the logits come from L2, mostly.
 constexpr int kAddThreads = 256;
 
 __global__ void __launch_bounds__(kAddThreads) weights_add_kernel(const SubsetArgs a) {
     pdl_trigger();
+    constexpr int QB = kBlockSize / 4;  // threads per block
     const int seg = blockIdx.x, b = seg / a.Hkv, kvh = seg % a.Hkv;
     const int lim = min(max(__ldg(a.ctx + b), 0), a.MBS * kBlockSize);
-    const int t0 = threadIdx.x % kBlockSize;
+    const int t0 = 4 * (threadIdx.x % QB);
     pdl_wait();
     float ls[kMaxGroup];
 #pragma unroll
     for (int h = 0; h < kMaxGroup; ++h) ls[h] = h < a.G ? __ldcg(a.lse + int64_t(b) * a.Hq + kvh * a.G + h) : INFINITY;
-    for (int j = blockIdx.y * (kAddThreads / kBlockSize) + threadIdx.x / kBlockSize; j * kBlockSize < lim;
-         j += gridDim.y * (kAddThreads / kBlockSize)) {
+    for (int j = blockIdx.y * (kAddThreads / QB) + threadIdx.x / QB; j * kBlockSize + t0 < lim;
+         j += gridDim.y * (kAddThreads / QB)) {
         const int phys = __ldg(a.bt + int64_t(b) * a.MBS + j);
-        if (phys < 0 || int64_t(phys) >= a.NB || j * kBlockSize + t0 >= lim) continue;
         const float *z = a.logits + (int64_t(seg) * a.MBS + j) * (a.G * kBlockSize) + t0;
-        float zz[kMaxGroup], w = 0.f;
+        float4 zz[kMaxGroup], w = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int h = 0; h < kMaxGroup; ++h) zz[h] = h < a.G ? __ldcg(z + h * kBlockSize) : 0.f;
+        for (int h = 0; h < kMaxGroup; ++h)
+            zz[h] = h < a.G ? __ldcg(reinterpret_cast<const float4 *>(z + h * kBlockSize)) : w;
+        if (phys < 0 || int64_t(phys) >= a.NB) continue;
 #pragma unroll
-        for (int h = 0; h < kMaxGroup; ++h) w += fast_exp2(zz[h] - ls[h]);  // 0 for h >= G
-        // a block of one sequence gets one addition: the same bits every time
-        atomicAdd(a.weights + (int64_t(phys) * a.Hkv + kvh) * kBlockSize + t0, w);
+        for (int h = 0; h < kMaxGroup; ++h) {  // 0 for h >= G, and for unseen tokens (logit -inf)
+            w.x += fast_exp2(zz[h].x - ls[h]);
+            w.y += fast_exp2(zz[h].y - ls[h]);
+            w.z += fast_exp2(zz[h].z - ls[h]);
+            w.w += fast_exp2(zz[h].w - ls[h]);
+        }
+        // tokens past the context get nothing (their weights may hold anything); a block of one sequence
+        // gets one addition: the same bits every time
+        float *dst = a.weights + (int64_t(phys) * a.Hkv + kvh) * kBlockSize + t0;
+        const int left = lim - (j * kBlockSize + t0);
+        if (left >= 4) {
+            atomicAdd(reinterpret_cast<float4 *>(dst), w);
+        } else {
+            atomicAdd(dst, w.x);
+            if (left > 1) atomicAdd(dst + 1, w.y);
+            if (left > 2) atomicAdd(dst + 2, w.z);
+        }
     }
 }
 
@@ -916,7 +933,7 @@ cudaError_t launch_stream_decode(const CUtensorMap &tk, const CUtensorMap &tv, c
         cudaError_t e = head_dim == 128 ? launch_t<128, kCacheBf16, true>(tk, tv, a, sms, stream)
                                         : launch_t<64, kCacheBf16, true>(tk, tv, a, sms, stream);
         if (e != cudaSuccess) return e;
-        const int per = kAddThreads / kBlockSize;  // blocks a CTA takes per turn
+        const int per = kAddThreads / (kBlockSize / 4);  // blocks a CTA takes per turn
         const int x = (a.MBS + per - 1) / per;
         return launch_pdl(weights_add_kernel, dim3(a.nseq * a.Hkv, x < 16 ? x : 16), dim3(kAddThreads), 0, stream, a);
     }
