@@ -17,6 +17,125 @@ namespace {
 constexpr int kSelThreads = 1024, kHistCopies = 8;
 constexpr int kKeysCap = 48 * 1024;  // keys held in shared memory; longer rows read them again
 
+// The k-th largest of n keys (n > k >= 1), key_of(j) in totalOrder: thr, and keq,
+// how many keys equal to it belong to the k (every key above it does). Radix
+// descent in digits of up to 8 bits from the highest bit in which the keys
+// differ; it ends early when a digit's keys are all taken (then thr is one below
+// them and keq 0). A histogram copy per four warps keeps the atomic adds of
+// equal digits apart, and a thread per bin sums and scans them: a pass over a
+// row of 12K keys takes about a microsecond.
+template <typename KeyOf>
+__device__ __forceinline__ void kth_largest(KeyOf key_of, int n, int k, int *hist, int *red, uint32_t &thr, int &keq) {
+    constexpr int NW = kSelThreads / 32, U = 4;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t lo = 0xffffffffu, hi = 0u;
+    for (int j = tid; j < n; j += kSelThreads) {
+        const uint32_t u = key_of(j);
+        lo = min(lo, u);
+        hi = max(hi, u);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+        red[warp] = int(lo);
+        red[NW + warp] = int(hi);
+    }
+    __syncthreads();
+    lo = __reduce_min_sync(0xffffffffu, uint32_t(red[lane]));
+    hi = __reduce_max_sync(0xffffffffu, uint32_t(red[NW + lane]));
+    static_assert(NW == 32, "one lane per warp");
+    thr = hi;
+    keq = k;
+    if (lo == hi) return;  // every key equal: the k lowest positions
+    const int top = 31 - __clz(lo ^ hi);
+    uint32_t mask = top == 31 ? 0u : ~((2u << top) - 1u);  // bits in which the keys left agree, with
+    uint32_t prefix = hi & mask;
+    for (int h = top; h >= 0;) {
+        const int l = h >= 7 ? h - 7 : 0;
+        const uint32_t dm = (2u << (h - l)) - 1u;  // digit of bits l..h
+        for (int i = tid; i < kHistCopies * 256; i += kSelThreads) hist[i] = 0;
+        __syncthreads();
+        int *mine = hist + (warp % kHistCopies) * 256;
+        for (int j0 = tid; j0 < n; j0 += U * kSelThreads) {
+            uint32_t u[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) u[i] = j0 + i * kSelThreads < n ? key_of(j0 + i * kSelThreads) : ~prefix;
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if ((u[i] & mask) == prefix && j0 + i * kSelThreads < n) atomicAdd(&mine[(u[i] >> l) & dm], 1);
+        }
+        __syncthreads();
+        int cnt = 0, incl = 0;
+        if (tid < 256) {  // digits descending
+#pragma unroll
+            for (int c = 0; c < kHistCopies; ++c) cnt += hist[c * 256 + 255 - tid];
+            incl = cnt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            if (lane == 31) red[warp] = incl;
+        }
+        __syncthreads();
+        if (tid < 256) {
+            for (int w = 0; w < warp; ++w) incl += red[w];
+            if (incl - cnt < k && k <= incl) {
+                red[2 * NW] = 255 - tid;
+                red[2 * NW + 1] = incl - cnt;
+                red[2 * NW + 2] = incl == k;
+            }
+        }
+        __syncthreads();
+        prefix |= uint32_t(red[2 * NW]) << l;
+        mask |= dm << l;
+        k -= red[2 * NW + 1];
+        h = l - 1;
+        if (red[2 * NW + 2] && prefix != 0u && h >= 0) {
+            thr = prefix - 1u;
+            keq = 0;
+            return;
+        }
+    }
+    thr = prefix;
+    keq = k;
+}
+
+// The selection for a threshold, ascending: emit(r, j) for the r-th selected
+// position j. Warps own consecutive ranges of 32-key rows, a lane per key.
+template <typename KeyOf, typename Emit>
+__device__ __forceinline__ void emit_selected(KeyOf key_of, int n, uint32_t thr, int keq, int *red, Emit emit) {
+    constexpr int NW = kSelThreads / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned below = (1u << lane) - 1u;
+    const int rows = ((n + 31) / 32 + NW - 1) / NW, j0 = warp * rows * 32, j1 = min(n, j0 + rows * 32);
+    int gt = 0, eq = 0;
+    for (int j = j0; j < j1; j += 32) {
+        const uint32_t u = j + lane < j1 ? key_of(j + lane) : 0u;
+        gt += __popc(__ballot_sync(0xffffffffu, j + lane < j1 && u > thr));
+        eq += __popc(__ballot_sync(0xffffffffu, j + lane < j1 && u == thr));
+    }
+    __syncthreads();  // red is free
+    if (lane == 0) {
+        red[warp] = gt;
+        red[NW + warp] = eq;
+    }
+    __syncthreads();
+    gt = __reduce_add_sync(0xffffffffu, lane < warp ? red[lane] : 0);
+    eq = __reduce_add_sync(0xffffffffu, lane < warp ? red[NW + lane] : 0);
+    for (int j = j0; j < j1; j += 32) {
+        const uint32_t u = j + lane < j1 ? key_of(j + lane) : 0u;
+        const unsigned g = __ballot_sync(0xffffffffu, j + lane < j1 && u > thr);
+        const unsigned e = __ballot_sync(0xffffffffu, j + lane < j1 && u == thr);
+        // taken before this key: those above thr, and of those equal to it the first keq
+        const int eqb = eq + __popc(e & below);
+        const bool take = (g >> lane) & 1u || ((e >> lane) & 1u && eqb < keq);
+        if (take) emit(gt + __popc(g & below) + min(eqb, keq), j + lane);
+        gt += __popc(g);
+        eq += __popc(e);
+    }
+}
+
 // one CTA per (sequence, KV head): the kept positions
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a, int cap) {
     extern __shared__ __align__(16) uint32_t keys[];
@@ -77,31 +196,33 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     auto key_of = [&](int j) -> uint32_t { return cached ? keys[j] : load(j); };
     uint32_t thr;
     int keq;
-    cta_topk_threshold<kSelThreads, kHistCopies>(key_of, n, top, hist, red, thr, keq);
-    cta_topk_emit<kSelThreads>(key_of, n, thr, keq, red, [&](int r, int j) { kept[r] = j; });
+    kth_largest(key_of, n, top, hist, red, thr, keq);
+    emit_selected(key_of, n, thr, keq, red, [&](int r, int j) { kept[r] = j; });
 }
 
-// The copy: a warp per `chunk` (8 or 32) kept tokens of a (sequence, KV head). Bound by HBM:
-// every kept row is read and written once. A lane finds one token's rows; then
-// the warp moves the tokens one after the other, K and V side by side (D = 128:
-// 16 lanes of 16 bytes each; D = 64: two tokens at once), kMove loads per lane
-// in flight.
+// The copy: a warp per 8 kept tokens of a (sequence, KV head) at D = 128, 16 at
+// D = 64. Bound by HBM: every kept row is read and written once (263 MB in 47 us,
+// 5.6 TB/s, at 16 sequences of 4096 kept tokens; warps of 32 tokens, with fewer
+// CTAs to spread over the SMs, took 2 us longer). A lane finds one token's rows;
+// then the warp moves them with K and V side by side (16 lanes of 16 bytes each,
+// or 8 and two tokens), kMove loads per lane in flight.
 // No early launch of the next kernel: it may read new_lens before it waits.
 constexpr int kMove = 8;
 
 template <int D>
-__global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a, int chunk) {
-    constexpr int LR = D / 8;         // lanes per row
-    constexpr int TP = 32 / (2 * LR); // tokens at once
+__global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
+    constexpr int LR = D / 8;          // lanes per row
+    constexpr int TP = 32 / (2 * LR);  // tokens at once
+    constexpr int CHUNK = kMove * TP;  // tokens per warp
     pdl_wait();
     const int lane = threadIdx.x & 31;
-    const int per = (a.budget + chunk - 1) / chunk;  // warps per (sequence, KV head)
+    const int per = (a.budget + CHUNK - 1) / CHUNK;  // warps per (sequence, KV head)
     const int64_t warp = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
     const int64_t seg = warp / per;
     if (seg >= int64_t(a.B) * a.Hkv) return;
-    const int i0 = int(warp - seg * per) * chunk, kvh = int(seg % a.Hkv), b = int(seg / a.Hkv);
+    const int i0 = int(warp - seg * per) * CHUNK, kvh = int(seg % a.Hkv), b = int(seg / a.Hkv);
     const int i = i0 + lane;
-    const int j = lane < chunk && i < a.budget ? __ldcg(a.kept + seg * a.budget + i) : -1;
+    const int j = lane < CHUNK && i < a.budget ? __ldcg(a.kept + seg * a.budget + i) : -1;
     // this lane's token: its row in the cache, before and after; -1: not copied
     int64_t from = -1, to = -1;
     if (j >= 0) {
@@ -117,21 +238,18 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a, int 
     if (!__any_sync(0xffffffffu, from >= 0)) return;
     const int half = lane / LR % 2, e = lane % LR;
     uint4 *cache = reinterpret_cast<uint4 *>(half ? a.vc : a.kc) + e;
-#pragma unroll 1
-    for (int t0 = 0; t0 < chunk; t0 += kMove * TP) {
-        uint4 v[kMove];
-        int64_t y[kMove];
+    uint4 v[kMove];
+    int64_t y[kMove];
 #pragma unroll
-        for (int u = 0; u < kMove; ++u) {
-            const int t = t0 + u * TP + lane / (2 * LR);
-            const int64_t x = __shfl_sync(0xffffffffu, from, t);
-            y[u] = __shfl_sync(0xffffffffu, to, t);
-            if (x >= 0) v[u] = __ldcs(cache + x * LR);
-        }
-#pragma unroll
-        for (int u = 0; u < kMove; ++u)
-            if (y[u] >= 0) __stcs(cache + y[u] * LR, v[u]);
+    for (int u = 0; u < kMove; ++u) {
+        const int t = u * TP + lane / (2 * LR);
+        const int64_t x = __shfl_sync(0xffffffffu, from, t);
+        y[u] = __shfl_sync(0xffffffffu, to, t);
+        if (x >= 0) v[u] = __ldcs(cache + x * LR);
     }
+#pragma unroll
+    for (int u = 0; u < kMove; ++u)
+        if (y[u] >= 0) __stcs(cache + y[u] * LR, v[u]);
 }
 
 __global__ void __launch_bounds__(256) reset_weights_kernel(float *weights, const int64_t *slots, int64_t T, int Hkv,
@@ -154,14 +272,11 @@ cudaError_t launch_evict(const EvictArgs &a, int head_dim, cudaStream_t stream) 
     if (e != cudaSuccess) return e;
     e = launch_pdl(evict_select_kernel, dim3(a.B * a.Hkv), dim3(kSelThreads), smem, stream, a, cap);
     if (e != cudaSuccess) return e;
-    // 32 tokens per warp read kept in whole lines; where that leaves SMs without work (fewer than about
-    // 8 warps each), 8 tokens per warp: one sequence of 1024 kept tokens 13.5 -> 11 us, select included
-    const int64_t segs = int64_t(a.B) * a.Hkv;
-    const int chunk = segs * ((a.budget + 31) / 32) < 1216 ? 8 : 32;
-    const int64_t warps = segs * ((a.budget + chunk - 1) / chunk);
+    const int chunk = head_dim == 128 ? kMove : 2 * kMove;  // kept tokens per warp
+    const int64_t warps = int64_t(a.B) * a.Hkv * ((a.budget + chunk - 1) / chunk);
     const dim3 grid(unsigned((warps + 7) / 8));
-    return head_dim == 128 ? launch_pdl(evict_move_kernel<128>, grid, dim3(256), 0, stream, a, chunk)
-                           : launch_pdl(evict_move_kernel<64>, grid, dim3(256), 0, stream, a, chunk);
+    return head_dim == 128 ? launch_pdl(evict_move_kernel<128>, grid, dim3(256), 0, stream, a)
+                           : launch_pdl(evict_move_kernel<64>, grid, dim3(256), 0, stream, a);
 }
 
 cudaError_t launch_reset_weights(float *weights, const int64_t *slots, int64_t T, int Hkv, int64_t NB,
