@@ -225,7 +225,11 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
     const int64_t total = int64_t(Hkv) * pre[np];
     const int64_t L = max((total + gridDim.x - 1) / gridDim.x, int64_t(a.min_items));
     const int64_t pos0 = int64_t(blockIdx.x) * L, pos1 = min(total, pos0 + L);
-    if (pos0 >= pos1) return;  // whole CTA: nothing to do
+    if (pos0 >= pos1) {  // whole CTA: nothing to do
+        // a call without any rows still ends after what came before it, which later kernels may need
+        if (!PREFIX) pdl_wait();
+        return;
+    }
 
     if (warp == 9) tmem_alloc(smem_u32(const_cast<int *>(misc)), 512);
     // ---- the first unit, by every warp

@@ -751,3 +751,65 @@ def test_prefix_with_many_groups_and_no_own_tokens():
         for b in range(int(cu[grp]), int(cu[grp + 1])):
             want, bound, _, _ = ref.attend(q[b].double(), k, v, 0.125)
             ref.check(out[b], want, bound, f"sequence {b}")
+
+
+def test_calls_after_one_without_rows_see_what_came_before():
+    """A windowed call whose sequences all have no rows still keeps its place in the stream: the call after it
+    reads the result of the call before it."""
+    B, Hq, Hkv, D, n = 16, 28, 4, 128, 8192
+    g, kc, vc, bt, perm, at = pool(77, [n] * B, Hkv, D, spoil=False)
+    q = bf16(g, B, Hq, D)
+    q_, kc_, vc_, bt_, ctx_ = dev(q, kc, vc, bt, torch.full((B,), n, dtype=torch.int32))
+    cu_ = torch.zeros(B + 1, dtype=torch.int32, device=DEV)
+    mid, untouched = torch.zeros_like(q_), torch.full_like(q_, 3.0)
+    ws = [torch.zeros(pg.pa_decode_workspace_size(B, Hq, Hkv, D), dtype=torch.uint8, device=DEV),
+          torch.zeros(pg.pa_decode_window_multi_workspace_size(B, B, Hq, Hkv, D), dtype=torch.uint8, device=DEV),
+          torch.zeros(pg.pa_decode_window_workspace_size(B, Hq, Hkv, D), dtype=torch.uint8, device=DEV)]
+    scale = D ** -0.5
+
+    def last(out):
+        pg.pa_decode_window(out, mid, kc_, vc_, bt_, ctx_, 200, 4, scale, workspace=ws[2])
+        return out
+
+    pg.pa_decode(mid, q_, kc_, vc_, bt_, ctx_, scale, workspace=ws[0])
+    torch.cuda.synchronize()
+    want = last(torch.empty_like(q_))
+    for _ in range(20):
+        mid.zero_()
+        pg.pa_decode(mid, q_, kc_, vc_, bt_, ctx_, scale, workspace=ws[0])
+        pg.pa_decode_window_multi(untouched, q_, kc_, vc_, bt_, cu_, ctx_, 200, 4, scale, workspace=ws[1])
+        got = last(torch.empty_like(q_))
+        torch.cuda.synchronize()
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+    assert bool((untouched == 3.0).all())
+
+
+def test_one_workspace_serves_every_operator_of_the_section():
+    """A buffer zeroed once serves the operators in any order, head shape and batch size."""
+    calls = []
+    for B, Hq, Hkv, D, n in [(2, 28, 4, 128, 900), (40, 16, 4, 64, 300), (150, 8, 2, 128, 65)]:
+        g, kc, vc, bt, perm, at = pool(B, [n] * B, Hkv, D, spoil=False)
+        q_, kc_, vc_, bt_, ctx_ = dev(bf16(g, B, Hq, D), kc, vc, bt, torch.full((B,), n, dtype=torch.int32))
+        cu_, cug_ = dev(torch.arange(B + 1, dtype=torch.int32), torch.tensor([0, B], dtype=torch.int32))
+        plen_ = torch.full((1,), n, dtype=torch.int32, device=DEV)
+        NB, MBS = kc.shape[0], bt.shape[1]
+        calls += [
+            (pg.pa_decode_window_workspace_size(B, Hq, Hkv, D),
+             lambda o, ws, q=q_, k=kc_, v=vc_, t=bt_, c=ctx_: pg.pa_decode_window(o, q, k, v, t, c, 64, 4, 0.1, workspace=ws), q_),
+            (pg.pa_decode_window_multi_workspace_size(B, B, Hq, Hkv, D),
+             lambda o, ws, q=q_, k=kc_, v=vc_, t=bt_, c=ctx_, u=cu_: pg.pa_decode_window_multi(
+                 o, q, k, v, t, u, c, 400, 4, 0.1, workspace=ws), q_),
+            (pg.pa_decode_prefix_workspace_size(B, 1, Hq, Hkv, D),
+             lambda o, ws, q=q_, k=kc_, v=vc_, t=bt_, c=ctx_, u=cug_, p=plen_: pg.pa_decode_prefix(
+                 o, q, k, v, t[:1].contiguous(), p, u, t, c, 0.1, workspace=ws), q_),
+            (pg.pa_decode_weights_workspace_size(B, Hq, Hkv, D, MBS),
+             lambda o, ws, q=q_, k=kc_, v=vc_, t=bt_, c=ctx_, s=(NB, Hkv, BS): pg.pa_decode_weights(
+                 o, torch.zeros(s, device=DEV), q, k, v, t, c, 0.1, workspace=ws), q_),
+        ]
+    alone = [f(torch.empty_like(q), torch.zeros(n, dtype=torch.uint8, device=DEV)) for n, f, q in calls]
+    shared = torch.zeros(max(n for n, _, _ in calls), dtype=torch.uint8, device=DEV)
+    order = torch.randperm(3 * len(calls), generator=torch.Generator().manual_seed(5)) % len(calls)
+    for i in order.tolist():
+        n, f, q = calls[i]
+        got = f(torch.empty_like(q), shared)
+        assert torch.equal(got.view(torch.int16), alone[i].view(torch.int16)), i
