@@ -1132,7 +1132,7 @@ int pa_reset_weights(float *weights, const int64_t *slot_mapping, int64_t num_to
     if (num_tokens < 0 || num_kv_heads <= 0 || block_size <= 0 || num_blocks <= 0) return PA_ERR_INVALID_ARG;
     if (num_tokens == 0) return PA_OK;
     if (!weights || !slot_mapping) return PA_ERR_INVALID_ARG;
-    if (block_size != kBlockSize || num_tokens > (int64_t(1) << 31) - 1 || num_kv_heads > 65535)
+    if (block_size != kBlockSize || num_kv_heads > 65535 || num_tokens > (int64_t(1) << 33) / num_kv_heads)
         return PA_ERR_UNSUPPORTED;
     const cudaError_t e = launch_reset_weights(weights, slot_mapping, num_tokens, num_kv_heads, num_blocks,
                                                static_cast<cudaStream_t>(stream));
@@ -1153,7 +1153,9 @@ int pa_evict(int32_t *kept, int32_t *new_lens, pa_bf16 *key_cache, pa_bf16 *valu
     if (int64_t(max_blocks_per_seq) * block_size > int64_t(1) << 30 || num_blocks > (int64_t(1) << 31) - 1)
         return PA_ERR_UNSUPPORTED;
     if (int64_t(max_dst_blocks) * block_size < budget) return PA_ERR_INVALID_ARG;  // no room for the kept tokens
-    if (int64_t(batch) * num_kv_heads * budget > int64_t(1) << 33) return PA_ERR_UNSUPPORTED;
+    if (budget > 1 << 30 || int64_t(batch) * num_kv_heads * budget > int64_t(1) << 33) return PA_ERR_UNSUPPORTED;
+    // the lengths are read by every (sequence, KV head), the new ones written by the first to get there
+    if (new_lens < context_lens + batch && context_lens < new_lens + batch) return PA_ERR_INVALID_ARG;
     if (!aligned16(key_cache) || !aligned16(value_cache) || !aligned16(weights)) return PA_ERR_INVALID_ARG;
     EvictArgs a{};
     a.kept = kept;

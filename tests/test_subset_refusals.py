@@ -8,7 +8,7 @@ import pytest
 import paged_gqa_decode_reshape_gb300 as pg
 import paged_gqa_decode_reshape_gb300.build as pgb
 
-P = ctypes.c_void_p(1 << 20)  # never dereferenced: the checks fail first
+P, P2 = ctypes.c_void_p(1 << 20), ctypes.c_void_p(1 << 21)  # never dereferenced: the checks fail first
 ODD = ctypes.c_void_p((1 << 20) + 2)
 INVALID, UNSUPPORTED = -1, -2
 
@@ -65,9 +65,11 @@ EVICT = "kept lens kc vc w bt MBS ctx dst DMBS B Hkv D BS NB budget recent st".s
     (dict(kc=ODD), INVALID), (dict(w=ODD), INVALID), (dict(B=0), INVALID), (dict(budget=0), INVALID),
     (dict(recent=-1), INVALID), (dict(budget=65), INVALID), (dict(D=80), UNSUPPORTED), (dict(BS=8), UNSUPPORTED),
     (dict(B=5000), UNSUPPORTED), (dict(Hkv=1 << 17), UNSUPPORTED), (dict(NB=1 << 33), UNSUPPORTED),
+    (dict(budget=(1 << 30) + 1, DMBS=1 << 27), UNSUPPORTED), (dict(B=4096, Hkv=4096, budget=1024, DMBS=64), UNSUPPORTED),
+    (dict(lens=P), INVALID), (dict(lens=ctypes.c_void_p((1 << 20) + 4)), INVALID),
 ])
 def test_evict_refusals(lib, over, status):
-    a = dict(kept=P, lens=P, kc=P, vc=P, w=P, bt=P, MBS=9, ctx=P, dst=P, DMBS=4, B=2, Hkv=4, D=128, BS=16, NB=64,
+    a = dict(kept=P, lens=P2, kc=P, vc=P, w=P, bt=P, MBS=9, ctx=P, dst=P, DMBS=4, B=2, Hkv=4, D=128, BS=16, NB=64,
              budget=64, recent=3, st=None)
     a.update(over)
     assert lib.pa_evict(*[a[k] for k in EVICT]) == status
@@ -79,6 +81,7 @@ def test_reset_weights_refusals(lib):
     assert lib.pa_reset_weights(P, None, 3, 4, 16, 8, None) == INVALID
     assert lib.pa_reset_weights(P, P, -1, 4, 16, 8, None) == INVALID
     assert lib.pa_reset_weights(P, P, 3, 4, 8, 8, None) == UNSUPPORTED
+    assert lib.pa_reset_weights(P, P, 1 << 32, 4, 16, 8, None) == UNSUPPORTED
 
 
 def test_workspace_sizes_of_bad_shapes_are_zero(lib):
