@@ -299,21 +299,40 @@ def quest_select_workspace_size(batch: int, num_kv_heads: int, max_blocks_per_se
     return int(load_library().quest_select_workspace_size(batch, num_kv_heads, max_blocks_per_seq))
 
 
+def _usual(key_cache, value_cache, query, out, block_tables, context_lens, cache_dtype) -> bool:
+    """Types, devices and contiguity of a decode call's tensors in one expression: what every correct call passes
+    (the one that is not goes through _need, which says what is wrong)."""
+    try:
+        d = key_cache.get_device()
+        return (d >= 0 and key_cache.dtype is cache_dtype and value_cache.dtype is cache_dtype
+                and query.dtype is torch.bfloat16 and out.dtype is torch.bfloat16
+                and block_tables.dtype is torch.int32 and context_lens.dtype is torch.int32
+                and key_cache.ndim == 4 and query.ndim == 3 and block_tables.ndim == 2 and context_lens.ndim == 1
+                and d == value_cache.get_device() == query.get_device() == out.get_device()
+                == block_tables.get_device() == context_lens.get_device()
+                and key_cache.is_contiguous() and value_cache.is_contiguous() and query.is_contiguous()
+                and out.is_contiguous() and block_tables.is_contiguous() and context_lens.is_contiguous())
+    except AttributeError:
+        return False
+
+
 def _attention_checks(out, query, key_cache, value_cache, block_tables, context_lens):
-    _need(key_cache, "key_cache", torch.bfloat16, 4)
-    dev = key_cache.device
-    _need(value_cache, "value_cache", torch.bfloat16, 4, dev)
-    _need(query, "query", torch.bfloat16, 3, dev)
-    _need(out, "out", torch.bfloat16, 3, dev)
-    _need(block_tables, "block_tables", torch.int32, 2, dev)
-    _need(context_lens, "context_lens", torch.int32, 1, dev)
+    if not _usual(key_cache, value_cache, query, out, block_tables, context_lens, torch.bfloat16):
+        _need(key_cache, "key_cache", torch.bfloat16, 4)
+        dev = key_cache.device
+        _need(value_cache, "value_cache", torch.bfloat16, 4, dev)
+        _need(query, "query", torch.bfloat16, 3, dev)
+        _need(out, "out", torch.bfloat16, 3, dev)
+        _need(block_tables, "block_tables", torch.int32, 2, dev)
+        _need(context_lens, "context_lens", torch.int32, 1, dev)
     B, Hq, D = query.shape
     NB, BS, Hkv, D2 = key_cache.shape
     if D != D2 or value_cache.shape != key_cache.shape or out.shape != query.shape:
         raise ValueError("shape mismatch between query/out and the caches")
-    if block_tables.shape[0] != B or context_lens.shape[0] != B:
+    BT, MBS = block_tables.shape
+    if BT != B or context_lens.shape[0] != B:
         raise ValueError("block_tables / context_lens batch mismatch")
-    return dev, B, Hq, Hkv, D, BS, NB, block_tables.shape[1]
+    return key_cache.device, B, Hq, Hkv, D, BS, NB, MBS
 
 
 def pa_decode(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
@@ -644,13 +663,15 @@ def quest_select_topk_fp8(selected: torch.Tensor, query: torch.Tensor, kmin: tor
 
 def _attention_checks_fp8(out, query, key_cache, value_cache, block_tables, context_lens,
                           k_scale, v_scale, per_block=False):
-    _need(key_cache, "key_cache", torch.uint8, 4)
+    if not _usual(key_cache, value_cache, query, out, block_tables, context_lens, torch.uint8):
+        _need(key_cache, "key_cache", torch.uint8, 4)
+        dev = key_cache.device
+        _need(value_cache, "value_cache", torch.uint8, 4, dev)
+        _need(query, "query", torch.bfloat16, 3, dev)
+        _need(out, "out", torch.bfloat16, 3, dev)
+        _need(block_tables, "block_tables", torch.int32, 2, dev)
+        _need(context_lens, "context_lens", torch.int32, 1, dev)
     dev = key_cache.device
-    _need(value_cache, "value_cache", torch.uint8, 4, dev)
-    _need(query, "query", torch.bfloat16, 3, dev)
-    _need(out, "out", torch.bfloat16, 3, dev)
-    _need(block_tables, "block_tables", torch.int32, 2, dev)
-    _need(context_lens, "context_lens", torch.int32, 1, dev)
     B, Hq, D = query.shape
     NB, BS, Hkv, D2 = key_cache.shape
     if D != D2 or value_cache.shape != (NB, Hkv, D, BS) or out.shape != query.shape:
@@ -1070,6 +1091,7 @@ class _Scratch(Workspace):
     def __init__(self):
         super().__init__()
         self._kept = []
+        self.at = {}  # (address, bytes) of the current buffer per device index
 
     def get(self, device: torch.device, nbytes: int) -> torch.Tensor:
         key = device.index if device.index is not None else torch.cuda.current_device()
@@ -1083,8 +1105,9 @@ class _Scratch(Workspace):
             self._kept.append(buf)
         # grown by half as much again, so that growing step by step keeps few buffers
         n = max(nbytes, 256, buf.numel() * 3 // 2 if buf is not None else 0)
-        self._buf[key] = torch.zeros(n, dtype=torch.uint8, device=device)
-        return self._buf[key]
+        buf = self._buf[key] = torch.zeros(n, dtype=torch.uint8, device=device)
+        self.at[key] = (buf.data_ptr(), n)
+        return buf
 
 
 _subset_ws = _Scratch()
@@ -1095,12 +1118,15 @@ def _tokens(n, name: str) -> int:
     n = int(n)
     if n < 0:
         raise ValueError(f"{name} must not be negative")
-    return min(n, 2 ** 31 - 1)
+    return n if n < 2 ** 31 else 2 ** 31 - 1
 
 
 def _scratch(workspace: Optional[torch.Tensor], dev: torch.device, nbytes: int):
     """(pointer, bytes) of the caller's workspace or of the binding's own."""
     if workspace is None:
+        at = _subset_ws.at.get(dev.index)
+        if at is not None and at[1] >= nbytes:
+            return at
         workspace = _subset_ws.get(dev, nbytes)
     else:
         if not isinstance(workspace, torch.Tensor):
@@ -1110,24 +1136,31 @@ def _scratch(workspace: Optional[torch.Tensor], dev: torch.device, nbytes: int):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-_sizes = {}  # workspace bytes per (query, device, shape): they depend on nothing else
+_calls = {}  # entry point and workspace bytes per (name, device, shape): they depend on nothing else
+
+
+def _lookup(key):
+    name, _, shape = key
+    L = load_library()
+    nbytes = None
+    if shape is not None:
+        size = name[:-len("_fp8_block")] if name.endswith("_fp8_block") else name.removesuffix("_fp8")
+        nbytes = getattr(L, size + "_workspace_size")(*shape)
+    found = _calls[key] = getattr(L, name), nbytes
+    return found
 
 
 def _run(name: str, dev: torch.device, args, workspace: Optional[torch.Tensor] = None, shape=None) -> None:
     """Call an entry point on dev's current stream; with a shape, its workspace (sized by
     <name>_workspace_size(*shape)) goes before the stream."""
-    if torch._C._cuda_getDevice() != dev.index:
+    index = dev.index
+    if torch._C._cuda_getDevice() != index:
         with torch.cuda.device(dev):
             return _run(name, dev, args, workspace, shape)
-    L = load_library()
-    if shape is not None:
-        key = (name, dev.index, shape)
-        nbytes = _sizes.get(key)
-        if nbytes is None:
-            size = name[:-len("_fp8_block")] if name.endswith("_fp8_block") else name.removesuffix("_fp8")
-            nbytes = _sizes[key] = getattr(L, size + "_workspace_size")(*shape)
-        args += _scratch(workspace, dev, nbytes)
-    status = getattr(L, name)(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    key = (name, index, shape)
+    fn, nbytes = _calls.get(key) or _lookup(key)
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    status = fn(*args, stream) if nbytes is None else fn(*args, *_scratch(workspace, dev, nbytes), stream)
     if status != PA_OK:
         raise PagedDecodeError(name, status)
 
@@ -1202,18 +1235,19 @@ def pa_decode_window_multi(out: torch.Tensor, query: torch.Tensor, key_cache: to
                            workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Windowed attention of several query rows per sequence: query / out [total_q, Hq, D], rows of sequence b
     cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1, right-aligned causal masks."""
-    _need(key_cache, "key_cache", torch.bfloat16, 4)
+    if not _usual(key_cache, value_cache, query, out, block_tables, context_lens, torch.bfloat16):
+        _need(key_cache, "key_cache", torch.bfloat16, 4)
+        _need(value_cache, "value_cache", torch.bfloat16, 4, key_cache.device)
+        _need(query, "query", torch.bfloat16, 3, key_cache.device)
+        _need(out, "out", torch.bfloat16, 3, key_cache.device)
+        _need(block_tables, "block_tables", torch.int32, 2, key_cache.device)
+        _need(context_lens, "context_lens", torch.int32, 1, key_cache.device)
     dev = key_cache.device
-    _need(value_cache, "value_cache", torch.bfloat16, 4, dev)
-    _need(query, "query", torch.bfloat16, 3, dev)
-    _need(out, "out", torch.bfloat16, 3, dev)
+    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1, dev)
     T, Hq, D = query.shape
     NB, BS, Hkv, D2 = key_cache.shape
     if D != D2 or value_cache.shape != key_cache.shape or out.shape != query.shape:
         raise ValueError("shape mismatch between query/out and the caches")
-    _need(block_tables, "block_tables", torch.int32, 2, dev)
-    _need(context_lens, "context_lens", torch.int32, 1, dev)
-    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1, dev)
     B, MBS = block_tables.shape
     if context_lens.shape[0] != B or cu_seqlens_q.shape[0] != B + 1:
         raise ValueError("block_tables / context_lens / cu_seqlens_q batch mismatch")
