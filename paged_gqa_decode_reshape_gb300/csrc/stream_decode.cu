@@ -47,6 +47,7 @@ namespace {
 
 constexpr int kPreCap = 512;   // entries of the items-per-sequence prefix in shared memory
 constexpr int kEndCost = 2;    // items that the end of a segment costs a warp
+constexpr int kFusedAddBlocks = 1024;
 constexpr int kMinPiece = 12;  // items of a CTA's piece at least, where there are as many
 
 #ifndef PA_STREAM_WARPS_F8
@@ -78,7 +79,8 @@ struct StreamCfg {
     static constexpr size_t off_scr = off_bars + size_t(NW) * R * 8;
     static constexpr size_t off_ml = off_scr + size_t(NW) * SCR * 4;
     static constexpr size_t off_flag = off_ml + size_t(NW) * 16 * 4;
-    static constexpr size_t off_pre = off_flag + 16;
+    static constexpr size_t off_lse = off_flag + 16;
+    static constexpr size_t off_pre = off_lse + kMaxGroup * 4;
     static constexpr size_t SMEM = 1024 + off_pre + (kPreCap + 1) * 8;
 };
 
@@ -106,6 +108,59 @@ __device__ __forceinline__ uint32_t bits_between(int a, int b, int t0) {
     return y > x ? ((1u << y) - 1u) & ~((1u << x) - 1u) : 0u;
 }
 
+// Accumulated weights: p_t = 2^(z_t - lse) summed over the group, added to the
+// cache's weights for the tokens t < lim of one segment; ls: the heads' lse
+// (infinite: no head). Four tokens of a block per turn, their logits of every
+// head in flight (they come from L2, mostly), U turns at a time.
+constexpr int kAddThreads = 256;
+
+template <int U>
+__device__ __forceinline__ void add_weights(const SubsetArgs &a, int b, int kvh, int lim, const float (&ls)[kMaxGroup],
+                                            int i0, int step) {
+    constexpr int QB = kBlockSize / 4;  // turns per block
+    const int nq = (lim + 3) / 4;
+    const int32_t *bt = a.bt + int64_t(b) * a.MBS;
+    const float *seg = a.logits + (int64_t(b) * a.Hkv + kvh) * a.MBS * (a.G * kBlockSize);
+    for (; i0 < nq; i0 += U * step) {
+        int phys[U];
+        float4 z[U][kMaxGroup];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = min(i0 + u * step, nq - 1), j = i / QB;
+            phys[u] = __ldg(bt + j);
+            const float *p = seg + int64_t(j) * (a.G * kBlockSize) + 4 * (i % QB);
+#pragma unroll
+            for (int h = 0; h < kMaxGroup; ++h)
+                z[u][h] = h < a.G ? __ldcg(reinterpret_cast<const float4 *>(p + h * kBlockSize))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * step;
+            if (i >= nq || phys[u] < 0 || int64_t(phys[u]) >= a.NB) continue;
+            float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int h = 0; h < kMaxGroup; ++h) {  // 0 for h >= G, and for unseen tokens (logit -inf)
+                w.x += fast_exp2(z[u][h].x - ls[h]);
+                w.y += fast_exp2(z[u][h].y - ls[h]);
+                w.z += fast_exp2(z[u][h].z - ls[h]);
+                w.w += fast_exp2(z[u][h].w - ls[h]);
+            }
+            // tokens past the context get nothing (their weights may hold anything); a block of one sequence
+            // gets one addition: the same bits every time
+            float *dst = a.weights + (int64_t(phys[u]) * a.Hkv + kvh) * kBlockSize + 4 * (i % QB);
+            const int left = lim - 4 * i;
+            if (left >= 4) {
+                atomicAdd(reinterpret_cast<float4 *>(dst), w);
+            } else {
+                atomicAdd(dst, w.x);
+                if (left > 1) atomicAdd(dst + 1, w.y);
+                if (left > 2) atomicAdd(dst + 2, w.z);
+            }
+        }
+    }
+}
+
 template <int D, CacheKind KIND, bool LOGITS>
 __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
     stream_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -122,6 +177,7 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
     float *scr = reinterpret_cast<float *>(bp + C::off_scr);
     float *sm_ml = reinterpret_cast<float *>(bp + C::off_ml);  // [NW][16]: m[8], l[8]
     volatile int *flag = reinterpret_cast<volatile int *>(bp + C::off_flag);
+    float *sm_lse = reinterpret_cast<float *>(bp + C::off_lse);
     int64_t *pre = reinterpret_cast<int64_t *>(bp + C::off_pre);
     const uint32_t ring = base + uint32_t(warp) * C::RING;
     const uint32_t bars = base + uint32_t(C::off_bars) + uint32_t(warp) * R * 8;
@@ -561,7 +617,11 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
         *reinterpret_cast<uint2 *>(a.out + row * D + d) =
             make_uint2(pack_bf16x2(O.x * inv, O.y * inv), pack_bf16x2(O.z * inv, O.w * inv));
         // a row without tokens: every weight 2^(z - inf) = 0 (it has none)
-        if (LOGITS && d == 0) a.lse[row] = Ls == 0.f ? INFINITY : M + log2f(Ls);
+        if (LOGITS && d == 0) {
+            const float lse = Ls == 0.f ? INFINITY : M + log2f(Ls);
+            if (a.fused_add) sm_lse[h] = lse;
+            else a.lse[row] = lse;
+        }
     };
 
     auto wait_item = [&](int k) {
@@ -697,6 +757,14 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
                 if (tid == 0) a.counters[w0] = 0;
             }
         }
+        if (LOGITS && a.fused_add && (npieces == 1 || *flag)) {
+            // the CTA that has the rows has their normalisers; every logit of the segment is published
+            __syncthreads();
+            float ls[kMaxGroup];
+#pragma unroll
+            for (int h = 0; h < kMaxGroup; ++h) ls[h] = h < G ? sm_lse[h] : INFINITY;
+            add_weights<2>(a, b, kvh, sp.lim, ls, tid, C::THREADS);
+        }
     } else {
         // ---- the segments of this warp's range
         int64_t rem;
@@ -798,49 +866,16 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
     if (a.ownres && blockIdx.x == 0) pdl_wait();
 }
 
-// ---- accumulated weights: p_t = 2^(z_t - lse) summed over the group, added
-// to the cache's weights. A thread per four tokens of a block, the logits of
-// every head in flight; the logits come from L2, mostly.
-constexpr int kAddThreads = 256;
-
+// Segments longer than the fused addition is for: a thread per four tokens over the whole grid.
 __global__ void __launch_bounds__(kAddThreads) weights_add_kernel(const SubsetArgs a) {
     pdl_trigger();
-    constexpr int QB = kBlockSize / 4;  // threads per block
     const int seg = blockIdx.x, b = seg / a.Hkv, kvh = seg % a.Hkv;
     const int lim = min(max(__ldg(a.ctx + b), 0), a.MBS * kBlockSize);
-    const int t0 = 4 * (threadIdx.x % QB);
     pdl_wait();
     float ls[kMaxGroup];
 #pragma unroll
     for (int h = 0; h < kMaxGroup; ++h) ls[h] = h < a.G ? __ldcg(a.lse + int64_t(b) * a.Hq + kvh * a.G + h) : INFINITY;
-    for (int j = blockIdx.y * (kAddThreads / QB) + threadIdx.x / QB; j * kBlockSize + t0 < lim;
-         j += gridDim.y * (kAddThreads / QB)) {
-        const int phys = __ldg(a.bt + int64_t(b) * a.MBS + j);
-        const float *z = a.logits + (int64_t(seg) * a.MBS + j) * (a.G * kBlockSize) + t0;
-        float4 zz[kMaxGroup], w = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int h = 0; h < kMaxGroup; ++h)
-            zz[h] = h < a.G ? __ldcg(reinterpret_cast<const float4 *>(z + h * kBlockSize)) : w;
-        if (phys < 0 || int64_t(phys) >= a.NB) continue;
-#pragma unroll
-        for (int h = 0; h < kMaxGroup; ++h) {  // 0 for h >= G, and for unseen tokens (logit -inf)
-            w.x += fast_exp2(zz[h].x - ls[h]);
-            w.y += fast_exp2(zz[h].y - ls[h]);
-            w.z += fast_exp2(zz[h].z - ls[h]);
-            w.w += fast_exp2(zz[h].w - ls[h]);
-        }
-        // tokens past the context get nothing (their weights may hold anything); a block of one sequence
-        // gets one addition: the same bits every time
-        float *dst = a.weights + (int64_t(phys) * a.Hkv + kvh) * kBlockSize + t0;
-        const int left = lim - (j * kBlockSize + t0);
-        if (left >= 4) {
-            atomicAdd(reinterpret_cast<float4 *>(dst), w);
-        } else {
-            atomicAdd(dst, w.x);
-            if (left > 1) atomicAdd(dst + 1, w.y);
-            if (left > 2) atomicAdd(dst + 2, w.z);
-        }
-    }
+    add_weights<1>(a, b, kvh, lim, ls, blockIdx.y * kAddThreads + threadIdx.x, gridDim.y * kAddThreads);
 }
 
 template <int D, CacheKind KIND, bool LOGITS>
@@ -930,9 +965,11 @@ cudaError_t launch_prefix_join(const SubsetArgs &a, int head_dim, cudaStream_t s
 cudaError_t launch_stream_decode(const CUtensorMap &tk, const CUtensorMap &tv, const SubsetArgs &a, int head_dim,
                                  CacheKind kind, int sms, cudaStream_t stream) {
     if (a.weights) {
-        cudaError_t e = head_dim == 128 ? launch_t<128, kCacheBf16, true>(tk, tv, a, sms, stream)
-                                        : launch_t<64, kCacheBf16, true>(tk, tv, a, sms, stream);
-        if (e != cudaSuccess) return e;
+        SubsetArgs f = a;
+        f.fused_add = int64_t(a.nseq) * a.Hkv <= sms && a.MBS <= kFusedAddBlocks;
+        cudaError_t e = head_dim == 128 ? launch_t<128, kCacheBf16, true>(tk, tv, f, sms, stream)
+                                        : launch_t<64, kCacheBf16, true>(tk, tv, f, sms, stream);
+        if (e != cudaSuccess || f.fused_add) return e;
         const int per = kAddThreads / (kBlockSize / 4);  // blocks a CTA takes per turn
         const int x = (a.MBS + per - 1) / per;
         return launch_pdl(weights_add_kernel, dim3(a.nseq * a.Hkv, x < 16 ? x : 16), dim3(kAddThreads), 0, stream, a);

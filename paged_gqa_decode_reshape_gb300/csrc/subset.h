@@ -46,6 +46,7 @@ struct SubsetArgs {
     float *lse;                   // weights: [nseq][Hq] log2 of the normaliser
     float *logits;                // weights: [nseq][Hkv][MBS][G][16] logits (log2 domain)
     uint64_t wait_ns;             // limit of every bounded wait
+    bool fused_add;               // weights: added by the streaming kernel itself
     int stop_item;                // failure tests: a warp's copies stop at this item (else INT_MAX)
     int min_items;                // row tiles: tiles of a CTA's range at least
 };
