@@ -1173,7 +1173,9 @@ int pa_evict(int32_t *kept, int32_t *new_lens, pa_bf16 *key_cache, pa_bf16 *valu
     a.Hkv = num_kv_heads;
     a.budget = budget;
     a.recent = recent;
-    const cudaError_t e = launch_evict(a, head_dim, static_cast<cudaStream_t>(stream));
+    DecodeGeometry geo;
+    cudaError_t e = decode_geometry(head_dim, &geo);
+    if (e == cudaSuccess) e = launch_evict(a, head_dim, geo.grid, static_cast<cudaStream_t>(stream));  // one CTA per SM
     return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 

@@ -15,6 +15,13 @@ namespace pa {
 namespace {
 
 constexpr int kSelThreads = 1024, kHistCopies = 8;
+// From this many SMs per (sequence, KV head) on, one launch in which every CTA
+// selects and copies a share; below, a CTA selects for all and a second launch
+// copies. One sequence of 1500 tokens, 1024 kept: 9.4 us in one launch, 10.0 in two
+// (and 2 us of the host); 9 of 2000, 512 kept: 11.4 and 13.0; 9 of 8192, 4096
+// kept: 42.3 and 42.0; 16 of those, two CTAs each: 68.1 and 63.5 (4 KV heads of
+// 128: the copy wants more warps than two CTAs of 1024 threads per head have).
+constexpr int kMinParts = 4;
 constexpr int kKeysCap = 48 * 1024;  // keys held in shared memory; longer rows read them again
 
 // The k-th largest of n keys (n > k >= 1), key_of(j) in totalOrder: thr, and keq,
@@ -136,24 +143,22 @@ __device__ __forceinline__ void emit_selected(KeyOf key_of, int n, uint32_t thr,
     }
 }
 
-// one CTA per (sequence, KV head): the kept positions
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a, int cap) {
+// The kept positions of segment (b, kvh) with ranks r0 <= r < r1, by a whole CTA.
+__device__ __forceinline__ void select_kept(const EvictArgs &a, int b, int kvh, int cap, int r0, int r1) {
     extern __shared__ __align__(16) uint32_t keys[];
     __shared__ int hist[kHistCopies * 256];
     __shared__ int red[2 * kSelThreads / 32 + 3];
-    const int b = blockIdx.x / a.Hkv, kvh = blockIdx.x % a.Hkv, tid = threadIdx.x;
-    pdl_trigger();  // the copy waits for this kernel's end before it reads anything
-    pdl_wait();
+    const int tid = threadIdx.x;
     const int ctx = min(max(__ldg(a.ctx + b), 0), a.MBS * kBlockSize);
-    int32_t *kept = a.kept + int64_t(blockIdx.x) * a.budget;
-    if (kvh == 0 && tid == 0) a.new_lens[b] = min(ctx, a.budget);
+    int32_t *kept = a.kept + (int64_t(b) * a.Hkv + kvh) * a.budget;
+    if (kvh == 0 && r0 == 0 && tid == 0) a.new_lens[b] = min(ctx, a.budget);
     if (ctx <= a.budget) {
-        for (int i = tid; i < a.budget; i += kSelThreads) kept[i] = i < ctx ? i : -1;
+        for (int i = r0 + tid; i < r1; i += kSelThreads) kept[i] = i < ctx ? i : -1;
         return;
     }
     const int recent = min(a.recent, a.budget), n = ctx - recent, top = a.budget - recent;
-    for (int i = tid; i < recent; i += kSelThreads) kept[top + i] = n + i;
-    if (top == 0) return;
+    for (int i = max(r0 - top, 0) + tid; top + i < r1; i += kSelThreads) kept[top + i] = n + i;
+    if (top <= r0) return;
     const int32_t *bt = a.bt + int64_t(b) * a.MBS;
     auto load = [&](int j) -> uint32_t {
         const int phys = __ldg(bt + j / kBlockSize);
@@ -197,32 +202,34 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     uint32_t thr;
     int keq;
     kth_largest(key_of, n, top, hist, red, thr, keq);
-    emit_selected(key_of, n, thr, keq, red, [&](int r, int j) { kept[r] = j; });
+    emit_selected(key_of, n, thr, keq, red, [&](int r, int j) {
+        if (r >= r0 && r < r1) kept[r] = j;
+    });
 }
 
-// The copy: a warp per 8 kept tokens of a (sequence, KV head) at D = 128, 16 at
-// D = 64. Bound by HBM: every kept row is read and written once (263 MB in 47 us,
-// 5.6 TB/s, at 16 sequences of 4096 kept tokens; warps of 32 tokens, with fewer
-// CTAs to spread over the SMs, took 2 us longer). A lane finds one token's rows;
-// then the warp moves them with K and V side by side (16 lanes of 16 bytes each,
-// or 8 and two tokens), kMove loads per lane in flight.
-// No early launch of the next kernel: it may read new_lens before it waits.
+// one CTA per segment: the kept positions
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a, int cap) {
+    pdl_trigger();  // the copy waits for this kernel's end before it reads anything
+    pdl_wait();
+    select_kept(a, blockIdx.x / a.Hkv, blockIdx.x % a.Hkv, cap, 0, a.budget);
+}
+
+// The copy, by a warp: kept tokens i0 .. i0 + CHUNK - 1 (below end) of segment
+// (b, kvh). A lane finds one token's rows; then the warp moves them with K and V
+// side by side (16 lanes of 16 bytes each, or 8 and two tokens), kMove loads per
+// lane in flight.
 constexpr int kMove = 8;
+template <int D>
+constexpr int kMoveChunk = kMove * 16 / (D / 8);  // tokens per warp and turn
 
 template <int D>
-__global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
+__device__ __forceinline__ void move_kept(const EvictArgs &a, int b, int kvh, int i0, int end) {
     constexpr int LR = D / 8;          // lanes per row
     constexpr int TP = 32 / (2 * LR);  // tokens at once
-    constexpr int CHUNK = kMove * TP;  // tokens per warp
-    pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int per = (a.budget + CHUNK - 1) / CHUNK;  // warps per (sequence, KV head)
-    const int64_t warp = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int64_t seg = warp / per;
-    if (seg >= int64_t(a.B) * a.Hkv) return;
-    const int i0 = int(warp - seg * per) * CHUNK, kvh = int(seg % a.Hkv), b = int(seg / a.Hkv);
-    const int i = i0 + lane;
-    const int j = lane < CHUNK && i < a.budget ? __ldcg(a.kept + seg * a.budget + i) : -1;
+    constexpr int CHUNK = kMove * TP;
+    static_assert(CHUNK == kMoveChunk<D>, "");
+    const int lane = threadIdx.x & 31, i = i0 + lane;
+    const int j = lane < CHUNK && i < end ? __ldcg(a.kept + (int64_t(b) * a.Hkv + kvh) * a.budget + i) : -1;
     // this lane's token: its row in the cache, before and after; -1: not copied
     int64_t from = -1, to = -1;
     if (j >= 0) {
@@ -252,6 +259,35 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
         if (y[u] >= 0) __stcs(cache + y[u] * LR, v[u]);
 }
 
+// Many segments: a warp per chunk. Bound by HBM: every kept row is read and
+// written once (263 MB in 47 us, 5.6 TB/s, at 16 sequences of 4096 kept tokens;
+// warps of 32 tokens, with fewer CTAs to spread over the SMs, took 2 us longer).
+// No early launch of the next kernel: it may read new_lens before it waits.
+template <int D>
+__global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
+    pdl_wait();
+    const int per = (a.budget + kMoveChunk<D> - 1) / kMoveChunk<D>;  // warps per segment
+    const int64_t warp = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t seg = warp / per;
+    if (seg >= int64_t(a.B) * a.Hkv) return;
+    move_kept<D>(a, int(seg / a.Hkv), int(seg % a.Hkv), int(warp - seg * per) * kMoveChunk<D>, a.budget);
+}
+
+// Few segments: `parts` CTAs per segment, each of which selects (the same, all of
+// them at once) and copies its share of the kept tokens.
+template <int D>
+__global__ void __launch_bounds__(kSelThreads) evict_parts_kernel(const EvictArgs a, int cap, int parts) {
+    pdl_wait();
+    const int seg = blockIdx.x / parts, part = blockIdx.x % parts, b = seg / a.Hkv, kvh = seg % a.Hkv;
+    const int share = ((a.budget + parts - 1) / parts + kMoveChunk<D> - 1) / kMoveChunk<D> * kMoveChunk<D>;
+    const int r0 = int(min(int64_t(part) * share, int64_t(a.budget))), r1 = min(r0 + share, a.budget);
+    if (r0 >= r1) return;  // fewer chunks than parts (part 0 has some: it writes the length)
+    select_kept(a, b, kvh, cap, r0, r1);
+    __syncthreads();
+    for (int i = r0 + int(threadIdx.x >> 5) * kMoveChunk<D>; i < r1; i += kSelThreads / 32 * kMoveChunk<D>)
+        move_kept<D>(a, b, kvh, i, r1);
+}
+
 __global__ void __launch_bounds__(256) reset_weights_kernel(float *weights, const int64_t *slots, int64_t T, int Hkv,
                                                             int64_t NB) {
     pdl_wait();
@@ -264,16 +300,24 @@ __global__ void __launch_bounds__(256) reset_weights_kernel(float *weights, cons
 
 }  // namespace
 
-cudaError_t launch_evict(const EvictArgs &a, int head_dim, cudaStream_t stream) {
+cudaError_t launch_evict(const EvictArgs &a, int head_dim, int sms, cudaStream_t stream) {
     const int64_t longest = int64_t(a.MBS) * kBlockSize;  // a multiple of four
     const int cap = longest < kKeysCap ? int(longest) : kKeysCap;
     const size_t smem = size_t(cap) * 4;
+    const int64_t segs = int64_t(a.B) * a.Hkv;
+    if (segs * kMinParts <= sms) {
+        const auto kernel = head_dim == 128 ? evict_parts_kernel<128> : evict_parts_kernel<64>;
+        const cudaError_t e = smem_once(reinterpret_cast<const void *>(kernel), size_t(kKeysCap) * 4);
+        if (e != cudaSuccess) return e;
+        const int parts = int(sms / segs);
+        return launch_pdl(kernel, dim3(unsigned(segs * parts)), dim3(kSelThreads), smem, stream, a, cap, parts);
+    }
     cudaError_t e = smem_once(reinterpret_cast<const void *>(evict_select_kernel), size_t(kKeysCap) * 4);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(evict_select_kernel, dim3(a.B * a.Hkv), dim3(kSelThreads), smem, stream, a, cap);
+    e = launch_pdl(evict_select_kernel, dim3(unsigned(segs)), dim3(kSelThreads), smem, stream, a, cap);
     if (e != cudaSuccess) return e;
-    const int chunk = head_dim == 128 ? kMove : 2 * kMove;  // kept tokens per warp
-    const int64_t warps = int64_t(a.B) * a.Hkv * ((a.budget + chunk - 1) / chunk);
+    const int chunk = head_dim == 128 ? kMoveChunk<128> : kMoveChunk<64>;  // kept tokens per warp
+    const int64_t warps = segs * ((a.budget + chunk - 1) / chunk);
     const dim3 grid(unsigned((warps + 7) / 8));
     return head_dim == 128 ? launch_pdl(evict_move_kernel<128>, grid, dim3(256), 0, stream, a)
                            : launch_pdl(evict_move_kernel<64>, grid, dim3(256), 0, stream, a);

@@ -47,8 +47,19 @@ namespace {
 
 constexpr int kPreCap = 512;   // entries of the items-per-sequence prefix in shared memory
 constexpr int kEndCost = 2;    // items that the end of a segment costs a warp
-constexpr int kFusedAddBlocks = 1024;
-constexpr int kMinPiece = 12;  // items of a CTA's piece at least, where there are as many
+// Items of a CTA's piece at least, where there are as many; while no segment has
+// more than twice that, all stay whole. A cut costs about 1.7 us at the end, an item less per warp
+// saves 0.85 us: 16 sequences of 500 tokens take 8.0 us in two pieces each, 6.3
+// whole; one of 2048 tokens 7.3 us in pieces of 12 items, 9.1 in pieces of 24; one
+// of 8192 tokens 9.4 us, in pieces of 6 or 24 10.3 (28 / 4 heads of 128).
+constexpr int kMinPiece = 12;
+// Accumulated weights, one piece per CTA: the CTA that has a segment's rows adds
+// its weights while the table has at most this many blocks per segment of the
+// call; longer ones are added by a launch of their own over the whole grid. One
+// CTA's addition takes 0.75 us per 1024 tokens, the launch 3 us or more and 1.6 us
+// of the host: one sequence of 2048 tokens 9.7 us fused, 10.1 separate; of 8192
+// tokens 15.5 and 13.0; 16 sequences of 8192 tokens 51.6 and 52.9.
+constexpr int kFusedAddBlocks = 64;
 
 #ifndef PA_STREAM_WARPS_F8
 #define PA_STREAM_WARPS_F8 10
@@ -106,6 +117,46 @@ __device__ __forceinline__ Span span_of(const SubsetArgs &a, int b) {
 __device__ __forceinline__ uint32_t bits_between(int a, int b, int t0) {
     const int x = min(max(a - t0, 0), 16), y = min(max(b - t0, 0), 16);
     return y > x ? ((1u << y) - 1u) & ~((1u << x) - 1u) : 0u;
+}
+
+// (M, Ls, O) += another part
+__device__ __forceinline__ void fold(float &M, float &Ls, float4 &O, float m, float l, float4 v) {
+    const float Mn = fmaxf(M, m);
+    const float f = M == -INFINITY ? 0.f : fast_exp2(M - Mn), w = m == -INFINITY ? 0.f : fast_exp2(m - Mn);
+    M = Mn;
+    Ls = Ls * f + l * w;
+    O = make_float4(O.x * f + v.x * w, O.y * f + v.y * w, O.z * f + v.z * w, O.w * f + v.w * w);
+}
+
+// The pieces i0, i0 + by, ... < n of a segment, piece i at slot_of(i), merged by a
+// warp: every head's values of two pieces in flight. A lane has the (head,
+// four dims) numbers lane + 32 t.
+template <int D, typename SlotOf>
+__device__ __forceinline__ void merge_pieces(SlotOf slot_of, int G, int i0, int n, int by, float (&M)[D / 16],
+                                             float (&Ls)[D / 16], float4 (&O)[D / 16]) {
+    constexpr int NT = D / 16;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        M[t] = -INFINITY;
+        Ls[t] = 0.f;
+        O[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll 2
+    for (int i = i0; i < n; i += by) {
+        const float *ps = slot_of(i);
+        float m[NT], l[NT];
+        float4 v[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int idx = lane + 32 * t, h = min(idx / (D / 4), G - 1);
+            m[t] = __ldcg(ps + 8 * D + h);
+            l[t] = __ldcg(ps + 8 * D + 8 + h);
+            v[t] = __ldcg(reinterpret_cast<const float4 *>(ps + h * D) + idx % (D / 4));
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) fold(M[t], Ls[t], O[t], m[t], l[t], v[t]);
+    }
 }
 
 // Accumulated weights: p_t = 2^(z_t - lse) summed over the group, added to the
@@ -215,7 +266,8 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
             nmax = max(nmax, __shfl_xor_sync(0xffffffffu, nmax, o));
         }
         // smallest piece size for which Hkv * sum ceil(n / size) <= CTAs, by NW warps at a time
-        int lo = int(min(max((sum * Hkv + gridDim.x - 1) / gridDim.x, int64_t(kMinPiece)), int64_t(nmax)));
+        int lo = nmax > 2 * kMinPiece ? int(min(max((sum * Hkv + gridDim.x - 1) / gridDim.x, int64_t(kMinPiece)), int64_t(nmax)))
+                                      : nmax;
         int hi = nmax;  // always fits: one piece per segment
         while (lo < hi) {
             const int at = min(lo + int((int64_t(hi) - lo) * warp / NW), hi);
@@ -690,14 +742,6 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
             sm_ml[warp * 16 + 8 + 2 * q4 + 1] = l1;
         }
     };
-    // (M, Ls, O) += another part
-    auto fold = [](float &M, float &Ls, float4 &O, float m, float l, float4 v) {
-        const float Mn = fmaxf(M, m);
-        const float f = M == -INFINITY ? 0.f : fast_exp2(M - Mn), w = m == -INFINITY ? 0.f : fast_exp2(m - Mn);
-        M = Mn;
-        Ls = Ls * f + l * w;
-        O = make_float4(O.x * f + v.x * w, O.y * f + v.y * w, O.z * f + v.z * w, O.w * f + v.w * w);
-    };
     auto put_piece = [&](float *ps, int h, int d, float M, float Ls, float4 O) {
         __stcg(reinterpret_cast<float4 *>(ps + h * D + d), O);
         if (d == 0) {
@@ -705,26 +749,7 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
             __stcg(ps + 8 * D + 8 + h, Ls);
         }
     };
-    // merge n pieces, piece i at slot_of(i), for head h, dims d .. d + 3; four pieces' loads in flight
-    auto merge_pieces = [&](auto slot_of, int n, int sb, int sh, int h, int d) {
-        float M = -INFINITY, Ls = 0.f;
-        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i0 = 0; i0 < n; i0 += 4) {
-            float m[4], l[4];
-            float4 v[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const float *ps = slot_of(min(i0 + u, n - 1));
-                m[u] = __ldcg(ps + 8 * D + h);
-                l[u] = __ldcg(ps + 8 * D + 8 + h);
-                v[u] = __ldcg(reinterpret_cast<const float4 *>(ps + h * D + d));
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (i0 + u < n) fold(M, Ls, O, m[u], l[u], v[u]);
-        }
-        emit(sb, sh, h, d, M, Ls, O);
-    };
+    constexpr int NT = D / 16;  // (head, four dims) per lane of a warp
     const int tasks = G * (D / 4);
 
     if (one) {
@@ -734,26 +759,43 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
         stream(kn, b, kvh);
         deposit();
         __syncthreads();
+        // the warps' states joined: the row, or this CTA's piece of it
         float *slot = a.part + int64_t(blockIdx.x) * C::PART;
-        for (int idx = tid; idx < tasks; idx += C::THREADS) {
-            const int h = idx / (D / 4), d = 4 * (idx % (D / 4));
-            float M = -INFINITY, Ls = 0.f;
-            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto join_warps = [&](bool row) {
+            for (int idx = tid; idx < tasks; idx += C::THREADS) {
+                const int h = idx / (D / 4), d = 4 * (idx % (D / 4));
+                float M = -INFINITY, Ls = 0.f;
+                float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < NW; ++w)
-                fold(M, Ls, O, sm_ml[w * 16 + h], sm_ml[w * 16 + 8 + h],
-                     *reinterpret_cast<const float4 *>(scr + w * C::SCR + h * C::ROW + d));
-            if (npieces == 1) emit(b, kvh, h, d, M, Ls, O);
-            else put_piece(slot, h, d, M, Ls, O);
-        }
+                for (int w = 0; w < NW; ++w)
+                    fold(M, Ls, O, sm_ml[w * 16 + h], sm_ml[w * 16 + 8 + h],
+                         *reinterpret_cast<const float4 *>(scr + w * C::SCR + h * C::ROW + d));
+                if (row) emit(b, kvh, h, d, M, Ls, O);
+                else put_piece(slot, h, d, M, Ls, O);
+            }
+        };
+        join_warps(npieces == 1);
         if (npieces > 1) {
             __syncthreads();  // the CTA's piece, published by the release below
             if (tid == 0) *flag = atomic_add_acq_rel_gpu(a.counters + w0, 1) == npieces - 1;
             __syncthreads();
             if (*flag) {
-                for (int idx = tid; idx < tasks; idx += C::THREADS)
-                    merge_pieces([&](int i) { return a.part + int64_t(w0 + i) * C::PART; }, npieces, b, kvh,
-                                 idx / (D / 4), 4 * (idx % (D / 4)));
+                // every warp takes each NW-th piece, so that many pieces cost few rounds of loads
+                float M[NT], Ls[NT];
+                float4 O[NT];
+                merge_pieces<D>([&](int i) { return a.part + int64_t(w0 + i) * C::PART; }, G, warp, npieces, NW, M, Ls, O);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const int idx = lane + 32 * t, h = idx / (D / 4), d = 4 * (idx % (D / 4));
+                    if (idx >= tasks) continue;
+                    *reinterpret_cast<float4 *>(scr + warp * C::SCR + h * C::ROW + d) = O[t];
+                    if (d == 0) {
+                        sm_ml[warp * 16 + h] = M[t];
+                        sm_ml[warp * 16 + 8 + h] = Ls[t];
+                    }
+                }
+                __syncthreads();
+                join_warps(true);
                 if (tid == 0) a.counters[w0] = 0;
             }
         }
@@ -812,31 +854,9 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
                     done = __shfl_sync(0xffffffffu, done, 0);
                     __syncwarp();  // every lane's reads of the pieces follow lane 0's acquire
                     if (done) {
-                        // the whole segment at once: every head's values of two pieces in flight
-                        constexpr int NT = 8 * (D / 4) / 32;  // (head, four dims) per lane
                         float M[NT], Ls[NT];
                         float4 O[NT];
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            M[t] = -INFINITY;
-                            Ls[t] = 0.f;
-                            O[t] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        }
-#pragma unroll 2
-                        for (int i = 0; i < n; ++i) {
-                            const float *ps = slot_of(i);
-                            float m[NT], l[NT];
-                            float4 v[NT];
-#pragma unroll
-                            for (int t = 0; t < NT; ++t) {
-                                const int idx = lane + 32 * t, h = min(idx / (D / 4), G - 1);
-                                m[t] = __ldcg(ps + 8 * D + h);
-                                l[t] = __ldcg(ps + 8 * D + 8 + h);
-                                v[t] = __ldcg(reinterpret_cast<const float4 *>(ps + h * D) + idx % (D / 4));
-                            }
-#pragma unroll
-                            for (int t = 0; t < NT; ++t) fold(M[t], Ls[t], O[t], m[t], l[t], v[t]);
-                        }
+                        merge_pieces<D>(slot_of, G, 0, n, 1, M, Ls, O);
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
                             const int idx = lane + 32 * t;
@@ -966,7 +986,7 @@ cudaError_t launch_stream_decode(const CUtensorMap &tk, const CUtensorMap &tv, c
                                  CacheKind kind, int sms, cudaStream_t stream) {
     if (a.weights) {
         SubsetArgs f = a;
-        f.fused_add = int64_t(a.nseq) * a.Hkv <= sms && a.MBS <= kFusedAddBlocks;
+        f.fused_add = int64_t(a.nseq) * a.Hkv <= sms && a.MBS <= kFusedAddBlocks * a.nseq * a.Hkv;
         cudaError_t e = head_dim == 128 ? launch_t<128, kCacheBf16, true>(tk, tv, f, sms, stream)
                                         : launch_t<64, kCacheBf16, true>(tk, tv, f, sms, stream);
         if (e != cudaSuccess || f.fused_add) return e;

@@ -93,7 +93,7 @@ struct EvictArgs {
     int MBS, DMBS, B, Hkv, budget, recent;
 };
 
-cudaError_t launch_evict(const EvictArgs &a, int head_dim, cudaStream_t stream);
+cudaError_t launch_evict(const EvictArgs &a, int head_dim, int sms, cudaStream_t stream);
 cudaError_t launch_reset_weights(float *weights, const int64_t *slots, int64_t T, int Hkv, int64_t NB,
                                  cudaStream_t stream);
 
