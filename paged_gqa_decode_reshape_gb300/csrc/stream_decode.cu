@@ -62,7 +62,7 @@ constexpr int kMinPiece = 12;
 constexpr int kFusedAddBlocks = 64;
 
 #ifndef PA_STREAM_WARPS_F8
-#define PA_STREAM_WARPS_F8 10
+#define PA_STREAM_WARPS_F8 8
 #endif
 #ifndef PA_STREAM_STAGES_F8
 #define PA_STREAM_STAGES_F8 2
@@ -92,6 +92,7 @@ struct StreamCfg {
     static constexpr size_t off_flag = off_ml + size_t(NW) * 16 * 4;
     static constexpr size_t off_lse = off_flag + 16;
     static constexpr size_t off_pre = off_lse + kMaxGroup * 4;
+    static_assert(off_scr % 16 == 0 && off_ml % 16 == 0 && off_pre % 8 == 0, "vector accesses");
     static constexpr size_t SMEM = 1024 + off_pre + (kPreCap + 1) * 8;
 };
 
@@ -689,15 +690,18 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
     int issued = min(kn, R);
     for (int i = 0; i < issued; ++i) issue(i);
     int k = 0;
+    // item k is in cur; the items up to k + R are in cur or nxt
+    auto shift_windows = [&]() {
+        if (k < wbase + 32) return;
+        cur = nxt;
+        wbase += 32;
+        nxt = resolve(wbase + 32);
+        scales(nxt);
+    };
     // the items k < k1 of segment (cb, ckvh)
     auto stream = [&](int k1, int cb, int ckvh) {
         while (k < k1) {
-            if (k >= wbase + 32) {
-                cur = nxt;
-                wbase += 32;
-                nxt = resolve(wbase + 32);
-                scales(nxt);
-            }
+            shift_windows();
             const uint32_t mask = __shfl_sync(0xffffffffu, cur.mask, k & 31);
             const uint32_t ma = mask & 0xffffu, mb = mask >> 16;
             float2 ca{0.f, 0.f}, cbk{0.f, 0.f};
@@ -866,16 +870,13 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
                     }
                 }
             }
-            // the end cost's empty items
-            for (; k < kn && first + k < min(end, last); ++k) {
-                if (k >= wbase + 32) {
-                    cur = nxt;
-                    wbase += 32;
-                    nxt = resolve(wbase + 32);
-                    scales(nxt);
-                }
+            // the end cost's empty items: nothing to wait for, but the next copies start one by one here too,
+            // while their entries are in the windows
+            while (k < kn && first + k < min(end, last)) {
+                shift_windows();
+                ++k;
+                if (issued < kn && issued < k + R) issue(issued++);
             }
-            for (; issued < kn && issued < k + R; ++issued) issue(issued);
             if (!more) break;
         }
     }
