@@ -14,33 +14,39 @@
 namespace pa {
 namespace {
 
-constexpr int kSelThreads = 1024, kHistCopies = 8;
+constexpr int kSelThreads = 1024;
+constexpr int kBins = 2 * kSelThreads;  // of a selection pass
+constexpr int kCand = 256;              // keys ranked against one another at the end
 // From this many SMs per (sequence, KV head) on, one launch in which every CTA
 // selects and copies a share; below, a CTA selects for all and a second launch
-// copies. One sequence of 1500 tokens, 1024 kept: 9.4 us in one launch, 10.0 in two
-// (and 2 us of the host); 9 of 2000, 512 kept: 11.4 and 13.0; 9 of 8192, 4096
-// kept: 42.3 and 42.0; 16 of those, two CTAs each: 68.1 and 63.5 (4 KV heads of
-// 128: the copy wants more warps than two CTAs of 1024 threads per head have).
+// copies. One sequence of 1500 tokens, 1024 kept: 6.7 us in one launch, 6.8 in two
+// (and 2 us of the host); 9 of 2000, 512 kept: 8.7 and 9.9; 9 of 8192, 4096 kept:
+// 37.7 and 38.0; 16 of those, two CTAs each: 62.6 and 59.6 (4 KV heads of 128: the
+// copy wants more warps than two CTAs of 1024 threads per head have).
 constexpr int kMinParts = 4;
 constexpr int kKeysCap = 48 * 1024;  // keys held in shared memory; longer rows read them again
 
-// The k-th largest of n keys (n > k >= 1), key_of(j) in totalOrder: thr, and keq,
-// how many keys equal to it belong to the k (every key above it does). Radix
-// descent in digits of up to 8 bits from the highest bit in which the keys
-// differ; it ends early when a digit's keys are all taken (then thr is one below
-// them and keq 0). A histogram copy per four warps keeps the atomic adds of
-// equal digits apart, and a thread per bin sums and scans them: a pass over a
-// row of 12K keys takes about a microsecond.
-template <typename KeyOf>
-__device__ __forceinline__ void kth_largest(KeyOf key_of, int n, int k, int *hist, int *red, uint32_t &thr, int &keq) {
-    constexpr int NW = kSelThreads / 32, U = 4;
+struct SelectScratch {
+    int hist[kBins];
+    uint4 cand[kCand / 4];
+    int red[2 * kSelThreads / 32 + 4];
+};
+
+// The k-th largest of n keys (n > k >= 1), keys4(j) the four from j on (j a multiple
+// of 4), in totalOrder: thr, and keq, how many keys equal to it belong to the k
+// (every key above it does). lo, hi: the least and the largest key that this
+// thread has seen. A pass sorts the keys of lo .. hi into 2048 bins of equal width
+// and goes on with the bin that holds the k-th; once that has at most kCand keys
+// they are ranked against one another: one or two passes are the usual case. (Fixed
+// digits of 8 bits took four, and weights, which lie within a few octaves, met in
+// few bins of the first: 8.2 us for 8.7K keys.)
+template <typename Keys4>
+__device__ __forceinline__ void kth_largest(Keys4 keys4, int n, int k, uint32_t lo, uint32_t hi, SelectScratch &sm,
+                                            uint32_t &thr, int &keq) {
+    constexpr int NW = kSelThreads / 32;
+    static_assert(NW == 32, "one lane per warp");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    uint32_t lo = 0xffffffffu, hi = 0u;
-    for (int j = tid; j < n; j += kSelThreads) {
-        const uint32_t u = key_of(j);
-        lo = min(lo, u);
-        hi = max(hi, u);
-    }
+    int *red = sm.red;
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
     if (lane == 0) {
@@ -50,104 +56,149 @@ __device__ __forceinline__ void kth_largest(KeyOf key_of, int n, int k, int *his
     __syncthreads();
     lo = __reduce_min_sync(0xffffffffu, uint32_t(red[lane]));
     hi = __reduce_max_sync(0xffffffffu, uint32_t(red[NW + lane]));
-    static_assert(NW == 32, "one lane per warp");
-    thr = hi;
-    keq = k;
-    if (lo == hi) return;  // every key equal: the k lowest positions
-    const int top = 31 - __clz(lo ^ hi);
-    uint32_t mask = top == 31 ? 0u : ~((2u << top) - 1u);  // bits in which the keys left agree, with
-    uint32_t prefix = hi & mask;
-    for (int h = top; h >= 0;) {
-        const int l = h >= 7 ? h - 7 : 0;
-        const uint32_t dm = (2u << (h - l)) - 1u;  // digit of bits l..h
-        for (int i = tid; i < kHistCopies * 256; i += kSelThreads) hist[i] = 0;
+    while (true) {
+        thr = hi;
+        keq = k;
+        if (lo == hi) return;  // every key left equal: the k lowest positions
+        const int sh = max(21 - __clz(hi - lo), 0);  // (hi - lo) >> sh < kBins
+        sm.hist[tid] = 0;
+        sm.hist[tid + kSelThreads] = 0;
+        if (tid == 0) red[2 * NW + 3] = 0;
         __syncthreads();
-        int *mine = hist + (warp % kHistCopies) * 256;
-        for (int j0 = tid; j0 < n; j0 += U * kSelThreads) {
-            uint32_t u[U];
+        for (int j = 4 * tid; j < n; j += 4 * kSelThreads) {
+            const uint4 u = keys4(j);
+            const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-            for (int i = 0; i < U; ++i) u[i] = j0 + i * kSelThreads < n ? key_of(j0 + i * kSelThreads) : ~prefix;
-#pragma unroll
-            for (int i = 0; i < U; ++i)
-                if ((u[i] & mask) == prefix && j0 + i * kSelThreads < n) atomicAdd(&mine[(u[i] >> l) & dm], 1);
+            for (int e = 0; e < 4; ++e)
+                if (j + e < n && v[e] - lo <= hi - lo) atomicAdd(&sm.hist[(v[e] - lo) >> sh], 1);
         }
         __syncthreads();
-        int cnt = 0, incl = 0;
-        if (tid < 256) {  // digits descending
+        // two bins per thread, descending
+        const int c0 = sm.hist[kBins - 1 - 2 * tid], c1 = sm.hist[kBins - 2 - 2 * tid];
+        int incl = c0 + c1;
 #pragma unroll
-            for (int c = 0; c < kHistCopies; ++c) cnt += hist[c * 256 + 255 - tid];
-            incl = cnt;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
-            }
-            if (lane == 31) red[warp] = incl;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) red[warp] = incl;
+        __syncthreads();
+        incl += __reduce_add_sync(0xffffffffu, lane < warp ? red[lane] : 0);
+        const int above = incl - c0 - c1;  // keys in higher bins
+        if (above < k && k <= incl) {
+            const bool first = k <= above + c0;
+            red[2 * NW] = kBins - 1 - 2 * tid - (first ? 0 : 1);
+            red[2 * NW + 1] = first ? above : above + c0;
+            red[2 * NW + 2] = first ? c0 : c1;
         }
         __syncthreads();
-        if (tid < 256) {
-            for (int w = 0; w < warp; ++w) incl += red[w];
-            if (incl - cnt < k && k <= incl) {
-                red[2 * NW] = 255 - tid;
-                red[2 * NW + 1] = incl - cnt;
-                red[2 * NW + 2] = incl == k;
-            }
-        }
-        __syncthreads();
-        prefix |= uint32_t(red[2 * NW]) << l;
-        mask |= dm << l;
+        const int m = red[2 * NW + 2];
         k -= red[2 * NW + 1];
-        h = l - 1;
-        if (red[2 * NW + 2] && prefix != 0u && h >= 0) {
-            thr = prefix - 1u;
+        lo += uint32_t(red[2 * NW]) << sh;
+        if (hi - lo >= 1u << sh) hi = lo + ((1u << sh) - 1u);
+        if (m == k && lo != 0u) {  // the whole bin
+            thr = lo - 1u;
             keq = 0;
             return;
         }
+        if (m <= kCand) {
+            uint32_t *cand = reinterpret_cast<uint32_t *>(sm.cand);
+            if (tid < 4 && m + tid < kCand) cand[m + tid] = 0u;  // read as part of the last four: below or equal to all
+            for (int j = 4 * tid; j < n; j += 4 * kSelThreads) {
+                const uint4 u = keys4(j);
+                const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (j + e < n && v[e] - lo <= hi - lo) cand[atomicAdd(&red[2 * NW + 3], 1)] = v[e];
+            }
+            __syncthreads();
+            if (tid < m) {
+                const uint32_t c = cand[tid];
+                int gt = 0, ge = 0;
+                for (int i = 0; i < (m + 3) / 4; ++i) {
+                    const uint4 o = sm.cand[i];
+                    gt += (o.x > c) + (o.y > c) + (o.z > c) + (o.w > c);
+                    ge += (o.x >= c) + (o.y >= c) + (o.z >= c) + (o.w >= c);
+                }
+                if (c == 0u) ge = m;  // not the padding
+                if (gt < k && k <= ge) {
+                    red[2 * NW] = int(c);
+                    red[2 * NW + 1] = k - gt;
+                }
+            }
+            __syncthreads();
+            thr = uint32_t(red[2 * NW]);
+            keq = red[2 * NW + 1];
+            return;
+        }
     }
-    thr = prefix;
-    keq = k;
 }
 
 // The selection for a threshold, ascending: emit(r, j) for the r-th selected
-// position j. Warps own consecutive ranges of 32-key rows, a lane per key.
-template <typename KeyOf, typename Emit>
-__device__ __forceinline__ void emit_selected(KeyOf key_of, int n, uint32_t thr, int keq, int *red, Emit emit) {
+// position j. Warps own consecutive ranges, a lane four keys at a time (a lane per
+// key, with ballots, took 3.4 us for 8.7K keys).
+template <typename Keys4, typename Emit>
+__device__ __forceinline__ void emit_selected(Keys4 keys4, int n, uint32_t thr, int keq, SelectScratch &sm, Emit emit) {
     constexpr int NW = kSelThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const unsigned below = (1u << lane) - 1u;
-    const int rows = ((n + 31) / 32 + NW - 1) / NW, j0 = warp * rows * 32, j1 = min(n, j0 + rows * 32);
+    const int rows = ((n + 127) / 128 + NW - 1) / NW, j0 = warp * rows * 128, j1 = min(n, j0 + rows * 128);
+    int *red = sm.red;
     int gt = 0, eq = 0;
-    for (int j = j0; j < j1; j += 32) {
-        const uint32_t u = j + lane < j1 ? key_of(j + lane) : 0u;
-        gt += __popc(__ballot_sync(0xffffffffu, j + lane < j1 && u > thr));
-        eq += __popc(__ballot_sync(0xffffffffu, j + lane < j1 && u == thr));
+    for (int j = j0 + 4 * lane; j < j1; j += 128) {
+        const uint4 u = keys4(j);
+        const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            gt += j + e < j1 && v[e] > thr;
+            eq += j + e < j1 && v[e] == thr;
+        }
     }
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
     __syncthreads();  // red is free
     if (lane == 0) {
         red[warp] = gt;
         red[NW + warp] = eq;
     }
     __syncthreads();
+    // taken before this warp's range: those above thr, and of those equal to it the first keq
     gt = __reduce_add_sync(0xffffffffu, lane < warp ? red[lane] : 0);
     eq = __reduce_add_sync(0xffffffffu, lane < warp ? red[NW + lane] : 0);
-    for (int j = j0; j < j1; j += 32) {
-        const uint32_t u = j + lane < j1 ? key_of(j + lane) : 0u;
-        const unsigned g = __ballot_sync(0xffffffffu, j + lane < j1 && u > thr);
-        const unsigned e = __ballot_sync(0xffffffffu, j + lane < j1 && u == thr);
-        // taken before this key: those above thr, and of those equal to it the first keq
-        const int eqb = eq + __popc(e & below);
-        const bool take = (g >> lane) & 1u || ((e >> lane) & 1u && eqb < keq);
-        if (take) emit(gt + __popc(g & below) + min(eqb, keq), j + lane);
-        gt += __popc(g);
-        eq += __popc(e);
+    for (int j = j0; j < j1; j += 128) {
+        const int jj = j + 4 * lane;
+        const uint4 u = jj < j1 ? keys4(jj) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+        uint32_t g = 0, q = 0;  // bits of this lane's keys above and at the threshold
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            g |= uint32_t(jj + e < j1 && v[e] > thr) << e;
+            q |= uint32_t(jj + e < j1 && v[e] == thr) << e;
+        }
+        const int mine = __popc(g) | __popc(q) << 16;
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        const int all = __shfl_sync(0xffffffffu, incl, 31);
+        int gb = gt + ((incl - mine) & 0xffff), qb = eq + ((incl - mine) >> 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool ge = (g >> e) & 1u, qe = (q >> e) & 1u;
+            if (ge || (qe && qb < keq)) emit(gb + min(qb, keq), jj + e);
+            gb += ge;
+            qb += qe;
+        }
+        gt += all & 0xffff;
+        eq += all >> 16;
     }
 }
 
 // The kept positions of segment (b, kvh) with ranks r0 <= r < r1, by a whole CTA.
 __device__ __forceinline__ void select_kept(const EvictArgs &a, int b, int kvh, int cap, int r0, int r1) {
     extern __shared__ __align__(16) uint32_t keys[];
-    __shared__ int hist[kHistCopies * 256];
-    __shared__ int red[2 * kSelThreads / 32 + 3];
+    __shared__ SelectScratch sm;
     const int tid = threadIdx.x;
     const int ctx = min(max(__ldg(a.ctx + b), 0), a.MBS * kBlockSize);
     int32_t *kept = a.kept + (int64_t(b) * a.Hkv + kvh) * a.budget;
@@ -166,6 +217,11 @@ __device__ __forceinline__ void select_kept(const EvictArgs &a, int b, int kvh, 
         return f32_order_key(__ldcg(a.weights + (int64_t(phys) * a.Hkv + kvh) * kBlockSize + j % kBlockSize));
     };
     const bool cached = n <= cap;
+    uint32_t lo = 0xffffffffu, hi = 0u;  // of this thread's keys
+    auto seen = [&](uint32_t u) {
+        lo = min(lo, u);
+        hi = max(hi, u);
+    };
     if (cached) {
         // four tokens of a block per load, U loads (and their table entries) in flight per thread
         constexpr int U = 4;
@@ -191,18 +247,28 @@ __device__ __forceinline__ void select_kept(const EvictArgs &a, int b, int kvh, 
                 const int q = q0 + u * kSelThreads;
                 if (q >= nq) continue;
                 const bool in = phys[u] >= 0;
-                *reinterpret_cast<uint4 *>(keys + 4 * q) =
-                    make_uint4(in ? f32_order_key(v[u].x) : 0u, in ? f32_order_key(v[u].y) : 0u,
-                               in ? f32_order_key(v[u].z) : 0u, in ? f32_order_key(v[u].w) : 0u);
+                const uint4 k4 = make_uint4(in ? f32_order_key(v[u].x) : 0u, in ? f32_order_key(v[u].y) : 0u,
+                                            in ? f32_order_key(v[u].z) : 0u, in ? f32_order_key(v[u].w) : 0u);
+                *reinterpret_cast<uint4 *>(keys + 4 * q) = k4;
+                seen(k4.x);
+                if (4 * q + 1 < n) seen(k4.y);
+                if (4 * q + 2 < n) seen(k4.z);
+                if (4 * q + 3 < n) seen(k4.w);
             }
         }
-        __syncthreads();
+    } else {
+        for (int j = tid; j < n; j += kSelThreads) seen(load(j));
     }
-    auto key_of = [&](int j) -> uint32_t { return cached ? keys[j] : load(j); };
+    __syncthreads();
+    auto keys4 = [&](int j) -> uint4 {
+        if (cached) return *reinterpret_cast<const uint4 *>(keys + j);
+        return make_uint4(load(j), j + 1 < n ? load(j + 1) : 0u, j + 2 < n ? load(j + 2) : 0u,
+                          j + 3 < n ? load(j + 3) : 0u);
+    };
     uint32_t thr;
     int keq;
-    kth_largest(key_of, n, top, hist, red, thr, keq);
-    emit_selected(key_of, n, thr, keq, red, [&](int r, int j) {
+    kth_largest(keys4, n, top, lo, hi, sm, thr, keq);
+    emit_selected(keys4, n, thr, keq, sm, [&](int r, int j) {
         if (r >= r0 && r < r1) kept[r] = j;
     });
 }

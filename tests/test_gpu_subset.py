@@ -366,6 +366,23 @@ def test_evict(ctx, budget, recent, Hkv, D, levels):
     _evict_run(*_evict_case(budget, ctx, budget, recent, Hkv, D, levels), ctx, budget, recent)
 
 
+@pytest.mark.parametrize("Hkv,D", [(4, 128), (2, 64)])
+def test_evict_many_heads(Hkv, D):
+    """More (sequence, KV head) pairs than the GPU has SMs for several CTAs each."""
+    ctx = [700, 64, 0, 300, 1, 299] * 13
+    _evict_run(*_evict_case(3, ctx, 130, 20, Hkv, D), ctx, 130, 20)
+
+
+@pytest.mark.parametrize("n,budget", [(6000, 2000), (6000, 3), (60001, 5000)])
+@pytest.mark.parametrize("spread", [0.0, 1e-6, 1e-3, 30.0])
+def test_evict_clustered_weights(n, budget, spread):
+    """Nearly all weights close together (or over many octaves) between one far below and one far above."""
+    kc, vc, bt, dst, w = _evict_case(n, [n], budget, 0, 1, 64)
+    w = torch.exp(w * spread)
+    w[bt[0, 3], 0, 5], w[bt[0, 9], 0, 2] = 3e38, -3e38
+    _evict_run(kc, vc, bt, dst, w, [n], budget, 0)
+
+
 def test_evict_long_row():
     """A row longer than the selection holds in shared memory."""
     ctx = [70001]
