@@ -40,9 +40,12 @@
  *     start while the previous kernel in the stream finishes, and waits for
  *     it before reading anything that kernel may write. The exceptions are
  *     context_lens (read before that wait by every decode and selection
- *     call, and cu_seqlens_q by pa_decode_multi) and block_tables (read
+ *     call, and cu_seqlens_q by pa_decode_multi and pa_decode_window_multi,
+ *     prefix_lens and cu_group by pa_decode_prefix) and block_tables (read
  *     before it by the bf16 dense decode and by the selection's score
- *     kernel). No kernel of this library writes them. A caller kernel that
+ *     kernel). No kernel of this library writes them but pa_evict's new_lens,
+ *     which may be the next call's context_lens: its last kernel lets nothing
+ *     start early. A caller kernel that
  *     writes them and lets dependent launches start early must not run just
  *     before such a call. A kernel that never triggers early starts its
  *     dependents only when it completes, so the usual case is safe.
@@ -630,9 +633,14 @@ PA_API int quest_decode_fp8_block(pa_bf16 *out, int32_t *selected, const pa_bf16
  * Three additions next to the dense and the Quest decode: attention over a
  * sliding window with visible first tokens, attention of a batch over shared
  * prefixes, and eviction by accumulated attention weight. Layouts, block
- * tables, masking of bad metadata, workspaces (zero-filled once; calls that
- * overlap in time need different ones; pa_workspace_status reads their
- * status) and errors as pa_decode; scale must be finite. */
+ * tables, masking of bad metadata and errors as pa_decode; scale must be
+ * finite. Workspaces are zero-filled once; one buffer serves all calls of this
+ * section in any order and shape, but not calls of other sections besides,
+ * and calls that overlap in time need different ones. pa_workspace_status
+ * reads their status. They take about 15 MB (pa_decode_window), 40 MB
+ * (pa_decode_window_multi), 55 MB (pa_decode_prefix), and 4 bytes per query
+ * head and table slot more for pa_decode_weights. Results are deterministic
+ * on a device, but for what pa_decode_weights says about shared blocks. */
 
 /* Sliding-window decode: as pa_decode, but sequence b's query sees only the
  * tokens t < ctx_b with
@@ -739,10 +747,11 @@ PA_API int pa_reset_weights(float *weights, const int64_t *slot_mapping, int64_t
  * cache: after quest_rebuild_meta on them) and its old ones can be freed.
  * No destination block may be a source block of the call (context_lens
  * tokens of any sequence) or another destination, and new_lens may not be
- * context_lens; destination slots from position new_lens[b] on are left as
+ * context_lens (nor overlap it); destination slots from position new_lens[b] on are left as
  * they are. Tokens of a block whose table entry is outside the pool count as
  * smaller than every weight; rows from or to such blocks are not copied.
- * max_dst_blocks * block_size >= budget. bf16 cache; no workspace. */
+ * max_dst_blocks * block_size >= budget, budget <= 2^30. bf16 cache; no
+ * workspace. */
 PA_API int pa_evict(int32_t *kept, int32_t *new_lens, pa_bf16 *key_cache, pa_bf16 *value_cache, float *weights,
                     const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
                     const int32_t *dst_tables, int max_dst_blocks, int batch, int num_kv_heads, int head_dim,

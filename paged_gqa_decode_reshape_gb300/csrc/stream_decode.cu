@@ -8,7 +8,11 @@
 //   out_h = sum_t 2^(z_t - m) V_t / sum_t 2^(z_t - m),   m = max_t z_t.
 //
 // Bound: every visible K/V byte is read once, at about 2 G flops per byte, so
-// HBM bandwidth bounds long calls and latency short ones.
+// HBM bandwidth bounds long calls and latency short ones. Measured (28 / 4 heads
+// of 128, all tokens seen): 500 sequences of 2000 tokens 306 us = 6.7 TB/s, 8-bit
+// cache 158 us = 6.5 TB/s; 16 of 4096 25.4 us = 5.3 TB/s, of which about 5 us are
+// the launch, the lengths, the table and the first copies one after another, and
+// the last merges; one of 256 tokens 4.6 us.
 //
 //  * Work list. A (sequence, KV head) is a segment with one item per two 16-token
 //    blocks that hold a visible token (sink blocks, then window blocks; at
@@ -46,7 +50,10 @@ namespace pa {
 namespace {
 
 constexpr int kPreCap = 512;   // entries of the items-per-sequence prefix in shared memory
-constexpr int kEndCost = 2;    // items that the end of a segment costs a warp
+// Items that the end of a segment costs a warp (its merge and the next one's query). 128 sequences of 33 to 20011
+// tokens in a window of 2048, 8-bit: 2 items 36.7 us, none 45.2, 4 items 35.2; 128 of 1 to 2049 own tokens beside
+// their prefixes: 37.0, 46.0 and 39.1.
+constexpr int kEndCost = 2;
 // Items of a CTA's piece at least, where there are as many; while no segment has
 // more than twice that, all stay whole. A cut costs about 1.7 us at the end, an item less per warp
 // saves 0.85 us: 16 sequences of 500 tokens take 8.0 us in two pieces each, 6.3
@@ -73,6 +80,10 @@ template <int D, CacheKind KIND>
 struct StreamCfg {
     static constexpr bool F8 = KIND != kCacheBf16;
     static_assert(!F8 || D == 128, "the E4M3 cache path is for head_dim 128");
+    // Warps x stages of 16 KB (bf16) or 8 KB fill the shared memory that the math's latency leaves room for.
+    // bf16, 16 sequences of 4096 tokens: 6 x 2 25.4 us, 5 x 2 25.6, 4 x 3 25.9, 3 x 4 28.3 (of 500 tokens 6.3, 7.4,
+    // 6.8, 8.7). 8-bit, 128 of 2048: 8 x 2 50.4 us, 10 x 2 53.4 (168 registers, and more pieces to merge), 9 x 2 54.1,
+    // 7 x 2 51.4, 5 x 4 63.6 (16 of 4096: 16.7, 17.3, 18.4, 18.8, 22.4).
     static constexpr int NW = F8 ? PA_STREAM_WARPS_F8 : 6;  // warps
     static_assert(NW <= kMaxStreamWarps, "pieces and counters of the workspace");
     static constexpr int KT = kBlockSize * D * (F8 ? 1 : 2);  // bytes of a K (or V) tile of one block
@@ -623,6 +634,7 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
             p[e] = fast_exp2(x[e] - (e & 1 ? r1 : r0));
             q[e] = fast_exp2(y[e] - (e & 1 ? r1 : r0));
         }
+        // P meets V as bf16 (f16 with E4M3 values): relative rounding 2^-9 (2^-12) per weight, as in the dense decode
         auto pk = [](float lo, float hi) { return F8 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi); };
         const uint32_t p01 = pk(p[0], p[1]), p23 = pk(p[2], p[3]), q01 = pk(q[0], q[1]), q23 = pk(q[2], q[3]);
         if constexpr (!LOGITS) {
@@ -914,7 +926,9 @@ cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const SubsetA
 size_t stream_workers(int sms) { return size_t(sms) * kMaxStreamWarps; }
 size_t stream_part_floats(int sms, int head_dim) { return 2 * stream_workers(sms) * (size_t(8) * head_dim + 16); }
 
-// ---- rows with a prefix: the own part and the prefix's parts, a warp per row
+// ---- rows with a prefix: the own part and the prefix's parts, a warp per row.
+// Bound by latency: where the parts are, then the parts, eight in flight; about
+// 4 us of a call.
 template <int D>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const SubsetArgs a) {
     pdl_trigger();

@@ -1,6 +1,6 @@
 // subset.h -- internal interface of the decode operators that read a part of
-// the cache, or share it between sequences, and of eviction (subset_decode.cu,
-// evict.cu).
+// the cache, or share it between sequences (stream_decode.cu, row_tiles.cu), and
+// of eviction (evict.cu).
 #pragma once
 
 #include <cuda.h>
@@ -36,7 +36,8 @@ struct SubsetArgs {
     float scale_log2;             // softmax scale * log2(e)
     // workspace
     int32_t *status;              // status word
-    int32_t *counters;            // [workers] arrivals at what begins in a worker's range and leaves it (zero between calls)
+    int32_t *counters;            // [workers] arrivals at what begins in a worker's range and leaves it (zero between calls);
+                                  // row tiles: two per CTA
     float *part;                  // [2 * workers] pieces of segments cut between workers: O, m, l
     float *slots;                 // [2 * CTAs] pieces of row-tile units cut between CTAs
     float *rowres, *rowml;        // prefixes: [rows][Hq][D] O and [rows][Hq][2] m, l of units that were not cut
