@@ -864,7 +864,7 @@ struct SubsetPlan {
 // The workspace's parts: status word, arrival counters, two piece slots per
 // worker and kernel, then what the operator keeps per row.
 struct SubsetWorkspace {
-    size_t part, slots, rowres, rowml, ownres, ownml, desc, lse, logits, bytes;
+    size_t part, slots, cuts, rowres, rowml, ownres, ownml, desc, lse, logits, bytes;
     int sms;
 };
 
@@ -880,9 +880,10 @@ int subset_workspace(SubsetWorkspace *w, const SubsetPlan &plan, int64_t rows, i
     };
     w->sms = geo.grid;  // one CTA per SM
     const size_t heads = size_t(rows) * Hq;
-    take(true, stream_workers(geo.grid) * 4);  // counters (of either kernel)
+    take(true, stream_workers(geo.grid) * 4);  // counters
     w->part = take(plan.stream, stream_part_floats(geo.grid, D) * 4);
     w->slots = take(plan.tiles, size_t(geo.grid) * 2 * row_tiles_slot_floats(D) * 4);
+    w->cuts = take(plan.tiles && !plan.prefix, size_t(geo.grid) * sizeof(CutUnit));
     w->rowres = take(plan.prefix, heads * D * 4);
     w->rowml = take(plan.prefix, heads * 8);
     w->ownres = take(plan.prefix, heads * D * 4);
@@ -960,6 +961,7 @@ int run_subset(SubsetArgs a, const SubsetPlan &plan, int D, CacheKind kind, void
     a.counters = reinterpret_cast<int32_t *>(p + 256);
     a.part = reinterpret_cast<float *>(p + w.part);
     a.slots = reinterpret_cast<float *>(p + w.slots);
+    a.cuts = reinterpret_cast<CutUnit *>(p + w.cuts);
     a.rowres = reinterpret_cast<float *>(p + w.rowres);
     a.rowml = reinterpret_cast<float *>(p + w.rowml);
     a.ownres = plan.prefix ? reinterpret_cast<float *>(p + w.ownres) : nullptr;

@@ -46,8 +46,9 @@
 //    is not 0 if V is not finite: a row whose result is not finite is computed
 //    again, over its own tokens only, by its warp.
 //  * Units cut between CTAs leave (O, m, l) per row and piece in the workspace;
-//    the CTA that completes the count merges them in piece order, its own from
-//    tensor memory (for prefixes the join kernel merges).
+//    the CTA that completes the count merges them, in piece order, or a join
+//    kernel does (for prefixes, with the own tokens' part).
+#include <algorithm>
 #include <climits>
 
 #include "common.cuh"
@@ -146,6 +147,44 @@ struct Work {
     }
 };
 
+// Head h of query row r of sequence s again, over the tokens before lim that it
+// sees and nothing else, by a warp in fp32: for rows whose result is not finite.
+template <int D>
+__device__ __forceinline__ void redo_row(const SubsetArgs &a, int s, int kvh, int r, int h, int lim) {
+    constexpr int V = D / 32, BS = kBlockSize;
+    const int lane = threadIdx.x & 31, s1 = min(a.sinks, lim), lo = max(s1, a.window >= lim ? 0 : lim - a.window);
+    const int cnt = s1 + max(lim - lo, 0);
+    const int64_t ro = (int64_t(r) * a.Hq + kvh * a.G + h) * D + lane * V;
+    float q[V], acc[V], M = -INFINITY, Ls = 0.f;
+    auto f32 = [](uint16_t v) { return __uint_as_float(uint32_t(v) << 16); };
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        q[k] = f32(a.q[ro + k]);
+        acc[k] = 0.f;
+    }
+    for (int k = 0; k < cnt; ++k) {
+        const int t = k < s1 ? k : k - s1 + lo;
+        const int phys = __ldg(a.bt + int64_t(s) * a.MBS + t / BS);
+        if (phys < 0 || int64_t(phys) >= a.NB) continue;
+        const int64_t off = ((int64_t(phys) * BS + t % BS) * a.Hkv + kvh) * D + lane * V;
+        float z = 0.f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) z = fmaf(q[e], f32(static_cast<const uint16_t *>(a.kc)[off + e]), z);
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        z *= a.scale_log2;
+        const float Mn = fmaxf(M, z);
+        const float f = M == -INFINITY ? 0.f : fast_exp2(M - Mn), p = fast_exp2(z - Mn);
+        M = Mn;
+        Ls = Ls * f + p;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = acc[e] * f + p * f32(static_cast<const uint16_t *>(a.vc)[off + e]);
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+        a.out[ro + e] = __bfloat16_as_ushort(__float2bfloat16_rn(Ls > 0.f ? acc[e] / Ls : Ls != Ls ? Ls : 0.f));
+}
+
 template <int D, bool PREFIX>
 __global__ void __launch_bounds__(kWarpsRT * 32, 1)
     row_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -163,7 +202,8 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
     const uint32_t ring = base + uint32_t(C::off_ring);
     const uint32_t full = base + uint32_t(C::off_bars), empty = full + kStages * 8;
     const uint32_t q_full = empty + kStages * 8, q_empty = q_full + 16, s_full = q_empty + 16;
-    const uint32_t p_ready = s_full + 16, o_full = p_ready + 32, drained = o_full + 16, piece_bar = drained + 8, last_bar = piece_bar + 16, seen_bar = last_bar + 16;
+    const uint32_t p_ready = s_full + 16, o_full = p_ready + 32, drained = o_full + 16, piece_bar = drained + 8, last_bar = piece_bar + 16;
+    const uint32_t ml_bar = last_bar + 16;
     volatile int *info = reinterpret_cast<volatile int *>(bp + C::off_info);
     volatile int *vfix = info + kInfo;  // V rows to zero: see the producers
     volatile int *misc = reinterpret_cast<volatile int *>(bp + C::off_misc);  // [0] tensor memory, [1] gave up, [2 + w] queries,
@@ -188,7 +228,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
             mbar_init(o_full + 8 * w, 1);
             mbar_init(piece_bar + 8 * w, 4);
             mbar_init(last_bar + 8 * w, 1);
-            mbar_init(seen_bar + 8 * w, 1);
+            mbar_init(ml_bar + 8 * w, 4);
         }
         mbar_init(drained, 1);
         fence_barrier_init();
@@ -239,7 +279,10 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
     const int64_t pos0 = int64_t(blockIdx.x) * L, pos1 = min(total, pos0 + L);
     if (pos0 >= pos1) {  // whole CTA: nothing to do
         // a call without any rows still ends after what came before it, which later kernels may need
-        if (!PREFIX) pdl_wait();
+        if constexpr (!PREFIX) {
+            pdl_wait();
+            if (a.cuts && tid == 0) a.cuts[blockIdx.x].pieces = 0;
+        }
         return;
     }
 
@@ -521,24 +564,22 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
         const uint32_t lane_base = uint32_t(warp & 3) << 21;  // this warp's 32 of the 128 lanes
         const uint32_t ts = tmem + lane_base + 256 * w, to = ts + 128;
         const int i = row / G, h = row - i * G;
-        uint32_t ph = 0, tile_no = 0, units = 0, cuts = 0, pubs = 0;
+        uint32_t ph = 0, tile_no = 0, units = 0, merges = 0, pubs = 0;
+        if (!PREFIX && a.cuts && tid == 0) a.cuts[blockIdx.x].pieces = 0;  // no unit is cut so far
         bool ok = true;
         for (int64_t p = pos0; ok && p < pos1;) {
             const int t0 = int(p - s0), t1 = int(min(pos1 - s0, int64_t(x.n)));
             const int ir = w * RQ + i;  // query row of the unit
             const bool act = i < RQ && ir < x.nr;
             if (w == 0 || x.nr > RQ) {
-                int lim = 0;
-                if (act) {
-                    if (PREFIX) {
-                        lim = x.lim1;
-                    } else {  // lim1 belongs to the unit's last row
-                        const int c = min(max(__ldg(a.ctx + x.s), 0), a.MBS * BS);
-                        int rr, nn;
-                        work.rows(x.s, rr, nn);
-                        lim = max(c - (nn - 1 - (x.r0 - rr + ir)), 0);
-                    }
+                // row ir of the unit sees tokens before base + ir (PREFIX: all rows before lim1)
+                int base = 0;
+                if (!PREFIX) {
+                    int rr, nn;
+                    work.rows(x.s, rr, nn);
+                    base = min(max(__ldg(a.ctx + x.s), 0), a.MBS * BS) - (nn - 1 - (x.r0 - rr));
                 }
+                const int lim = !act ? 0 : PREFIX ? x.lim1 : max(base + ir, 0);
                 const int S1 = min(work.sinks(), lim), lo = max(S1, work.lower(lim));
                 float m = -INFINITY, l = 0.f;
                 for (int t = t0; t < t1; ++t) {
@@ -631,11 +672,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                 // ---- the end of the unit, or of this CTA's piece of it
                 const bool whole = t0 == 0 && t1 == x.n;
                 const int c0 = int(s0 / L), npieces = int((s0 + x.n - 1) / L) - c0 + 1, mine = int(blockIdx.x) - c0;
-                // pieces of the row tile already counted (read while the products end)
-                int seen = 0;
-                if (!PREFIX && !whole && (warp & 3) == 0 && lane == 0) seen = ld_acquire_s32(a.counters + 2 * c0 + w);
-                if (ok) ok = wait(o_full + 8 * w, units++);
-                if (!ok) break;
+                if (!(ok = wait(o_full + 8 * w, units++))) break;
                 tc_fence_after();
                 const int64_t orow = int64_t(x.r0 + ir) * a.Hq + x.kvh * G + h;
                 auto piece_of = [&](int k) {
@@ -698,17 +735,41 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                     if (act && h == 0 && t0 == 0)  // where this row's parts are
                         a.desc[int64_t(x.r0 + ir) * Hkv + x.kvh] = make_int4(c0, npieces, w, row);
                 } else {
-                    bool last = whole;  // this CTA writes the rows
-                    if (!whole) {
-                        // all other pieces counted: this one need not be published
-                        if ((warp & 3) == 0 && lane == 0) {
-                            misc[4 + w] = seen == npieces - 1;
-                            mbar_arrive(seen_bar + 8 * w);
+                    if (whole) {
+                        const float iv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
+                        bool fine = true;
+#pragma unroll 1
+                        for (int c2 = 0; c2 < HV; ++c2) {
+                            uint4 y[8];
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                float v[32];
+                                own(2 * c2 + q, v);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) {
+                                    v[e] *= iv;
+                                    fine = fine && fabsf(v[e]) <= 3.4028234e38f;
+                                }
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    y[4 * q + e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]),
+                                                              pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
+                                                              pack_bf16x2(v[8 * e + 4], v[8 * e + 5]),
+                                                              pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+                            }
+                            store_rows(y, [&](int, int64_t ro) { return a.out + ro * D + 64 * c2; });
                         }
-                        if (!(ok = wait(seen_bar + 8 * w, cuts++))) break;
-                        last = misc[4 + w];
-                        if (!last) {
-                            publish();
+                        __syncwarp();
+                        for (unsigned again = __ballot_sync(0xffffffffu, act && !fine); again; again &= again - 1) {
+                            const int r = (warp & 3) * 32 + __ffs(again) - 1, rir = w * RQ + r / G;
+                            redo_row<D>(a, x.s, x.kvh, x.r0 + rir, r % G, max(base + rir, 0));
+                        }
+                    } else {
+                        publish();
+                        if (a.cuts) {  // the join kernel merges
+                            if (tid == 0 && t0 == 0)
+                                a.cuts[blockIdx.x] = CutUnit{x.s, x.kvh, x.r0, x.nr, base, npieces, {}};
+                        } else {
                             // the row tile's four warps publish their part; the piece that completes the count merges
                             __syncwarp();
                             if (lane == 0) mbar_arrive(piece_bar + 8 * w);
@@ -720,142 +781,105 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                                 }
                             }
                             if (!(ok = wait(last_bar + 8 * w, pubs++))) break;
-                            last = misc[4 + w];
-                        }
-                        if (last && row == 0) a.counters[2 * c0 + w] = 0;
-                    }
-                    unsigned bad = 0;  // rows of this warp whose result is not finite
-                    if (last) {
-                        // weights of the pieces, in their order (one, if whole)
-                        constexpr int KW = 4;  // kept in registers
-                        float M = m, Ls = l, mk[KW];
-                        if (!whole) {
-                            M = -INFINITY;
-                            Ls = 0.f;
-                            for (int k = 0; k < npieces; k += KW) {
-                                float lk[KW];
+                            if (misc[4 + w]) {
+                                if (row == 0) a.counters[2 * c0 + w] = 0;
+                                // The pieces' common maximum and sum, a row per thread; then the rows, each by a warp with
+                                // its columns side by side, RB rows of KB pieces in flight: bound by the latency of L2
+                                // loads (2 x 8: 52.9 us for 32 sequences of 1 to 6 rows, 3 x 8 53.3, 4 x 4 53.6; with
+                                // rows kept to their thread, a piece at a time, 55.8).
+                                float2 *ml = reinterpret_cast<float2 *>(bp + C::off_stage + 4 * w * 4096);  // [128] M, 1 / l
+                                if (act) {
+                                    constexpr int KW = 8;
+                                    float M = -INFINITY, Ls = 0.f;
+                                    for (int k = 0; k < npieces; k += KW) {
+                                        float mk[KW], lk[KW];
 #pragma unroll
-                                for (int e = 0; e < KW; ++e) {
-                                    const float *ps = piece_of(min(k + e, npieces - 1)) + 128 * D + row;
-                                    const bool me = k + e == mine;
-                                    mk[e] = me ? m : act ? __ldcg(ps) : -INFINITY;
-                                    lk[e] = me ? l : act ? __ldcg(ps + 128) : 0.f;
+                                        for (int e = 0; e < KW; ++e) {
+                                            const float *ps = piece_of(min(k + e, npieces - 1)) + 128 * D + row;
+                                            mk[e] = __ldcg(ps);
+                                            lk[e] = __ldcg(ps + 128);
+                                        }
+#pragma unroll
+                                        for (int e = 0; e < KW; ++e) {
+                                            if (k + e >= npieces) break;
+                                            const float Mn = fmaxf(M, mk[e]);
+                                            const float f = M == -INFINITY ? 0.f : fast_exp2(M - Mn);
+                                            Ls = Ls * f + (mk[e] == -INFINITY ? lk[e] : lk[e] * fast_exp2(mk[e] - Mn));
+                                            M = Mn;
+                                        }
+                                    }
+                                    ml[row] = make_float2(M == -INFINITY ? 0.f : M, Ls == 0.f ? 0.f : 1.f / Ls);
                                 }
-#pragma unroll
-                                for (int e = 0; e < KW; ++e) {
-                                    if (k + e >= npieces) break;
-                                    const float Mn = fmaxf(M, mk[e]);
-                                    const float f = M == -INFINITY ? 0.f : fast_exp2(M - Mn);
-                                    Ls = Ls * f + (mk[e] == -INFINITY ? lk[e] : lk[e] * fast_exp2(mk[e] - Mn));
-                                    M = Mn;
-                                }
-                            }
-                        }
-                        const float Mr = M == -INFINITY ? 0.f : M, iv = Ls == 0.f ? 0.f : 1.f / Ls;  // NaN stays NaN
-                        bool fine = true;
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(ml_bar + 8 * w);
+                                if (!(ok = wait(ml_bar + 8 * w, merges++))) break;
+                                constexpr int V = D / 32, RB = 8, KB = 2;
+                                const int rows = min(x.nr - w * RQ, RQ) * G;
 #pragma unroll 1
-                        for (int c2 = 0; c2 < HV; ++c2) {
-                            uint4 y[8];
+                                for (int g0 = warp & 3; g0 < rows; g0 += 4 * RB) {
+                                    float acc[RB][V];
+                                    float2 mr[RB];
 #pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                const int c = 2 * c2 + q;
-                                float v[32];
-                                if (whole) {
-                                    own(c, v);
+                                    for (int u = 0; u < RB; ++u) {
+                                        mr[u] = ml[min(g0 + 4 * u, rows - 1)];
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e) v[e] *= iv;
-                                } else {
-#pragma unroll
-                                    for (int e = 0; e < 32; ++e) v[e] = 0.f;
+                                        for (int e = 0; e < V; ++e) acc[u][e] = 0.f;
+                                    }
 #pragma unroll 1
-                                    for (int k = 0; k < npieces; ++k) {
-                                        const float *ps = piece_of(k);
-                                        float o[32], mw = m;
-                                        if (k == mine) {
-                                            own(c, o);
-                                        } else {
-                                            // rows by eight lanes each, to one per lane
-                                            mw = act ? __ldcg(ps + 128 * D + row) : -INFINITY;
-                                            uint4 in[8];
+                                    for (int k = 0; k < npieces; k += KB) {
+                                        float o[KB][RB][V], mk[KB][RB];
 #pragma unroll
-                                            for (int j = 0; j < 8; ++j) {
-                                                const int r = 4 * j + sr;
-                                                in[j] = (acts >> r) & 1u
-                                                            ? __ldcg(reinterpret_cast<const uint4 *>(
-                                                                         ps + ((warp & 3) * 32 + r) * D + 32 * c) + sj)
-                                                            : make_uint4(0u, 0u, 0u, 0u);
-                                            }
-                                            __syncwarp();
+                                        for (int kk = 0; kk < KB; ++kk) {
+                                            const float *ps = piece_of(min(k + kk, npieces - 1));
 #pragma unroll
-                                            for (int j = 0; j < 8; ++j) {
-                                                const int r = 4 * j + sr;
-                                                *reinterpret_cast<uint4 *>(stage + r * 128 + ((sj ^ (r & 7)) << 4)) = in[j];
-                                            }
-                                            __syncwarp();
-#pragma unroll
-                                            for (int j = 0; j < 8; ++j) {
-                                                const float4 z = *reinterpret_cast<const float4 *>(
-                                                    stage + lane * 128 + ((j ^ (lane & 7)) << 4));
-                                                o[4 * j] = z.x, o[4 * j + 1] = z.y, o[4 * j + 2] = z.z, o[4 * j + 3] = z.w;
+                                            for (int u = 0; u < RB; ++u) {
+                                                const int r = min(g0 + 4 * u, rows - 1);
+                                                mk[kk][u] = __ldcg(ps + 128 * D + r);
+                                                if constexpr (V == 4) {
+                                                    const float4 z = __ldcg(reinterpret_cast<const float4 *>(ps + r * D) + lane);
+                                                    o[kk][u][0] = z.x, o[kk][u][1] = z.y, o[kk][u][2] = z.z, o[kk][u][3] = z.w;
+                                                } else {
+                                                    const float2 z = __ldcg(reinterpret_cast<const float2 *>(ps + r * D) + lane);
+                                                    o[kk][u][0] = z.x, o[kk][u][1] = z.y;
+                                                }
                                             }
                                         }
-                                        const float f = fast_exp2(mw - Mr) * iv;
 #pragma unroll
-                                        for (int e = 0; e < 32; ++e) v[e] += f * o[e];
+                                        for (int kk = 0; kk < KB; ++kk) {
+                                            if (k + kk >= npieces) break;
+#pragma unroll
+                                            for (int u = 0; u < RB; ++u) {
+                                                const float f = fast_exp2(mk[kk][u] - mr[u].x) * mr[u].y;
+#pragma unroll
+                                                for (int e = 0; e < V; ++e) acc[u][e] += f * o[kk][u][e];
+                                            }
+                                        }
+                                    }
+                                    unsigned bad = 0;  // rows that are not finite
+#pragma unroll
+                                    for (int u = 0; u < RB; ++u) {
+                                        const int r = g0 + 4 * u;
+                                        if (r >= rows) break;
+                                        bool fine = true;
+#pragma unroll
+                                        for (int e = 0; e < V; ++e) fine = fine && fabsf(acc[u][e]) <= 3.4028234e38f;
+                                        if (!__all_sync(0xffffffffu, fine)) bad |= 1u << u;
+                                        uint32_t *dst = reinterpret_cast<uint32_t *>(
+                                            a.out + (int64_t(x.r0 + w * RQ + r / G) * a.Hq + x.kvh * G + r % G) * D) + lane * (V / 2);
+                                        if constexpr (V == 4)
+                                            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(acc[u][0], acc[u][1]),
+                                                                                         pack_bf16x2(acc[u][2], acc[u][3]));
+                                        else
+                                            *dst = pack_bf16x2(acc[u][0], acc[u][1]);
+                                    }
+                                    for (; bad; bad &= bad - 1) {
+                                        const int r = g0 + 4 * (__ffs(bad) - 1), rir = w * RQ + r / G;
+                                        redo_row<D>(a, x.s, x.kvh, x.r0 + rir, r % G, max(base + rir, 0));
                                     }
                                 }
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) fine = fine && fabsf(v[e]) <= 3.4028234e38f;
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    y[4 * q + e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]),
-                                                              pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
-                                                              pack_bf16x2(v[8 * e + 4], v[8 * e + 5]),
-                                                              pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+                                __syncwarp();
                             }
-                            store_rows(y, [&](int, int64_t ro) { return a.out + ro * D + 64 * c2; });
                         }
-                        bad = __ballot_sync(0xffffffffu, act && !fine);
-                    }
-                    // ---- rows that are not finite, again over their own tokens only (in fp32, a row per warp)
-                    __syncwarp();
-                    for (unsigned again = bad; again;) {
-                        const int src = __ffs(again) - 1;
-                        again &= again - 1;
-                        const int rs1 = __shfl_sync(0xffffffffu, S1, src), rlo = __shfl_sync(0xffffffffu, lo, src);
-                        const int rlim = __shfl_sync(0xffffffffu, lim, src);
-                        const int64_t ro = __shfl_sync(0xffffffffu, orow, src);
-                        constexpr int V = D / 32;
-                        float q[V], acc[V], M = -INFINITY, Ls = 0.f;
-#pragma unroll
-                        for (int k = 0; k < V; ++k) {
-                            q[k] = __uint_as_float(uint32_t(a.q[ro * D + lane * V + k]) << 16);
-                            acc[k] = 0.f;
-                        }
-                        const int cnt = rs1 + max(rlim - rlo, 0);
-                        for (int k = 0; k < cnt; ++k) {
-                            const int tk = k < rs1 ? k : k - rs1 + rlo;
-                            const int phb = __ldg(a.bt + int64_t(x.s) * a.MBS + tk / BS);
-                            if (phb < 0 || int64_t(phb) >= a.NB) continue;
-                            const int64_t off = ((int64_t(phb) * BS + tk % BS) * Hkv + x.kvh) * D + lane * V;
-                            float z = 0.f;
-#pragma unroll
-                            for (int e = 0; e < V; ++e)
-                                z = fmaf(q[e], __uint_as_float(uint32_t(static_cast<const uint16_t *>(a.kc)[off + e]) << 16), z);
-#pragma unroll
-                            for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-                            z *= a.scale_log2;
-                            const float Mn = fmaxf(M, z);
-                            const float f = M == -INFINITY ? 0.f : fast_exp2(M - Mn), pp = fast_exp2(z - Mn);
-                            M = Mn;
-                            Ls = Ls * f + pp;
-#pragma unroll
-                            for (int e = 0; e < V; ++e)
-                                acc[e] = acc[e] * f + pp * __uint_as_float(uint32_t(static_cast<const uint16_t *>(a.vc)[off + e]) << 16);
-                        }
-#pragma unroll
-                        for (int e = 0; e < V; ++e)
-                            a.out[ro * D + lane * V + e] = __bfloat16_as_ushort(__float2bfloat16_rn(Ls > 0.f ? acc[e] / Ls : Ls != Ls ? Ls : 0.f));
                     }
                 }
             }
@@ -882,13 +906,129 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
     }
 }
 
+// The rows of the units that were cut between CTAs: the unit that begins in CTA
+// blockIdx.x's range and leaves it, if there is one; a warp per row (RB of them at
+// a time), its columns side by side, KB pieces in flight. Bound by latency. For
+// calls with fewer units than half the CTAs, whose units have several pieces each:
+// one CTA would read them all. Merged by the last piece's CTA and by this kernel
+// (which costs 1.6 us of the host as well): 8 sequences of 5 rows on 4000 tokens
+// 31.7 and 27.1 us, 2 of 64 rows 47.0 and 30.4; with 128 units on 152 CTAs, 32
+// sequences of 2 rows on 3000 tokens, 49.2 and 55.2.
+template <int D>
+__global__ void __launch_bounds__(256) cut_join_kernel(const SubsetArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    constexpr int V = D / 32, RB = 4, KB = 4, SLOT = RowCfg<D>::SLOT;
+    const int4 *rec = reinterpret_cast<const int4 *>(a.cuts + blockIdx.x);
+    const int4 c0 = __ldcg(rec), c1 = __ldcg(rec + 1);
+    const CutUnit u{c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, {}};
+    if (u.pieces < 2) return;
+    const int lane = threadIdx.x & 31, step = int(gridDim.y) * 8;
+    const int G = a.G, RQ = kTileTok / G, rows = u.nr * G, np = u.pieces;
+    auto slot = [&](int k) { return a.slots + (2 * int64_t(blockIdx.x + k) + (k == 0)) * SLOT; };
+    for (int g0 = int(blockIdx.y) * 8 + int(threadIdx.x >> 5); g0 < rows; g0 += RB * step) {
+        int at[RB];  // the row's place in its row tile, -1: none; floats of the row tiles before
+        int before[RB];
+        float acc[RB][V], M[RB], L[RB], o[KB][RB][V];
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+            const int g = g0 + i * step, w = g >= RQ * G;
+            at[i] = g < rows ? g - w * RQ * G : -1;
+            before[i] = w * (SLOT / 2);
+            M[i] = -INFINITY;
+            L[i] = 0.f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[i][e] = 0.f;
+        }
+        auto load = [&](int k) {  // pieces k ...
+#pragma unroll
+            for (int j = 0; j < KB; ++j)
+#pragma unroll
+                for (int i = 0; i < RB; ++i) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) o[j][i][e] = 0.f;
+                    if (k + j >= np || at[i] < 0) continue;
+                    const float *ps = slot(k + j) + before[i] + at[i] * D;
+                    if constexpr (V == 4) {
+                        const float4 z = __ldcg(reinterpret_cast<const float4 *>(ps) + lane);
+                        o[j][i][0] = z.x, o[j][i][1] = z.y, o[j][i][2] = z.z, o[j][i][3] = z.w;
+                    } else {
+                        const float2 z = __ldcg(reinterpret_cast<const float2 *>(ps) + lane);
+                        o[j][i][0] = z.x, o[j][i][1] = z.y;
+                    }
+                }
+        };
+        for (int k0 = 0; k0 < np; k0 += 32) {
+            load(k0);
+            float m[RB], l[RB], f[RB];  // of piece k0 + lane
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                const bool in = k0 + lane < np && at[i] >= 0;
+                const float *ps = slot(in ? k0 + lane : 0) + before[i] + 128 * D + max(at[i], 0);
+                m[i] = in ? __ldcg(ps) : -INFINITY;
+                l[i] = in ? __ldcg(ps + 128) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                float mx = m[i];
+#pragma unroll
+                for (int s = 16; s >= 1; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+                const float Mn = fmaxf(M[i], mx), old = M[i] == -INFINITY ? 0.f : fast_exp2(M[i] - Mn);
+                f[i] = m[i] == -INFINITY ? 0.f : fast_exp2(m[i] - Mn);
+                float sum = m[i] == -INFINITY ? l[i] : l[i] * f[i];
+#pragma unroll
+                for (int s = 16; s >= 1; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+                L[i] = L[i] * old + sum;
+                M[i] = Mn;
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[i][e] *= old;
+            }
+            for (int k = k0; k < min(k0 + 32, np); k += KB) {
+                if (k > k0) load(k);
+#pragma unroll
+                for (int j = 0; j < KB; ++j)
+#pragma unroll
+                    for (int i = 0; i < RB; ++i) {
+                        const float w = __shfl_sync(0xffffffffu, f[i], (k - k0 + j) & 31);  // 0 past the last piece
+#pragma unroll
+                        for (int e = 0; e < V; ++e) acc[i][e] += w * o[j][i][e];
+                    }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+            if (at[i] < 0) break;
+            const float iv = L[i] == 0.f ? 0.f : 1.f / L[i];  // NaN stays NaN
+            bool fine = true;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                acc[i][e] *= iv;
+                fine = fine && fabsf(acc[i][e]) <= 3.4028234e38f;
+            }
+            const int g = g0 + i * step, ir = g / G, h = g - ir * G;
+            if (!__all_sync(0xffffffffu, fine)) {
+                redo_row<D>(a, u.s, u.kvh, u.r0 + ir, h, max(u.base + ir, 0));
+                continue;
+            }
+            uint32_t *out = reinterpret_cast<uint32_t *>(a.out + (int64_t(u.r0 + ir) * a.Hq + u.kvh * G + h) * D) +
+                            lane * (V / 2);
+#pragma unroll
+            for (int e = 0; e < V; e += 2) out[e / 2] = pack_bf16x2(acc[i][e], acc[i][e + 1]);
+        }
+    }
+}
+
 template <int D, bool PREFIX>
 cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tq, const SubsetArgs &a,
                      int grid, cudaStream_t stream) {
     const auto kernel = row_tiles_kernel<D, PREFIX>;
     const cudaError_t e = smem_once(reinterpret_cast<const void *>(kernel), RowCfg<D>::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3(grid), dim3(kWarpsRT * 32), RowCfg<D>::SMEM, stream, tk, tv, tq, a);
+    const cudaError_t f = launch_pdl(kernel, dim3(grid), dim3(kWarpsRT * 32), RowCfg<D>::SMEM, stream, tk, tv, tq, a);
+    if (PREFIX || f != cudaSuccess || !a.cuts) return f;
+    // 32 rows per slice, by the average unit
+    const int rows = std::min(2 * (kTileTok / a.G), (a.rows + a.nseq - 1) / a.nseq) * a.G;
+    return launch_pdl(cut_join_kernel<D>, dim3(grid, (rows + 31) / 32), dim3(256), 0, stream, a);
 }
 
 }  // namespace
@@ -899,6 +1039,8 @@ cudaError_t launch_row_tiles(const CUtensorMap &tk, const CUtensorMap &tv, const
                              const SubsetArgs &args, int head_dim, int sms, cudaStream_t stream) {
     SubsetArgs a = args;
     a.min_items = kMinTiles;
+    const int per_unit = 2 * (kTileTok / a.G);  // query rows
+    if (int64_t(a.Hkv) * std::max(a.nseq, (a.rows + per_unit - 1) / per_unit) * 2 > sms) a.cuts = nullptr;
     const int grid = a.pt ? a.pgrid : sms;
     if (a.pt) return head_dim == 128 ? launch_t<128, true>(tk, tv, tq, a, grid, stream) : launch_t<64, true>(tk, tv, tq, a, grid, stream);
     return head_dim == 128 ? launch_t<128, false>(tk, tv, tq, a, grid, stream) : launch_t<64, false>(tk, tv, tq, a, grid, stream);

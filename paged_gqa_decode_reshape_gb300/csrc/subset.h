@@ -17,6 +17,13 @@ constexpr int kMaxWindowRows = 1 << 20;  // query rows of a windowed multi-token
 
 enum CacheKind { kCacheBf16 = 0, kCacheE4m3 = 1, kCacheE4m3Block = 2 };
 
+// A unit of the row-tile kernel that was cut between CTAs: query rows r0 ..
+// r0 + nr - 1 of sequence s and KV head kvh, row r0 + i seeing tokens before
+// base + i, in `pieces` pieces from the CTA on in whose range it begins.
+struct alignas(16) CutUnit {
+    int s, kvh, r0, nr, base, pieces, pad[2];
+};
+
 // Attention of query rows over the tokens a row sees:
 //   its sequence's prefix (pt / plen: the prefix blocks of its group), then
 //   its own tokens t < lim with t < sinks or t >= lim - window.
@@ -36,11 +43,11 @@ struct SubsetArgs {
     float scale_log2;             // softmax scale * log2(e)
     // workspace
     int32_t *status;              // status word
-    int32_t *counters;            // [workers] arrivals at what begins in a worker's range and leaves it (zero between calls);
-                                  // row tiles: two per CTA
+    int32_t *counters;            // [workers] arrivals at what begins in a worker's range and leaves it (zero between calls)
     float *part;                  // [2 * workers] pieces of segments cut between workers: O, m, l
     float *slots;                 // [2 * CTAs] pieces of row-tile units cut between CTAs
     float *rowres, *rowml;        // prefixes: [rows][Hq][D] O and [rows][Hq][2] m, l of units that were not cut
+    CutUnit *cuts;                // row tiles over windows: [CTAs] the cut unit that begins in each range
     int4 *desc;                   // prefixes: [rows][Hkv] first CTA, pieces, row tile, first row in it
     int pgrid;                    // prefixes: CTAs of the row-tile kernel
     float *ownres, *ownml;        // prefixes: [rows][Hq][D] O and [rows][Hq][2] m, l of the own tokens (else null)
