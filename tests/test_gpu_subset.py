@@ -605,11 +605,13 @@ def test_no_workspace_is_allocated_during_capture():
 # ----------------------------------------------- values, extents, long calls
 
 
-def test_window_multi_keeps_nan_and_inf_of_unseen_tokens_out():
+@pytest.mark.parametrize("more", [0, 60])  # cut units: merged by a kernel of their own, or by the last CTA
+@pytest.mark.parametrize("window", [64, 350])
+def test_window_multi_keeps_nan_and_inf_of_unseen_tokens_out(window, more):
     """A token whose K or V is not finite reaches the rows that see it and no
     other row, although rows of one tile share its matrix products."""
     Hq, Hkv, D = 14, 2, 128
-    ctx, ql, window, sinks = [400, 300], [30, 300], 64, 3
+    ctx, ql, sinks = [400, 300] + [500] * more, [30, 300] + [2] * more, 3
     g, kc, vc, bt, _, _ = pool(41, ctx, Hkv, D)
     bad = {0: [390, 399], 1: [1, 40, 200, 299]}
     for b, ts in bad.items():
@@ -618,9 +620,9 @@ def test_window_multi_keeps_nan_and_inf_of_unseen_tokens_out():
             vc[blk, o, 0, 5 * n:5 * n + 3] = float("inf") if n % 2 else NAN
             if n == 1:
                 kc[blk, o, 1, 7] = NAN
-    cu = torch.tensor([0, 30, 330], dtype=torch.int32)
-    q = bf16(g, 330, Hq, D)
-    out = torch.full((330, Hq, D), 7.0, dtype=torch.bfloat16, device=DEV)
+    cu = torch.tensor([0] + torch.tensor(ql).cumsum(0).tolist(), dtype=torch.int32)
+    q = bf16(g, sum(ql), Hq, D)
+    out = torch.full((sum(ql), Hq, D), 7.0, dtype=torch.bfloat16, device=DEV)
     pg.pa_decode_window_multi(out, *dev(q, kc, vc, bt, cu, torch.tensor(ctx, dtype=torch.int32)), window, sinks, 0.1)
     got = out.cpu()
     for b in range(2):

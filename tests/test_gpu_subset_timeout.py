@@ -38,11 +38,12 @@ def flib():
 
 
 @pytest.mark.parametrize("stop_item", [0, 1])  # every warp and CTA here has at least two copies to make
-@pytest.mark.parametrize("op", ["window", "window_many", "window_multi", "prefix", "weights"])
+@pytest.mark.parametrize("op", ["window", "window_many", "window_multi", "multi_many", "prefix", "weights"])
 def test_wait_runs_out_then_status_and_recovery(flib, op, stop_item):
     Hq, Hkv, D, scale = 28, 4, 128, 0.0884
     # window: a piece of a segment per CTA; window_many: a range of segments per warp
-    lens = [200] * 250 if op == "window_many" else [3000, 1700, 2999, 800]
+    # window_multi: cut units merged by a kernel of their own; multi_many: by the CTA of the last piece
+    lens = [200] * 250 if op == "window_many" else [700] * 40 if op == "multi_many" else [3000, 1700, 2999, 800]
     B = len(lens)
     g, kc, vc, bt, _, _ = pool(7, lens + [900], Hkv, D)
     bt, pt = bt[:B].contiguous(), bt[B:].contiguous()
@@ -54,6 +55,7 @@ def test_wait_runs_out_then_status_and_recovery(flib, op, stop_item):
     out = torch.empty_like(q_)
     MBS, NB = bt.shape[1], kc.shape[0]
     size = {"window_multi": lambda: pg.pa_decode_window_multi_workspace_size(B, B, Hq, Hkv, D),
+            "multi_many": lambda: pg.pa_decode_window_multi_workspace_size(B, B, Hq, Hkv, D),
             "prefix": lambda: pg.pa_decode_prefix_workspace_size(B, 1, Hq, Hkv, D),
             "weights": lambda: pg.pa_decode_weights_workspace_size(B, Hq, Hkv, D, MBS)}
     ws = torch.zeros(size.get(op, lambda: pg.pa_decode_window_workspace_size(B, Hq, Hkv, D))(), dtype=torch.uint8,
@@ -65,7 +67,7 @@ def test_wait_runs_out_then_status_and_recovery(flib, op, stop_item):
     def call():
         if op in ("window", "window_many"):
             rc = flib.pa_decode_window(o, x, k, v, t, MBS, c, B, *shape, 1 << 20, 0, *tail)
-        elif op == "window_multi":
+        elif op in ("window_multi", "multi_many"):
             rc = flib.pa_decode_window_multi(o, x, k, v, t, MBS, cu.data_ptr(), c, B, B, *shape, 1 << 20, 0, *tail)
         elif op == "prefix":
             one, grp = i32(900), i32(0, B)
