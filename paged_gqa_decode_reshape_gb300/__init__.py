@@ -1146,6 +1146,8 @@ def _lookup(key):
     if shape is not None:
         size = name[:-len("_fp8_block")] if name.endswith("_fp8_block") else name.removesuffix("_fp8")
         nbytes = getattr(L, size + "_workspace_size")(*shape)
+    if len(_calls) >= 4096:  # row counts that change with every call
+        _calls.clear()
     found = _calls[key] = getattr(L, name), nbytes
     return found
 

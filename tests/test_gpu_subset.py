@@ -832,3 +832,19 @@ def test_one_workspace_serves_every_operator_of_the_section():
         n, f, q = calls[i]
         got = f(torch.empty_like(q), shared)
         assert torch.equal(got.view(torch.int16), alone[i].view(torch.int16)), i
+
+
+def test_row_counts_that_change_with_every_call():
+    """The binding's table of workspace sizes stays bounded, and calls are right before and after it is emptied."""
+    Hq, Hkv, D = 8, 2, 64
+    g, kc, vc, bt, _, _ = pool(9, [40], Hkv, D, spoil=False)
+    q = bf16(g, 5000, Hq, D)
+    q_, kc_, vc_, bt_, ctx_ = dev(q, kc, vc, bt, torch.tensor([40], dtype=torch.int32))
+    cu_ = torch.tensor([0, 3], dtype=torch.int32, device=DEV)
+    first = None
+    for T in range(3, 4600, 1):
+        out = pg.pa_decode_window_multi(torch.empty_like(q_[:T]), q_[:T], kc_, vc_, bt_, cu_, ctx_, 16, 1, 0.1)
+        if T % 500 == 3 or T > 4590:
+            first = out[:3].clone() if first is None else first
+            assert torch.equal(out[:3].view(torch.int16), first.view(torch.int16)), T
+    assert len(pg._calls) <= 4096
