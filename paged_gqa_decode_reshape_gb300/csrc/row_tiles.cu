@@ -10,9 +10,9 @@
 // Bound: 4 D flops per (row, token) against 4 D bytes per token and KV head:
 // with R rows sharing the tokens R flops per byte, so a call is bound by HBM
 // below a few hundred rows and by the products above. Measured (28 / 4 heads of
-// 128, windows of 4096): 3 prompt chunks of 517 to 2048 rows 248 us = 1.25 PFLOP/s,
-// 66 % of what a large library product reaches; 32 sequences of 1 to 6 rows 55 us
-// = 3.5 TB/s. What holds the products back (the same call with parts left out):
+// 128, windows of 4096): 3 prompt chunks of 517 to 2048 rows 250 us = 1.24 PFLOP/s,
+// 66 % of what a large library product reaches; 32 sequences of 1 to 6 rows 53 us
+// = 3.7 TB/s. What holds the products back (the same call with parts left out):
 // without any softmax 203 us, without its exponentials, maxima and sums 226, with
 // a quarter of the K/V copies 229. S = Q K^T out of shared memory moves 128 bytes
 // per clock, all there is, next to the copies' 64 KB per step; one row tile's

@@ -37,8 +37,12 @@
 //    mask per block says which tokens are seen; the V rows of the others (they
 //    may hold NaN) are zeroed in the stage, which only edge blocks need.
 //  * A segment cut between workers leaves (O, m, l) per piece in the workspace,
-//    and the worker that completes its arrival counter merges them, in piece
-//    order: the result does not depend on who is last.
+//    and the worker that completes its arrival counter merges them (a CTA:
+//    each warp every NW-th piece, then the warps), in an order that does not
+//    depend on who is last.
+//  * Accumulated weights (LOGITS): the logits go to the workspace on the way, and
+//    once the normaliser is known p_t = 2^(z_t - lse) is added to the weights, by
+//    the CTA that has it or by a second launch. The normaliser sums the fp32 p_t.
 #include <climits>
 
 #include "common.cuh"
