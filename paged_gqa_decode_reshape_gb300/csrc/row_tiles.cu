@@ -237,7 +237,19 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
     }
     // ---- tiles per KV head of groups of `str` sequences, and their prefix sums
     const int ns = work.count(), str = (ns + kPreCap - 1) / kPreCap, np = (ns + str - 1) / str;
+    // by a thread where sequences have a unit or two, so that many are looked up at once, else by a warp
+    for (int i = tid; i < np; i += kWarpsRT * 32) {
+        int64_t t = 0;
+        for (int s = i * str; t >= 0 && s < min((i + 1) * str, ns); ++s) {
+            const int nu = work.units(s);
+            for (int u = 0; u < min(nu, 2); ++u) t += work.unit(s, 0, u).n;
+            if (nu > 2) t = -1;
+        }
+        pre[i + 1] = t;
+    }
+    __syncthreads();
     for (int i = warp; i < np; i += kWarpsRT) {
+        if (pre[i + 1] >= 0) continue;
         int64_t t = 0;
         for (int s = i * str; s < min((i + 1) * str, ns); ++s) t += work.tiles(s);
         if (lane == 0) pre[i + 1] = t;
