@@ -855,7 +855,7 @@ SubsetArgs subset_args(pa_bf16 *out, const pa_bf16 *query, const void *kc, const
 }
 
 // What a call of this section needs: the streaming kernel (one query row per
-// sequence), the row-tile kernel (many), or one after the other (prefixes).
+// sequence), the row-tile kernel (many), or both (prefixes, unless they are small).
 struct SubsetPlan {
     bool stream, tiles, prefix;
     int64_t logit_blocks;  // accumulated weights: max_blocks_per_seq
@@ -949,6 +949,19 @@ int prefix_ctas(const SubsetArgs &a, int D, int sms) {
     return n < 1 ? 1 : n > sms - 1 ? (sms > 1 ? sms - 1 : 1) : n;
 }
 
+// Small calls read a prefix once per sequence (from L2, but for the first time):
+// one launch of the streaming kernel over prefix and own tokens, instead of three
+// launches one after another. By what the tables hold at most, the own tokens at
+// half of it, up to kEachReads bytes. Each and shared, 28 / 4 heads of 128: 2
+// sequences behind 500 tokens (2 MB) 6.1 and 14.9 us, 8 behind 2000 (33 MB) 9.9 and
+// 16.2, 32 behind 1000 (69 MB) 11.5 and 17.6, 8 behind 8000 (127 MB) 18.6 and 20.5, 64
+// behind 1000 (131 MB) 20.7 and 19.6, 64 behind 8192 90 and 34; and 4 us of the host.
+constexpr int64_t kEachReads = int64_t(120) << 20;
+
+bool reads_each(const SubsetArgs &a, int D) {
+    return int64_t(a.rows) * a.Hkv * (int64_t(a.PMBS) + a.MBS / 2) * kBlockSize * D * 4 <= kEachReads;
+}
+
 // the launches, after the argument checks
 int run_subset(SubsetArgs a, const SubsetPlan &plan, int D, CacheKind kind, void *workspace, size_t workspace_bytes,
                void *stream) {
@@ -969,6 +982,8 @@ int run_subset(SubsetArgs a, const SubsetPlan &plan, int D, CacheKind kind, void
     a.desc = reinterpret_cast<int4 *>(p + w.desc);
     a.lse = reinterpret_cast<float *>(p + w.lse);
     a.logits = reinterpret_cast<float *>(p + w.logits);
+    const bool each = plan.prefix && reads_each(a, D);
+    if (each) a.ownres = nullptr;
     if (plan.prefix) a.pgrid = prefix_ctas(a, D, w.sms);
     a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
     a.stop_item = g_stop_item.load(std::memory_order_relaxed);
@@ -981,16 +996,16 @@ int run_subset(SubsetArgs a, const SubsetPlan &plan, int D, CacheKind kind, void
     if (plan.stream && (rc = fp8 ? make_cache_map(&tk, a.kc, a.Hkv, D, kBlockSize, a.NB, true)
                                  : make_block_map(&tk, a.kc, a.Hkv, D, a.NB)) != PA_OK)
         return rc;
-    if (plan.tiles && (rc = make_cache_map(&tk_half, a.kc, a.Hkv, D, kBlockSize, a.NB)) != PA_OK) return rc;
+    if (plan.tiles && !each && (rc = make_cache_map(&tk_half, a.kc, a.Hkv, D, kBlockSize, a.NB)) != PA_OK) return rc;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
-    if (plan.tiles) {
+    if (plan.tiles && !each) {
         CUtensorMap tq;
         if ((rc = make_query_map(&tq, a.q, a.rows, a.Hq, a.G, D)) != PA_OK) return rc;
         e = launch_row_tiles(tk_half, tv, tq, a, D, w.sms, st);
     }
-    if (e == cudaSuccess && plan.stream) e = launch_stream_decode(tk, tv, a, D, kind, plan.prefix ? w.sms - a.pgrid : w.sms, st);
-    if (e == cudaSuccess && plan.prefix) e = launch_prefix_join(a, D, st);
+    if (e == cudaSuccess && plan.stream) e = launch_stream_decode(tk, tv, a, D, kind, plan.prefix && !each ? w.sms - a.pgrid : w.sms, st);
+    if (e == cudaSuccess && plan.prefix && !each) e = launch_prefix_join(a, D, st);
     return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 

@@ -1,7 +1,7 @@
 // stream_decode.cu -- one-query-row decode over a part of the cache (sm_103a):
 // the sliding window with sinks, the dense decode that also stores its logits
-// (for the accumulated weights), and the own tokens of a sequence whose
-// prefix was attended to separately.
+// (for the accumulated weights), short prefixes with the own tokens behind them,
+// and the own tokens of a sequence whose prefix is attended to separately.
 //
 // For KV head g of sequence b and the query heads h of its group, over the
 // tokens t the row sees (z_t = scale * log2(e) * q_h . K_t):
@@ -111,19 +111,38 @@ struct StreamCfg {
     static constexpr size_t SMEM = 1024 + off_pre + (kPreCap + 1) * 8;
 };
 
-// a sequence's visible tokens [0, s1) and [lo, lim), as items
+// what the streaming kernel is run for
+enum StreamMode { kPlain, kLogits, kPrefixed };
+
+// a sequence's visible tokens [0, s1) and [lo, lim), as items; kPrefixed: the s1
+// tokens of its group's prefix (group pg, -1: none), then its own [0, lim)
 struct Span {
     int lim, s1, lo, nb1, jw, nb, n;  // nb1 sink blocks, then blocks jw, jw + 1, ...; nb blocks, n items (at least one)
+    int pg;
     __device__ int block(int e) const { return e < nb1 ? e : e - nb1 + jw; }  // logical block of list entry e
 };
 
+template <StreamMode MODE>
 __device__ __forceinline__ Span span_of(const SubsetArgs &a, int b) {
     Span s;
     s.lim = min(max(__ldg(a.ctx + b), 0), a.MBS * kBlockSize);
-    s.s1 = min(a.sinks, s.lim);
-    s.lo = max(s.s1, a.window >= s.lim ? 0 : s.lim - a.window);
-    s.nb1 = (s.s1 + kBlockSize - 1) / kBlockSize;
-    s.jw = max(s.lo / kBlockSize, s.nb1);
+    if constexpr (MODE == kPrefixed) {
+        int lo = 0, hi = a.ngroups;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (__ldg(a.cu_g + mid) <= b) lo = mid; else hi = mid;
+        }
+        s.pg = b >= __ldg(a.cu_g + lo) && b < __ldg(a.cu_g + lo + 1) ? lo : -1;
+        s.s1 = s.pg < 0 ? 0 : min(max(__ldg(a.plen + lo), 0), a.PMBS * kBlockSize);
+        s.lo = s.jw = 0;
+        s.nb1 = (s.s1 + kBlockSize - 1) / kBlockSize;
+    } else {
+        s.pg = -1;
+        s.s1 = min(a.sinks, s.lim);
+        s.lo = max(s.s1, a.window >= s.lim ? 0 : s.lim - a.window);
+        s.nb1 = (s.s1 + kBlockSize - 1) / kBlockSize;
+        s.jw = max(s.lo / kBlockSize, s.nb1);
+    }
     s.nb = s.nb1 + max((s.lim + kBlockSize - 1) / kBlockSize - s.jw, 0);
     s.n = max((s.nb + 1) / 2, 1);
     return s;
@@ -228,13 +247,13 @@ __device__ __forceinline__ void add_weights(const SubsetArgs &a, int b, int kvh,
     }
 }
 
-template <int D, CacheKind KIND, bool LOGITS>
+template <int D, CacheKind KIND, StreamMode MODE>
 __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
     stream_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const SubsetArgs a) {
     using C = StreamCfg<D, KIND>;
     constexpr int NW = C::NW, R = C::R, NKK = C::NKK, BS = kBlockSize;
-    constexpr bool F8 = C::F8, PSC = KIND == kCacheE4m3Block;
+    constexpr bool F8 = C::F8, PSC = KIND == kCacheE4m3Block, LOGITS = MODE == kLogits;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -269,7 +288,7 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
         int *cnt = reinterpret_cast<int *>(pre);  // items, then pieces per sequence and their prefix
         int *found = reinterpret_cast<int *>(sm_ml);
         int nmax = 0;
-        for (int i = tid; i < a.nseq; i += C::THREADS) cnt[i + 1] = span_of(a, i).n;
+        for (int i = tid; i < a.nseq; i += C::THREADS) cnt[i + 1] = span_of<MODE>(a, i).n;
         __syncthreads();
         int64_t sum = 0;
         for (int i = lane; i < a.nseq; i += 32) {
@@ -331,7 +350,7 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
         kvh = rem / npieces;
         piece = rem - kvh * npieces;
         w0 = int(blockIdx.x) - piece;
-        sp = span_of(a, b);
+        sp = span_of<MODE>(a, b);
         first = int64_t(sp.n) * piece / npieces + warp;
         last = int64_t(sp.n) * (piece + 1) / npieces;
     } else {
@@ -340,7 +359,7 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
         np = (a.nseq + str - 1) / str;
         for (int i = tid; i < np; i += C::THREADS) {
             int64_t n = 0;
-            for (int j = i * str; j < min((i + 1) * str, a.nseq); ++j) n += span_of(a, j).n + kEndCost;
+            for (int j = i * str; j < min((i + 1) * str, a.nseq); ++j) n += span_of<MODE>(a, j).n + kEndCost;
             pre[i + 1] = n;
         }
         if (tid == 0) pre[0] = 0;
@@ -377,10 +396,10 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
         }
         int q = lo * str;
         rem = p - int64_t(Hkv) * pre[lo];
-        s = span_of(a, q);
+        s = span_of<MODE>(a, q);
         while (rem >= int64_t(Hkv) * (s.n + kEndCost) && q + 1 < a.nseq) {
             rem -= int64_t(Hkv) * (s.n + kEndCost);
-            s = span_of(a, ++q);
+            s = span_of<MODE>(a, ++q);
         }
         return q;
     };
@@ -408,12 +427,22 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
             w.head = int(rem / (s.n + kEndCost));
             e = 2 * int(rem - int64_t(w.head) * (s.n + kEndCost));
         }
-        const int32_t *row = a.bt + int64_t(q) * a.MBS;
-        const int j0 = s.block(e), j1 = s.block(e + 1);
-        const int ph0 = e < s.nb ? __ldg(row + j0) : -1, ph1 = e + 1 < s.nb ? __ldg(row + j1) : -1;
-        w.j = j0;
-        const uint32_t m0 = bits_between(0, s.s1, j0 * BS) | bits_between(s.lo, s.lim, j0 * BS);
-        const uint32_t m1 = bits_between(0, s.s1, j1 * BS) | bits_between(s.lo, s.lim, j1 * BS);
+        // physical block and token mask of list entry e
+        auto entry = [&](int e, int &phys, uint32_t &mask) {
+            const int j = s.block(e), t = j * BS;
+            if (MODE == kPrefixed && e < s.nb1) {
+                phys = __ldg(a.pt + int64_t(s.pg) * a.PMBS + e);
+                mask = bits_between(0, s.s1, t);
+            } else {
+                phys = e < s.nb ? __ldg(a.bt + int64_t(q) * a.MBS + j) : -1;
+                mask = (MODE == kPrefixed ? 0u : bits_between(0, s.s1, t)) | bits_between(s.lo, s.lim, t);
+            }
+        };
+        int ph0, ph1;
+        uint32_t m0, m1;
+        entry(e, ph0, m0);
+        entry(e + 1, ph1, m1);
+        w.j = s.block(e);
         if (ph0 >= 0 && int64_t(ph0) < a.NB) {
             w.p0 = ph0;
             w.mask = m0;
@@ -430,8 +459,8 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
             w.sc = make_float4(__ldg(a.k_scale + i0), __ldg(a.v_scale + i0), __ldg(a.k_scale + i1), __ldg(a.v_scale + i1));
         }
     };
-    // with a prefix: what came before the row-tile kernel is complete already, and nothing of
-    // that kernel's is read here
+    // beside the row-tile kernel: what came before that is complete already, and nothing of its
+    // results is read here
     if (!a.ownres) pdl_wait();
     Win cur = resolve(0), nxt = resolve(32);
     scales(cur);
@@ -846,7 +875,7 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
                 s0 = end;
                 if (++kvh == Hkv) {
                     kvh = 0;
-                    sp = span_of(a, ++b);
+                    sp = span_of<MODE>(a, ++b);
                 }
                 fetch_q(b, kvh);
             }
@@ -899,7 +928,7 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
     // after a wait that gave up: no copy may land in memory of a CTA that is gone
     if (dead && lane == 0)
         for (int st = 0; st < R; ++st) mbar_wait_bounded(bars + st * 8, ((armed >> st) & 1u) ^ 1u, a.wait_ns);
-    // with a prefix: this kernel is complete when the row-tile kernel is, so that the next need wait for one only
+    // beside the row-tile kernel: this one is complete when that is, so that the next need wait for one only
     if (a.ownres && blockIdx.x == 0) pdl_wait();
 }
 
@@ -915,11 +944,11 @@ __global__ void __launch_bounds__(kAddThreads) weights_add_kernel(const SubsetAr
     add_weights<1>(a, b, kvh, lim, ls, blockIdx.y * kAddThreads + threadIdx.x, gridDim.y * kAddThreads);
 }
 
-template <int D, CacheKind KIND, bool LOGITS>
+template <int D, CacheKind KIND, StreamMode MODE>
 cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const SubsetArgs &a, int grid,
                      cudaStream_t stream) {
     using C = StreamCfg<D, KIND>;
-    const auto kernel = stream_decode_kernel<D, KIND, LOGITS>;
+    const auto kernel = stream_decode_kernel<D, KIND, MODE>;
     const cudaError_t e = smem_once(reinterpret_cast<const void *>(kernel), C::SMEM);
     if (e != cudaSuccess) return e;
     return launch_pdl(kernel, dim3(grid), dim3(C::THREADS), C::SMEM, stream, tk, tv, a);
@@ -1006,17 +1035,20 @@ cudaError_t launch_stream_decode(const CUtensorMap &tk, const CUtensorMap &tv, c
     if (a.weights) {
         SubsetArgs f = a;
         f.fused_add = int64_t(a.nseq) * a.Hkv <= sms && a.MBS <= kFusedAddBlocks * a.nseq * a.Hkv;
-        cudaError_t e = head_dim == 128 ? launch_t<128, kCacheBf16, true>(tk, tv, f, sms, stream)
-                                        : launch_t<64, kCacheBf16, true>(tk, tv, f, sms, stream);
+        cudaError_t e = head_dim == 128 ? launch_t<128, kCacheBf16, kLogits>(tk, tv, f, sms, stream)
+                                        : launch_t<64, kCacheBf16, kLogits>(tk, tv, f, sms, stream);
         if (e != cudaSuccess || f.fused_add) return e;
         const int per = kAddThreads / (kBlockSize / 4);  // blocks a CTA takes per turn
         const int x = (a.MBS + per - 1) / per;
         return launch_pdl(weights_add_kernel, dim3(a.nseq * a.Hkv, x < 16 ? x : 16), dim3(kAddThreads), 0, stream, a);
     }
-    if (kind == kCacheE4m3) return launch_t<128, kCacheE4m3, false>(tk, tv, a, sms, stream);
-    if (kind == kCacheE4m3Block) return launch_t<128, kCacheE4m3Block, false>(tk, tv, a, sms, stream);
-    return head_dim == 128 ? launch_t<128, kCacheBf16, false>(tk, tv, a, sms, stream)
-                           : launch_t<64, kCacheBf16, false>(tk, tv, a, sms, stream);
+    if (a.pt && !a.ownres)
+        return head_dim == 128 ? launch_t<128, kCacheBf16, kPrefixed>(tk, tv, a, sms, stream)
+                               : launch_t<64, kCacheBf16, kPrefixed>(tk, tv, a, sms, stream);
+    if (kind == kCacheE4m3) return launch_t<128, kCacheE4m3, kPlain>(tk, tv, a, sms, stream);
+    if (kind == kCacheE4m3Block) return launch_t<128, kCacheE4m3Block, kPlain>(tk, tv, a, sms, stream);
+    return head_dim == 128 ? launch_t<128, kCacheBf16, kPlain>(tk, tv, a, sms, stream)
+                           : launch_t<64, kCacheBf16, kPlain>(tk, tv, a, sms, stream);
 }
 
 }  // namespace pa

@@ -50,7 +50,7 @@ struct SubsetArgs {
     CutUnit *cuts;                // row tiles over windows: [CTAs] the cut unit that begins in each range
     int4 *desc;                   // prefixes: [rows][Hkv] first CTA, pieces, row tile, first row in it
     int pgrid;                    // prefixes: CTAs of the row-tile kernel
-    float *ownres, *ownml;        // prefixes: [rows][Hq][D] O and [rows][Hq][2] m, l of the own tokens (else null)
+    float *ownres, *ownml;        // prefixes beside the row tiles: [rows][Hq][D] O and [rows][Hq][2] m, l of the own tokens (else null)
     float *lse;                   // weights: [nseq][Hq] log2 of the normaliser
     float *logits;                // weights: [nseq][Hkv][MBS][G][16] logits (log2 domain)
     uint64_t wait_ns;             // limit of every bounded wait
@@ -75,7 +75,8 @@ inline cudaError_t smem_once(const void *kernel, size_t bytes) {
 }
 
 // one query row per sequence, window and sinks, or (weights set) the dense
-// decode that adds up the attention weights; tk, tv: tensor maps of the caches
+// decode that adds up the attention weights, or (pt set) prefix and own tokens,
+// with ownres the own ones only; tk, tv: tensor maps of the caches
 size_t stream_workers(int sms);
 size_t stream_part_floats(int sms, int head_dim);
 cudaError_t launch_stream_decode(const CUtensorMap &tk, const CUtensorMap &tv, const SubsetArgs &a, int head_dim,

@@ -196,12 +196,18 @@ def test_window_multi_malformed_offsets_stay_in_bounds():
 # ------------------------------------------------------------------ prefix
 
 
+def widened(pt, B, Hkv, D):
+    """Prefix tables so wide that a call for these shapes shares its reads of the prefixes, however short they are."""
+    return torch.nn.functional.pad(pt, (0, (128 << 20) // (B * Hkv * BS * D * 4) + 1), value=-1)
+
+
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("heads", [(28, 4, 128), (8, 8, 128), (32, 4, 64), (5, 5, 64), (6, 2, 128)])
 @pytest.mark.parametrize("plens,sizes,free", [
     ([1], [3], 0), ([130], [1], 2), ([0, 17, 640], [2, 5, 1], 1), ([1000, 129, 16], [40, 2, 20], 0),
     ([2500], [70], 3),
 ])
-def test_prefix(heads, plens, sizes, free):
+def test_prefix(heads, plens, sizes, free, wide):
     Hq, Hkv, D = heads
     B = sum(sizes) + free
     own = [(37 * i * i) % 261 for i in range(B)]
@@ -210,7 +216,8 @@ def test_prefix(heads, plens, sizes, free):
     bt, pt = bt[:B].contiguous(), bt[B:].contiguous()
     cu = torch.tensor([0] + torch.tensor(sizes).cumsum(0).tolist(), dtype=torch.int32)
     q, scale = bf16(g, B, Hq, D, std=2.0), D ** -0.5
-    args = dev(q, kc, vc, pt, torch.tensor(plens, dtype=torch.int32), cu, bt, torch.tensor(own, dtype=torch.int32))
+    args = dev(q, kc, vc, widened(pt, B, Hkv, D) if wide else pt, torch.tensor(plens, dtype=torch.int32), cu, bt,
+               torch.tensor(own, dtype=torch.int32))
     out = torch.full_like(args[0], NAN)
     first = None
     for _ in range(2):
@@ -229,7 +236,8 @@ def test_prefix(heads, plens, sizes, free):
         ref.check(out[b], want, bound, f"sequence {b}")
 
 
-def test_prefix_bad_metadata():
+@pytest.mark.parametrize("wide", [False, True])
+def test_prefix_bad_metadata(wide):
     """A prefix entry outside the pool reads as empty; malformed offsets and lengths stay in bounds."""
     Hq, Hkv, D = 8, 2, 128
     own, plens = [20, 0, 33], [300, 50]
@@ -237,7 +245,8 @@ def test_prefix_bad_metadata():
     bt, pt = bt[:3].contiguous(), bt[3:].contiguous()
     pt[0, 3], pt[0, 18] = -1, kc.shape[0]
     q = bf16(g, 3, Hq, D)
-    q_, kc_, vc_, pt_, bt_, ctx_ = dev(q, kc, vc, pt, bt, torch.tensor(own, dtype=torch.int32))
+    q_, kc_, vc_, pt_, bt_, ctx_ = dev(q, kc, vc, widened(pt, 3, Hkv, D) if wide else pt, bt,
+                                       torch.tensor(own, dtype=torch.int32))
     out = torch.full_like(q_, NAN)
     pl = torch.tensor(plens, dtype=torch.int32, device=DEV)
     pg.pa_decode_prefix(out, q_, kc_, vc_, pt_, pl, torch.tensor([0, 3, 3], dtype=torch.int32, device=DEV), bt_,
@@ -491,10 +500,11 @@ def test_graph_replay_and_other_stream():
     i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)
     ctx, cu, plen, cug = i32(*lens), i32(0, 20, 25, 39, 40), i32(500), i32(0, 3)
     outs = [torch.empty_like(q_) for _ in range(3)] + [torch.empty_like(qm_)]
+    wide = widened(pt_, B, Hkv, D)
     kept, new = torch.empty(B, Hkv, 128, dtype=torch.int32, device=DEV), i32(0, 0, 0, 0)
     calls = [
         lambda: pg.pa_decode_window(outs[0], q_, kc_, vc_, bt_, ctx, 128, 4, 0.1),
-        lambda: pg.pa_decode_prefix(outs[1], q_, kc_, vc_, pt_, plen, cug, bt_, ctx, 0.1),
+        lambda: pg.pa_decode_prefix(outs[1], q_, kc_, vc_, wide, plen, cug, bt_, ctx, 0.1),
         lambda: pg.pa_decode_weights(outs[2], w_, q_, kc_, vc_, bt_, ctx, 0.1),
         lambda: pg.pa_decode_window_multi(outs[3], qm_, kc_, vc_, bt_, cu, ctx, 100, 8, 0.1),
         lambda: pg.pa_evict(kept, new, kc_, vc_, w_, bt_, ctx, dst_, 16),
@@ -669,7 +679,7 @@ def test_sharp_and_growing_logits(scale, std):
     out = torch.empty(24, Hq, D, dtype=torch.bfloat16, device=DEV)
     pg.pa_decode_window_multi(out, *dev(q, kc, vc, bt, cu, ctx), 1 << 30, 0, scale)
     pre = torch.empty(2, Hq, D, dtype=torch.bfloat16, device=DEV)
-    pg.pa_decode_prefix(pre, *dev(q[[0, 20]], kc, vc, bt[:1], ctx[:1], i32(0, 1), bt, ctx), scale)
+    pg.pa_decode_prefix(pre, *dev(q[[0, 20]], kc, vc, widened(bt[:1], 2, Hkv, D), ctx[:1], i32(0, 1), bt, ctx), scale)
     one = torch.empty_like(pre)
     pg.pa_decode_window(one, *dev(q[[0, 20]], kc, vc, bt, ctx), 1 << 30, 0, scale)
     rows = lambda b, n: (ref.rows_at(kc, bt[b], torch.arange(n))[0], ref.rows_at(vc, bt[b], torch.arange(n))[0])
@@ -726,7 +736,7 @@ def test_blocks_past_32_bit_offsets():
     outs = [torch.empty_like(q_) for _ in range(4)]
     pg.pa_decode_window(outs[0], q_, kc_, vc_, bt_, ctx_, 50, 2, 0.1)
     pg.pa_decode_window_multi(outs[1], q_, kc_, vc_, bt_, i32(0, 1, 2).to(DEV), ctx_, 50, 2, 0.1)
-    pg.pa_decode_prefix(outs[2], q_, kc_, vc_, pt_, i32(plen).to(DEV), i32(0, 2).to(DEV), bt_, ctx_, 0.1)
+    pg.pa_decode_prefix(outs[2], q_, kc_, vc_, widened(pt_, 2, Hkv, D), i32(plen).to(DEV), i32(0, 2).to(DEV), bt_, ctx_, 0.1)
     pg.pa_decode_weights(outs[3], w_, q_, kc_, vc_, bt_, ctx_, 0.1)
     total = w_.sum().item()
     kept = torch.empty(2, Hkv, 48, dtype=torch.int32, device=DEV)
@@ -752,7 +762,8 @@ def test_blocks_past_32_bit_offsets():
     assert abs(total - 2 * Hq) < 1e-3  # every head's weights sum to 1
 
 
-def test_prefix_with_many_groups_and_no_own_tokens():
+@pytest.mark.parametrize("wide", [False, True])
+def test_prefix_with_many_groups_and_no_own_tokens(wide):
     """Groups of one to three sequences, prefixes of every length, own tokens missing."""
     Hq, Hkv, D = 6, 2, 64
     sizes = [1 + i % 3 for i in range(150)]
@@ -763,7 +774,8 @@ def test_prefix_with_many_groups_and_no_own_tokens():
     q = bf16(g, B, Hq, D, std=2.0)
     own, zero = torch.full((B, 1), -1, dtype=torch.int32), torch.zeros(B, dtype=torch.int32)
     out = torch.full((B, Hq, D), NAN, dtype=torch.bfloat16, device=DEV)
-    pg.pa_decode_prefix(out, *dev(q, kc, vc, bt, torch.tensor(plens, dtype=torch.int32), cu, own, zero), 0.125)
+    pt = widened(bt, B, Hkv, D) if wide else bt
+    pg.pa_decode_prefix(out, *dev(q, kc, vc, pt, torch.tensor(plens, dtype=torch.int32), cu, own, zero), 0.125)
     for grp, p in enumerate(plens):
         t = torch.arange(p)
         k, v = ref.rows_at(kc, bt[grp], t)[0], ref.rows_at(vc, bt[grp], t)[0]
@@ -819,8 +831,8 @@ def test_one_workspace_serves_every_operator_of_the_section():
              lambda o, ws, q=q_, k=kc_, v=vc_, t=bt_, c=ctx_, u=cu_: pg.pa_decode_window_multi(
                  o, q, k, v, t, u, c, 400, 4, 0.1, workspace=ws), q_),
             (pg.pa_decode_prefix_workspace_size(B, 1, Hq, Hkv, D),
-             lambda o, ws, q=q_, k=kc_, v=vc_, t=bt_, c=ctx_, u=cug_, p=plen_: pg.pa_decode_prefix(
-                 o, q, k, v, t[:1].contiguous(), p, u, t, c, 0.1, workspace=ws), q_),
+             lambda o, ws, q=q_, k=kc_, v=vc_, t=bt_, c=ctx_, u=cug_, p=plen_, s=(B, Hkv, D): pg.pa_decode_prefix(
+                 o, q, k, v, widened(t[:1], *s), p, u, t, c, 0.1, workspace=ws), q_),
             (pg.pa_decode_weights_workspace_size(B, Hq, Hkv, D, MBS),
              lambda o, ws, q=q_, k=kc_, v=vc_, t=bt_, c=ctx_, s=(NB, Hkv, BS): pg.pa_decode_weights(
                  o, torch.zeros(s, device=DEV), q, k, v, t, c, 0.1, workspace=ws), q_),

@@ -38,7 +38,7 @@ def flib():
 
 
 @pytest.mark.parametrize("stop_item", [0, 1])  # every warp and CTA here has at least two copies to make
-@pytest.mark.parametrize("op", ["window", "window_many", "window_multi", "multi_many", "prefix", "weights"])
+@pytest.mark.parametrize("op", ["window", "window_many", "window_multi", "multi_many", "prefix", "prefix_each", "weights"])
 def test_wait_runs_out_then_status_and_recovery(flib, op, stop_item):
     Hq, Hkv, D, scale = 28, 4, 128, 0.0884
     # window: a piece of a segment per CTA; window_many: a range of segments per warp
@@ -47,6 +47,8 @@ def test_wait_runs_out_then_status_and_recovery(flib, op, stop_item):
     B = len(lens)
     g, kc, vc, bt, _, _ = pool(7, lens + [900], Hkv, D)
     bt, pt = bt[:B].contiguous(), bt[B:].contiguous()
+    if op == "prefix":  # tables wide enough for the kernels that share the prefix's reads
+        pt = torch.nn.functional.pad(pt, (0, 4096), value=-1)
     q = bf16(g, B, Hq, D, std=2.0)
     i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)
     q_, kc_, vc_, bt_, pt_ = dev(q, kc, vc, bt, pt)
@@ -57,6 +59,7 @@ def test_wait_runs_out_then_status_and_recovery(flib, op, stop_item):
     size = {"window_multi": lambda: pg.pa_decode_window_multi_workspace_size(B, B, Hq, Hkv, D),
             "multi_many": lambda: pg.pa_decode_window_multi_workspace_size(B, B, Hq, Hkv, D),
             "prefix": lambda: pg.pa_decode_prefix_workspace_size(B, 1, Hq, Hkv, D),
+            "prefix_each": lambda: pg.pa_decode_prefix_workspace_size(B, 1, Hq, Hkv, D),
             "weights": lambda: pg.pa_decode_weights_workspace_size(B, Hq, Hkv, D, MBS)}
     ws = torch.zeros(size.get(op, lambda: pg.pa_decode_window_workspace_size(B, Hq, Hkv, D))(), dtype=torch.uint8,
                      device=DEV)
@@ -69,7 +72,7 @@ def test_wait_runs_out_then_status_and_recovery(flib, op, stop_item):
             rc = flib.pa_decode_window(o, x, k, v, t, MBS, c, B, *shape, 1 << 20, 0, *tail)
         elif op in ("window_multi", "multi_many"):
             rc = flib.pa_decode_window_multi(o, x, k, v, t, MBS, cu.data_ptr(), c, B, B, *shape, 1 << 20, 0, *tail)
-        elif op == "prefix":
+        elif op in ("prefix", "prefix_each"):
             one, grp = i32(900), i32(0, B)
             rc = flib.pa_decode_prefix(o, x, k, v, pt_.data_ptr(), pt.shape[1], one.data_ptr(), grp.data_ptr(), 1, t,
                                        MBS, c, B, *shape, *tail)
@@ -92,7 +95,7 @@ def test_wait_runs_out_then_status_and_recovery(flib, op, stop_item):
     for b in range(0, B, 1 if B < 10 else 49):
         pos = torch.arange(lens[b])
         kk, vv = ref.rows_at(kc, bt[b], pos)[0], ref.rows_at(vc, bt[b], pos)[0]
-        if op == "prefix":
+        if op in ("prefix", "prefix_each"):
             u = torch.arange(900)
             kk, vv = torch.cat([ref.rows_at(kc, pt[0], u)[0], kk]), torch.cat([ref.rows_at(vc, pt[0], u)[0], vv])
         want, bound, _, _ = ref.attend(q[b].double(), kk, vv, scale)
