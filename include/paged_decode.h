@@ -637,10 +637,11 @@ PA_API int quest_decode_fp8_block(pa_bf16 *out, int32_t *selected, const pa_bf16
  * finite. Workspaces are zero-filled once; one buffer serves all calls of this
  * section in any order and shape, but not calls of other sections besides,
  * and calls that overlap in time need different ones. pa_workspace_status
- * reads their status. They take about 15 MB (pa_decode_window), 40 MB
- * (pa_decode_window_multi), 55 MB (pa_decode_prefix), and 4 bytes per query
- * head and table slot more for pa_decode_weights. Results are deterministic
- * on a device, but for what pa_decode_weights says about shared blocks. */
+ * reads their status. They take about 15 MB (pa_decode_window), 55 MB
+ * (pa_decode_window_multi, pa_decode_prefix), and 4 bytes per query head and
+ * table slot more for pa_decode_weights. The same call gives the same bits on a
+ * device, but for what pa_decode_weights says about shared blocks; how the work
+ * is cut, and so the rounding, depends on the call's sizes. */
 
 /* Sliding-window decode: as pa_decode, but sequence b's query sees only the
  * tokens t < ctx_b with
@@ -698,8 +699,8 @@ PA_API int pa_decode_window_multi(pa_bf16 *out, const pa_bf16 *query, const pa_b
  * prefix_tables[g][0..max_prefix_blocks). Sequence b sees its group's prefix
  * and then its own tokens t < context_lens[b], in the blocks of
  * block_tables[b] (which do not repeat the prefix's). The prefix length need
- * not be a multiple of the block size. A group's prefix is read once for all
- * its sequences. cu_group is [num_groups + 1] int32 on the device, ascending
+ * not be a multiple of the block size. A group's prefix is read from memory once
+ * for all its sequences. cu_group is [num_groups + 1] int32 on the device, ascending
  * from 0; a sequence of no group has no prefix; a sequence with neither
  * prefix nor own tokens gets a zero output. num_groups <= 4096. bf16 cache. */
 PA_API size_t pa_decode_prefix_workspace_size(int batch, int num_groups, int num_q_heads, int num_kv_heads,

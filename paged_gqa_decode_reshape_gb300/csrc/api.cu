@@ -1,6 +1,7 @@
 // api.cu -- the C ABI (include/paged_decode.h): argument checks on the host,
 // TMA descriptors, workspace carving, and the kernel launches. Nothing here
 // allocates device memory.
+#include <algorithm>
 #include <atomic>
 #include <climits>
 #include <cstring>
@@ -855,7 +856,8 @@ SubsetArgs subset_args(pa_bf16 *out, const pa_bf16 *query, const void *kc, const
 }
 
 // What a call of this section needs: the streaming kernel (one query row per
-// sequence), the row-tile kernel (many), or both (prefixes, unless they are small).
+// sequence), the row-tile kernel (many), or both (prefixes); small calls of the
+// latter two use the streaming kernel alone.
 struct SubsetPlan {
     bool stream, tiles, prefix;
     int64_t logit_blocks;  // accumulated weights: max_blocks_per_seq
@@ -959,7 +961,19 @@ int prefix_ctas(const SubsetArgs &a, int D, int sms) {
 constexpr int64_t kEachReads = int64_t(120) << 20;
 
 bool reads_each(const SubsetArgs &a, int D) {
-    return int64_t(a.rows) * a.Hkv * (int64_t(a.PMBS) + a.MBS / 2) * kBlockSize * D * 4 <= kEachReads;
+    return double(a.rows) * a.Hkv * (a.PMBS + a.MBS * 0.5) * kBlockSize * D * 4 <= double(kEachReads);
+}
+
+// The same for several query rows per sequence: each reads its window for itself,
+// by one launch of the streaming kernel, up to kEachReads bytes where every (row, KV
+// head) has an SM, and up to half of it beyond. Each row and row tiles: 4 sequences of
+// 1 row on 700 tokens (5 MB) 7.3 and 12.7 us, 48 of 3 on 100 (28 MB) 12.3 and 12.9, one
+// of 64 on 400 (50 MB) 13.6 and 20.6, 8 of 2 on 2000 (62 MB, one SM each) 14.3 and 18.3, on
+// 4000 (125 MB) 20.0 and 27.5, 32 of 2 on 500 (62 MB) 17.1 and 15.4.
+bool rows_each(const SubsetArgs &a, int D, int sms) {
+    const double seen = std::min(double(a.MBS) * kBlockSize, double(a.window) + a.sinks + 2 * kBlockSize);
+    const int64_t segs = int64_t(a.rows) * a.Hkv;
+    return segs * seen * D * 4 <= double(segs <= sms ? kEachReads : kEachReads / 2 - (int64_t(4) << 20));
 }
 
 // the launches, after the argument checks
@@ -982,7 +996,8 @@ int run_subset(SubsetArgs a, const SubsetPlan &plan, int D, CacheKind kind, void
     a.desc = reinterpret_cast<int4 *>(p + w.desc);
     a.lse = reinterpret_cast<float *>(p + w.lse);
     a.logits = reinterpret_cast<float *>(p + w.logits);
-    const bool each = plan.prefix && reads_each(a, D);
+    const bool rows = plan.tiles && !plan.prefix;  // of windows
+    const bool each = plan.tiles && (rows ? rows_each(a, D, w.sms) : reads_each(a, D));
     if (each) a.ownres = nullptr;
     if (plan.prefix) a.pgrid = prefix_ctas(a, D, w.sms);
     a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
@@ -993,7 +1008,8 @@ int run_subset(SubsetArgs a, const SubsetPlan &plan, int D, CacheKind kind, void
     CUtensorMap tv, tk, tk_half;
     std::memset(&tv, 0, sizeof tv);
     if (!fp8 && (rc = make_block_map(&tv, a.vc, a.Hkv, D, a.NB)) != PA_OK) return rc;
-    if (plan.stream && (rc = fp8 ? make_cache_map(&tk, a.kc, a.Hkv, D, kBlockSize, a.NB, true)
+    const bool stream_too = !rows || each;
+    if (stream_too && (rc = fp8 ? make_cache_map(&tk, a.kc, a.Hkv, D, kBlockSize, a.NB, true)
                                  : make_block_map(&tk, a.kc, a.Hkv, D, a.NB)) != PA_OK)
         return rc;
     if (plan.tiles && !each && (rc = make_cache_map(&tk_half, a.kc, a.Hkv, D, kBlockSize, a.NB)) != PA_OK) return rc;
@@ -1004,12 +1020,12 @@ int run_subset(SubsetArgs a, const SubsetPlan &plan, int D, CacheKind kind, void
         if ((rc = make_query_map(&tq, a.q, a.rows, a.Hq, a.G, D)) != PA_OK) return rc;
         e = launch_row_tiles(tk_half, tv, tq, a, D, w.sms, st);
     }
-    if (e == cudaSuccess && plan.stream) e = launch_stream_decode(tk, tv, a, D, kind, plan.prefix && !each ? w.sms - a.pgrid : w.sms, st);
+    if (e == cudaSuccess && stream_too) e = launch_stream_decode(tk, tv, a, D, kind, plan.prefix && !each ? w.sms - a.pgrid : w.sms, st);
     if (e == cudaSuccess && plan.prefix && !each) e = launch_prefix_join(a, D, st);
     return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 
-constexpr SubsetPlan kWindowPlan{true, false, false, 0}, kWindowMultiPlan{false, true, false, 0},
+constexpr SubsetPlan kWindowPlan{true, false, false, 0}, kWindowMultiPlan{true, true, false, 0},
     kPrefixPlan{true, true, true, 0};
 SubsetPlan weights_plan(int MBS) { return SubsetPlan{true, false, false, MBS}; }
 

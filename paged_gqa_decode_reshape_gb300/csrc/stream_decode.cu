@@ -1,7 +1,7 @@
 // stream_decode.cu -- one-query-row decode over a part of the cache (sm_103a):
 // the sliding window with sinks, the dense decode that also stores its logits
 // (for the accumulated weights), short prefixes with the own tokens behind them,
-// and the own tokens of a sequence whose prefix is attended to separately.
+// few query rows per sequence each for itself, and the own tokens of a sequence whose prefix is attended to separately.
 //
 // For KV head g of sequence b and the query heads h of its group, over the
 // tokens t the row sees (z_t = scale * log2(e) * q_h . K_t):
@@ -112,10 +112,12 @@ struct StreamCfg {
 };
 
 // what the streaming kernel is run for
-enum StreamMode { kPlain, kLogits, kPrefixed };
+enum StreamMode { kPlain, kLogits, kPrefixed, kRows };
 
 // a sequence's visible tokens [0, s1) and [lo, lim), as items; kPrefixed: the s1
-// tokens of its group's prefix (group pg, -1: none), then its own [0, lim)
+// tokens of its group's prefix (group pg, -1: none), then its own [0, lim);
+// kRows: what query row b of a call with several per sequence sees (its sequence
+// is pg, -1: none; a.cu_g and a.ngroups are the sequences' row offsets)
 struct Span {
     int lim, s1, lo, nb1, jw, nb, n;  // nb1 sink blocks, then blocks jw, jw + 1, ...; nb blocks, n items (at least one)
     int pg;
@@ -125,19 +127,25 @@ struct Span {
 template <StreamMode MODE>
 __device__ __forceinline__ Span span_of(const SubsetArgs &a, int b) {
     Span s;
-    s.lim = min(max(__ldg(a.ctx + b), 0), a.MBS * kBlockSize);
-    if constexpr (MODE == kPrefixed) {
+    s.pg = -1;
+    int after = 0;  // kRows: rows of the sequence behind this one
+    if constexpr (MODE == kPrefixed || MODE == kRows) {
         int lo = 0, hi = a.ngroups;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (__ldg(a.cu_g + mid) <= b) lo = mid; else hi = mid;
         }
-        s.pg = b >= __ldg(a.cu_g + lo) && b < __ldg(a.cu_g + lo + 1) ? lo : -1;
-        s.s1 = s.pg < 0 ? 0 : min(max(__ldg(a.plen + lo), 0), a.PMBS * kBlockSize);
+        const int end = __ldg(a.cu_g + lo + 1);
+        if (b >= __ldg(a.cu_g + lo) && b < end) s.pg = lo;
+        after = min(end, a.rows) - 1 - b;
+    }
+    const int seq = MODE == kRows ? s.pg : b;
+    s.lim = seq < 0 ? 0 : max(min(max(__ldg(a.ctx + seq), 0), a.MBS * kBlockSize) - (MODE == kRows ? after : 0), 0);
+    if constexpr (MODE == kPrefixed) {
+        s.s1 = s.pg < 0 ? 0 : min(max(__ldg(a.plen + s.pg), 0), a.PMBS * kBlockSize);
         s.lo = s.jw = 0;
         s.nb1 = (s.s1 + kBlockSize - 1) / kBlockSize;
     } else {
-        s.pg = -1;
         s.s1 = min(a.sinks, s.lim);
         s.lo = max(s.s1, a.window >= s.lim ? 0 : s.lim - a.window);
         s.nb1 = (s.s1 + kBlockSize - 1) / kBlockSize;
@@ -434,7 +442,7 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
                 phys = __ldg(a.pt + int64_t(s.pg) * a.PMBS + e);
                 mask = bits_between(0, s.s1, t);
             } else {
-                phys = e < s.nb ? __ldg(a.bt + int64_t(q) * a.MBS + j) : -1;
+                phys = e < s.nb ? __ldg(a.bt + int64_t(MODE == kRows ? s.pg : q) * a.MBS + j) : -1;
                 mask = (MODE == kPrefixed ? 0u : bits_between(0, s.s1, t)) | bits_between(s.lo, s.lim, t);
             }
         };
@@ -710,6 +718,8 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
             if (d == 0) __stcg(reinterpret_cast<float2 *>(a.ownml) + r, make_float2(M, Ls));
             return;
         }
+        // rows of no sequence stay as they are
+        if (MODE == kRows && (b < __ldg(a.cu_g) || b >= __ldg(a.cu_g + a.ngroups))) return;
         const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
         const int64_t row = int64_t(b) * a.Hq + kvh * G + h;
         *reinterpret_cast<uint2 *>(a.out + row * D + d) =
@@ -1041,6 +1051,14 @@ cudaError_t launch_stream_decode(const CUtensorMap &tk, const CUtensorMap &tv, c
         const int per = kAddThreads / (kBlockSize / 4);  // blocks a CTA takes per turn
         const int x = (a.MBS + per - 1) / per;
         return launch_pdl(weights_add_kernel, dim3(a.nseq * a.Hkv, x < 16 ? x : 16), dim3(kAddThreads), 0, stream, a);
+    }
+    if (a.cu_q) {
+        SubsetArgs f = a;
+        f.nseq = a.rows;
+        f.ngroups = a.nseq;
+        f.cu_g = a.cu_q;
+        return head_dim == 128 ? launch_t<128, kCacheBf16, kRows>(tk, tv, f, sms, stream)
+                               : launch_t<64, kCacheBf16, kRows>(tk, tv, f, sms, stream);
     }
     if (a.pt && !a.ownres)
         return head_dim == 128 ? launch_t<128, kCacheBf16, kPrefixed>(tk, tv, a, sms, stream)

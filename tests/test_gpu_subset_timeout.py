@@ -38,7 +38,7 @@ def flib():
 
 
 @pytest.mark.parametrize("stop_item", [0, 1])  # every warp and CTA here has at least two copies to make
-@pytest.mark.parametrize("op", ["window", "window_many", "window_multi", "multi_many", "prefix", "prefix_each", "weights"])
+@pytest.mark.parametrize("op", ["window", "window_many", "window_multi", "multi_many", "multi_each", "prefix", "prefix_each", "weights"])
 def test_wait_runs_out_then_status_and_recovery(flib, op, stop_item):
     Hq, Hkv, D, scale = 28, 4, 128, 0.0884
     # window: a piece of a segment per CTA; window_many: a range of segments per warp
@@ -47,8 +47,11 @@ def test_wait_runs_out_then_status_and_recovery(flib, op, stop_item):
     B = len(lens)
     g, kc, vc, bt, _, _ = pool(7, lens + [900], Hkv, D)
     bt, pt = bt[:B].contiguous(), bt[B:].contiguous()
-    if op == "prefix":  # tables wide enough for the kernels that share the prefix's reads
+    # tables wide enough for the kernels that share reads between rows
+    if op == "prefix":
         pt = torch.nn.functional.pad(pt, (0, 4096), value=-1)
+    if op in ("window_multi", "multi_many"):
+        bt = torch.nn.functional.pad(bt, (0, 4096), value=-1)
     q = bf16(g, B, Hq, D, std=2.0)
     i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)
     q_, kc_, vc_, bt_, pt_ = dev(q, kc, vc, bt, pt)
@@ -58,6 +61,7 @@ def test_wait_runs_out_then_status_and_recovery(flib, op, stop_item):
     MBS, NB = bt.shape[1], kc.shape[0]
     size = {"window_multi": lambda: pg.pa_decode_window_multi_workspace_size(B, B, Hq, Hkv, D),
             "multi_many": lambda: pg.pa_decode_window_multi_workspace_size(B, B, Hq, Hkv, D),
+            "multi_each": lambda: pg.pa_decode_window_multi_workspace_size(B, B, Hq, Hkv, D),
             "prefix": lambda: pg.pa_decode_prefix_workspace_size(B, 1, Hq, Hkv, D),
             "prefix_each": lambda: pg.pa_decode_prefix_workspace_size(B, 1, Hq, Hkv, D),
             "weights": lambda: pg.pa_decode_weights_workspace_size(B, Hq, Hkv, D, MBS)}
@@ -70,7 +74,7 @@ def test_wait_runs_out_then_status_and_recovery(flib, op, stop_item):
     def call():
         if op in ("window", "window_many"):
             rc = flib.pa_decode_window(o, x, k, v, t, MBS, c, B, *shape, 1 << 20, 0, *tail)
-        elif op in ("window_multi", "multi_many"):
+        elif op in ("window_multi", "multi_many", "multi_each"):
             rc = flib.pa_decode_window_multi(o, x, k, v, t, MBS, cu.data_ptr(), c, B, B, *shape, 1 << 20, 0, *tail)
         elif op in ("prefix", "prefix_each"):
             one, grp = i32(900), i32(0, B)
