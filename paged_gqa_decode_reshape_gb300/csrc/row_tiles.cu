@@ -176,7 +176,8 @@ __device__ __forceinline__ void redo_row(const SubsetArgs &a, int s, int kvh, in
         for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
         z *= a.scale_log2;
         const float Mn = fmaxf(M, z);
-        const float f = M == -INFINITY ? 0.f : fast_exp2(M - Mn), p = fast_exp2(z - Mn);
+        // a logit of -inf has weight 0, also while no other has come
+        const float f = M == -INFINITY ? 0.f : fast_exp2(M - Mn), p = fast_exp2(z - (Mn == -INFINITY ? 0.f : Mn));
         M = Mn;
         Ls = Ls * f + p;
 #pragma unroll
