@@ -43,8 +43,8 @@
 //  * Masks: a 16-bit mask per block and row on the tiles at an edge, none
 //    inside. V rows no row of the unit sees are zeroed in shared memory. A
 //    token that only other rows of the tile see meets them as 0 * V, which
-//    is not 0 if V is not finite: a row whose result is not finite is computed
-//    again, over its own tokens only, by its warp.
+//    is not 0 if V is not finite: a row whose result is not finite, in a unit with
+//    such a token, is computed again, over its own tokens only, at the CTA's end.
 //  * Units cut between CTAs leave (O, m, l) per row and piece in the workspace;
 //    the CTA that completes the count merges them, in piece order, or a join
 //    kernel does (for prefixes, with the own tokens' part).
@@ -70,6 +70,28 @@ constexpr float kGrow = 8.f;     // log2 growth of a maximum that rescales O
 // 21.5 us, 2 15.8, 3 15.6, 4 19.3; 8 sequences behind a shared prefix of 2001: 15.9, 16.2, 20.1, 18.9.
 constexpr int kMinTiles = 2;
 
+// One unit of work, the same in every role.
+struct Unit {
+    int s, kvh, u;         // sequence (or group), KV head, index of the 2 RQ-row unit
+    int r0, nr;            // first query row, query rows (<= 2 RQ)
+    int lim0, lim1;        // tokens before which the first and the last row see
+    int nb, nb1, jw;       // blocks: nb1 sink blocks, then jw, jw + 1, ...
+    int n;                 // tiles (at least one)
+};
+
+// What the end of a CTA has to know about rows that came out not finite.
+struct After {
+    int64_t s0;     // the CTA's first unit, the position of its first tile,
+    Unit x;
+    int nu;         // and the units per KV head of its sequence
+    int odd;        // a row is not finite
+    int merged[2];  // cut units merged here, by row tile: kMergedBefore, kMergedHere
+    int pad;
+};
+constexpr int kMergedBefore = 1;  // the unit that began before the CTA's range
+constexpr int kMergedHere = 2;    // the unit that begins in it
+static_assert(sizeof(After) % 8 == 0, "the prefix sums behind it");
+
 template <int D>
 struct RowCfg {
     static constexpr int HV = D / 64;                      // 64-dim halves
@@ -81,18 +103,10 @@ struct RowCfg {
     static constexpr size_t off_bars = off_stage + 8 * 4096;
     static constexpr size_t off_info = off_bars + 224;
     static constexpr size_t off_misc = off_info + 2 * kInfo * 4;
-    static constexpr size_t off_pre = off_misc + 32;
+    static constexpr size_t off_after = off_misc + 32;
+    static constexpr size_t off_pre = off_after + sizeof(After);
     static constexpr size_t SMEM = 1024 + off_pre + (kPreCap + 1) * 8;
     static constexpr int SLOT = 2 * 128 * (D + 2);         // floats of a piece: per row tile O[128][D], m[128], l[128]
-};
-
-// One unit of work, the same in every role.
-struct Unit {
-    int s, kvh, u;         // sequence (or group), KV head, index of the 2 RQ-row unit
-    int r0, nr;            // first query row, query rows (<= 2 RQ)
-    int lim0, lim1;        // tokens before which the first and the last row see
-    int nb, nb1, jw;       // blocks: nb1 sink blocks, then jw, jw + 1, ...
-    int n;                 // tiles (at least one)
 };
 
 template <bool PREFIX>
@@ -150,42 +164,101 @@ struct Work {
 };
 
 // Head h of query row r of sequence s again, over the tokens before lim that it
-// sees and nothing else, by a warp in fp32: for rows whose result is not finite.
+// sees and nothing else, by a warp in fp32: for rows that other rows' tokens may have
+// reached. 32 tokens at a time, a lane per token for its logit, D / 32 dims for V.
 template <int D>
 __device__ __forceinline__ void redo_row(const SubsetArgs &a, int s, int kvh, int r, int h, int lim) {
     constexpr int V = D / 32, BS = kBlockSize;
     const int lane = threadIdx.x & 31, s1 = min(a.sinks, lim), lo = max(s1, a.window >= lim ? 0 : lim - a.window);
     const int cnt = s1 + max(lim - lo, 0);
-    const int64_t ro = (int64_t(r) * a.Hq + kvh * a.G + h) * D + lane * V;
-    float q[V], acc[V], M = -INFINITY, Ls = 0.f;
-    auto f32 = [](uint16_t v) { return __uint_as_float(uint32_t(v) << 16); };
+    const int64_t ro = (int64_t(r) * a.Hq + kvh * a.G + h) * D;
+    const uint4 *q = reinterpret_cast<const uint4 *>(a.q + ro);
+    float acc[V], M = -INFINITY, Ls = 0.f;  // Ls: of this lane's tokens
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-        q[k] = f32(a.q[ro + k]);
-        acc[k] = 0.f;
-    }
-    for (int k = 0; k < cnt; ++k) {
-        const int t = k < s1 ? k : k - s1 + lo;
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+#pragma unroll 1
+    for (int k0 = 0; k0 < cnt; k0 += 32) {
+        const int k = min(k0 + lane, cnt - 1), t = k < s1 ? k : k - s1 + lo;
         const int phys = __ldg(a.bt + int64_t(s) * a.MBS + t / BS);
-        if (phys < 0 || int64_t(phys) >= a.NB) continue;
-        const int64_t off = ((int64_t(phys) * BS + t % BS) * a.Hkv + kvh) * D + lane * V;
+        const bool in = k0 + lane < cnt && phys >= 0 && int64_t(phys) < a.NB;
+        const int64_t off = ((int64_t(in ? phys : 0) * BS + t % BS) * a.Hkv + kvh) * D;  // not in: of any row
+        const uint4 *kr = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.kc) + off);
         float z = 0.f;
 #pragma unroll
-        for (int e = 0; e < V; ++e) z = fmaf(q[e], f32(static_cast<const uint16_t *>(a.kc)[off + e]), z);
+        for (int c = 0; c < D / 8; ++c) {
+            const uint4 x = __ldg(kr + c), y = __ldg(q + c);
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-        z *= a.scale_log2;
-        const float Mn = fmaxf(M, z);
+            for (int e = 0; e < 4; ++e) z = fmaf(bf16_hi(ys[e]), bf16_hi(xs[e]), fmaf(bf16_lo(ys[e]), bf16_lo(xs[e]), z));
+        }
+        z = in ? z * a.scale_log2 : -INFINITY;
+        float Mn = z;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xffffffffu, Mn, o));
+        Mn = fmaxf(M, Mn);
         // a logit of -inf has weight 0, also while no other has come
         const float f = M == -INFINITY ? 0.f : fast_exp2(M - Mn), p = fast_exp2(z - (Mn == -INFINITY ? 0.f : Mn));
         M = Mn;
         Ls = Ls * f + p;
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = acc[e] * f + p * f32(static_cast<const uint16_t *>(a.vc)[off + e]);
+        for (int e = 0; e < V; ++e) acc[e] *= f;
+        const unsigned ins = __ballot_sync(0xffffffffu, in);
+#pragma unroll 8
+        for (int u = 0; u < 32; ++u) {
+            const float pu = __shfl_sync(0xffffffffu, p, u);
+            const int64_t at = __shfl_sync(0xffffffffu, off, u) + lane * V;
+            const uint32_t *vr = reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(a.vc) + at);
+#pragma unroll
+            for (int e = 0; e < V; e += 2) {
+                const uint32_t v = __ldg(vr + e / 2);
+                if ((ins >> u) & 1u) {
+                    acc[e] += pu * bf16_lo(v);
+                    acc[e + 1] += pu * bf16_hi(v);
+                }
+            }
+        }
     }
 #pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
+#pragma unroll
     for (int e = 0; e < V; ++e)
-        a.out[ro + e] = __bfloat16_as_ushort(__float2bfloat16_rn(Ls > 0.f ? acc[e] / Ls : Ls != Ls ? Ls : 0.f));
+        a.out[ro + lane * V + e] =
+            __bfloat16_as_ushort(__float2bfloat16_rn(Ls > 0.f ? acc[e] / Ls : Ls != Ls ? Ls : 0.f));
+}
+
+// Does a unit whose first row sees tokens before lim0 and whose last one before lim1
+// hold a token that its row with the limit lim does not see, with a V row that is
+// not finite? By a warp; there are at most a few hundred such tokens, at the ends of
+// the window and of the sinks. Without one, a row that is not finite owes it to a
+// token it sees itself.
+template <int D>
+__device__ __forceinline__ bool reached_by_others(const SubsetArgs &a, int s, int kvh, int lim0, int lim1, int lim) {
+    constexpr int LR = D / 8, TP = 32 / LR, U = 4, BS = kBlockSize;  // lanes per row, rows at once
+    const int lane = threadIdx.x & 31;
+    auto lower = [&](int lim) { return a.window >= lim ? 0 : lim - a.window; };
+    const int l0 = lower(lim0), l1 = lower(lim1), lo = lower(lim), nb1 = (min(a.sinks, lim1) + BS - 1) / BS;
+    bool bad = false;
+    auto scan = [&](int from, int to) {
+#pragma unroll 1
+        for (int t0 = from + lane / LR; t0 - lane / LR < to; t0 += TP * U) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int t = t0 + u * TP;
+                const int phys = t < to && !(t >= lo && t < lim) ? __ldg(a.bt + int64_t(s) * a.MBS + t / BS) : -1;
+                if (phys < 0 || int64_t(phys) >= a.NB) continue;
+                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(a.vc) +
+                                      ((int64_t(phys) * BS + t % BS) * a.Hkv + kvh) * LR + lane % LR);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    bad = bad || (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+            }
+        }
+    };
+    scan(min(a.sinks, lim), min(nb1 * BS, lim1));
+    scan(max(l0 / BS, nb1) * BS, l1);
+    scan(lim0, lim1);
+    return __any_sync(0xffffffffu, bad);
 }
 
 template <int D, bool PREFIX>
@@ -341,6 +414,13 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
         }
         x = work.unit(s, kvh, u);
         s0 = pos0 - rem;
+    }
+    After &after = *reinterpret_cast<After *>(bp + C::off_after);
+    if (!PREFIX && tid == 0) {
+        after.s0 = s0;
+        after.x = x;
+        after.nu = nu;
+        after.odd = after.merged[0] = after.merged[1] = 0;
     }
     auto next_unit = [&]() {
         s0 += x.n;
@@ -774,11 +854,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                             }
                             store_rows(y, [&](int, int64_t ro) { return a.out + ro * D + 64 * c2; });
                         }
-                        __syncwarp();
-                        for (unsigned again = __ballot_sync(0xffffffffu, act && !fine); again; again &= again - 1) {
-                            const int r = (warp & 3) * 32 + __ffs(again) - 1, rir = w * RQ + r / G;
-                            redo_row<D>(a, x.s, x.kvh, x.r0 + rir, r % G, max(base + rir, 0));
-                        }
+                        if (act && !fine) after.odd = 1;
                     } else {
                         publish();
                         if (a.cuts) {  // the join kernel merges
@@ -797,7 +873,10 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                             }
                             if (!(ok = wait(last_bar + 8 * w, pubs++))) break;
                             if (misc[4 + w]) {
-                                if (row == 0) a.counters[2 * c0 + w] = 0;
+                                if (row == 0) {
+                                    a.counters[2 * c0 + w] = 0;
+                                    after.merged[w] |= t0 == 0 ? kMergedHere : kMergedBefore;
+                                }
                                 // The pieces' common maximum and sum, a row per thread; then the rows, each by a warp with
                                 // its columns side by side, RB rows of KB pieces in flight: bound by the latency of L2
                                 // loads (2 x 8: 52.9 us for 32 sequences of 1 to 6 rows, 3 x 8 53.3, 4 x 4 53.6; with
@@ -870,7 +949,6 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                                             }
                                         }
                                     }
-                                    unsigned bad = 0;  // rows that are not finite
 #pragma unroll
                                     for (int u = 0; u < RB; ++u) {
                                         const int r = g0 + 4 * u;
@@ -878,7 +956,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                                         bool fine = true;
 #pragma unroll
                                         for (int e = 0; e < V; ++e) fine = fine && fabsf(acc[u][e]) <= 3.4028234e38f;
-                                        if (!__all_sync(0xffffffffu, fine)) bad |= 1u << u;
+                                        if (!fine) after.odd = 1;
                                         uint32_t *dst = reinterpret_cast<uint32_t *>(
                                             a.out + (int64_t(x.r0 + w * RQ + r / G) * a.Hq + x.kvh * G + r % G) * D) + lane * (V / 2);
                                         if constexpr (V == 4)
@@ -886,10 +964,6 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                                                                                          pack_bf16x2(acc[u][2], acc[u][3]));
                                         else
                                             *dst = pack_bf16x2(acc[u][0], acc[u][1]);
-                                    }
-                                    for (; bad; bad &= bad - 1) {
-                                        const int r = g0 + 4 * (__ffs(bad) - 1), rir = w * RQ + r / G;
-                                        redo_row<D>(a, x.s, x.kvh, x.r0 + rir, r % G, max(base + rir, 0));
                                     }
                                 }
                                 __syncwarp();
@@ -918,6 +992,43 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
             mbar_wait_bounded(full + 8 * (i % kStages), uint32_t(i / kStages) & 1u, a.wait_ns);
         for (int w = 0; w < 2; ++w)
             if (misc[2 + w] > 0) mbar_wait_bounded(q_full + 8 * w, uint32_t(misc[2 + w] - 1) & 1u, a.wait_ns);
+    }
+    // ---- the rows written here that are not finite, a warp per row, over their own tokens. Only now: this may take
+    // long (5 ms of a warp for a row of 40000 tokens), and nothing waits for these warps any more.
+    if constexpr (!PREFIX) {
+        if (after.odd == 0 || misc[1]) return;
+        if (warp >= 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");  // the launch's share for every warp again
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 168;");
+        s0 = after.s0;
+        x = after.x;
+        nu = after.nu;
+#pragma unroll 1
+        for (int64_t p = pos0; p < pos1;) {
+            const int t0 = int(p - s0), t1 = int(min(pos1 - s0, int64_t(x.n)));
+#pragma unroll 1
+            for (int r = warp; r < x.nr * G; r += kWarpsRT) {
+                const int ir = r / G;
+                const bool written = (t0 == 0 && t1 == x.n) ||
+                                     (after.merged[ir >= RQ] & (t0 == 0 ? kMergedHere : kMergedBefore));
+                if (!written) continue;
+                const uint32_t *o = reinterpret_cast<const uint32_t *>(
+                    a.out + (int64_t(x.r0 + ir) * a.Hq + x.kvh * G + r % G) * D) + lane * (D / 64);
+                bool fine = true;
+#pragma unroll
+                for (int e = 0; e < D / 64; ++e) {
+                    const uint32_t v = __ldcg(o + e);
+                    fine = fine && (v & 0x7f80u) != 0x7f80u && (v & 0x7f800000u) != 0x7f800000u;
+                }
+                if (__all_sync(0xffffffffu, fine)) continue;
+                int rr, nn;
+                work.rows(x.s, rr, nn);
+                const int lim = work.limit(x.s, x.r0 + ir - rr, nn);
+                if (reached_by_others<D>(a, x.s, x.kvh, x.lim0, x.lim1, lim))
+                    redo_row<D>(a, x.s, x.kvh, x.r0 + ir, r % G, lim);
+            }
+            p = s0 + t1;
+            if (p < pos1) next_unit();
+        }
     }
 }
 
@@ -1021,7 +1132,8 @@ __global__ void __launch_bounds__(256) cut_join_kernel(const SubsetArgs a) {
                 fine = fine && fabsf(acc[i][e]) <= 3.4028234e38f;
             }
             const int g = g0 + i * step, ir = g / G, h = g - ir * G;
-            if (!__all_sync(0xffffffffu, fine)) {
+            if (!__all_sync(0xffffffffu, fine) &&
+                reached_by_others<D>(a, u.s, u.kvh, max(u.base, 0), max(u.base + u.nr - 1, 0), max(u.base + ir, 0))) {
                 redo_row<D>(a, u.s, u.kvh, u.r0 + ir, h, max(u.base + ir, 0));
                 continue;
             }
