@@ -307,6 +307,10 @@ PA_API int quest_decode(pa_bf16 *out, int32_t *selected, const pa_bf16 *query,
  * again before reuse). */
 PA_API int pa_workspace_status(const void *workspace, void *stream);
 
+/* The id of the CUDA graph capture that `stream` is part of into *id (host), 0
+ * for none: for callers that keep workspaces per graph. */
+PA_API int pa_capture_id(uint64_t *id, void *stream);
+
 /* Input checker (not on the hot path). Counts, on the device, into
  * counts[0..3] (device int32, overwritten):
  *   [0] slots >= num_blocks * block_size,
@@ -634,14 +638,17 @@ PA_API int quest_decode_fp8_block(pa_bf16 *out, int32_t *selected, const pa_bf16
  * sliding window with visible first tokens, attention of a batch over shared
  * prefixes, and eviction by accumulated attention weight. Layouts, block
  * tables, masking of bad metadata and errors as pa_decode; scale must be
- * finite. Workspaces are zero-filled once; one buffer serves all calls of this
- * section in any order and shape, but not calls of other sections besides,
- * and calls that overlap in time need different ones. pa_workspace_status
- * reads their status. They take about 15 MB (pa_decode_window), 55 MB
+ * finite. The first PA_PARTIAL_ZERO_BYTES of a workspace (or all of it) are
+ * zero-filled once; one buffer serves all calls of this section in any order
+ * and shape, but not calls of other sections besides, and calls that overlap in
+ * time (on different streams, in graphs that are replayed beside other calls)
+ * need different ones. pa_workspace_status reads their status. They take about 15 MB (pa_decode_window), 55 MB
  * (pa_decode_window_multi, pa_decode_prefix), and 4 bytes per query head and
  * table slot more for pa_decode_weights. The same call gives the same bits on a
  * device, but for what pa_decode_weights says about shared blocks; how the work
  * is cut, and so the rounding, depends on the call's sizes. */
+
+#define PA_PARTIAL_ZERO_BYTES (64u << 10)
 
 /* Sliding-window decode: as pa_decode, but sequence b's query sees only the
  * tokens t < ctx_b with

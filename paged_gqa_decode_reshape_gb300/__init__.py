@@ -52,7 +52,7 @@ __all__ = [
     "pa_decode_window_multi_workspace_size", "pa_decode_window_multi",
     "pa_decode_prefix_workspace_size", "pa_decode_prefix",
     "pa_decode_weights_workspace_size", "pa_decode_weights", "pa_reset_weights", "pa_evict",
-    "pa_workspace_status", "pa_check_metadata", "Workspace",
+    "pa_workspace_status", "pa_capture_id", "pa_check_metadata", "Workspace",
 ]
 
 
@@ -197,6 +197,8 @@ def load_library(path: Optional[str] = None):
         L.pa_decode_weights.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i64, f32, vp, sz,
                                         vp]
         L.pa_decode_weights.restype = i32
+        L.pa_capture_id.argtypes = [vp, vp]
+        L.pa_capture_id.restype = i32
         L.pa_reset_weights.argtypes = [vp, vp, i64, i32, i32, i64, vp]
         L.pa_reset_weights.restype = i32
         L.pa_evict.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i64, i32, i32, vp]
@@ -1083,30 +1085,49 @@ def quest_reshape_and_decode(out: torch.Tensor, selected: torch.Tensor, query: t
 # ------------------------------------------- decode over a part of the cache
 
 
-class _Scratch(Workspace):
-    """A Workspace for calls that may be captured into CUDA graphs: a buffer
-    that has been handed out is kept for good (a captured graph may hold its
-    address), and none is allocated during a capture."""
+PARTIAL_ZERO_BYTES = 64 << 10  # PA_PARTIAL_ZERO_BYTES: what of a workspace has to be zero before its first use
+
+
+class _Scratch:
+    """Workspaces for calls without one: a buffer per device and stream, as calls on different streams may run beside
+    one another. A CUDA graph's calls get buffers of their own from the graph's memory pool, one per captured stream,
+    which the graph clears before its first use of them, so it shares none with eager calls or with other graphs."""
 
     def __init__(self):
-        super().__init__()
-        self._kept = []
-        self.at = {}  # (address, bytes) of the current buffer per device index
+        self.at = {}  # (device index, stream) -> (address, bytes) of the buffer of calls outside captures
+        self._buf = {}
+        self._largest = {}  # device index -> bytes of the largest of them
+        self._captured = {}  # device index -> (id of the last capture seen, {stream: buffer})
 
-    def get(self, device: torch.device, nbytes: int) -> torch.Tensor:
-        key = device.index if device.index is not None else torch.cuda.current_device()
-        buf = self._buf.get(key)
+    def held(self, index: int, stream: int) -> Optional[torch.Tensor]:
+        if not torch.cuda.is_current_stream_capturing():
+            return self._buf.get((index, stream))
+        capture, bufs = self._captured.get(index, (None, {}))
+        return bufs.get(stream) if capture == pa_capture_id(stream) else None
+
+    def get(self, device: torch.device, nbytes: int, stream: int) -> torch.Tensor:
+        """The buffer of this device's current stream, of at least nbytes."""
+        index = device.index
+        buf = self.held(index, stream)
         if buf is not None and buf.numel() >= nbytes:
             return buf
-        if torch.cuda.is_current_stream_capturing():
+        capturing = torch.cuda.is_current_stream_capturing()
+        if capturing and self._largest.get(index, 0) < nbytes:
             raise RuntimeError(f"no workspace of {nbytes} bytes yet: make one such call before the capture, or pass "
                                "workspace=")
-        if buf is not None:
-            self._kept.append(buf)
-        # grown by half as much again, so that growing step by step keeps few buffers
+        # grown by half as much again, so that growing step by step takes few buffers
         n = max(nbytes, 256, buf.numel() * 3 // 2 if buf is not None else 0)
-        buf = self._buf[key] = torch.zeros(n, dtype=torch.uint8, device=device)
-        self.at[key] = (buf.data_ptr(), n)
+        buf = torch.empty(n, dtype=torch.uint8, device=device)
+        buf[:PARTIAL_ZERO_BYTES].zero_()
+        if capturing:
+            capture = pa_capture_id(stream)
+            if self._captured.get(index, (None,))[0] != capture:
+                self._captured[index] = (capture, {})
+            self._captured[index][1][stream] = buf
+        else:
+            self._buf[index, stream] = buf
+            self.at[index, stream] = (buf.data_ptr(), n)
+            self._largest[index] = max(n, self._largest.get(index, 0))
         return buf
 
 
@@ -1121,13 +1142,30 @@ def _tokens(n, name: str) -> int:
     return n if n < 2 ** 31 else 2 ** 31 - 1
 
 
-def _scratch(workspace: Optional[torch.Tensor], dev: torch.device, nbytes: int):
+def partial_cache_workspace(device: Optional[torch.device] = None) -> Optional[torch.Tensor]:
+    """The buffer that the calls of this section without workspace= use on the current stream of `device` (None:
+    none yet): for pa_workspace_status, and to be zeroed after a device failure. While a CUDA graph is captured, the
+    graph's own: keep it to ask for the status after a replay (the next replay clears it)."""
+    device = torch.device("cuda") if device is None else torch.device(device)
+    index = torch.cuda.current_device() if device.index is None else device.index
+    with torch.cuda.device(index):
+        return _subset_ws.held(index, torch.cuda.current_stream().cuda_stream)
+
+
+def pa_capture_id(stream: int) -> int:
+    """The id of the capture that a stream (its handle) is part of, 0 for none."""
+    found = ctypes.c_uint64(0)
+    _check("pa_capture_id", load_library().pa_capture_id(ctypes.byref(found), stream))
+    return found.value
+
+
+def _scratch(workspace: Optional[torch.Tensor], dev: torch.device, nbytes: int, stream: int):
     """(pointer, bytes) of the caller's workspace or of the binding's own."""
     if workspace is None:
-        at = _subset_ws.at.get(dev.index)
-        if at is not None and at[1] >= nbytes:
+        at = _subset_ws.at.get((dev.index, stream))
+        if at is not None and at[1] >= nbytes and not torch._C._cuda_isCurrentStreamCapturing():
             return at
-        workspace = _subset_ws.get(dev, nbytes)
+        workspace = _subset_ws.get(dev, nbytes, stream)
     else:
         if not isinstance(workspace, torch.Tensor):
             raise TypeError("workspace must be a torch.Tensor")
@@ -1162,7 +1200,7 @@ def _run(name: str, dev: torch.device, args, workspace: Optional[torch.Tensor] =
     key = (name, index, shape)
     fn, nbytes = _calls.get(key) or _lookup(key)
     stream = torch._C._cuda_getCurrentRawStream(index)
-    status = fn(*args, stream) if nbytes is None else fn(*args, *_scratch(workspace, dev, nbytes), stream)
+    status = fn(*args, stream) if nbytes is None else fn(*args, *_scratch(workspace, dev, nbytes, stream), stream)
     if status != PA_OK:
         raise PagedDecodeError(name, status)
 

@@ -483,6 +483,16 @@ int pa_workspace_status(const void *workspace, void *stream) {
     return st == 0 ? PA_OK : PA_ERR_DEVICE;
 }
 
+int pa_capture_id(uint64_t *id, void *stream) {
+    if (!id) return PA_ERR_INVALID_ARG;
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    unsigned long long found = 0;
+    const cudaError_t e = cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &status, &found);
+    if (e != cudaSuccess) return cuda_fail(e);
+    *id = status == cudaStreamCaptureStatusNone ? 0 : found;
+    return PA_OK;
+}
+
 int pa_check_metadata(int32_t *counts, const int64_t *slot_mapping, int64_t num_tokens,
                       const int32_t *block_tables, int max_blocks_per_seq,
                       const int32_t *context_lens, int batch, int block_size, int64_t num_blocks,
@@ -883,6 +893,7 @@ int subset_workspace(SubsetWorkspace *w, const SubsetPlan &plan, int64_t rows, i
     w->sms = geo.grid;  // one CTA per SM
     const size_t heads = size_t(rows) * Hq;
     take(true, stream_workers(geo.grid) * 4);  // counters
+    if (at > PA_PARTIAL_ZERO_BYTES) return PA_ERR_UNSUPPORTED;  // what has to be zero before the first call ends here
     w->part = take(plan.stream, stream_part_floats(geo.grid, D) * 4);
     w->slots = take(plan.tiles, size_t(geo.grid) * 2 * row_tiles_slot_floats(D) * 4);
     w->cuts = take(plan.tiles && !plan.prefix, size_t(geo.grid) * sizeof(CutUnit));
