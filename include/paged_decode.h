@@ -109,9 +109,11 @@ PA_API int pa_reshape_and_cache(const pa_bf16 *key, const pa_bf16 *value,
  * device for this batch and head shape (0 on invalid arguments). The
  * workspace holds split-KV partial outputs, their log-sum-exp, per-sequence
  * arrival counters and a status word. It must be ZERO-FILLED before its first
- * use; every successful call leaves it zeroed again, so one buffer can serve
- * any number of sequential calls on one stream. Calls that overlap in time
- * must use different workspaces. */
+ * use; every successful call leaves the status word and the counters, which
+ * have the same place for every batch and head shape, zeroed again, so one
+ * buffer can serve any number of sequential calls on one stream, of any of the
+ * decode calls up to the ones over a part of the cache. Calls that overlap in
+ * time must use different workspaces. */
 PA_API size_t pa_decode_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim);
 
 /* Dense GQA paged decode attention ([P1] "GQA Paged Attention"; split-KV and

@@ -251,8 +251,9 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int, device=None
 class Workspace:
     """A zero-filled device scratch buffer, grown on demand, per device.
 
-    The decode kernels leave their workspace zeroed after every call, so one
-    buffer serves every sequential call on one stream. Calls that may overlap
+    The decode kernels leave their counters zeroed after every call, at the
+    same place for every shape, so one buffer serves every sequential call on
+    one stream. Calls that may overlap
     in time (several streams) need separate Workspace objects."""
 
     def __init__(self):

@@ -8,6 +8,7 @@
 
 #include "../../include/paged_decode.h"
 #include "kernels.h"
+#include "no_alloc.h"
 #include "subset.h"
 
 using namespace pa;
@@ -87,14 +88,31 @@ struct DecodeWorkspace {
     float *part;
 };
 
-DecodeWorkspace carve_decode_ws(void *ws, int B, int Hkv, int per_seg = 1) {
+// The arrival counters have a place of their own for every batch and head shape:
+// a call must not find them where another one left partial results. 65536 of
+// them (dense: 1024 sequences of 64 KV heads; several rows per sequence: 2048
+// rows of 8) are zero between calls. What a larger call has beyond those is
+// cleared before it.
+constexpr size_t kCounterArea = 256 << 10;
+
+size_t counter_bytes(int64_t B, int Hkv, bool multi) {
+    return (size_t(B) * Hkv * (multi ? kMultiRowGroup : 1) * 4 + 255) / 256 * 256;
+}
+
+// compact: as many counters as the call has, for a caller that clears them itself
+size_t decode_bytes(int B, int Hkv, int D, int workers, bool multi, bool compact = false) {
+    const size_t counters = counter_bytes(B, Hkv, multi);
+    const size_t all = multi ? decode_multi_workspace_bytes(B, Hkv, D, workers) : decode_workspace_bytes(B, Hkv, D, workers);
+    return compact || counters >= kCounterArea ? all : all - counters + kCounterArea;
+}
+
+DecodeWorkspace carve_decode_ws(void *ws, int B, int Hkv, bool multi, bool compact) {
     uint8_t *p = static_cast<uint8_t *>(ws);
-    const size_t segs = size_t(B) * Hkv;
-    const size_t counters = (segs * per_seg * 4 + 255) / 256 * 256;
+    const size_t counters = counter_bytes(B, Hkv, multi);
     DecodeWorkspace d;
     d.status = reinterpret_cast<int32_t *>(p);
     d.counters = reinterpret_cast<int32_t *>(p + 256);
-    d.part = reinterpret_cast<float *>(p + 256 + counters);
+    d.part = reinterpret_cast<float *>(p + 256 + (compact || counters >= kCounterArea ? counters : kCounterArea));
     return d;
 }
 
@@ -121,7 +139,7 @@ int run_decode(pa_bf16 *out, const pa_bf16 *query, const void *key_cache, const 
                const float *k_scale = nullptr, const float *v_scale = nullptr, bool fp8 = false,
                const int32_t *cu_q = nullptr, int nseq = 0, int max_ctas = 0,
                const float *scores = nullptr, int32_t *sel_out = nullptr, bool bscale = false,
-               const ScoreWrite *sw = nullptr) {
+               const ScoreWrite *sw = nullptr, bool compact = false) {
     int rc = check_attention_args(out, query, key_cache, value_cache, block_tables, MBS,
                                   context_lens, B, Hq, Hkv, D, BS, NB, scale, workspace);
     if (rc != PA_OK) return rc;
@@ -131,15 +149,19 @@ int run_decode(pa_bf16 *out, const pa_bf16 *query, const void *key_cache, const 
     DecodeGeometry geo;
     cudaError_t e = decode_geometry(D, &geo, fp8);
     if (e != cudaSuccess) return cuda_fail(e);
-    const size_t need = cu_q ? decode_multi_workspace_bytes(B, Hkv, D, geo.workers)
-                             : decode_workspace_bytes(B, Hkv, D, geo.workers);
-    if (workspace_bytes < need) return PA_ERR_WORKSPACE;
+    if (workspace_bytes < decode_bytes(B, Hkv, D, geo.workers, cu_q, compact)) return PA_ERR_WORKSPACE;
     CUtensorMap tk, tv;
     if ((rc = make_cache_map(&tk, key_cache, Hkv, D, BS, NB, fp8)) != PA_OK) return rc;
     // an E4M3 V cache is read with plain bulk copies (its tiles are contiguous)
     if (fp8) std::memset(&tv, 0, sizeof tv);
     else if ((rc = make_cache_map(&tv, value_cache, Hkv, D, BS, NB)) != PA_OK) return rc;
-    const DecodeWorkspace w = carve_decode_ws(workspace, B, Hkv, cu_q ? kMultiRowGroup : 1);
+    const DecodeWorkspace w = carve_decode_ws(workspace, B, Hkv, cu_q, compact);
+    const size_t counters = counter_bytes(B, Hkv, cu_q);
+    if (!compact && counters > kCounterArea) {
+        e = cudaMemsetAsync(reinterpret_cast<uint8_t *>(w.counters) + kCounterArea, 0, counters - kCounterArea,
+                            static_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
     DecodeArgs a;
     a.q = query;
     a.bt = block_tables;
@@ -182,6 +204,24 @@ int run_decode(pa_bf16 *out, const pa_bf16 *query, const void *key_cache, const 
 
 }  // namespace
 
+namespace pa {
+
+size_t no_alloc_bytes(int B, int Hq, int Hkv, int D) {
+    DecodeGeometry geo;
+    if (pa_decode_workspace_size(B, Hq, Hkv, D) == 0 || decode_geometry(D, &geo) != cudaSuccess) return 0;
+    return decode_bytes(B, Hkv, D, geo.workers, false, true);
+}
+
+int decode_no_alloc(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *key_cache, const pa_bf16 *value_cache,
+                    const int32_t *block_tables, int MBS, const int32_t *context_lens, int B, int Hq, int Hkv, int D,
+                    int BS, int64_t NB, float scale, void *scratch, size_t scratch_bytes, void *stream) {
+    return run_decode(out, query, key_cache, value_cache, block_tables, MBS, context_lens, nullptr, 0, B, Hq, Hkv, D,
+                      BS, NB, scale, scratch, scratch_bytes, stream, false, nullptr, nullptr, false, nullptr, 0, 0,
+                      nullptr, nullptr, false, nullptr, true);
+}
+
+}  // namespace pa
+
 extern "C" {
 
 const char *pa_status_string(int status) {
@@ -222,7 +262,7 @@ size_t pa_decode_workspace_size(int batch, int num_q_heads, int num_kv_heads, in
     if (!shape_supported(head_dim, kBlockSize) || batch > kMaxBatch) return 0;
     DecodeGeometry geo;
     if (decode_geometry(head_dim, &geo) != cudaSuccess) return 0;
-    return decode_workspace_bytes(batch, num_kv_heads, head_dim, geo.workers);
+    return decode_bytes(batch, num_kv_heads, head_dim, geo.workers, false);
 }
 
 int pa_decode(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *key_cache,
@@ -796,7 +836,7 @@ size_t pa_decode_multi_workspace_size(int total_q, int num_q_heads, int num_kv_h
     if (total_q > kMaxMultiRows || !shape_supported(head_dim, kBlockSize)) return 0;
     DecodeGeometry geo;
     if (decode_geometry(head_dim, &geo) != cudaSuccess) return 0;
-    return decode_multi_workspace_bytes(total_q, num_kv_heads, head_dim, geo.workers);
+    return decode_bytes(total_q, num_kv_heads, head_dim, geo.workers, true);
 }
 
 int pa_decode_multi(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *key_cache,

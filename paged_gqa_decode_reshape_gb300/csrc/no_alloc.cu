@@ -21,7 +21,7 @@
 #include <mutex>
 
 #include "../../include/paged_decode.h"
-#include "kernels.h"
+#include "no_alloc.h"
 
 namespace {
 
@@ -55,7 +55,7 @@ extern "C" int pa_decode_no_alloc(pa_bf16 *out, const pa_bf16 *query, const pa_b
         }
         scratch = g_scratch_ptr[dev];
     }
-    const size_t need = pa_decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim);
+    const size_t need = pa::no_alloc_bytes(batch, num_q_heads, num_kv_heads, head_dim);
     if (need == 0)  // invalid or unsupported shape: let pa_decode name the error
         return pa_decode(out, query, key_cache, value_cache, block_tables, max_blocks_per_seq,
                          context_lens, batch, num_q_heads, num_kv_heads, head_dim, block_size,
@@ -66,9 +66,9 @@ extern "C" int pa_decode_no_alloc(pa_bf16 *out, const pa_bf16 *query, const pa_b
     const size_t counters = (size_t(batch) * size_t(num_kv_heads) * 4 + 255) / 256 * 256;
     e = cudaMemsetAsync(scratch, 0, 256 + counters, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return PA_ERR_CUDA;
-    return pa_decode(out, query, key_cache, value_cache, block_tables, max_blocks_per_seq,
-                     context_lens, batch, num_q_heads, num_kv_heads, head_dim, block_size,
-                     num_blocks, scale, scratch, kNoAllocScratchBytes, stream);
+    return pa::decode_no_alloc(out, query, key_cache, value_cache, block_tables, max_blocks_per_seq, context_lens,
+                               batch, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, scratch,
+                               kNoAllocScratchBytes, stream);
 }
 
 extern "C" int pa_decode_no_alloc_status(void *stream) {
