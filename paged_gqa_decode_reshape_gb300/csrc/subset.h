@@ -7,9 +7,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <mutex>
-#include <utility>
-#include <vector>
+#include <atomic>
 
 namespace pa {
 
@@ -59,18 +57,26 @@ struct SubsetArgs {
     int min_items;                // row tiles: tiles of a CTA's range at least
 };
 
-// Dynamic shared memory limit of a kernel, set once per device.
-inline cudaError_t smem_once(const void *kernel, size_t bytes) {
-    static std::mutex mu;
-    static std::vector<std::pair<int, const void *>> done;
+// Dynamic shared memory limit of a kernel, set once per device (or at every call
+// beyond the table's devices and kernels). Allocates nothing and throws nothing:
+// it runs below C entry points.
+inline cudaError_t smem_once(const void *kernel, size_t bytes) noexcept {
+    constexpr int kDevices = 64, kKernels = 32;
+    static std::atomic<const void *> done[kDevices][kKernels];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lock(mu);
-    for (const auto &d : done)
-        if (d.first == dev && d.second == kernel) return cudaSuccess;
+    const bool known = dev >= 0 && dev < kDevices;
+    for (int i = 0; known && i < kKernels; ++i) {
+        const void *at = done[dev][i].load(std::memory_order_acquire);
+        if (at == kernel) return cudaSuccess;
+        if (!at) break;
+    }
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
-    if (e == cudaSuccess) done.emplace_back(dev, kernel);
+    for (int i = 0; e == cudaSuccess && known && i < kKernels; ++i) {
+        const void *at = nullptr;
+        if (done[dev][i].compare_exchange_strong(at, kernel, std::memory_order_acq_rel) || at == kernel) break;
+    }
     return e;
 }
 
