@@ -645,8 +645,12 @@ PA_API int quest_decode_fp8_block(pa_bf16 *out, int32_t *selected, const pa_bf16
  * and shape, but not calls of other sections besides, and calls that overlap in
  * time (on different streams, in graphs that are replayed beside other calls)
  * need different ones. pa_workspace_status reads their status. They take about 15 MB (pa_decode_window), 55 MB
- * (pa_decode_window_multi, pa_decode_prefix), and 4 bytes per query head and
- * table slot more for pa_decode_weights. The same call gives the same bits on a
+ * (pa_decode_window_multi, pa_decode_prefix), for pa_decode_prefix 8 bytes more per
+ * element of out, and for pa_decode_weights 4 bytes more per query head and
+ * table slot (of block_tables as wide as they are passed). Which kernels a call
+ * takes goes by the width of its tables as well, since the lengths are on the
+ * device: tables no wider than the longest sequence needs make small calls of
+ * pa_decode_window_multi and pa_decode_prefix up to twice as fast. The same call gives the same bits on a
  * device, but for what pa_decode_weights says about shared blocks; how the work
  * is cut, and so the rounding, depends on the call's sizes. */
 
@@ -708,8 +712,9 @@ PA_API int pa_decode_window_multi(pa_bf16 *out, const pa_bf16 *query, const pa_b
  * prefix_tables[g][0..max_prefix_blocks). Sequence b sees its group's prefix
  * and then its own tokens t < context_lens[b], in the blocks of
  * block_tables[b] (which do not repeat the prefix's). The prefix length need
- * not be a multiple of the block size. A group's prefix is read from memory once
- * for all its sequences. cu_group is [num_groups + 1] int32 on the device, ascending
+ * not be a multiple of the block size. A group's prefix is read once for all its
+ * sequences, by small calls once per sequence (out of L2, but for the first
+ * time). cu_group is [num_groups + 1] int32 on the device, ascending
  * from 0; a sequence of no group has no prefix; a sequence with neither
  * prefix nor own tokens gets a zero output. num_groups <= 4096. bf16 cache. */
 PA_API size_t pa_decode_prefix_workspace_size(int batch, int num_groups, int num_q_heads, int num_kv_heads,

@@ -1004,11 +1004,13 @@ int prefix_ctas(const SubsetArgs &a, int D, int sms) {
 
 // Small calls read a prefix once per sequence (from L2, but for the first time):
 // one launch of the streaming kernel over prefix and own tokens, instead of three
-// launches one after another. By what the tables hold at most, the own tokens at
-// half of it, up to kEachReads bytes. Each and shared, 28 / 4 heads of 128: 2
-// sequences behind 500 tokens (2 MB) 6.1 and 14.9 us, 8 behind 2000 (33 MB) 9.9 and
-// 16.2, 32 behind 1000 (69 MB) 11.5 and 17.6, 8 behind 8000 (127 MB) 18.6 and 20.5, 64
-// behind 1000 (131 MB) 20.7 and 19.6, 64 behind 8192 90 and 34; and 4 us of the host.
+// launches one after another. By what the tables can hold, the own tokens at half of
+// it, up to kEachReads bytes; the lengths are not known here, so tables wider than
+// they need be make a small call a large one. Each for itself and shared, 28 / 4 heads
+// of 128, 100 own tokens: 2 sequences behind 500 tokens (2 MB) 7.1 and 15.2 us, 8
+// behind 2000 (32 MB) 10.2 and 16.4, 32 behind 1000 (66 MB) 11.5 and 17.7, 8 behind
+// 8000 (126 MB, shared by this rule) 18.8 and 20.8, 64 behind 1000 (133 MB) 21.2 and
+// 19.4, 64 behind 8192 89 and 33; and 4 us of the host.
 constexpr int64_t kEachReads = int64_t(120) << 20;
 
 bool reads_each(const SubsetArgs &a, int D) {
@@ -1017,14 +1019,17 @@ bool reads_each(const SubsetArgs &a, int D) {
 
 // The same for several query rows per sequence: each reads its window for itself,
 // by one launch of the streaming kernel, up to kEachReads bytes where every (row, KV
-// head) has an SM, and up to half of it beyond. Each row and row tiles: 4 sequences of
-// 1 row on 700 tokens (5 MB) 7.3 and 12.7 us, 48 of 3 on 100 (28 MB) 12.3 and 12.9, one
-// of 64 on 400 (50 MB) 13.6 and 20.6, 8 of 2 on 2000 (62 MB, one SM each) 14.3 and 18.3, on
-// 4000 (125 MB) 20.0 and 27.5, 32 of 2 on 500 (62 MB) 17.1 and 15.4.
+// head) has an SM, and up to kEachReadsMany where there are more of them. Each row and row
+// tiles: 4 sequences of 1 row on 700 tokens (5 MB) 7.5 and 13.9 us, 48 of 3 on 100 (31 MB)
+// 12.3 and 13.0, one of 64 on 400 (50 MB) 13.7 and 20.3, 8 of 2 on 2000 (62 MB, an SM
+// each) 14.4 and 19.1, on 4000 (125 MB, row tiles by this rule) 20.1 and 28.5, 32 of 2
+// on 500 (64 MB) 16.6 and 14.8.
+constexpr int64_t kEachReadsMany = int64_t(56) << 20;
+
 bool rows_each(const SubsetArgs &a, int D, int sms) {
     const double seen = std::min(double(a.MBS) * kBlockSize, double(a.window) + a.sinks + 2 * kBlockSize);
     const int64_t segs = int64_t(a.rows) * a.Hkv;
-    return segs * seen * D * 4 <= double(segs <= sms ? kEachReads : kEachReads / 2 - (int64_t(4) << 20));
+    return segs * seen * D * 4 <= double(segs <= sms ? kEachReads : kEachReadsMany);
 }
 
 // the launches, after the argument checks

@@ -19,9 +19,9 @@ constexpr int kBins = 2 * kSelThreads;  // of a selection pass
 constexpr int kCand = 256;              // keys ranked against one another at the end
 // From this many SMs per (sequence, KV head) on, one launch in which every CTA
 // selects and copies a share; below, a CTA selects for all and a second launch
-// copies. One sequence of 1500 tokens, 1024 kept: 6.7 us in one launch, 6.8 in two
-// (and 2 us of the host); 9 of 2000, 512 kept: 8.7 and 9.9; 9 of 8192, 4096 kept:
-// 37.7 and 38.0; 16 of those, two CTAs each: 62.6 and 59.6 (4 KV heads of 128: the
+// copies. One sequence of 1500 tokens, 1024 kept: 6.5 us in one launch, 6.8 in two
+// (and 2 us of the host); 9 of 2000, 512 kept: 8.5 and 9.6; 9 of 8192, 4096 kept:
+// 37.5 and 37.8; 16 of those, two CTAs each: 62.7 and 59.4 (4 KV heads of 128: the
 // copy wants more warps than two CTAs of 1024 threads per head have).
 constexpr int kMinParts = 4;
 constexpr int kKeysCap = 48 * 1024;  // keys held in shared memory; longer rows read them again

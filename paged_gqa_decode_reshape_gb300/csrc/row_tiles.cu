@@ -38,7 +38,7 @@
 //    than 2^8 since the last time: until then probabilities up to 2^8 are exact
 //    multiples, bf16 keeps its 8 bits at any magnitude, and l is fp32 (rescaling
 //    at every new maximum: 274 against 248 us). P is rounded to bf16 for the product
-//    (2^-9 per weight); l sums it before that: the sum of rounded values took 277
+//    (by at most 2^-8 of a weight); l sums it before that: the sum of rounded values took 277
 //    us and gave an error of 2.2e-3 against 2.3e-3 of a row's norm.
 //  * Masks: a 16-bit mask per block and row on the tiles at an edge, none
 //    inside. V rows no row of the unit sees are zeroed in shared memory. A
@@ -1037,9 +1037,9 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
 // a time), its columns side by side, KB pieces in flight. Bound by latency. For
 // calls with fewer units than half the CTAs, whose units have several pieces each:
 // one CTA would read them all. Merged by the last piece's CTA and by this kernel
-// (which costs 1.6 us of the host as well): 8 sequences of 5 rows on 4000 tokens
-// 31.7 and 27.1 us, 2 of 64 rows 47.0 and 30.4; with 128 units on 152 CTAs, 32
-// sequences of 2 rows on 3000 tokens, 49.2 and 55.2.
+// (which costs 1.6 us of the host as well), on 4000 tokens: 8 sequences of 5 rows
+// 32.9 and 28.8 us, 2 of 64 rows 40.8 and 26.8; with 128 units on 152 CTAs, 32
+// sequences of 2 rows on 3000 tokens, 49.1 and 54.5.
 template <int D>
 __global__ void __launch_bounds__(256) cut_join_kernel(const SubsetArgs a) {
     pdl_trigger();

@@ -9,8 +9,8 @@
 //
 // Bound: every visible K/V byte is read once, at about 2 G flops per byte, so
 // HBM bandwidth bounds long calls and latency short ones. Measured (28 / 4 heads
-// of 128, all tokens seen): 500 sequences of 2000 tokens 306 us = 6.7 TB/s, 8-bit
-// cache 158 us = 6.5 TB/s; 16 of 4096 25.4 us = 5.3 TB/s, of which about 5 us are
+// of 128, all tokens seen): 500 sequences of 2000 tokens 316 us = 6.5 TB/s, 8-bit
+// cache 158 us = 6.5 TB/s (161 with a scale per block); 16 of 4096 25.2 us = 5.3 TB/s, of which about 5 us are
 // the launch, the lengths, the table and the first copies one after another, and
 // the last merges; one of 256 tokens 4.6 us.
 //
@@ -60,16 +60,16 @@ constexpr int kPreCap = 512;   // entries of the items-per-sequence prefix in sh
 constexpr int kEndCost = 2;
 // Items of a CTA's piece at least, where there are as many; while no segment has
 // more than twice that, all stay whole. A cut costs about 1.7 us at the end, an item less per warp
-// saves 0.85 us: 16 sequences of 500 tokens take 8.0 us in two pieces each, 6.3
-// whole; one of 2048 tokens 7.3 us in pieces of 12 items, 9.1 in pieces of 24; one
-// of 8192 tokens 9.4 us, in pieces of 6 or 24 10.3 (28 / 4 heads of 128).
+// saves 0.85 us: 16 sequences of 500 tokens take 8.4 us in pieces of 6 and more, 6.5
+// whole; one of 2048 tokens 7.5 us in pieces of 12 items, 9.3 of 24, 7.2 of 6; one of
+// 8192 tokens 10.4 us, of 24 10.6, of 6 11.0 (28 / 4 heads of 128).
 constexpr int kMinPiece = 12;
 // Accumulated weights, one piece per CTA: the CTA that has a segment's rows adds
 // its weights while the table has at most this many blocks per segment of the
 // call; longer ones are added by a launch of their own over the whole grid. One
 // CTA's addition takes 0.75 us per 1024 tokens, the launch 3 us or more and 1.6 us
-// of the host: one sequence of 2048 tokens 9.7 us fused, 10.1 separate; of 8192
-// tokens 15.5 and 13.0; 16 sequences of 8192 tokens 51.6 and 52.9.
+// of the host: one sequence of 2048 tokens 9.8 us fused, 10.3 separate; of 8192
+// tokens 16.8 and 13.6; 16 sequences of 8192 tokens 55.0 and 56.5.
 constexpr int kFusedAddBlocks = 64;
 
 #ifndef PA_STREAM_WARPS_F8
@@ -675,7 +675,7 @@ __global__ void __launch_bounds__(StreamCfg<D, KIND>::THREADS, 1)
             p[e] = fast_exp2(x[e] - (e & 1 ? r1 : r0));
             q[e] = fast_exp2(y[e] - (e & 1 ? r1 : r0));
         }
-        // P meets V as bf16 (f16 with E4M3 values): relative rounding 2^-9 (2^-12) per weight, as in the dense decode
+        // P meets V as bf16 (f16 with E4M3 values): off by at most 2^-8 (2^-11) of each weight, as in the dense decode
         auto pk = [](float lo, float hi) { return F8 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi); };
         const uint32_t p01 = pk(p[0], p[1]), p23 = pk(p[2], p[3]), q01 = pk(q[0], q[1]), q23 = pk(q[2], q[3]);
         if constexpr (!LOGITS) {
