@@ -1089,22 +1089,35 @@ def quest_reshape_and_decode(out: torch.Tensor, selected: torch.Tensor, query: t
 PARTIAL_ZERO_BYTES = 64 << 10  # PA_PARTIAL_ZERO_BYTES: what of a workspace has to be zero before its first use
 
 
+def _in_graph_pool(buf: torch.Tensor) -> bool:
+    """Whether a buffer allocated during a capture came from a CUDA graph's own memory pool, which lives as long as
+    the graph (torch.cuda.graph), and not from the general one."""
+    try:
+        for seg in torch.cuda.memory_snapshot():
+            if 0 <= buf.data_ptr() - seg["address"] < seg["total_size"]:
+                return tuple(seg["segment_pool_id"]) != (0, 0)
+    except Exception:  # an allocator without snapshots
+        pass
+    return False
+
+
 class _Scratch:
     """Workspaces for calls without one: a buffer per device and stream, as calls on different streams may run beside
-    one another. A CUDA graph's calls get buffers of their own from the graph's memory pool, one per captured stream,
-    which the graph clears before its first use of them, so it shares none with eager calls or with other graphs."""
+    one another. A CUDA graph's calls get buffers of their own, one per captured stream, which the graph clears before
+    its first use of them, so it shares none with eager calls or with other graphs. They come from the graph's memory
+    pool; those of a graph without one are kept for good, as the graph holds their addresses."""
 
     def __init__(self):
         self.at = {}  # (device index, stream) -> (address, bytes) of the buffer of calls outside captures
         self._buf = {}
         self._largest = {}  # device index -> bytes of the largest of them
-        self._captured = {}  # device index -> (id of the last capture seen, {stream: buffer})
+        self._captured = {}  # (device index, capture id) of the last captures seen -> {stream: buffer}
+        self._for_good = []
 
     def held(self, index: int, stream: int) -> Optional[torch.Tensor]:
         if not torch.cuda.is_current_stream_capturing():
             return self._buf.get((index, stream))
-        capture, bufs = self._captured.get(index, (None, {}))
-        return bufs.get(stream) if capture == pa_capture_id(stream) else None
+        return self._captured.get((index, pa_capture_id(stream)), {}).get(stream)
 
     def get(self, device: torch.device, nbytes: int, stream: int) -> torch.Tensor:
         """The buffer of this device's current stream, of at least nbytes."""
@@ -1121,10 +1134,12 @@ class _Scratch:
         buf = torch.empty(n, dtype=torch.uint8, device=device)
         buf[:PARTIAL_ZERO_BYTES].zero_()
         if capturing:
-            capture = pa_capture_id(stream)
-            if self._captured.get(index, (None,))[0] != capture:
-                self._captured[index] = (capture, {})
-            self._captured[index][1][stream] = buf
+            key = (index, pa_capture_id(stream))
+            if key not in self._captured and len(self._captured) >= 8:  # captures that are over, but for a few
+                del self._captured[next(iter(self._captured))]
+            self._captured.setdefault(key, {})[stream] = buf
+            if not _in_graph_pool(buf):
+                self._for_good.append(buf)
         else:
             self._buf[index, stream] = buf
             self.at[index, stream] = (buf.data_ptr(), n)

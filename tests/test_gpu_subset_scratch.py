@@ -90,6 +90,8 @@ def test_graphs_beside_one_another_and_beside_eager_calls():
             held.append(pg.partial_cache_workspace())
         graphs.append(graph)
     assert held[0].data_ptr() != held[1].data_ptr()
+    assert all(pg._in_graph_pool(h) for h in held) and not pg._in_graph_pool(pg.partial_cache_workspace())
+    assert not any(t is h for t in pg._subset_ws._for_good for h in held)
     streams = [torch.cuda.Stream() for _ in work]
     torch.cuda.synchronize()
     for _ in range(20):

@@ -2,6 +2,8 @@
 (streams and captures stood in for): streams that may run beside one another
 and captures never share a buffer."""
 
+import weakref
+
 import pytest
 import torch
 
@@ -75,3 +77,26 @@ def test_a_capture_before_any_call_is_refused(on):
     on(1000, handle=3, capture=11)
     with pytest.raises(RuntimeError, match="before the capture"):
         on(5000, handle=3, capture=11)
+
+
+def test_captures_in_turn_keep_their_buffers(on):
+    """Captures of several threads, whose calls come in turn."""
+    on(1000, handle=0)
+    held = []
+    for _ in range(3):
+        for handle, capture in ((3, 11), (4, 12)):
+            on(1000, handle=handle, capture=capture)
+            held.append(pg._subset_ws.held(0, handle))
+    assert all(h is held[i % 2] for i, h in enumerate(held)) and held[0] is not held[1]
+
+
+@pytest.mark.parametrize("pooled", [False, True])
+def test_buffers_outside_a_graphs_pool_are_kept(on, monkeypatch, pooled):
+    """A graph that was not captured into a memory pool of its own holds its buffer's address for good."""
+    monkeypatch.setattr(pg, "_in_graph_pool", lambda buf: pooled)
+    on(1000, handle=0)
+    on(1000, handle=3, capture=100)
+    first = weakref.ref(pg._subset_ws.held(0, 3))
+    for i in range(20):
+        on(1000, handle=3, capture=200 + i)
+    assert (first() is None) == pooled
