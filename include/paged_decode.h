@@ -43,9 +43,10 @@
  *     call, and cu_seqlens_q by pa_decode_multi and pa_decode_window_multi,
  *     prefix_lens and cu_group by pa_decode_prefix) and block_tables (read
  *     before it by the bf16 dense decode and by the selection's score
- *     kernel). No kernel of this library writes them but pa_evict's new_lens,
- *     which may be the next call's context_lens: its last kernel lets nothing
- *     start early. A caller kernel that
+ *     kernel). No kernel of this library writes them but those of pa_plan_step
+ *     and pa_release_blocks and pa_evict's for new_lens, which may be the next
+ *     call's context_lens: their last kernels let nothing start early. A caller
+ *     kernel that
  *     writes them and lets dependent launches start early must not run just
  *     before such a call. A kernel that never triggers early starts its
  *     dependents only when it completes, so the usual case is safe.
@@ -706,6 +707,26 @@ PA_API int pa_decode_window_multi(pa_bf16 *out, const pa_bf16 *query, const pa_b
                                   int64_t num_blocks, int window, int sinks, float scale, void *workspace,
                                   size_t workspace_bytes, void *stream);
 
+/* pa_decode_window_multi over an 8-bit cache: prompt chunks and speculative
+ * rows read K and V as pa_decode_fp8 (scales per KV head) or pa_decode_fp8_block
+ * (powers of two per block) do. head_dim 128. With window >= every context a
+ * row sees all tokens before it. Workspace: pa_decode_window_multi_workspace_size. */
+PA_API int pa_decode_window_multi_fp8(pa_bf16 *out, const pa_bf16 *query, const pa_e4m3 *key_cache,
+                                      const pa_e4m3 *value_cache, const float *k_scale, const float *v_scale,
+                                      const int32_t *block_tables, int max_blocks_per_seq,
+                                      const int32_t *cu_seqlens_q, const int32_t *context_lens, int batch, int total_q,
+                                      int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                      int64_t num_blocks, int window, int sinks, float scale, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
+PA_API int pa_decode_window_multi_fp8_block(pa_bf16 *out, const pa_bf16 *query, const pa_e4m3 *key_cache,
+                                            const pa_e4m3 *value_cache, const float *k_bscale, const float *v_bscale,
+                                            const int32_t *block_tables, int max_blocks_per_seq,
+                                            const int32_t *cu_seqlens_q, const int32_t *context_lens, int batch,
+                                            int total_q, int num_q_heads, int num_kv_heads, int head_dim,
+                                            int block_size, int64_t num_blocks, int window, int sinks, float scale,
+                                            void *workspace, size_t workspace_bytes, void *stream);
+
 /* Decode attention of a batch whose sequences share long prefixes (one query
  * token per sequence): sequences cu_group[g] .. cu_group[g+1]-1 form group g
  * and all begin with the same prefix_lens[g] tokens, which are in the blocks
@@ -771,6 +792,109 @@ PA_API int pa_evict(int32_t *kept, int32_t *new_lens, pa_bf16 *key_cache, pa_bf1
                     const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
                     const int32_t *dst_tables, int max_dst_blocks, int batch, int num_kv_heads, int head_dim,
                     int block_size, int64_t num_blocks, int budget, int recent, void *stream);
+
+/* ----------------------------------------- a step around its attention ----
+ * What a serving step does between its requests and its attention: block
+ * tables, row offsets, positions and slots from request lengths; the norm and
+ * the rotation of queries and keys with the cache write. No workspace. */
+
+/* Plans a step. Sequence b has c = context_lens[b] tokens in the cache (clamped
+ * to [0, MBS * BS]) and q = query_lens[b] new ones (negative: 0), whose rows
+ * follow each other in the order of b:
+ *   cu_seqlens_q[b + 1] = min(q_0 + ... + q_b, total_q), cu_seqlens_q[0] = 0.
+ * A sequence is granted its tokens if c + q <= MBS * BS, its rows end within
+ * total_q and the blocks it lacks are there. free_blocks [free_capacity] is a
+ * stack, its first *num_free entries free (clamped to [0, free_capacity]);
+ * needing n = ceil((c + q) / BS) - ceil(c / BS) blocks after the earlier
+ * sequences' r, b takes
+ *   block_tables[b][ceil(c / BS) + j] = free_blocks[*num_free - 1 - (r + j)],
+ * j < n, if r + n <= *num_free. (r counts the blocks of refused sequences too:
+ * once one does not get its blocks, no later one gets any.) Then
+ *   granted[b] = q,  new_lens[b] = c + q,
+ * and for row i of b, at position p = c + i: positions = p, slot_mapping =
+ * block_tables[b][p / BS] * BS + p % BS (-1 where that block is not in
+ * [0, num_blocks)). Of a sequence that is refused the table stays as it is,
+ * granted[b] = 0, new_lens[b] = c, and its rows' slots are -1 (its attention
+ * rows mean nothing). *new_free = *num_free minus the blocks taken. Rows of no
+ * sequence: position 0, slot -1. Every element of the outputs is written.
+ * In place: new_lens may be context_lens and new_free may be num_free;
+ * otherwise no output may overlap an input. 1 <= total_q <= 1048576,
+ * batch <= 4096. Its kernels let nothing start early, so the attention calls,
+ * which read lengths and tables before they wait, may follow directly. */
+PA_API int pa_plan_step(int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                        const int32_t *query_lens, int batch, int block_size, int64_t num_blocks,
+                        const int32_t *free_blocks, int64_t free_capacity, const int32_t *num_free, int32_t *new_lens,
+                        int32_t *new_free, int32_t *granted, int32_t *cu_seqlens_q, int32_t *positions,
+                        int64_t *slot_mapping, int total_q, void *stream);
+
+/* Gives blocks back: of sequence b's c = context_lens[b] tokens (clamped as
+ * above) the first k = min(max(keep_lens[b], 0), c) stay, and the blocks
+ * block_tables[b][ceil(k / BS) .. ceil(c / BS) - 1] go to the stack, in the
+ * order of (b, position): free_blocks[*num_free + r] for the r-th of them. For
+ * sequences that are over (keep 0) and for tokens that are taken back (rejected
+ * speculative ones). new_lens[b] = k, *new_free = *num_free + their number.
+ * Entries outside [0, num_blocks) (already freed) are passed over; blocks past
+ * free_capacity are not pushed. The tables are not written: what lies past a
+ * sequence's blocks is not read. A block in several tables would be pushed
+ * several times: shared prefixes belong in tables of their own
+ * (pa_decode_prefix). In place and early starts: as pa_plan_step. */
+PA_API int pa_release_blocks(const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                             const int32_t *keep_lens, int batch, int block_size, int64_t num_blocks,
+                             int32_t *free_blocks, int64_t free_capacity, const int32_t *num_free, int32_t *new_lens,
+                             int32_t *new_free, void *stream);
+
+/* Norm and rotation of queries and keys. Each head x of a token's query
+ * [Hq][D] and key [Hkv][D] becomes
+ *   y_d = x_d / sqrt(mean_d x_d^2 + eps) * weight_d    (q_weight / k_weight [D];
+ *                                                      null: y = x)
+ * and then its first rotary_dim = R dims are rotated in pairs (i, i + R / 2), or
+ * (2 i, 2 i + 1) with interleaved != 0, i < R / 2:
+ *   first' = first cos - second sin,  second' = second cos + first sin,
+ * cos = cos_sin[p][i], sin = cos_sin[p][R / 2 + i]; cos_sin is [max_positions][R]
+ * fp32. p = positions[token], or with num_axes > 1 (time, height, width of
+ * images and video) positions[axes[i]][token]: positions [num_axes][num_tokens],
+ * axes [R / 2] int32. Positions outside the table and axes outside
+ * [0, num_axes) are clamped. Everything in fp32, rounded once to bf16.
+ * Row strides (in elements, from one token to the next) may be larger than a
+ * row's heads, so q, k and v may be parts of one projection's output; q_out and
+ * k_out may be query and key themselves (with the same strides), else no output
+ * may overlap an input. Strides are multiples of 8, pointers 16-byte aligned,
+ * R a multiple of 16 up to D, num_axes <= 4, eps >= 0. num_tokens 0 is a
+ * no-op. */
+PA_API int pa_norm_rope(pa_bf16 *q_out, int64_t q_out_stride, pa_bf16 *k_out, int64_t k_out_stride,
+                        const pa_bf16 *query, int64_t query_stride, const pa_bf16 *key, int64_t key_stride,
+                        const pa_bf16 *q_weight, const pa_bf16 *k_weight, float eps, const float *cos_sin,
+                        int64_t max_positions, int rotary_dim, const int32_t *positions, const int32_t *axes,
+                        int num_axes, int interleaved, int64_t num_tokens, int num_q_heads, int num_kv_heads,
+                        int head_dim, void *stream);
+
+/* pa_norm_rope and pa_reshape_and_cache in one pass: the rotated keys and the
+ * values go to the cache (slots and skip rules as pa_reshape_and_cache), the
+ * rotated queries to q_out, and the rotated keys to k_out as well unless it is
+ * null (a Quest cache's metadata are updated from it: quest_update_meta). */
+PA_API int pa_norm_rope_and_cache(pa_bf16 *q_out, int64_t q_out_stride, pa_bf16 *k_out, int64_t k_out_stride,
+                                  const pa_bf16 *query, int64_t query_stride, const pa_bf16 *key, int64_t key_stride,
+                                  const pa_bf16 *value, int64_t value_stride, const pa_bf16 *q_weight,
+                                  const pa_bf16 *k_weight, float eps, const float *cos_sin, int64_t max_positions,
+                                  int rotary_dim, const int32_t *positions, const int32_t *axes, int num_axes,
+                                  int interleaved, pa_bf16 *key_cache, pa_bf16 *value_cache,
+                                  const int64_t *slot_mapping, int64_t num_tokens, int num_q_heads, int num_kv_heads,
+                                  int head_dim, int block_size, int64_t num_blocks, void *stream);
+
+/* The same into an 8-bit cache with scales per KV head (codes as
+ * pa_reshape_and_cache_fp8's, of the fp32 rotated keys: not rounded to bf16 on
+ * the way; k_out is). head_dim 128. A cache with per-block scales is written by
+ * pa_norm_rope and pa_reshape_and_cache_fp8_block. */
+PA_API int pa_norm_rope_and_cache_fp8(pa_bf16 *q_out, int64_t q_out_stride, pa_bf16 *k_out, int64_t k_out_stride,
+                                      const pa_bf16 *query, int64_t query_stride, const pa_bf16 *key,
+                                      int64_t key_stride, const pa_bf16 *value, int64_t value_stride,
+                                      const pa_bf16 *q_weight, const pa_bf16 *k_weight, float eps,
+                                      const float *cos_sin, int64_t max_positions, int rotary_dim,
+                                      const int32_t *positions, const int32_t *axes, int num_axes, int interleaved,
+                                      pa_e4m3 *key_cache, pa_e4m3 *value_cache, const float *k_scale,
+                                      const float *v_scale, const int64_t *slot_mapping, int64_t num_tokens,
+                                      int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                      int64_t num_blocks, void *stream);
 
 #ifdef __cplusplus
 }

@@ -12,10 +12,13 @@ Names follow the C ABI: ``pa_reshape_and_cache``, ``pa_decode``,
 launch), ``quest_rebuild_meta``, ``quest_select_topk``,
 ``quest_sparse_decode``; ``pa_decode_multi`` for several query rows per
 sequence; the ``*_fp8`` variants for an 8-bit (E4M3) cache;
-``pa_decode_window`` (``_multi``, ``_fp8``, ``_fp8_block``) over a sliding
-window and first tokens; ``pa_decode_prefix`` over shared prefixes;
+``pa_decode_window`` (``_fp8``, ``_fp8_block``, and ``_multi`` of each) over a
+sliding window and first tokens; ``pa_decode_prefix`` over shared prefixes;
 ``pa_decode_weights``, ``pa_reset_weights`` and ``pa_evict`` for eviction by
-accumulated attention weight; plus the workspace-size queries and checks.
+accumulated attention weight; ``pa_plan_step`` and ``pa_release_blocks`` for
+block tables and slots from request lengths; ``pa_norm_rope`` (``_and_cache``,
+``_and_cache_fp8``) for norm and rotation of queries and keys with the cache
+write; plus the workspace-size queries and checks.
 """
 
 from __future__ import annotations
@@ -49,9 +52,11 @@ __all__ = [
     "pa_decode_fp8_block", "pa_decode_fp8_block_budget", "quest_sparse_decode_fp8_block", "quest_decode_fp8_block",
     "pa_reshape_and_decode", "quest_reshape_and_decode",
     "pa_decode_window_workspace_size", "pa_decode_window", "pa_decode_window_fp8", "pa_decode_window_fp8_block",
-    "pa_decode_window_multi_workspace_size", "pa_decode_window_multi",
+    "pa_decode_window_multi_workspace_size", "pa_decode_window_multi", "pa_decode_window_multi_fp8",
+    "pa_decode_window_multi_fp8_block",
     "pa_decode_prefix_workspace_size", "pa_decode_prefix",
     "pa_decode_weights_workspace_size", "pa_decode_weights", "pa_reset_weights", "pa_evict",
+    "pa_plan_step", "pa_release_blocks", "pa_norm_rope", "pa_norm_rope_and_cache", "pa_norm_rope_and_cache_fp8",
     "pa_workspace_status", "pa_capture_id", "pa_check_metadata", "Workspace",
 ]
 
@@ -187,6 +192,11 @@ def load_library(path: Optional[str] = None):
         L.pa_decode_window_multi.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, i64,
                                              i32, i32, f32, vp, sz, vp]
         L.pa_decode_window_multi.restype = i32
+        L.pa_decode_window_multi_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32,
+                                                 i64, i32, i32, f32, vp, sz, vp]
+        L.pa_decode_window_multi_fp8.restype = i32
+        L.pa_decode_window_multi_fp8_block.argtypes = L.pa_decode_window_multi_fp8.argtypes
+        L.pa_decode_window_multi_fp8_block.restype = i32
         L.pa_decode_prefix_workspace_size.argtypes = [i32, i32, i32, i32, i32]
         L.pa_decode_prefix_workspace_size.restype = sz
         L.pa_decode_prefix.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, i32, vp, i32, vp, i32, i32, i32, i32, i32,
@@ -203,6 +213,19 @@ def load_library(path: Optional[str] = None):
         L.pa_reset_weights.restype = i32
         L.pa_evict.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i64, i32, i32, vp]
         L.pa_evict.restype = i32
+        L.pa_plan_step.argtypes = [vp, i32, vp, vp, i32, i32, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, i32, vp]
+        L.pa_plan_step.restype = i32
+        L.pa_release_blocks.argtypes = [vp, i32, vp, vp, i32, i32, i64, vp, i64, vp, vp, vp, vp]
+        L.pa_release_blocks.restype = i32
+        L.pa_norm_rope.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, f32, vp, i64, i32, vp, vp, i32, i32, i64,
+                                   i32, i32, i32, vp]
+        L.pa_norm_rope.restype = i32
+        L.pa_norm_rope_and_cache.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, f32, vp, i64, i32, vp,
+                                             vp, i32, i32, vp, vp, vp, i64, i32, i32, i32, i32, i64, vp]
+        L.pa_norm_rope_and_cache.restype = i32
+        L.pa_norm_rope_and_cache_fp8.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, f32, vp, i64, i32,
+                                                 vp, vp, i32, i32, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, i64, vp]
+        L.pa_norm_rope_and_cache_fp8.restype = i32
         _lib = L
         return _lib
 
@@ -1285,15 +1308,11 @@ def pa_decode_window_fp8_block(out: torch.Tensor, query: torch.Tensor, key_cache
                        block_tables, context_lens, window, sinks, scale, workspace)
 
 
-def pa_decode_window_multi(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
-                           value_cache: torch.Tensor, block_tables: torch.Tensor, cu_seqlens_q: torch.Tensor,
-                           context_lens: torch.Tensor, window: int, sinks: int, scale: float,
-                           workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """Windowed attention of several query rows per sequence: query / out [total_q, Hq, D], rows of sequence b
-    cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1, right-aligned causal masks."""
-    if not _usual(key_cache, value_cache, query, out, block_tables, context_lens, torch.bfloat16):
-        _need(key_cache, "key_cache", torch.bfloat16, 4)
-        _need(value_cache, "value_cache", torch.bfloat16, 4, key_cache.device)
+def _window_multi(name, cache_dtype, out, query, key_cache, value_cache, scales, block_tables, cu_seqlens_q,
+                  context_lens, window, sinks, scale, workspace):
+    if not _usual(key_cache, value_cache, query, out, block_tables, context_lens, cache_dtype):
+        _need(key_cache, "key_cache", cache_dtype, 4)
+        _need(value_cache, "value_cache", cache_dtype, 4, key_cache.device)
         _need(query, "query", torch.bfloat16, 3, key_cache.device)
         _need(out, "out", torch.bfloat16, 3, key_cache.device)
         _need(block_tables, "block_tables", torch.int32, 2, key_cache.device)
@@ -1302,17 +1321,51 @@ def pa_decode_window_multi(out: torch.Tensor, query: torch.Tensor, key_cache: to
     _need(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1, dev)
     T, Hq, D = query.shape
     NB, BS, Hkv, D2 = key_cache.shape
-    if D != D2 or value_cache.shape != key_cache.shape or out.shape != query.shape:
+    if D != D2 or value_cache.shape != ((NB, Hkv, D, BS) if scales else key_cache.shape) or out.shape != query.shape:
         raise ValueError("shape mismatch between query/out and the caches")
     B, MBS = block_tables.shape
     if context_lens.shape[0] != B or cu_seqlens_q.shape[0] != B + 1:
         raise ValueError("block_tables / context_lens / cu_seqlens_q batch mismatch")
+    if scales:
+        (_block_scales if name.endswith("_block") else lambda k, v, _, *a: _scales(k, v, *a))(*scales, NB, Hkv, dev)
     window, sinks = _tokens(window, "window"), _tokens(sinks, "sinks")
-    _run("pa_decode_window_multi", dev,
-         (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(), MBS,
-          cu_seqlens_q.data_ptr(), context_lens.data_ptr(), B, T, Hq, Hkv, D, BS, NB, window, sinks, float(scale)),
+    _run(name, dev,
+         (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+          *[s.data_ptr() for s in scales], block_tables.data_ptr(), MBS, cu_seqlens_q.data_ptr(),
+          context_lens.data_ptr(), B, T, Hq, Hkv, D, BS, NB, window, sinks, float(scale)),
          workspace, (B, T, Hq, Hkv, D))
     return out
+
+
+def pa_decode_window_multi(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                           value_cache: torch.Tensor, block_tables: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                           context_lens: torch.Tensor, window: int, sinks: int, scale: float,
+                           workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Windowed attention of several query rows per sequence: query / out [total_q, Hq, D], rows of sequence b
+    cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1, right-aligned causal masks."""
+    return _window_multi("pa_decode_window_multi", torch.bfloat16, out, query, key_cache, value_cache, (), block_tables,
+                         cu_seqlens_q, context_lens, window, sinks, scale, workspace)
+
+
+def pa_decode_window_multi_fp8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                               value_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                               block_tables: torch.Tensor, cu_seqlens_q: torch.Tensor, context_lens: torch.Tensor,
+                               window: int, sinks: int, scale: float,
+                               workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """pa_decode_window_multi over an 8-bit cache with per-KV-head scales: prompt chunks and speculative rows."""
+    return _window_multi("pa_decode_window_multi_fp8", torch.uint8, out, query, key_cache, value_cache,
+                         (k_scale, v_scale), block_tables, cu_seqlens_q, context_lens, window, sinks, scale, workspace)
+
+
+def pa_decode_window_multi_fp8_block(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                                     value_cache: torch.Tensor, k_bscale: torch.Tensor, v_bscale: torch.Tensor,
+                                     block_tables: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                                     context_lens: torch.Tensor, window: int, sinks: int, scale: float,
+                                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """pa_decode_window_multi over an 8-bit cache with per-block scales."""
+    return _window_multi("pa_decode_window_multi_fp8_block", torch.uint8, out, query, key_cache, value_cache,
+                         (k_bscale, v_bscale), block_tables, cu_seqlens_q, context_lens, window, sinks, scale,
+                         workspace)
 
 
 def pa_decode_prefix(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Tensor,
@@ -1392,3 +1445,181 @@ def pa_evict(kept: torch.Tensor, new_lens: torch.Tensor, key_cache: torch.Tensor
          (kept.data_ptr(), new_lens.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), weights.data_ptr(),
           block_tables.data_ptr(), MBS, context_lens.data_ptr(), dst_tables.data_ptr(), dst_tables.shape[1], B, Hkv,
           D, BS, NB, kept.shape[2], _tokens(recent, "recent")))
+
+
+# ------------------------------------------------ a step around its attention
+
+
+def _ints(dev, *named):
+    """int32 vectors [n] on dev: (tensor, name, n)."""
+    for t, name, n in named:
+        _need(t, name, torch.int32, 1, dev)
+        if n is not None and t.shape[0] != n:
+            raise ValueError(f"{name} must have {n} elements, got {t.shape[0]}")
+
+
+def pa_plan_step(block_tables: torch.Tensor, context_lens: torch.Tensor, query_lens: torch.Tensor,
+                 free_blocks: torch.Tensor, num_free: torch.Tensor, num_blocks: int, new_lens: torch.Tensor,
+                 new_free: torch.Tensor, granted: torch.Tensor, cu_seqlens_q: torch.Tensor, positions: torch.Tensor,
+                 slot_mapping: torch.Tensor, block_size: int = 16) -> None:
+    """Block tables, row offsets [B + 1], positions [total_q] and slots [total_q] of a step that adds query_lens[b]
+    tokens to the context_lens[b] cached ones, with blocks from the stack free_blocks[:num_free]; granted [B] is what
+    each sequence got (all or nothing). new_lens / new_free may be context_lens / num_free."""
+    _need(block_tables, "block_tables", torch.int32, 2)
+    dev = block_tables.device
+    B, MBS = block_tables.shape
+    _ints(dev, (context_lens, "context_lens", B), (query_lens, "query_lens", B), (free_blocks, "free_blocks", None),
+          (num_free, "num_free", 1), (new_lens, "new_lens", B), (new_free, "new_free", 1), (granted, "granted", B),
+          (cu_seqlens_q, "cu_seqlens_q", B + 1), (positions, "positions", None))
+    _need(slot_mapping, "slot_mapping", torch.int64, 1, dev)
+    T = positions.shape[0]
+    if slot_mapping.shape[0] != T:
+        raise ValueError("positions and slot_mapping must have the same length")
+    _run("pa_plan_step", dev,
+         (block_tables.data_ptr(), MBS, context_lens.data_ptr(), query_lens.data_ptr(), B, int(block_size),
+          int(num_blocks), free_blocks.data_ptr(), free_blocks.shape[0], num_free.data_ptr(), new_lens.data_ptr(),
+          new_free.data_ptr(), granted.data_ptr(), cu_seqlens_q.data_ptr(), positions.data_ptr(),
+          slot_mapping.data_ptr(), T))
+
+
+def pa_release_blocks(block_tables: torch.Tensor, context_lens: torch.Tensor, keep_lens: torch.Tensor,
+                      free_blocks: torch.Tensor, num_free: torch.Tensor, num_blocks: int, new_lens: torch.Tensor,
+                      new_free: torch.Tensor, block_size: int = 16) -> None:
+    """Push the blocks behind each sequence's first keep_lens[b] tokens back onto the stack free_blocks[:num_free]:
+    sequences that are over (keep 0), tokens that are taken back. new_lens / new_free may be context_lens / num_free."""
+    _need(block_tables, "block_tables", torch.int32, 2)
+    dev = block_tables.device
+    B, MBS = block_tables.shape
+    _ints(dev, (context_lens, "context_lens", B), (keep_lens, "keep_lens", B), (free_blocks, "free_blocks", None),
+          (num_free, "num_free", 1), (new_lens, "new_lens", B), (new_free, "new_free", 1))
+    _run("pa_release_blocks", dev,
+         (block_tables.data_ptr(), MBS, context_lens.data_ptr(), keep_lens.data_ptr(), B, int(block_size),
+          int(num_blocks), free_blocks.data_ptr(), free_blocks.shape[0], num_free.data_ptr(), new_lens.data_ptr(),
+          new_free.data_ptr()))
+
+
+def _heads(t: torch.Tensor, name: str, rows: Optional[int] = None, device=None):
+    """(heads, head_dim, row stride) of a bf16 tensor [T, H, D] whose rows' heads are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor with 3 dims, got shape {tuple(t.shape)} on {t.device}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    T, H, D = t.shape
+    row, head, one = t.stride()
+    if (one != 1 and D > 1) or (head != D and H > 1):
+        raise ValueError(f"the heads of a row of {name} must be contiguous")
+    if rows is not None and T != rows:
+        raise ValueError(f"{name} must have {rows} rows, got {T}")
+    return H, D, row if T > 1 else H * D  # one row: its stride says nothing
+
+
+def _rope(name, q_out, k_out, query, key, value, cos_sin, positions, q_weight, k_weight, eps, axes, interleaved, cache):
+    T = query.shape[0] if isinstance(query, torch.Tensor) and query.dim() == 3 else None
+    Hq, D, qs = _heads(query, "query")
+    dev = query.device
+    Hkv, D2, ks = _heads(key, "key", T, dev)
+    if D2 != D:
+        raise ValueError("query and key must have the same head_dim")
+    h, d, qos = _heads(q_out, "q_out", T, dev)
+    if (h, d) != (Hq, D):
+        raise ValueError("q_out must have query's shape")
+    kos = vs = 0
+    if k_out is not None:
+        h, d, kos = _heads(k_out, "k_out", T, dev)
+        if (h, d) != (Hkv, D):
+            raise ValueError("k_out must have key's shape")
+    if value is not None:
+        h, d, vs = _heads(value, "value", T, dev)
+        if (h, d) != (Hkv, D):
+            raise ValueError("value must have key's shape")
+    _need(cos_sin, "cos_sin", torch.float32, 2, dev)
+    P, R = cos_sin.shape
+    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, n, torch.bfloat16, 1, dev)
+            if w.shape[0] != D:
+                raise ValueError(f"{n} must be [head_dim]")
+    if axes is None:
+        A = 1
+        _need(positions, "positions", torch.int32, 1, dev)
+    else:
+        _need(positions, "positions", torch.int32, 2, dev)
+        A = positions.shape[0]
+        _need(axes, "axes", torch.int32, 1, dev)
+        if axes.shape[0] * 2 != R:
+            raise ValueError("axes must be [rotary_dim / 2]")
+    if positions.shape[-1] != T:
+        raise ValueError("positions must have a column per token")
+    v = () if value is None else (value.data_ptr(), vs)
+    _run(name, dev,
+         (q_out.data_ptr(), qos, None if k_out is None else k_out.data_ptr(), kos, query.data_ptr(), qs, key.data_ptr(), ks,
+          *v, None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
+          float(eps), cos_sin.data_ptr(), P, R, positions.data_ptr(), None if axes is None else axes.data_ptr(), A,
+          int(bool(interleaved)), *cache(T, Hkv, D, dev), T, Hq, Hkv, D, *(() if value is None else cache.sizes)))
+    return q_out
+
+
+def pa_norm_rope(q_out: torch.Tensor, k_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
+                 cos_sin: torch.Tensor, positions: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, axes: Optional[torch.Tensor] = None,
+                 interleaved: bool = False) -> torch.Tensor:
+    """Norm (weights [D]; None: none) and rotation of every head of query [T, Hq, D] and key [T, Hkv, D] by the rows
+    positions [T] of cos_sin [max_positions, R] (cosines, then sines); with axes [R / 2], frequency i by positions
+    [num_axes, T] row axes[i]. q_out / k_out may be query / key; rows may be strided (parts of one projection)."""
+    if k_out is None:
+        raise TypeError("k_out must be a torch.Tensor")
+    return _rope("pa_norm_rope", q_out, k_out, query, key, None, cos_sin, positions, q_weight, k_weight, eps, axes,
+                 interleaved, lambda *_: ())
+
+
+class _CacheArgs:
+    """The cache arguments of pa_norm_rope_and_cache and its 8-bit form, checked against the tokens' shape."""
+
+    def __init__(self, key_cache, value_cache, slot_mapping, scales=()):
+        self.at = key_cache, value_cache, slot_mapping, scales
+        self.sizes = ()
+
+    def __call__(self, T, Hkv, D, dev):
+        kc, vc, slots, scales = self.at
+        dtype = torch.uint8 if scales else torch.bfloat16
+        _need(kc, "key_cache", dtype, 4, dev)
+        _need(vc, "value_cache", dtype, 4, dev)
+        _need(slots, "slot_mapping", torch.int64, 1, dev)
+        NB, BS, H, D2 = kc.shape
+        if (H, D2) != (Hkv, D) or vc.shape != ((NB, H, D, BS) if scales else kc.shape) or slots.shape[0] != T:
+            raise ValueError("shape mismatch between key/value, slot_mapping and the caches")
+        if scales:
+            _scales(*scales, Hkv, dev)
+        self.sizes = BS, NB
+        return kc.data_ptr(), vc.data_ptr(), *[s.data_ptr() for s in scales], slots.data_ptr()
+
+
+def pa_norm_rope_and_cache(q_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
+                           key_cache: torch.Tensor, value_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                           cos_sin: torch.Tensor, positions: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                           k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                           axes: Optional[torch.Tensor] = None, interleaved: bool = False,
+                           k_out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """pa_norm_rope whose rotated keys go, with the values, to the slots of the paged caches (and to k_out if given)."""
+    if value is None:
+        raise TypeError("value must be a torch.Tensor")
+    return _rope("pa_norm_rope_and_cache", q_out, k_out, query, key, value, cos_sin, positions, q_weight, k_weight, eps,
+                 axes, interleaved, _CacheArgs(key_cache, value_cache, slot_mapping))
+
+
+def pa_norm_rope_and_cache_fp8(q_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
+                               key_cache: torch.Tensor, value_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                               k_scale: torch.Tensor, v_scale: torch.Tensor, cos_sin: torch.Tensor,
+                               positions: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                               k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                               axes: Optional[torch.Tensor] = None, interleaved: bool = False,
+                               k_out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """pa_norm_rope_and_cache into an 8-bit cache with per-KV-head scales."""
+    if value is None:
+        raise TypeError("value must be a torch.Tensor")
+    return _rope("pa_norm_rope_and_cache_fp8", q_out, k_out, query, key, value, cos_sin, positions, q_weight, k_weight,
+                 eps, axes, interleaved, _CacheArgs(key_cache, value_cache, slot_mapping, (k_scale, v_scale)))

@@ -9,6 +9,7 @@
 #include "../../include/paged_decode.h"
 #include "kernels.h"
 #include "no_alloc.h"
+#include "step.h"
 #include "subset.h"
 
 using namespace pa;
@@ -1053,7 +1054,7 @@ int run_subset(SubsetArgs a, const SubsetPlan &plan, int D, CacheKind kind, void
     a.lse = reinterpret_cast<float *>(p + w.lse);
     a.logits = reinterpret_cast<float *>(p + w.logits);
     const bool rows = plan.tiles && !plan.prefix;  // of windows
-    const bool each = plan.tiles && (rows ? rows_each(a, D, w.sms) : reads_each(a, D));
+    const bool each = plan.tiles && (rows ? kind != kCacheBf16 || rows_each(a, D, w.sms) : reads_each(a, D));
     if (each) a.ownres = nullptr;
     if (plan.prefix) a.pgrid = prefix_ctas(a, D, w.sms);
     a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
@@ -1164,6 +1165,30 @@ int pa_decode_window_multi(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *ke
                       head_dim, block_size, num_blocks, window, sinks, scale, workspace, workspace_bytes, stream);
 }
 
+int pa_decode_window_multi_fp8(pa_bf16 *out, const pa_bf16 *query, const pa_e4m3 *key_cache,
+                               const pa_e4m3 *value_cache, const float *k_scale, const float *v_scale,
+                               const int32_t *block_tables, int max_blocks_per_seq, const int32_t *cu_seqlens_q,
+                               const int32_t *context_lens, int batch, int total_q, int num_q_heads, int num_kv_heads,
+                               int head_dim, int block_size, int64_t num_blocks, int window, int sinks, float scale,
+                               void *workspace, size_t workspace_bytes, void *stream) {
+    if (!cu_seqlens_q) return PA_ERR_INVALID_ARG;
+    return run_window(out, query, key_cache, value_cache, k_scale, v_scale, kCacheE4m3, block_tables,
+                      max_blocks_per_seq, cu_seqlens_q, context_lens, batch, total_q, num_q_heads, num_kv_heads,
+                      head_dim, block_size, num_blocks, window, sinks, scale, workspace, workspace_bytes, stream);
+}
+
+int pa_decode_window_multi_fp8_block(pa_bf16 *out, const pa_bf16 *query, const pa_e4m3 *key_cache,
+                                     const pa_e4m3 *value_cache, const float *k_bscale, const float *v_bscale,
+                                     const int32_t *block_tables, int max_blocks_per_seq, const int32_t *cu_seqlens_q,
+                                     const int32_t *context_lens, int batch, int total_q, int num_q_heads,
+                                     int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, int window,
+                                     int sinks, float scale, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!cu_seqlens_q) return PA_ERR_INVALID_ARG;
+    return run_window(out, query, key_cache, value_cache, k_bscale, v_bscale, kCacheE4m3Block, block_tables,
+                      max_blocks_per_seq, cu_seqlens_q, context_lens, batch, total_q, num_q_heads, num_kv_heads,
+                      head_dim, block_size, num_blocks, window, sinks, scale, workspace, workspace_bytes, stream);
+}
+
 size_t pa_decode_prefix_workspace_size(int batch, int num_groups, int num_q_heads, int num_kv_heads, int head_dim) {
     if (num_groups <= 0 || num_groups > kMaxBatch) return 0;
     return subset_workspace_bytes(kPrefixPlan, batch, kMaxBatch, num_q_heads, num_kv_heads, head_dim);
@@ -1266,6 +1291,191 @@ int pa_evict(int32_t *kept, int32_t *new_lens, pa_bf16 *key_cache, pa_bf16 *valu
     cudaError_t e = decode_geometry(head_dim, &geo);
     if (e == cudaSuccess) e = launch_evict(a, head_dim, geo.grid, static_cast<cudaStream_t>(stream));  // one CTA per SM
     return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+}  // extern "C"
+
+/* ------------------------------------------- a step around its attention ---- */
+
+namespace {
+
+// bytes [p, p + n) and [q, q + m) share one
+bool overlap(const void *p, size_t n, const void *q, size_t m) {
+    const auto a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + m && b < a + n;
+}
+
+// the checks that planning and releasing share
+int check_stack(const int32_t *bt, int MBS, const int32_t *ctx, const int32_t *lens, int B, int BS, int64_t NB,
+                const int32_t *free_blocks, int64_t F, const int32_t *num_free, const int32_t *new_lens,
+                const int32_t *new_free) {
+    if (!bt || !ctx || !lens || !free_blocks || !num_free || !new_lens || !new_free) return PA_ERR_INVALID_ARG;
+    if (MBS <= 0 || B <= 0 || BS <= 0 || NB <= 0 || F <= 0) return PA_ERR_INVALID_ARG;
+    if (BS != kBlockSize || B > kMaxBatch || int64_t(MBS) * BS > int64_t(1) << 30) return PA_ERR_UNSUPPORTED;
+    if (NB > (int64_t(1) << 31) - 1 || F > (int64_t(1) << 31) - 1) return PA_ERR_UNSUPPORTED;
+    // in place, or apart
+    if (new_lens != ctx && overlap(new_lens, size_t(B) * 4, ctx, size_t(B) * 4)) return PA_ERR_INVALID_ARG;
+    if (new_lens == lens || overlap(new_lens, size_t(B) * 4, lens, size_t(B) * 4)) return PA_ERR_INVALID_ARG;
+    return PA_OK;
+}
+
+struct RopeShape {
+    int64_t T;
+    int Hq, Hkv, D, R, axes, BS;
+    int64_t NB;
+};
+
+int check_rope(const RopeArgs &a, const RopeShape &s, RopeCache cache) {
+    if (s.T < 0 || s.Hq <= 0 || s.Hkv <= 0 || s.D <= 0 || s.R <= 0 || a.P <= 0 || s.axes <= 0) return PA_ERR_INVALID_ARG;
+    if (!(a.eps >= 0.f) || a.eps > 3.4028234e38f) return PA_ERR_INVALID_ARG;
+    if (cache != kRopeNone && (s.BS <= 0 || s.NB <= 0)) return PA_ERR_INVALID_ARG;
+    if (!shape_supported(s.D, cache == kRopeNone ? kBlockSize : s.BS) || (cache == kRopeE4m3 && s.D != 128))
+        return PA_ERR_UNSUPPORTED;
+    if (s.R % 16 != 0 || s.R > s.D || s.axes > 4) return PA_ERR_UNSUPPORTED;
+    if (s.Hq > 65535 || s.Hkv > 65535 || s.NB > (int64_t(1) << 31) - 1) return PA_ERR_UNSUPPORTED;
+    if (s.T > (int64_t(1) << 31) / (s.Hq + 2 * s.Hkv)) return PA_ERR_UNSUPPORTED;
+    if (s.T == 0) return PA_OK;
+    if (!a.q || !a.k || !a.qo || !a.table || !a.pos) return PA_ERR_INVALID_ARG;
+    if (s.axes > 1 && !a.axis) return PA_ERR_INVALID_ARG;
+    if (cache == kRopeNone ? !a.ko : (!a.v || !a.kc || !a.vc || !a.slots)) return PA_ERR_INVALID_ARG;
+    if (cache == kRopeE4m3 && (!a.k_scale || !a.v_scale)) return PA_ERR_INVALID_ARG;
+    for (const void *p : {static_cast<const void *>(a.q), static_cast<const void *>(a.k), static_cast<const void *>(a.v),
+                          static_cast<const void *>(a.qo), static_cast<const void *>(a.ko),
+                          static_cast<const void *>(a.qw), static_cast<const void *>(a.kw),
+                          static_cast<const void *>(a.table), static_cast<const void *>(a.kc),
+                          static_cast<const void *>(a.vc)})
+        if (!aligned16(p)) return PA_ERR_INVALID_ARG;
+    const int64_t q = int64_t(s.Hq) * s.D, k = int64_t(s.Hkv) * s.D;  // elements of a row
+    if (a.qs < q || a.qos < q || a.ks < k || (a.ko && a.kos < k) || (a.v && a.vs < k)) return PA_ERR_INVALID_ARG;
+    if ((a.qs | a.qos | a.ks | (a.ko ? a.kos : 0) | (a.v ? a.vs : 0)) % 8 != 0) return PA_ERR_INVALID_ARG;
+    for (const int64_t x : {a.qs, a.qos, a.ks, a.kos, a.vs})
+        if (x > int64_t(1) << 31) return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+int run_rope(RopeArgs a, const RopeShape &s, RopeCache cache, int interleaved, void *stream) {
+    const int rc = check_rope(a, s, cache);
+    if (rc != PA_OK || s.T == 0) return rc;
+    a.T = s.T;
+    a.Hq = s.Hq;
+    a.Hkv = s.Hkv;
+    a.R = s.R;
+    a.naxes = s.axes;
+    a.NB = s.NB;
+    if (s.axes == 1) a.axis = nullptr;
+    const cudaError_t e = launch_norm_rope(a, s.D, interleaved != 0, cache, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+int pa_plan_step(int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens, const int32_t *query_lens,
+                 int batch, int block_size, int64_t num_blocks, const int32_t *free_blocks, int64_t free_capacity,
+                 const int32_t *num_free, int32_t *new_lens, int32_t *new_free, int32_t *granted,
+                 int32_t *cu_seqlens_q, int32_t *positions, int64_t *slot_mapping, int total_q, void *stream) {
+    const int rc = check_stack(block_tables, max_blocks_per_seq, context_lens, query_lens, batch, block_size, num_blocks,
+                               free_blocks, free_capacity, num_free, new_lens, new_free);
+    if (rc != PA_OK) return rc;
+    if (!granted || !cu_seqlens_q || !positions || !slot_mapping || total_q <= 0) return PA_ERR_INVALID_ARG;
+    if (total_q > kMaxWindowRows) return PA_ERR_UNSUPPORTED;
+    PlanArgs a{};
+    a.bt = block_tables;
+    a.ctx = context_lens;
+    a.q = query_lens;
+    a.free_blocks = free_blocks;
+    a.num_free = num_free;
+    a.new_lens = new_lens;
+    a.new_free = new_free;
+    a.granted = granted;
+    a.cu = cu_seqlens_q;
+    a.pos = positions;
+    a.slots = slot_mapping;
+    a.NB = num_blocks;
+    a.F = free_capacity;
+    a.MBS = max_blocks_per_seq;
+    a.B = batch;
+    a.T = total_q;
+    const cudaError_t e = launch_plan(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+int pa_release_blocks(const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                      const int32_t *keep_lens, int batch, int block_size, int64_t num_blocks, int32_t *free_blocks,
+                      int64_t free_capacity, const int32_t *num_free, int32_t *new_lens, int32_t *new_free,
+                      void *stream) {
+    const int rc = check_stack(block_tables, max_blocks_per_seq, context_lens, keep_lens, batch, block_size, num_blocks,
+                               free_blocks, free_capacity, num_free, new_lens, new_free);
+    if (rc != PA_OK) return rc;
+    ReleaseArgs a{};
+    a.bt = block_tables;
+    a.ctx = context_lens;
+    a.keep = keep_lens;
+    a.free_blocks = free_blocks;
+    a.num_free = num_free;
+    a.new_lens = new_lens;
+    a.new_free = new_free;
+    a.NB = num_blocks;
+    a.F = free_capacity;
+    a.MBS = max_blocks_per_seq;
+    a.B = batch;
+    const cudaError_t e = launch_release(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+int pa_norm_rope(pa_bf16 *q_out, int64_t q_out_stride, pa_bf16 *k_out, int64_t k_out_stride, const pa_bf16 *query,
+                 int64_t query_stride, const pa_bf16 *key, int64_t key_stride, const pa_bf16 *q_weight,
+                 const pa_bf16 *k_weight, float eps, const float *cos_sin, int64_t max_positions, int rotary_dim,
+                 const int32_t *positions, const int32_t *axes, int num_axes, int interleaved, int64_t num_tokens,
+                 int num_q_heads, int num_kv_heads, int head_dim, void *stream) {
+    RopeArgs a{};
+    a.q = query, a.k = key;
+    a.qo = q_out, a.ko = k_out;
+    a.qs = query_stride, a.ks = key_stride, a.qos = q_out_stride, a.kos = k_out_stride;
+    a.qw = q_weight, a.kw = k_weight, a.eps = eps;
+    a.table = cos_sin, a.P = max_positions, a.pos = positions, a.axis = axes;
+    return run_rope(a, {num_tokens, num_q_heads, num_kv_heads, head_dim, rotary_dim, num_axes, 0, 0}, kRopeNone,
+                    interleaved, stream);
+}
+
+int pa_norm_rope_and_cache(pa_bf16 *q_out, int64_t q_out_stride, pa_bf16 *k_out, int64_t k_out_stride,
+                           const pa_bf16 *query, int64_t query_stride, const pa_bf16 *key, int64_t key_stride,
+                           const pa_bf16 *value, int64_t value_stride, const pa_bf16 *q_weight,
+                           const pa_bf16 *k_weight, float eps, const float *cos_sin, int64_t max_positions,
+                           int rotary_dim, const int32_t *positions, const int32_t *axes, int num_axes,
+                           int interleaved, pa_bf16 *key_cache, pa_bf16 *value_cache, const int64_t *slot_mapping,
+                           int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                           int64_t num_blocks, void *stream) {
+    RopeArgs a{};
+    a.q = query, a.k = key, a.v = value;
+    a.qo = q_out, a.ko = k_out;
+    a.qs = query_stride, a.ks = key_stride, a.vs = value_stride, a.qos = q_out_stride, a.kos = k_out_stride;
+    a.qw = q_weight, a.kw = k_weight, a.eps = eps;
+    a.table = cos_sin, a.P = max_positions, a.pos = positions, a.axis = axes;
+    a.kc = key_cache, a.vc = value_cache, a.slots = slot_mapping;
+    return run_rope(a, {num_tokens, num_q_heads, num_kv_heads, head_dim, rotary_dim, num_axes, block_size, num_blocks},
+                    kRopeBf16, interleaved, stream);
+}
+
+int pa_norm_rope_and_cache_fp8(pa_bf16 *q_out, int64_t q_out_stride, pa_bf16 *k_out, int64_t k_out_stride,
+                               const pa_bf16 *query, int64_t query_stride, const pa_bf16 *key, int64_t key_stride,
+                               const pa_bf16 *value, int64_t value_stride, const pa_bf16 *q_weight,
+                               const pa_bf16 *k_weight, float eps, const float *cos_sin, int64_t max_positions,
+                               int rotary_dim, const int32_t *positions, const int32_t *axes, int num_axes,
+                               int interleaved, pa_e4m3 *key_cache, pa_e4m3 *value_cache, const float *k_scale,
+                               const float *v_scale, const int64_t *slot_mapping, int64_t num_tokens, int num_q_heads,
+                               int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, void *stream) {
+    RopeArgs a{};
+    a.q = query, a.k = key, a.v = value;
+    a.qo = q_out, a.ko = k_out;
+    a.qs = query_stride, a.ks = key_stride, a.vs = value_stride, a.qos = q_out_stride, a.kos = k_out_stride;
+    a.qw = q_weight, a.kw = k_weight, a.eps = eps;
+    a.table = cos_sin, a.P = max_positions, a.pos = positions, a.axis = axes;
+    a.kc = key_cache, a.vc = value_cache, a.slots = slot_mapping;
+    a.k_scale = k_scale, a.v_scale = v_scale;
+    return run_rope(a, {num_tokens, num_q_heads, num_kv_heads, head_dim, rotary_dim, num_axes, block_size, num_blocks},
+                    kRopeE4m3, interleaved, stream);
 }
 
 }  // extern "C"

@@ -1057,6 +1057,8 @@ cudaError_t launch_stream_decode(const CUtensorMap &tk, const CUtensorMap &tv, c
         f.nseq = a.rows;
         f.ngroups = a.nseq;
         f.cu_g = a.cu_q;
+        if (kind == kCacheE4m3) return launch_t<128, kCacheE4m3, kRows>(tk, tv, f, sms, stream);
+        if (kind == kCacheE4m3Block) return launch_t<128, kCacheE4m3Block, kRows>(tk, tv, f, sms, stream);
         return head_dim == 128 ? launch_t<128, kCacheBf16, kRows>(tk, tv, f, sms, stream)
                                : launch_t<64, kCacheBf16, kRows>(tk, tv, f, sms, stream);
     }
