@@ -1027,10 +1027,10 @@ bool reads_each(const SubsetArgs &a, int D) {
 // on 500 (64 MB) 16.6 and 14.8.
 constexpr int64_t kEachReadsMany = int64_t(56) << 20;
 
-bool rows_each(const SubsetArgs &a, int D, int sms) {
+bool rows_each(const SubsetArgs &a, int D, CacheKind kind, int sms) {
     const double seen = std::min(double(a.MBS) * kBlockSize, double(a.window) + a.sinks + 2 * kBlockSize);
     const int64_t segs = int64_t(a.rows) * a.Hkv;
-    return segs * seen * D * 4 <= double(segs <= sms ? kEachReads : kEachReadsMany);
+    return segs * seen * D * (kind == kCacheBf16 ? 4 : 2) <= double(segs <= sms ? kEachReads : kEachReadsMany);
 }
 
 // the launches, after the argument checks
@@ -1054,7 +1054,7 @@ int run_subset(SubsetArgs a, const SubsetPlan &plan, int D, CacheKind kind, void
     a.lse = reinterpret_cast<float *>(p + w.lse);
     a.logits = reinterpret_cast<float *>(p + w.logits);
     const bool rows = plan.tiles && !plan.prefix;  // of windows
-    const bool each = plan.tiles && (rows ? kind != kCacheBf16 || rows_each(a, D, w.sms) : reads_each(a, D));
+    const bool each = plan.tiles && (rows ? rows_each(a, D, kind, w.sms) : reads_each(a, D));
     if (each) a.ownres = nullptr;
     if (plan.prefix) a.pgrid = prefix_ctas(a, D, w.sms);
     a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
@@ -1066,16 +1066,16 @@ int run_subset(SubsetArgs a, const SubsetPlan &plan, int D, CacheKind kind, void
     std::memset(&tv, 0, sizeof tv);
     if (!fp8 && (rc = make_block_map(&tv, a.vc, a.Hkv, D, a.NB)) != PA_OK) return rc;
     const bool stream_too = !rows || each;
-    if (stream_too && (rc = fp8 ? make_cache_map(&tk, a.kc, a.Hkv, D, kBlockSize, a.NB, true)
+    if ((stream_too || fp8) && (rc = fp8 ? make_cache_map(&tk, a.kc, a.Hkv, D, kBlockSize, a.NB, true)
                                  : make_block_map(&tk, a.kc, a.Hkv, D, a.NB)) != PA_OK)
         return rc;
-    if (plan.tiles && !each && (rc = make_cache_map(&tk_half, a.kc, a.Hkv, D, kBlockSize, a.NB)) != PA_OK) return rc;
+    if (plan.tiles && !each && !fp8 && (rc = make_cache_map(&tk_half, a.kc, a.Hkv, D, kBlockSize, a.NB)) != PA_OK) return rc;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
     if (plan.tiles && !each) {
         CUtensorMap tq;
         if ((rc = make_query_map(&tq, a.q, a.rows, a.Hq, a.G, D)) != PA_OK) return rc;
-        e = launch_row_tiles(tk_half, tv, tq, a, D, w.sms, st);
+        e = launch_row_tiles(fp8 ? tk : tk_half, tv, tq, a, D, kind, w.sms, st);
     }
     if (e == cudaSuccess && stream_too) e = launch_stream_decode(tk, tv, a, D, kind, plan.prefix && !each ? w.sms - a.pgrid : w.sms, st);
     if (e == cudaSuccess && plan.prefix && !each) e = launch_prefix_join(a, D, st);

@@ -45,6 +45,15 @@
 //    token that only other rows of the tile see meets them as 0 * V, which
 //    is not 0 if V is not finite: a row whose result is not finite, in a unit with
 //    such a token, is computed again, over its own tokens only, at the CTA's end.
+//  * E4M3 caches (query rows over windows): S = Q K^T takes K's codes as they are, by products of E4M3 inputs: a bf16
+//    query is two E4M3 parts (split_query, by the softmax warps: a thread per row), 2 x 128 codes deep at twice the
+//    rate, from half as much of K. P V takes bf16: P in E4M3 would lose small weights. V's codes become bf16 on
+//    the way: two warps copy blocks of codes into a ring, eight convert them and lay them down dim by token, as the
+//    cache has them, with the contraction over tokens contiguous. A scale per KV head goes to the logits and the output; a
+//    scale per block to the block's 16 logits and, in the conversion, to its V. Chunks of 517 to 2048 rows behind 9000 to
+//    16000 tokens 622 us = 1.28 PFLOP/s, the rate of the bf16 cache. On the way there: K and V converted, by loads to
+//    registers 1615 us (a loop unrolled over a half step runs out of instruction cache at 7 cycles an instruction), by
+//    asynchronous copies and rolled loops 790; V alone converted, one warp issuing its copies (330 cycles each) 830.
 //  * Units cut between CTAs leave (O, m, l) per row and piece in the workspace;
 //    the CTA that completes the count merges them, in piece order, or a join
 //    kernel does (for prefixes, with the own tokens' part).
@@ -65,6 +74,12 @@ constexpr int kTileBlk = kTileTok / kBlockSize;
 constexpr int kStages = 2;       // K tiles, and V tiles, in flight
 constexpr int kInfo = 8;         // tile descriptions in flight
 constexpr int kWarpsRT = 12;     // 2 x 4 softmax, K producer, products, V producer, one that fills the warpgroup
+constexpr int kWarpsF8 = 20;     // E4M3 cache: 2 x 4 softmax, K producer, products, 2 V producers, 8 that convert V
+constexpr int kConv = 8;
+// Places for blocks of V codes in flight. Even: blocks of one parity are converted by the same warps, and these have to see
+// every time that one of their places is filled (a wait tells a phase from the next one only).
+constexpr int kRaw = 14;
+static_assert(kRaw % 2 == 0, "a place belongs to one half of the converting warps");
 constexpr float kGrow = 8.f;     // log2 growth of a maximum that rescales O
 // Tiles of a CTA's range at least: a piece costs more to merge than a second tile takes. 4 rows on 700 tokens: 1 tile
 // 21.5 us, 2 15.8, 3 15.6, 4 19.3; 8 sequences behind a shared prefix of 2001: 15.9, 16.2, 20.1, 18.9.
@@ -92,6 +107,9 @@ constexpr int kMergedBefore = 1;  // the unit that began before the CTA's range
 constexpr int kMergedHere = 2;    // the unit that begins in it
 static_assert(sizeof(After) % 8 == 0, "the prefix sums behind it");
 
+template <CacheKind KIND>
+constexpr int kRowWarps = KIND == kCacheBf16 ? kWarpsRT : kWarpsF8;
+
 template <int D>
 struct RowCfg {
     static constexpr int HV = D / 64;                      // 64-dim halves
@@ -100,6 +118,14 @@ struct RowCfg {
     static constexpr int BLK = kBlockSize * 128;           // a block's 64 dims
     static constexpr size_t off_ring = 2 * size_t(TILE);   // after the two Q tiles
     static constexpr size_t off_stage = off_ring + 2 * size_t(kStages) * TILE;  // 32 rows of 128 bytes per softmax warp
+    // E4M3: K tiles of codes are half as large; the rest of the ring has blocks of V codes
+    static constexpr size_t off_v8 = off_ring + kStages * size_t(HALF);
+    static constexpr int RAW = kBlockSize * 128;
+    static constexpr size_t off_raw = off_v8 + kStages * size_t(TILE);
+    static constexpr size_t off_rawbars = off_raw + kRaw * size_t(RAW);   // filled, free
+    static constexpr size_t off_slot = off_rawbars + 2 * kRaw * 8;        // [kRaw] tokens, [kRaw] scales of V
+    static constexpr size_t off_kscale = off_slot + 2 * kRaw * 4;         // [kInfo][8] scales of a K tile
+    static_assert(D != 128 || off_kscale + kInfo * kTileBlk * 4 <= off_stage, "in the ring");
     static constexpr size_t off_bars = off_stage + 8 * 4096;
     static constexpr size_t off_info = off_bars + 224;
     static constexpr size_t off_misc = off_info + 2 * kInfo * 4;
@@ -166,9 +192,11 @@ struct Work {
 // Head h of query row r of sequence s again, over the tokens before lim that it
 // sees and nothing else, by a warp in fp32: for rows that other rows' tokens may have
 // reached. 32 tokens at a time, a lane per token for its logit, D / 32 dims for V.
-template <int D>
+template <int D, CacheKind KIND>
 __device__ __forceinline__ void redo_row(const SubsetArgs &a, int s, int kvh, int r, int h, int lim) {
     constexpr int V = D / 32, BS = kBlockSize;
+    constexpr bool F8 = KIND != kCacheBf16, PSC = KIND == kCacheE4m3Block;
+    const float ksc = F8 && !PSC ? __ldg(a.k_scale + kvh) : 1.f, vsc = F8 && !PSC ? __ldg(a.v_scale + kvh) : 1.f;
     const int lane = threadIdx.x & 31, s1 = min(a.sinks, lim), lo = max(s1, a.window >= lim ? 0 : lim - a.window);
     const int cnt = s1 + max(lim - lo, 0);
     const int64_t ro = (int64_t(r) * a.Hq + kvh * a.G + h) * D;
@@ -182,14 +210,30 @@ __device__ __forceinline__ void redo_row(const SubsetArgs &a, int s, int kvh, in
         const int phys = __ldg(a.bt + int64_t(s) * a.MBS + t / BS);
         const bool in = k0 + lane < cnt && phys >= 0 && int64_t(phys) < a.NB;
         const int64_t off = ((int64_t(in ? phys : 0) * BS + t % BS) * a.Hkv + kvh) * D;  // not in: of any row
-        const uint4 *kr = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.kc) + off);
         float z = 0.f;
+        if constexpr (F8) {
+            const uint2 *kr = reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.kc) + off);
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-            const uint4 x = __ldg(kr + c), y = __ldg(q + c);
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+            for (int c = 0; c < D / 8; ++c) {
+                const uint2 x = __ldg(kr + c);
+                const uint4 y = __ldg(q + c);
+                const uint32_t ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) z = fmaf(bf16_hi(ys[e]), bf16_hi(xs[e]), fmaf(bf16_lo(ys[e]), bf16_lo(xs[e]), z));
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t h = e4m3x2_to_f16x2((e < 2 ? x.x : x.y) >> (16 * (e & 1)));
+                    z = fmaf(bf16_hi(ys[e]), f16_hi(h), fmaf(bf16_lo(ys[e]), f16_lo(h), z));
+                }
+            }
+            z *= PSC ? __ldg(a.k_scale + int64_t(in ? phys : 0) * a.Hkv + kvh) : ksc;
+        } else {
+            const uint4 *kr = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.kc) + off);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                const uint4 x = __ldg(kr + c), y = __ldg(q + c);
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z = fmaf(bf16_hi(ys[e]), bf16_hi(xs[e]), fmaf(bf16_lo(ys[e]), bf16_lo(xs[e]), z));
+            }
         }
         z = in ? z * a.scale_log2 : -INFINITY;
         float Mn = z;
@@ -206,14 +250,25 @@ __device__ __forceinline__ void redo_row(const SubsetArgs &a, int s, int kvh, in
 #pragma unroll 8
         for (int u = 0; u < 32; ++u) {
             const float pu = __shfl_sync(0xffffffffu, p, u);
-            const int64_t at = __shfl_sync(0xffffffffu, off, u) + lane * V;
-            const uint32_t *vr = reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(a.vc) + at);
+            if constexpr (F8) {
+                const int o = __shfl_sync(0xffffffffu, t % BS, u);
+                const int64_t blk = int64_t(__shfl_sync(0xffffffffu, in ? phys : 0, u)) * a.Hkv + kvh;
+                const float f = pu * (PSC ? __ldg(a.v_scale + blk) : vsc);
+                const uint8_t *vr = static_cast<const uint8_t *>(a.vc) + (blk * D + lane * V) * BS +
+                                    (4 * ((o & 7) >> 1) + 2 * (o >> 3) + (o & 1));
 #pragma unroll
-            for (int e = 0; e < V; e += 2) {
-                const uint32_t v = __ldg(vr + e / 2);
-                if ((ins >> u) & 1u) {
-                    acc[e] += pu * bf16_lo(v);
-                    acc[e + 1] += pu * bf16_hi(v);
+                for (int e = 0; e < V; ++e)
+                    if ((ins >> u) & 1u) acc[e] += f * f16_lo(e4m3x2_to_f16x2(__ldg(vr + e * BS)));
+            } else {
+                const int64_t at = __shfl_sync(0xffffffffu, off, u) + lane * V;
+                const uint32_t *vr = reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(a.vc) + at);
+#pragma unroll
+                for (int e = 0; e < V; e += 2) {
+                    const uint32_t v = __ldg(vr + e / 2);
+                    if ((ins >> u) & 1u) {
+                        acc[e] += pu * bf16_lo(v);
+                        acc[e + 1] += pu * bf16_hi(v);
+                    }
                 }
             }
         }
@@ -231,9 +286,10 @@ __device__ __forceinline__ void redo_row(const SubsetArgs &a, int s, int kvh, in
 // not finite? By a warp; there are at most a few hundred such tokens, at the ends of
 // the window and of the sinks. Without one, a row that is not finite owes it to a
 // token it sees itself.
-template <int D>
+template <int D, CacheKind KIND>
 __device__ __forceinline__ bool reached_by_others(const SubsetArgs &a, int s, int kvh, int lim0, int lim1, int lim) {
-    constexpr int LR = D / 8, TP = 32 / LR, U = 4, BS = kBlockSize;  // lanes per row, rows at once
+    // lanes per row, rows at once; an 8-bit row of 128 codes by 16 lanes as well
+    constexpr int LR = D / 8, TP = 32 / LR, U = 4, BS = kBlockSize;
     const int lane = threadIdx.x & 31;
     auto lower = [&](int lim) { return a.window >= lim ? 0 : lim - a.window; };
     const int l0 = lower(lim0), l1 = lower(lim1), lo = lower(lim), nb1 = (min(a.sinks, lim1) + BS - 1) / BS;
@@ -246,12 +302,24 @@ __device__ __forceinline__ bool reached_by_others(const SubsetArgs &a, int s, in
                 const int t = t0 + u * TP;
                 const int phys = t < to && !(t >= lo && t < lim) ? __ldg(a.bt + int64_t(s) * a.MBS + t / BS) : -1;
                 if (phys < 0 || int64_t(phys) >= a.NB) continue;
-                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(a.vc) +
-                                      ((int64_t(phys) * BS + t % BS) * a.Hkv + kvh) * LR + lane % LR);
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                if constexpr (KIND != kCacheBf16) {
+                    const int o = t % BS;
+                    const int64_t blk = int64_t(phys) * a.Hkv + kvh;
+                    const uint8_t *vr = static_cast<const uint8_t *>(a.vc) + (blk * D + (lane % LR) * 8) * BS +
+                                        (4 * ((o & 7) >> 1) + 2 * (o >> 3) + (o & 1));
+                    // codes have no infinity, but a block's scale can make one
+                    const float s = KIND == kCacheE4m3Block ? __ldg(a.v_scale + blk) : 1.f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    bad = bad || (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+                    for (int e = 0; e < 8; ++e)
+                        bad = bad || !(fabsf(f16_lo(e4m3x2_to_f16x2(__ldg(vr + e * BS))) * s) <= 3.3895314e38f);
+                } else {
+                    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(a.vc) +
+                                          ((int64_t(phys) * BS + t % BS) * a.Hkv + kvh) * LR + lane % LR);
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        bad = bad || (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+                }
             }
         }
     };
@@ -261,12 +329,82 @@ __device__ __forceinline__ bool reached_by_others(const SubsetArgs &a, int s, in
     return __any_sync(0xffffffffu, bad);
 }
 
-template <int D, bool PREFIX>
-__global__ void __launch_bounds__(kWarpsRT * 32, 1)
+// Sixteen E4M3 codes, four words in their order, as eight bf16 pairs, exact; SCALED: times s, rounded to bf16 (exact for
+// a power of two, but for results outside bf16's normal range).
+template <bool SCALED>
+__device__ __forceinline__ void codes_to_bf16(const uint4 &c, float s, uint32_t (&out)[8]) {
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t h[2];
+        e4m3x4_to_f16x2x2(w[i], h[0], h[1]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float lo = f16_lo(h[k]), hi = f16_hi(h[k]);
+            out[2 * i + k] = SCALED ? pack_bf16x2(lo * s, hi * s)
+                                    : __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);  // nothing below
+        }
+    }
+}
+
+__device__ __forceinline__ uint4 load_shared16(uint32_t src) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
+    return v;
+}
+
+// A query row of 128 bf16 values for products with E4M3 codes: x = 2^k (hi + lo), hi the nearest E4M3 value of x / 2^k (the
+// largest is in [128, 256)) and lo that of what is left. The eight bits of a bf16 value are four and four: exact for values of
+// at least 2^-10 of the row's largest, the others are off by at most 2^-18 of it. Written to rows `to` (hi) and `to` +
+// next (lo), 16-byte chunks swizzled by sw; returns 2^k (1 for a row of zeros or none; NaN for one that is not finite).
+__device__ __forceinline__ float split_query(const uint16_t *q, uint8_t *to, int next, int sw) {
+    uint4 v[16];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = q ? __ldg(reinterpret_cast<const uint4 *>(q) + i) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m = max(m, max(w[e] & 0x7fff0000u, (w[e] << 16) & 0x7fff0000u));
+    }
+    const int k = m == 0 ? 0 : max(int(m >> 23) - 127 - 7, -119);
+    const float inv = __uint_as_float(uint32_t(127 - k) << 23);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {  // 16 values
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint4 &y = v[2 * c + e / 2];
+            const uint32_t w[2] = {e & 1 ? y.z : y.x, e & 1 ? y.w : y.y};
+            uint32_t h = 0, l = 0;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float a = bf16_lo(w[j]) * inv, b = bf16_hi(w[j]) * inv;
+                const uint32_t p = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+                const uint32_t f = e4m3x2_to_f16x2(p);
+                const uint32_t r = __nv_cvt_float2_to_fp8x2(make_float2(a - f16_lo(f), b - f16_hi(f)), __NV_SATFINITE, __NV_E4M3);
+                h |= p << (16 * j);
+                l |= r << (16 * j);
+            }
+            hi[e] = h;
+            lo[e] = l;
+        }
+        uint8_t *at = to + ((c ^ sw) << 4);
+        *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(at + next) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    return m >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(uint32_t(k + 127) << 23);
+}
+
+template <int D, bool PREFIX, CacheKind KIND>
+__global__ void __launch_bounds__(kRowWarps<KIND> * 32, 1)
     row_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CUtensorMap tm_q, const SubsetArgs a) {
     using C = RowCfg<D>;
-    constexpr int BS = kBlockSize, HV = C::HV;
+    constexpr int BS = kBlockSize, HV = C::HV, NWARP = kRowWarps<KIND>;
+    constexpr bool F8 = KIND != kCacheBf16, PSC = KIND == kCacheE4m3Block;
+    static_assert(!F8 || (D == 128 && !PREFIX), "an E4M3 cache has head_dim 128");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -280,6 +418,11 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
     const uint32_t q_full = empty + kStages * 8, q_empty = q_full + 16, s_full = q_empty + 16;
     const uint32_t p_ready = s_full + 16, o_full = p_ready + 32, drained = o_full + 16, piece_bar = drained + 8, last_bar = piece_bar + 16;
     const uint32_t ml_bar = last_bar + 16;
+    // E4M3: blocks of V codes
+    const uint32_t raw_full = base + uint32_t(C::off_rawbars), raw_empty = raw_full + kRaw * 8;
+    volatile int *slot_tokens = reinterpret_cast<volatile int *>(bp + C::off_slot);
+    volatile float *slot_scale = reinterpret_cast<volatile float *>(bp + C::off_slot) + kRaw;
+    volatile float *kscale = reinterpret_cast<volatile float *>(bp + C::off_kscale);
     volatile int *info = reinterpret_cast<volatile int *>(bp + C::off_info);
     volatile int *vfix = info + kInfo;  // V rows to zero: see the producers
     volatile int *misc = reinterpret_cast<volatile int *>(bp + C::off_misc);  // [0] tensor memory, [1] gave up, [2 + w] queries,
@@ -289,14 +432,21 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
     if (!PREFIX) pdl_trigger();
     if (tid == 0) {
         prefetch_tensormap(&tm_k);
-        prefetch_tensormap(&tm_v);
-        prefetch_tensormap(&tm_q);
+        if (F8) {
+            for (int i = 0; i < kRaw; ++i) {
+                mbar_init(raw_full + 8 * i, 1);
+                mbar_init(raw_empty + 8 * i, kConv / 2);
+            }
+        } else {
+            prefetch_tensormap(&tm_v);
+            prefetch_tensormap(&tm_q);
+        }
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(full + 8 * i, 2);  // K's producer and V's
+            mbar_init(full + 8 * i, 1 + (F8 ? kConv : 1));  // K's producer and V's, or the warps that convert V
             mbar_init(empty + 8 * i, 1);
         }
         for (int w = 0; w < 2; ++w) {
-            mbar_init(q_full + 8 * w, 1);
+            mbar_init(q_full + 8 * w, F8 ? 128 : 1);
             mbar_init(q_empty + 8 * w, 1);
             mbar_init(s_full + 8 * w, 1);
             mbar_init(p_ready + 16 * w, 128);
@@ -314,7 +464,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
     // ---- tiles per KV head of groups of `str` sequences, and their prefix sums
     const int ns = work.count(), str = (ns + kPreCap - 1) / kPreCap, np = (ns + str - 1) / str;
     // by a thread where sequences have a unit or two, so that many are looked up at once, else by a warp
-    for (int i = tid; i < np; i += kWarpsRT * 32) {
+    for (int i = tid; i < np; i += NWARP * 32) {
         int64_t t = 0;
         for (int s = i * str; t >= 0 && s < min((i + 1) * str, ns); ++s) {
             const int nu = work.units(s);
@@ -324,7 +474,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
         pre[i + 1] = t;
     }
     __syncthreads();
-    for (int i = warp; i < np; i += kWarpsRT) {
+    for (int i = warp; i < np; i += NWARP) {
         if (pre[i + 1] >= 0) continue;
         int64_t t = 0;
         for (int s = i * str; s < min((i + 1) * str, ns); ++s) t += work.tiles(s);
@@ -352,7 +502,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
         pdl_trigger();
     }
     if constexpr (PREFIX) {  // sequences of no group have no prefix part
-        for (int b = blockIdx.x * (kWarpsRT * 32) + tid; b < a.rows; b += gridDim.x * (kWarpsRT * 32)) {
+        for (int b = blockIdx.x * (NWARP * 32) + tid; b < a.rows; b += gridDim.x * (NWARP * 32)) {
             int lo = 0, hi = a.ngroups;
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
@@ -455,10 +605,60 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
         return false;
     };
 
-    // registers: the 168 per thread of the launch, 224 + 224 + 56 over its three warpgroups
-    if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 8 || warp == 10) {
+    // registers: the 168 per thread of the launch, 224 + 224 + 56 over its three warpgroups; E4M3: 96, and
+    // 176 + 176 + 48 + 40 + 40 over five
+    if (F8 && warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        // ======================================== E4M3: V codes to bf16 in shared memory
+        // In step i V of tile i - 1. Of every second block a warp has a quarter, 32 dims by 16 tokens; a lane 16 codes.
+        // The loop stays rolled: beside the softmax's code the instruction cache has no room for more.
+        const uint32_t odd = warp >= 16;  // blocks 2 j + odd
+        uint32_t slot = odd, phase = 0;
+        const int vd = (warp & 3) * 32 + lane;  // dim
+        const uint32_t from = base + uint32_t(C::off_raw) + vd * 16, steps = uint32_t(pos1 - pos0);
+        bool ok = true;
+#pragma unroll 1
+        for (uint32_t i = 1; i <= steps; ++i) {
+            const uint32_t st = i % kStages;
+            if (i >= kStages && !(ok = wait(empty + 8 * st, i / kStages + 1))) break;
+            uint8_t *vb = bp + C::off_v8 + st * C::TILE + vd * 128;
+#pragma unroll 1
+            for (int b = odd; b < kTileBlk; b += 2) {
+                if (!(ok = wait(raw_full + 8 * slot, phase))) break;
+                const uint4 c = load_shared16(from + slot * C::RAW);
+                const float scale = PSC ? slot_scale[slot] : 1.f;
+                const int tokens = slot_tokens[slot];
+                uint32_t o[8];
+                codes_to_bf16<PSC>(c, scale, o);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(raw_empty + 8 * slot);  // every lane has its codes
+                if ((slot += 2) >= kRaw) {
+                    slot -= kRaw;
+                    phase ^= 1;
+                }
+                if (tokens < BS) {  // V that no row sees: 0
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int tk = 2 * (k >> 1) + 8 * (k & 1);  // pair k: tokens tk, tk + 1
+                        if (tk >= tokens) o[k] = 0u;
+                        else if (tk + 1 >= tokens) o[k] &= 0xffffu;
+                    }
+                }
+                // dim row vd, tokens 16 b ..: pairs 0 2 4 6 are tokens 0 .. 7, pairs 1 3 5 7 tokens 8 .. 15
+                uint8_t *row = vb + (b >> 2) * C::HALF;
+                const int c0 = (b & 3) * 2;
+                *reinterpret_cast<uint4 *>(row + ((c0 ^ (vd & 7)) << 4)) = make_uint4(o[0], o[2], o[4], o[6]);
+                *reinterpret_cast<uint4 *>(row + (((c0 + 1) ^ (vd & 7)) << 4)) = make_uint4(o[1], o[3], o[5], o[7]);
+            }
+            if (!ok) break;
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full + 8 * st);
+        }
+    } else if (warp >= 8) {
+    if constexpr (F8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 8 || warp == 10 || (F8 && warp == 11)) {
         // =========================================== producers: K and queries, V
         // step i of the CTA reads K of its tile i and V of its tile i - 1, in buffer pair i % 2
         const bool is_k = warp == 8;
@@ -469,11 +669,17 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
         uint32_t i = 0;           // the next step
         uint32_t nq[2] = {0, 0};  // query tiles so far
         bool ok = true;
-        auto next_step = [&]() -> bool {  // step i's buffers are free
-            return (i < kStages || wait(empty + 8 * (i % kStages), i / kStages + 1)) && int(i) < a.stop_item;
+        // step i's buffers are free (E4M3: V's codes go to places of their own)
+        auto next_step = [&]() -> bool {
+            return ((F8 && !is_k) || i < kStages || wait(empty + 8 * (i % kStages), i / kStages + 1)) &&
+                   int(i) < a.stop_item;
         };
+        // E4M3: two warps for V, a copy takes one of them 330 cycles to issue; each has every second block: the next place,
+        // times round, blocks so far
+        const int odd = F8 ? warp & 1 : 0;
+        uint32_t slot = odd, turn = 0, codes = 0;
         if (!is_k) {  // no V in the first step
-            if (lane == 0) mbar_arrive(full);
+            for (int c = 0; lane == 0 && !odd && c < (F8 ? kConv : 1); ++c) mbar_arrive(full);
             i = 1;
         }
         for (int64_t p = pos0; ok && p < pos1;) {
@@ -484,10 +690,16 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                 return __ldg(table + int64_t(x.s) * mbs + (e < x.nb1 ? e : e - x.nb1 + x.jw));
             };
             int cur = entry(t0 * kTileBlk + lane), nxt = entry(t0 * kTileBlk + 32 + lane), at = t0;
+            auto scale_of = [&](int ph) -> float {
+                if (!PSC || ph < 0 || int64_t(ph) >= a.NB) return 0.f;
+                return __ldcg((is_k ? a.k_scale : a.v_scale) + int64_t(ph) * Hkv + x.kvh);
+            };
+            float scale = scale_of(cur);
             for (int t = t0; t < t1; ++t, ++i) {
                 if (t == at + 4) {
                     at = t;
                     cur = nxt;
+                    scale = scale_of(cur);
                     nxt = entry(t * kTileBlk + 32 + lane);
                 }
                 // bit b: block b of the tile is in the pool
@@ -495,6 +707,39 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                                          ((t - at) * kTileBlk)) & 0xffu;
                 if (!(ok = next_step())) break;
                 const uint32_t st = i % kStages, bar = full + 8 * st;
+                if (F8 && !is_k) {
+                    const int tail = x.lim1 % BS, lb = x.nb - 1 - t * kTileBlk;  // lb: the unit's last block
+                    for (int b = odd; b < kTileBlk; b += 2) {
+                        const int ph = __shfl_sync(0xffffffffu, cur, (t - at) * kTileBlk + b);
+                        const float sc = PSC ? __shfl_sync(0xffffffffu, scale, (t - at) * kTileBlk + b) : 1.f;
+                        if (turn > 0 && !(ok = wait(raw_empty + 8 * slot, turn + 1))) break;
+                        if (lane == 0) {
+                            const bool in = (blocks >> b) & 1u;
+                            const uint32_t filled = raw_full + 8 * slot;
+                            if (PSC) slot_scale[slot] = sc;
+                            slot_tokens[slot] = !in ? 0 : tail && b == lb ? tail : BS;
+                            if (in) {
+                                mbar_arrive_expect_tx(filled, C::RAW);
+                                bulk_load_1d(base + uint32_t(C::off_raw) + slot * C::RAW,
+                                             static_cast<const uint8_t *>(a.vc) + (int64_t(ph) * Hkv + x.kvh) * C::RAW,
+                                             C::RAW, filled, policy);
+                            } else {
+                                mbar_arrive(filled);
+                            }
+                        }
+                        __syncwarp();
+                        ++codes;
+                        if ((slot += 2) >= kRaw) {
+                            slot -= kRaw;
+                            ++turn;
+                        }
+                    }
+                    if (!ok) break;
+                    continue;
+                }
+                if (PSC && lane >= (t - at) * kTileBlk && lane < (t - at + 1) * kTileBlk)
+                    kscale[i % kInfo * kTileBlk + (lane & 7)] = scale;
+                if (PSC) __syncwarp();
                 if (lane == 0) {
                     if (is_k) {
                         info[i % kInfo] = int(blocks);
@@ -504,7 +749,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                         const bool cut = tail && lb >= 0 && lb < kTileBlk;
                         vfix[i % kInfo] = blocks == 0xffu && !cut ? 0 : int(blocks | 0x100u | (cut ? (lb << 12 | tail << 16) : 0));
                     }
-                    const uint32_t bytes = uint32_t(__popc(blocks)) * C::BLK * HV;
+                    const uint32_t bytes = uint32_t(__popc(blocks)) * (F8 ? C::RAW : C::BLK * HV);
                     if (bytes) mbar_arrive_expect_tx(bar, bytes);
                     else mbar_arrive(bar);
                 }
@@ -512,7 +757,9 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                 for (int b = 0; b < kTileBlk; ++b) {
                     const int ph = __shfl_sync(0xffffffffu, cur, (t - at) * kTileBlk + b);
                     if (!((blocks >> b) & 1u) || !tc_elect()) continue;
-                    if (is_k) {
+                    if constexpr (F8) {
+                        tma_load_4d(ring + st * C::HALF + b * C::RAW, &tm_k, bar, 0, x.kvh, 0, ph, policy);
+                    } else if (is_k) {
 #pragma unroll
                         for (int hf = 0; hf < HV; ++hf)
                             tma_load_4d(buf + st * C::TILE + hf * C::HALF + b * C::BLK, &tm_k, bar, hf * 64, x.kvh, 0, ph,
@@ -522,7 +769,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                     }
                 }
                 __syncwarp();
-                if (is_k && t == t0) {
+                if (!F8 && is_k && t == t0) {
                     // the unit's queries: rows (query row, head) are consecutive; rows past the
                     // unit's are read too and dropped at the end
                     for (int w = 0; ok && w < (x.nr > RQ ? 2 : 1); ++w) {
@@ -546,28 +793,31 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
             if (next_step() && lane == 0) mbar_arrive(full + 8 * (i % kStages));
         }
         if (lane == 0) {  // what was started, for an end after giving up
-            misc[is_k ? 6 : 7] = int(i);
-            if (is_k) {
+            misc[is_k ? 6 : F8 ? 2 + odd : 7] = F8 && !is_k ? int(codes) : int(i);
+            if (!F8 && is_k) {
                 misc[2] = int(nq[0]);
                 misc[3] = int(nq[1]);
             }
         }
     } else if (warp == 9) {
         // ====================================================== matrix products
-        constexpr uint32_t id_s = tc_idesc(128, 128, false), id_o = tc_idesc(128, D, true);
+        constexpr uint32_t id_s = F8 ? tc_idesc_e4m3(128, 128) : tc_idesc(128, 128, false), id_o = tc_idesc(128, D, !F8);
         // the same value in every lane, known as such: the products take uniform operands
         auto uniform = [](uint32_t v) -> uint32_t { return __shfl_sync(0xffffffffu, v, 0); };
         const uint32_t td = uniform(tmem), qd = uniform(tc_desc_lo(base, 16)), kd = uniform(tc_desc_lo(ring, 16));
-        // V block-major: 16 tokens of 64 dims, then the next 64
-        const uint32_t vd = uniform(tc_desc_lo(ring + kStages * C::TILE, C::BLK));
+        // V block-major: 16 tokens of 64 dims, then the next 64; E4M3: dim by token, 64 tokens, then the next 64
+        const uint32_t vd = uniform(F8 ? tc_desc_lo(base + uint32_t(C::off_v8), 16) : tc_desc_lo(ring + kStages * C::TILE, C::BLK));
         // S_w = Q_w K^T
         auto qk = [&](int w, uint32_t st) {
-            const uint32_t q = qd + w * (C::TILE >> 4), k = uniform(kd + st * (C::TILE >> 4));
+            const uint32_t q = qd + w * (C::TILE >> 4), k = uniform(kd + st * ((F8 ? C::HALF : C::TILE) >> 4));
             if (tc_elect()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t o = ((kk / 4) * C::HALF + (kk % 4) * 32) >> 4;
-                    tc_mma_ss(td + 256 * w, q + o, kTcDescHi, k + o, kTcDescHi, id_s, kk > 0);
+                    if constexpr (F8)  // the queries' two parts, one after the other
+                        tc_mma_ss_e4m3(td + 256 * w, q + o, kTcDescHi, k + ((kk % 4) * 32 >> 4), kTcDescHi, id_s, kk > 0);
+                    else
+                        tc_mma_ss(td + 256 * w, q + o, kTcDescHi, k + o, kTcDescHi, id_s, kk > 0);
                 }
                 tc_commit(s_full + 8 * w);
             }
@@ -580,8 +830,8 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
 #pragma unroll
                 for (int k = 0; k < kTileTok / 32; ++k) {
                     const int kk = hf * (kTileTok / 32) + k;
-                    tc_mma_ts(td + 256 * w + 128, td + 256 * w + 8 * kk, v + (kk * C::BLK * HV >> 4), kTcDescHi, id_o,
-                              more || kk > 0);
+                    const uint32_t o = F8 ? ((kk / 4) * C::HALF + (kk % 4) * 32) >> 4 : kk * C::BLK * HV >> 4;
+                    tc_mma_ts(td + 256 * w + 128, td + 256 * w + 8 * kk, v + o, kTcDescHi, id_o, more || kk > 0);
                 }
             }
         };
@@ -592,7 +842,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
         auto step = [&](bool q0, bool cur, bool cur2, bool qlast) -> bool {
             const uint32_t st = i % kStages;
             if (!wait(full + 8 * st, i / kStages)) return false;
-            if (i > 0) {
+            if (!F8 && i > 0) {
                 const int fix = vfix[i % kInfo];
                 if (fix) {
                     uint8_t *v = bp + C::off_ring + (kStages + st) * C::TILE;
@@ -609,24 +859,30 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                     __syncwarp();
                 }
             }
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                if (i > 0 && (w == 0 || two)) {
-                    uint32_t &n = w ? np1 : np0;
-                    if (!wait(p_ready + 16 * w, n)) return false;
-                    tc_fence_after();
-                    pv(w, st, more, 0);
-                    if (!wait(p_ready + 16 * w + 8, n++)) return false;
-                    tc_fence_after();
-                    pv(w, st, true, 1);
-                    if (q0 && tc_elect()) tc_commit(o_full + 8 * w);
-                }
-                if (cur && (w == 0 || cur2)) {
-                    if (q0 && !wait(q_full + 8 * w, w ? nq1++ : nq0++)) return false;
-                    tc_fence_after();
-                    qk(w, st);
-                    if (qlast && tc_elect()) tc_commit(q_empty + 8 * w);
-                }
+            auto finish = [&](int w) -> bool {  // the tile before
+                if (i == 0 || (w == 1 && !two)) return true;
+                uint32_t &n = w ? np1 : np0;
+                if (!wait(p_ready + 16 * w, n)) return false;
+                tc_fence_after();
+                pv(w, st, more, 0);
+                if (!wait(p_ready + 16 * w + 8, n++)) return false;
+                tc_fence_after();
+                pv(w, st, true, 1);
+                if (q0 && tc_elect()) tc_commit(o_full + 8 * w);
+                return true;
+            };
+            auto begin = [&](int w) -> bool {
+                if (!cur || (w == 1 && !cur2)) return true;
+                if (q0 && !wait(q_full + 8 * w, w ? nq1++ : nq0++)) return false;
+                tc_fence_after();
+                qk(w, st);
+                if (qlast && tc_elect()) tc_commit(q_empty + 8 * w);
+                return true;
+            };
+            if (F8 && q0) {  // the queries come from the softmax warps, once they have their output
+                if (!finish(0) || !finish(1) || !begin(0) || !begin(1)) return false;
+            } else {
+                if (!finish(0) || !begin(0) || !finish(1) || !begin(1)) return false;
             }
             if (tc_elect()) tc_commit(empty + 8 * st);
             ++i;
@@ -654,7 +910,8 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
     }
     } else {
         // ============================================================= softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        if constexpr (F8) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         const int w = warp >> 2, row = tid & 127;
         const uint32_t lane_base = uint32_t(warp & 3) << 21;  // this warp's 32 of the 128 lanes
         const uint32_t ts = tmem + lane_base + 256 * w, to = ts + 128;
@@ -676,6 +933,17 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                 }
                 const int lim = !act ? 0 : PREFIX ? x.lim1 : max(base + ir, 0);
                 const int S1 = min(work.sinks(), lim), lo = max(S1, work.lower(lim));
+                // E4M3: this thread's query row, as two parts (the last unit's products are complete), and the factor of
+                // its logits; a scale per KV head goes to the logits and to the output
+                float scale_log2 = a.scale_log2;
+                if constexpr (F8) {
+                    const uint16_t *qrow = a.q + (int64_t(x.r0 + ir) * a.Hq + x.kvh * G + h) * D;
+                    scale_log2 *= split_query(act && lim > 0 ? qrow : nullptr, bp + w * C::TILE + row * 128, C::HALF, row & 7);
+                    if (!PSC) scale_log2 *= __ldg(a.k_scale + x.kvh);
+                    fence_proxy_async();
+                    mbar_arrive(q_full + 8 * w);
+                }
+                const float vsc = F8 && !PSC ? __ldg(a.v_scale + x.kvh) : 1.f;
                 float m = -INFINITY, l = 0.f;
                 for (int t = t0; t < t1; ++t) {
                     if (!(ok = wait(s_full + 8 * w, ph++))) break;
@@ -711,6 +979,14 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
                         if (hf == 1) tc_wait_ld();
+                        if constexpr (PSC) {
+#pragma unroll
+                            for (int b = 4 * hf; b < 4 * hf + 4; ++b) {
+                                const float f = kscale[(tile_no + (t - t0)) % kInfo * kTileBlk + b];
+#pragma unroll
+                                for (int c = 16 * b; c < 16 * b + 16; ++c) s[c] *= f;
+                            }
+                        }
                         if (masked) {
 #pragma unroll
                             for (int b = 0; b < kTileBlk / 2; ++b) mask(hf * (kTileBlk / 2) + b);
@@ -720,7 +996,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[c + 2 * e], s[c + 2 * e + 1]);
                     }
-                    const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale_log2;
+                    const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale_log2;
                     const bool grow = mt > m + kGrow || (m == -INFINITY && mt > m);
                     if (__any_sync(0xffffffffu, grow)) {
                         const float f = grow ? (m == -INFINITY ? 0.f : fast_exp2(m - mt)) : 1.f;
@@ -739,7 +1015,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                         }
                     }
                     const float mr = m == -INFINITY ? 0.f : m;
-                    const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), mr2 = make_float2(-mr, -mr);
+                    const float2 sc2 = make_float2(scale_log2, scale_log2), mr2 = make_float2(-mr, -mr);
                     float2 la = make_float2(0.f, 0.f), lb = la;
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
@@ -798,7 +1074,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                     tmem_ld32(to + 32 * c, o);
                     tc_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = l == 0.f ? 0.f : __uint_as_float(o[e]);
+                    for (int e = 0; e < 32; ++e) v[e] = l == 0.f ? 0.f : F8 && !PSC ? __uint_as_float(o[e]) * vsc : __uint_as_float(o[e]);
                 };
                 // the O of a piece, with m and l per row; PREFIX: of a whole unit too, by row
                 auto publish = [&]() {
@@ -987,18 +1263,28 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
     if (misc[1] && warp == 8) {
         // the CTA gave up: nothing that was started may land after it is gone (otherwise the products have
         // waited for every copy)
-        const int steps = max(misc[6], misc[7]);
+        const int steps = F8 ? misc[6] : max(misc[6], misc[7]);
         for (int i = max(steps - kStages, 0); i < steps; ++i)
             mbar_wait_bounded(full + 8 * (i % kStages), uint32_t(i / kStages) & 1u, a.wait_ns);
-        for (int w = 0; w < 2; ++w)
-            if (misc[2 + w] > 0) mbar_wait_bounded(q_full + 8 * w, uint32_t(misc[2 + w] - 1) & 1u, a.wait_ns);
+        for (int w = 0; w < 2; ++w) {
+            const int n = misc[2 + w];
+            for (int i = F8 ? max(n - kRaw / 2, 0) : n; i < n; ++i)  // blocks of codes
+                mbar_wait_bounded(raw_full + 8 * (i % (kRaw / 2) * 2 + w), uint32_t(i / (kRaw / 2)) & 1u, a.wait_ns);
+            if (!F8 && n > 0) mbar_wait_bounded(q_full + 8 * w, uint32_t(n - 1) & 1u, a.wait_ns);
+        }
     }
     // ---- the rows written here that are not finite, a warp per row, over their own tokens. Only now: this may take
     // long (5 ms of a warp for a row of 40000 tokens), and nothing waits for these warps any more.
     if constexpr (!PREFIX) {
         if (after.odd == 0 || misc[1]) return;
-        if (warp >= 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");  // the launch's share for every warp again
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 168;");
+        // the launch's share for every warp again
+        if constexpr (F8) {
+            if (warp >= 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+            else asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        } else {
+            if (warp >= 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+            else asm volatile("setmaxnreg.dec.sync.aligned.u32 168;");
+        }
         s0 = after.s0;
         x = after.x;
         nu = after.nu;
@@ -1006,7 +1292,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
         for (int64_t p = pos0; p < pos1;) {
             const int t0 = int(p - s0), t1 = int(min(pos1 - s0, int64_t(x.n)));
 #pragma unroll 1
-            for (int r = warp; r < x.nr * G; r += kWarpsRT) {
+            for (int r = warp; r < x.nr * G; r += NWARP) {
                 const int ir = r / G;
                 const bool written = (t0 == 0 && t1 == x.n) ||
                                      (after.merged[ir >= RQ] & (t0 == 0 ? kMergedHere : kMergedBefore));
@@ -1023,8 +1309,8 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
                 int rr, nn;
                 work.rows(x.s, rr, nn);
                 const int lim = work.limit(x.s, x.r0 + ir - rr, nn);
-                if (reached_by_others<D>(a, x.s, x.kvh, x.lim0, x.lim1, lim))
-                    redo_row<D>(a, x.s, x.kvh, x.r0 + ir, r % G, lim);
+                if (reached_by_others<D, KIND>(a, x.s, x.kvh, x.lim0, x.lim1, lim))
+                    redo_row<D, KIND>(a, x.s, x.kvh, x.r0 + ir, r % G, lim);
             }
             p = s0 + t1;
             if (p < pos1) next_unit();
@@ -1040,7 +1326,7 @@ __global__ void __launch_bounds__(kWarpsRT * 32, 1)
 // (which costs 1.6 us of the host as well), on 4000 tokens: 8 sequences of 5 rows
 // 32.9 and 28.8 us, 2 of 64 rows 40.8 and 26.8; with 128 units on 152 CTAs, 32
 // sequences of 2 rows on 3000 tokens, 49.1 and 54.5.
-template <int D>
+template <int D, CacheKind KIND>
 __global__ void __launch_bounds__(256) cut_join_kernel(const SubsetArgs a) {
     pdl_trigger();
     pdl_wait();
@@ -1133,8 +1419,8 @@ __global__ void __launch_bounds__(256) cut_join_kernel(const SubsetArgs a) {
             }
             const int g = g0 + i * step, ir = g / G, h = g - ir * G;
             if (!__all_sync(0xffffffffu, fine) &&
-                reached_by_others<D>(a, u.s, u.kvh, max(u.base, 0), max(u.base + u.nr - 1, 0), max(u.base + ir, 0))) {
-                redo_row<D>(a, u.s, u.kvh, u.r0 + ir, h, max(u.base + ir, 0));
+                reached_by_others<D, KIND>(a, u.s, u.kvh, max(u.base, 0), max(u.base + u.nr - 1, 0), max(u.base + ir, 0))) {
+                redo_row<D, KIND>(a, u.s, u.kvh, u.r0 + ir, h, max(u.base + ir, 0));
                 continue;
             }
             uint32_t *out = reinterpret_cast<uint32_t *>(a.out + (int64_t(u.r0 + ir) * a.Hq + u.kvh * G + h) * D) +
@@ -1145,17 +1431,17 @@ __global__ void __launch_bounds__(256) cut_join_kernel(const SubsetArgs a) {
     }
 }
 
-template <int D, bool PREFIX>
+template <int D, bool PREFIX, CacheKind KIND = kCacheBf16>
 cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tq, const SubsetArgs &a,
                      int grid, cudaStream_t stream) {
-    const auto kernel = row_tiles_kernel<D, PREFIX>;
+    const auto kernel = row_tiles_kernel<D, PREFIX, KIND>;
     const cudaError_t e = smem_once(reinterpret_cast<const void *>(kernel), RowCfg<D>::SMEM);
     if (e != cudaSuccess) return e;
-    const cudaError_t f = launch_pdl(kernel, dim3(grid), dim3(kWarpsRT * 32), RowCfg<D>::SMEM, stream, tk, tv, tq, a);
+    const cudaError_t f = launch_pdl(kernel, dim3(grid), dim3(kRowWarps<KIND> * 32), RowCfg<D>::SMEM, stream, tk, tv, tq, a);
     if (PREFIX || f != cudaSuccess || !a.cuts) return f;
     // 32 rows per slice, by the average unit
     const int rows = std::min(2 * (kTileTok / a.G), (a.rows + a.nseq - 1) / a.nseq) * a.G;
-    return launch_pdl(cut_join_kernel<D>, dim3(grid, (rows + 31) / 32), dim3(256), 0, stream, a);
+    return launch_pdl(cut_join_kernel<D, KIND>, dim3(grid, (rows + 31) / 32), dim3(256), 0, stream, a);
 }
 
 }  // namespace
@@ -1163,12 +1449,14 @@ cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const CUtenso
 size_t row_tiles_slot_floats(int head_dim) { return size_t(2) * 128 * (head_dim + 2); }
 
 cudaError_t launch_row_tiles(const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tq,
-                             const SubsetArgs &args, int head_dim, int sms, cudaStream_t stream) {
+                             const SubsetArgs &args, int head_dim, CacheKind kind, int sms, cudaStream_t stream) {
     SubsetArgs a = args;
     a.min_items = kMinTiles;
     const int per_unit = 2 * (kTileTok / a.G);  // query rows
     if (int64_t(a.Hkv) * std::max(a.nseq, (a.rows + per_unit - 1) / per_unit) * 2 > sms) a.cuts = nullptr;
     const int grid = a.pt ? a.pgrid : sms;
+    if (kind == kCacheE4m3) return launch_t<128, false, kCacheE4m3>(tk, tv, tq, a, grid, stream);
+    if (kind == kCacheE4m3Block) return launch_t<128, false, kCacheE4m3Block>(tk, tv, tq, a, grid, stream);
     if (a.pt) return head_dim == 128 ? launch_t<128, true>(tk, tv, tq, a, grid, stream) : launch_t<64, true>(tk, tv, tq, a, grid, stream);
     return head_dim == 128 ? launch_t<128, false>(tk, tv, tq, a, grid, stream) : launch_t<64, false>(tk, tv, tq, a, grid, stream);
 }

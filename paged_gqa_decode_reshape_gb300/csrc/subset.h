@@ -89,12 +89,12 @@ cudaError_t launch_stream_decode(const CUtensorMap &tk, const CUtensorMap &tv, c
                                  CacheKind kind, int sms, cudaStream_t stream);
 
 // query rows of any number per sequence over window and sinks, or (pt set) the
-// rows of groups of sequences over their prefixes, left in slots / rowres / desc;
+// rows of groups of sequences over their prefixes (bf16 cache), left in slots / rowres / desc;
 // tq: tensor map of the queries
 constexpr int kRowTile = 128;  // rows (query row, head) of a row tile
 size_t row_tiles_slot_floats(int head_dim);
 cudaError_t launch_row_tiles(const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tq, const SubsetArgs &a,
-                             int head_dim, int sms, cudaStream_t stream);
+                             int head_dim, CacheKind kind, int sms, cudaStream_t stream);
 
 // rows of own part and prefix parts joined, written out
 cudaError_t launch_prefix_join(const SubsetArgs &a, int head_dim, cudaStream_t stream);

@@ -79,10 +79,25 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a_tmem, uint32_t 
         : "memory");
 }
 
+// The same of E4M3 inputs, 32 deep.
+__device__ __forceinline__ void tc_mma_ss_e4m3(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                               uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(uint32_t(accumulate))
+        : "memory");
+}
+
 // Instruction descriptor: bf16 x bf16 -> fp32, M x N; b_mn: B is stored with N contiguous.
 constexpr uint32_t tc_idesc(int M, int N, bool b_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | (uint32_t(N >> 3) << 17) |
            (uint32_t(M >> 4) << 24);
+}
+
+// E4M3 x E4M3 -> fp32, both with K contiguous.
+constexpr uint32_t tc_idesc_e4m3(int M, int N) {
+    return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
 
 // Descriptor of a 128-byte-swizzled operand: 8 rows of 128 bytes repeat every
