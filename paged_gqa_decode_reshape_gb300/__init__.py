@@ -1452,6 +1452,16 @@ def pa_evict(kept: torch.Tensor, new_lens: torch.Tensor, key_cache: torch.Tensor
 
 def _ints(dev, *named):
     """int32 vectors [n] on dev: (tensor, name, n)."""
+    d = dev.index
+    try:  # the usual case first
+        for t, _, n in named:
+            if not (t.dtype is torch.int32 and t.ndim == 1 and t.get_device() == d and t.is_contiguous()
+                    and (n is None or t.numel() == n)):
+                break
+        else:
+            return
+    except AttributeError:
+        pass
     for t, name, n in named:
         _need(t, name, torch.int32, 1, dev)
         if n is not None and t.shape[0] != n:
@@ -1500,6 +1510,14 @@ def pa_release_blocks(block_tables: torch.Tensor, context_lens: torch.Tensor, ke
 
 def _heads(t: torch.Tensor, name: str, rows: Optional[int] = None, device=None):
     """(heads, head_dim, row stride) of a bf16 tensor [T, H, D] whose rows' heads are contiguous."""
+    try:  # the usual case first
+        if t.dtype is torch.bfloat16 and t.ndim == 3:
+            (T, H, D), (row, head, one), d = t.shape, t.stride(), t.get_device()
+            if (T > 1 and one == 1 and head == D and d >= 0 and (device is None or d == device.index)
+                    and (rows is None or T == rows)):
+                return H, D, row
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not torch.bfloat16:
@@ -1517,49 +1535,78 @@ def _heads(t: torch.Tensor, name: str, rows: Optional[int] = None, device=None):
     return H, D, row if T > 1 else H * D  # one row: its stride says nothing
 
 
-def _rope(name, q_out, k_out, query, key, value, cos_sin, positions, q_weight, k_weight, eps, axes, interleaved, cache):
-    T = query.shape[0] if isinstance(query, torch.Tensor) and query.dim() == 3 else None
+def _fits(t, dtype, ndim, d) -> bool:
+    """The usual case of _need: a contiguous tensor of this type and rank on device number d."""
+    return t.dtype is dtype and t.ndim == ndim and t.get_device() == d and t.is_contiguous()
+
+
+def _rope(name, q_out, k_out, query, key, value, cos_sin, positions, q_weight, k_weight, eps, axes, interleaved,
+          cache=None):
+    """cache: (key_cache, value_cache, slot_mapping, *scales) of the forms that write one."""
     Hq, D, qs = _heads(query, "query")
-    dev = query.device
+    dev, T = query.device, query.shape[0]
+    d = dev.index
     Hkv, D2, ks = _heads(key, "key", T, dev)
     if D2 != D:
         raise ValueError("query and key must have the same head_dim")
-    h, d, qos = _heads(q_out, "q_out", T, dev)
-    if (h, d) != (Hq, D):
+    h, d2, qos = _heads(q_out, "q_out", T, dev)
+    if h != Hq or d2 != D:
         raise ValueError("q_out must have query's shape")
-    kos = vs = 0
+    ko, kos = None, 0
     if k_out is not None:
-        h, d, kos = _heads(k_out, "k_out", T, dev)
-        if (h, d) != (Hkv, D):
+        h, d2, kos = _heads(k_out, "k_out", T, dev)
+        if h != Hkv or d2 != D:
             raise ValueError("k_out must have key's shape")
-    if value is not None:
-        h, d, vs = _heads(value, "value", T, dev)
-        if (h, d) != (Hkv, D):
-            raise ValueError("value must have key's shape")
-    _need(cos_sin, "cos_sin", torch.float32, 2, dev)
+        ko = k_out.data_ptr()
+    if not (isinstance(cos_sin, torch.Tensor) and _fits(cos_sin, torch.float32, 2, d)):
+        _need(cos_sin, "cos_sin", torch.float32, 2, dev)
     P, R = cos_sin.shape
-    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _need(w, n, torch.bfloat16, 1, dev)
-            if w.shape[0] != D:
-                raise ValueError(f"{n} must be [head_dim]")
+    qw = kw = ax = None
+    if q_weight is not None:
+        _need(q_weight, "q_weight", torch.bfloat16, 1, dev)
+        if q_weight.numel() != D:
+            raise ValueError("q_weight must be [head_dim]")
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        _need(k_weight, "k_weight", torch.bfloat16, 1, dev)
+        if k_weight.numel() != D:
+            raise ValueError("k_weight must be [head_dim]")
+        kw = k_weight.data_ptr()
+    A = 1
     if axes is None:
-        A = 1
         _need(positions, "positions", torch.int32, 1, dev)
     else:
         _need(positions, "positions", torch.int32, 2, dev)
         A = positions.shape[0]
         _need(axes, "axes", torch.int32, 1, dev)
-        if axes.shape[0] * 2 != R:
+        if axes.numel() * 2 != R:
             raise ValueError("axes must be [rotary_dim / 2]")
-    if positions.shape[-1] != T:
+        ax = axes.data_ptr()
+    if positions.numel() != A * T:
         raise ValueError("positions must have a column per token")
-    v = () if value is None else (value.data_ptr(), vs)
-    _run(name, dev,
-         (q_out.data_ptr(), qos, None if k_out is None else k_out.data_ptr(), kos, query.data_ptr(), qs, key.data_ptr(), ks,
-          *v, None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
-          float(eps), cos_sin.data_ptr(), P, R, positions.data_ptr(), None if axes is None else axes.data_ptr(), A,
-          int(bool(interleaved)), *cache(T, Hkv, D, dev), T, Hq, Hkv, D, *(() if value is None else cache.sizes)))
+    head = q_out.data_ptr(), qos, ko, kos, query.data_ptr(), qs, key.data_ptr(), ks
+    tail = (qw, kw, eps, cos_sin.data_ptr(), P, R, positions.data_ptr(), ax, A, 1 if interleaved else 0)
+    if cache is None:
+        _run(name, dev, (*head, *tail, T, Hq, Hkv, D))
+        return q_out
+    h, d2, vs = _heads(value, "value", T, dev)
+    if h != Hkv or d2 != D:
+        raise ValueError("value must have key's shape")
+    kc, vc, slots, *scales = cache
+    dtype = torch.uint8 if scales else torch.bfloat16
+    _need(kc, "key_cache", dtype, 4, dev)
+    _need(vc, "value_cache", dtype, 4, dev)
+    _need(slots, "slot_mapping", torch.int64, 1, dev)
+    NB, BS, h, d2 = kc.shape
+    if h != Hkv or d2 != D or vc.shape != ((NB, h, D, BS) if scales else kc.shape) or slots.numel() != T:
+        raise ValueError("shape mismatch between key/value, slot_mapping and the caches")
+    if scales:
+        _scales(*scales, Hkv, dev)
+        _run(name, dev, (*head, value.data_ptr(), vs, *tail, kc.data_ptr(), vc.data_ptr(), scales[0].data_ptr(),
+                         scales[1].data_ptr(), slots.data_ptr(), T, Hq, Hkv, D, BS, NB))
+    else:
+        _run(name, dev, (*head, value.data_ptr(), vs, *tail, kc.data_ptr(), vc.data_ptr(), slots.data_ptr(), T, Hq,
+                         Hkv, D, BS, NB))
     return q_out
 
 
@@ -1573,29 +1620,7 @@ def pa_norm_rope(q_out: torch.Tensor, k_out: torch.Tensor, query: torch.Tensor, 
     if k_out is None:
         raise TypeError("k_out must be a torch.Tensor")
     return _rope("pa_norm_rope", q_out, k_out, query, key, None, cos_sin, positions, q_weight, k_weight, eps, axes,
-                 interleaved, lambda *_: ())
-
-
-class _CacheArgs:
-    """The cache arguments of pa_norm_rope_and_cache and its 8-bit form, checked against the tokens' shape."""
-
-    def __init__(self, key_cache, value_cache, slot_mapping, scales=()):
-        self.at = key_cache, value_cache, slot_mapping, scales
-        self.sizes = ()
-
-    def __call__(self, T, Hkv, D, dev):
-        kc, vc, slots, scales = self.at
-        dtype = torch.uint8 if scales else torch.bfloat16
-        _need(kc, "key_cache", dtype, 4, dev)
-        _need(vc, "value_cache", dtype, 4, dev)
-        _need(slots, "slot_mapping", torch.int64, 1, dev)
-        NB, BS, H, D2 = kc.shape
-        if (H, D2) != (Hkv, D) or vc.shape != ((NB, H, D, BS) if scales else kc.shape) or slots.shape[0] != T:
-            raise ValueError("shape mismatch between key/value, slot_mapping and the caches")
-        if scales:
-            _scales(*scales, Hkv, dev)
-        self.sizes = BS, NB
-        return kc.data_ptr(), vc.data_ptr(), *[s.data_ptr() for s in scales], slots.data_ptr()
+                 interleaved)
 
 
 def pa_norm_rope_and_cache(q_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
@@ -1605,10 +1630,8 @@ def pa_norm_rope_and_cache(q_out: torch.Tensor, query: torch.Tensor, key: torch.
                            axes: Optional[torch.Tensor] = None, interleaved: bool = False,
                            k_out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """pa_norm_rope whose rotated keys go, with the values, to the slots of the paged caches (and to k_out if given)."""
-    if value is None:
-        raise TypeError("value must be a torch.Tensor")
     return _rope("pa_norm_rope_and_cache", q_out, k_out, query, key, value, cos_sin, positions, q_weight, k_weight, eps,
-                 axes, interleaved, _CacheArgs(key_cache, value_cache, slot_mapping))
+                 axes, interleaved, (key_cache, value_cache, slot_mapping))
 
 
 def pa_norm_rope_and_cache_fp8(q_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
@@ -1619,7 +1642,5 @@ def pa_norm_rope_and_cache_fp8(q_out: torch.Tensor, query: torch.Tensor, key: to
                                axes: Optional[torch.Tensor] = None, interleaved: bool = False,
                                k_out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """pa_norm_rope_and_cache into an 8-bit cache with per-KV-head scales."""
-    if value is None:
-        raise TypeError("value must be a torch.Tensor")
     return _rope("pa_norm_rope_and_cache_fp8", q_out, k_out, query, key, value, cos_sin, positions, q_weight, k_weight,
-                 eps, axes, interleaved, _CacheArgs(key_cache, value_cache, slot_mapping, (k_scale, v_scale)))
+                 eps, axes, interleaved, (key_cache, value_cache, slot_mapping, k_scale, v_scale))

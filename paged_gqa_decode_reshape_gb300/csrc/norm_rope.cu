@@ -20,11 +20,13 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "step.h"
+#include "tcgen05.cuh"
 
 namespace pa {
 namespace {
 
-constexpr int kRopeWarps = 4;  // per CTA
+constexpr int kRopeWarps = 2;  // per CTA
+constexpr int kRopeSteps = 3;  // steps of heads of a warp
 
 // The E4M3 code of fl32(x / scale), nearest with ties to even, saturated; one NaN code.
 __device__ __forceinline__ uint32_t encode2(float x, float y, float scale) {
@@ -35,17 +37,19 @@ __device__ __forceinline__ uint32_t encode2(float x, float y, float scale) {
     return pair & 0xffffu;
 }
 
-__device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16_lo(w[i]);
-        x[2 * i + 1] = bf16_hi(w[i]);
-    }
+__device__ __forceinline__ void unpack8(const uint4 &u, float2 (&x)[4]) {
+    x[0] = make_float2(bf16_lo(u.x), bf16_hi(u.x));
+    x[1] = make_float2(bf16_lo(u.y), bf16_hi(u.y));
+    x[2] = make_float2(bf16_lo(u.z), bf16_hi(u.z));
+    x[3] = make_float2(bf16_lo(u.w), bf16_hi(u.w));
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                      pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ uint4 pack8(const float2 (&x)[4]) {
+    return make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y), pack_bf16x2(x[2].x, x[2].y),
+                      pack_bf16x2(x[3].x, x[3].y));
+}
+__device__ __forceinline__ uint2 encode8(const float2 (&x)[4], float scale) {
+    return make_uint2(encode2(x[0].x, x[0].y, scale) | encode2(x[1].x, x[1].y, scale) << 16,
+                      encode2(x[2].x, x[2].y, scale) | encode2(x[3].x, x[3].y, scale) << 16);
 }
 
 // V of the tokens of one 8-bit block that start with row t, for one KV head, by a warp:
@@ -98,36 +102,27 @@ __device__ __forceinline__ void write_v8(const RopeArgs &a, int64_t t, int h) {
     }
 }
 
-// One warp: heads [first, last) of token t. Heads 0 .. Hq - 1 are the queries, then the
-// keys, then (bf16 cache) the values.
-template <int D, bool INTER, RopeCache CACHE>
-__device__ __forceinline__ void rope_heads(const RopeArgs &a, int64_t t, int first, int last) {
+// One warp: heads first .. first + NS * HPS - 1 (before `heads`) of token t, HPS at a time. Heads 0 .. Hq - 1 are the
+// queries, then the keys, then (bf16 cache) the values. All of them are on their way before the position is asked for.
+template <int D, bool INTER, RopeCache CACHE, int NS>
+__device__ __forceinline__ void rope_heads(const RopeArgs &a, int64_t t, int first, int heads) {
     constexpr int LPH = D / 16, HPS = 32 / LPH, BS = kBlockSize;  // lanes per head, heads per step
     const int lane = threadIdx.x & 31, sub = lane % LPH, half = a.R / 2, rc = a.R / 16;  // rc: pairs of chunks
     // this lane's chunks of 8 dims
     const bool turns = sub < rc;
     const int c0 = turns ? (INTER ? 2 * sub : sub) : 2 * rc + 2 * (sub - rc);
     const int c1 = turns && !INTER ? sub + rc : c0 + 1;
-    float cs[8], sn[8];
-    if (turns) {
-        const int f0 = INTER ? 8 * sub : 8 * c0;  // 8 frequencies: of pairs with chunk c1, or of both chunks
-        if (a.axis == nullptr) {
-            const int64_t row = min(max(int64_t(__ldg(a.pos + t)), int64_t(0)), a.P - 1);
-            const float4 *at = reinterpret_cast<const float4 *>(a.table + row * a.R + f0);
+    const uint16_t *const q = a.q + t * a.qs, *const k = a.k + t * a.ks - a.Hq * D,
+                   *const v = a.v + t * a.vs - (a.Hq + a.Hkv) * D;  // head hh at hh * D
+    uint4 r0[NS], r1[NS];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float4 x = __ldg(at + i), y = __ldg(at + i + half / 4);
-                cs[4 * i] = x.x, cs[4 * i + 1] = x.y, cs[4 * i + 2] = x.z, cs[4 * i + 3] = x.w;
-                sn[4 * i] = y.x, sn[4 * i + 1] = y.y, sn[4 * i + 2] = y.z, sn[4 * i + 3] = y.w;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int ax = min(max(__ldg(a.axis + f0 + i), 0), a.naxes - 1);
-                const int64_t row = min(max(int64_t(__ldg(a.pos + ax * a.T + t)), int64_t(0)), a.P - 1);
-                cs[i] = __ldg(a.table + row * a.R + f0 + i);
-                sn[i] = __ldg(a.table + row * a.R + half + f0 + i);
-            }
+    for (int s = 0; s < NS; ++s) {
+        const int hh = first + s * HPS + lane / LPH;
+        const uint16_t *src = (hh < a.Hq ? q : CACHE != kRopeBf16 || hh < a.Hq + a.Hkv ? k : v) + hh * D;
+        r0[s] = r1[s] = make_uint4(0, 0, 0, 0);
+        if (hh < heads) {
+            r0[s] = __ldcg(reinterpret_cast<const uint4 *>(src) + c0);
+            r1[s] = __ldcg(reinterpret_cast<const uint4 *>(src) + c1);
         }
     }
     int64_t slot = -1;
@@ -135,93 +130,127 @@ __device__ __forceinline__ void rope_heads(const RopeArgs &a, int64_t t, int fir
         slot = __ldg(a.slots + t);
         if (slot < 0 || slot >= a.NB * BS) slot = -1;
     }
-#pragma unroll 3
-    for (int h0 = first; h0 < last; h0 += HPS) {
-        const int hh = h0 + lane / LPH;
+    float2 cs[4], sn[4];
+    const int f0 = INTER ? 8 * sub : 8 * c0;  // 8 frequencies: of pairs with chunk c1, or of both chunks
+    int pos = 0;  // on axis lane % 4
+    uint32_t axes = 0;  // of the lane's frequencies, two bits each
+    if (a.axis) {
+        pos = __ldg(a.pos + min(lane & 3, a.naxes - 1) * a.T + t);
+        if (turns) {
+            int ax[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ax[i] = __ldg(a.axis + f0 + i);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) axes |= uint32_t(min(max(ax[i], 0), a.naxes - 1)) << (2 * i);
+        }
+    } else {
+        pos = __ldg(a.pos + t);
+    }
+    auto row = [&](int i) -> const float * {  // of frequency f0 + i
+        const int p = __shfl_sync(0xffffffffu, pos, (axes >> (2 * i)) & 3u);
+        return a.table + min(max(int64_t(p), int64_t(0)), a.P - 1) * a.R + f0;
+    };
+    // four frequencies at once where every lane's are of one axis
+    const uint32_t rest = axes & 0xffu, more = axes >> 8;
+    if (__all_sync(0xffffffffu, rest == (rest & 3u) * 0x55u && more == (more & 3u) * 0x55u)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float *from = row(4 * i) + 4 * i;
+            if (!turns) continue;
+            const float4 x = __ldg(reinterpret_cast<const float4 *>(from)), y = __ldg(reinterpret_cast<const float4 *>(from + half));
+            cs[2 * i] = make_float2(x.x, x.y), cs[2 * i + 1] = make_float2(x.z, x.w);
+            sn[2 * i] = make_float2(y.x, y.y), sn[2 * i + 1] = make_float2(y.z, y.w);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float *from = row(i) + i;
+            const float c = turns ? __ldg(from) : 0.f, s = turns ? __ldg(from + half) : 0.f;
+            if (i & 1) cs[i / 2].y = c, sn[i / 2].y = s;
+            else cs[i / 2].x = c, sn[i / 2].x = s;
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+        const int hh = first + s * HPS + lane / LPH;
         const bool is_q = hh < a.Hq, is_k = !is_q && hh < a.Hq + a.Hkv;
         const int h = is_q ? hh : is_k ? hh - a.Hq : hh - a.Hq - a.Hkv;
-        // a key or value without a place is not read
-        const bool in = hh < last && (is_q || (is_k && a.ko) || slot >= 0);
-        const uint16_t *src = (is_q ? a.q + t * a.qs : is_k ? a.k + t * a.ks : a.v + t * a.vs) + h * D;
-        uint4 r0 = make_uint4(0, 0, 0, 0), r1 = r0;
-        if (in) {
-            r0 = __ldcg(reinterpret_cast<const uint4 *>(src) + c0);
-            r1 = __ldcg(reinterpret_cast<const uint4 *>(src) + c1);
-        }
-        const bool is_v = CACHE == kRopeBf16 && !is_q && !is_k;
-        float x[8], y[8];
-        unpack8(r0, x);
-        unpack8(r1, y);
+        float2 x[4], y[4];
+        unpack8(r0[s], x);
+        unpack8(r1[s], y);
         const uint16_t *w = is_q ? a.qw : a.kw;
         if (a.qw || a.kw) {
-            float s = 0.f;
+            float2 m2 = mul2(x[0], x[0]), n2 = mul2(y[0], y[0]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], fmaf(y[i], y[i], s));
+            for (int i = 1; i < 4; ++i) {
+                m2 = fma2(x[i], x[i], m2);
+                n2 = fma2(y[i], y[i], n2);
+            }
+            float m = (m2.x + m2.y) + (n2.x + n2.y);
 #pragma unroll
-            for (int o = LPH / 2; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            for (int o = LPH / 2; o >= 1; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
             if (w) {
-                const float f = __frsqrt_rn(fmaf(s, 1.f / D, a.eps));
-                float w0[8], w1[8];
+                const float f = rsqrtf(fmaf(m, 1.f / D, a.eps));
+                float2 w0[4], w1[4];
                 unpack8(__ldg(reinterpret_cast<const uint4 *>(w) + c0), w0);
                 unpack8(__ldg(reinterpret_cast<const uint4 *>(w) + c1), w1);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[i] = x[i] * f * w0[i];
-                    y[i] = y[i] * f * w1[i];
-                }
-            }
-        }
-        if (turns) {
-            if (INTER) {
-#pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float p = x[2 * i], q = x[2 * i + 1], u = y[2 * i], v = y[2 * i + 1];
-                    x[2 * i] = p * cs[i] - q * sn[i];
-                    x[2 * i + 1] = q * cs[i] + p * sn[i];
-                    y[2 * i] = u * cs[4 + i] - v * sn[4 + i];
-                    y[2 * i + 1] = v * cs[4 + i] + u * sn[4 + i];
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float p = x[i], q = y[i];
-                    x[i] = p * cs[i] - q * sn[i];
-                    y[i] = q * cs[i] + p * sn[i];
+                    x[i] = mul2(mul2(x[i], make_float2(f, f)), w0[i]);
+                    y[i] = mul2(mul2(y[i], make_float2(f, f)), w1[i]);
                 }
             }
         }
-        if (!in) continue;
-        if (is_v) {  // as it is
+        if (INTER) {
+            if (turns) {
+                auto turn = [](float2 &p, float c, float s) { p = make_float2(p.x * c - p.y * s, p.y * c + p.x * s); };
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    turn(x[2 * i], cs[i].x, sn[i].x);
+                    turn(x[2 * i + 1], cs[i].y, sn[i].y);
+                    turn(y[2 * i], cs[2 + i].x, sn[2 + i].x);
+                    turn(y[2 * i + 1], cs[2 + i].y, sn[2 + i].y);
+                }
+            }
+        } else if (turns) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 p = x[i];
+                x[i] = fma2(p, cs[i], mul2(y[i], make_float2(-sn[i].x, -sn[i].y)));
+                y[i] = fma2(y[i], cs[i], mul2(p, sn[i]));
+            }
+        }
+        if (hh >= heads) continue;
+        if (CACHE == kRopeBf16 && !is_q && !is_k) {  // a value, as it is
+            if (slot < 0) continue;
             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.vc) + (slot * a.Hkv + h) * D);
-            dst[c0] = r0;
-            dst[c1] = r1;
+            dst[c0] = r0[s];
+            dst[c1] = r1[s];
             continue;
         }
+        const uint4 lo = pack8(x), hi = pack8(y);
         if (is_q || a.ko) {
-            uint4 *dst = reinterpret_cast<uint4 *>(is_q ? a.qo + t * a.qos + h * D : a.ko + t * a.kos + h * D);
-            dst[c0] = pack8(x);
-            dst[c1] = pack8(y);
+            uint4 *dst = reinterpret_cast<uint4 *>((is_q ? a.qo + t * a.qos : a.ko + t * a.kos) + h * D);
+            dst[c0] = lo;
+            dst[c1] = hi;
         }
-        if (CACHE == kRopeNone || !is_k || slot < 0) continue;
+        if (CACHE == kRopeNone || is_q || slot < 0) continue;
         if (CACHE == kRopeBf16) {
             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.kc) + (slot * a.Hkv + h) * D);
-            dst[c0] = pack8(x);
-            dst[c1] = pack8(y);
+            dst[c0] = lo;
+            dst[c1] = hi;
         } else {
             const float scale = __ldg(a.k_scale + h);
             uint2 *dst = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.kc) + (slot * a.Hkv + h) * D);
-            dst[c0] = make_uint2(encode2(x[0], x[1], scale) | encode2(x[2], x[3], scale) << 16,
-                                 encode2(x[4], x[5], scale) | encode2(x[6], x[7], scale) << 16);
-            dst[c1] = make_uint2(encode2(y[0], y[1], scale) | encode2(y[2], y[3], scale) << 16,
-                                 encode2(y[4], y[5], scale) | encode2(y[6], y[7], scale) << 16);
+            dst[c0] = encode8(x, scale);
+            dst[c1] = encode8(y, scale);
         }
     }
 }
 
-// per: heads of a warp (a multiple of a step's); parts: warps of a token; the 8-bit V after them,
-// a warp per token and KV head
-template <int D, bool INTER, RopeCache CACHE>
-__global__ void __launch_bounds__(kRopeWarps * 32) norm_rope_kernel(const RopeArgs a, int per, int parts) {
+// parts: warps of a token, NS steps of heads each; the 8-bit V after them, a warp per token and KV head
+template <int D, bool INTER, RopeCache CACHE, int NS>
+__global__ void __launch_bounds__(kRopeWarps * 32) norm_rope_kernel(const RopeArgs a, int parts) {
     pdl_trigger();
     pdl_wait();
     const int heads = a.Hq + a.Hkv + (CACHE == kRopeBf16 ? a.Hkv : 0);
@@ -234,19 +263,22 @@ __global__ void __launch_bounds__(kRopeWarps * 32) norm_rope_kernel(const RopeAr
         write_v8(a, t, part - parts);
         return;
     }
-    rope_heads<D, INTER, CACHE>(a, t, part * per, min((part + 1) * per, heads));
+    rope_heads<D, INTER, CACHE, NS>(a, t, part * NS * (512 / D), heads);
+}
+
+template <int D, bool INTER, RopeCache CACHE, int NS>
+cudaError_t launch_n(const RopeArgs &a, cudaStream_t stream) {
+    constexpr int per = NS * (512 / D);
+    const int heads = a.Hq + a.Hkv + (CACHE == kRopeBf16 ? a.Hkv : 0), parts = (heads + per - 1) / per;
+    const int64_t warps = a.T * (parts + (CACHE == kRopeE4m3 ? a.Hkv : 0));
+    return launch_pdl(norm_rope_kernel<D, INTER, CACHE, NS>, dim3(unsigned((warps + kRopeWarps - 1) / kRopeWarps)),
+                      dim3(kRopeWarps * 32), 0, stream, a, parts);
 }
 
 template <int D, bool INTER, RopeCache CACHE>
 cudaError_t launch_t(const RopeArgs &a, cudaStream_t stream) {
-    constexpr int step = 32 / (D / 16);
-    const int heads = a.Hq + a.Hkv + (CACHE == kRopeBf16 ? a.Hkv : 0);
-    const int steps = (heads + step - 1) / step;
-    const int per = (a.T * steps < 4096 ? 1 : 3) * step;
-    const int parts = (heads + per - 1) / per;
-    const int64_t warps = a.T * (parts + (CACHE == kRopeE4m3 ? a.Hkv : 0));
-    return launch_pdl(norm_rope_kernel<D, INTER, CACHE>, dim3(unsigned((warps + kRopeWarps - 1) / kRopeWarps)),
-                      dim3(kRopeWarps * 32), 0, stream, a, per, parts);
+    const int steps = (a.Hq + 2 * a.Hkv + 512 / D - 1) / (512 / D);
+    return a.T * steps < 4096 ? launch_n<D, INTER, CACHE, 1>(a, stream) : launch_n<D, INTER, CACHE, kRopeSteps>(a, stream);
 }
 
 template <int D, bool INTER>
