@@ -7,8 +7,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
-
 namespace pa {
 
 constexpr int kMaxWindowRows = 1 << 20;  // query rows of a windowed multi-token call
@@ -56,29 +54,6 @@ struct SubsetArgs {
     int stop_item;                // failure tests: a warp's copies stop at this item (else INT_MAX)
     int min_items;                // row tiles: tiles of a CTA's range at least
 };
-
-// Dynamic shared memory limit of a kernel, set once per device (or at every call
-// beyond the table's devices and kernels). Allocates nothing and throws nothing:
-// it runs below C entry points.
-inline cudaError_t smem_once(const void *kernel, size_t bytes) noexcept {
-    constexpr int kDevices = 64, kKernels = 32;
-    static std::atomic<const void *> done[kDevices][kKernels];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const bool known = dev >= 0 && dev < kDevices;
-    for (int i = 0; known && i < kKernels; ++i) {
-        const void *at = done[dev][i].load(std::memory_order_acquire);
-        if (at == kernel) return cudaSuccess;
-        if (!at) break;
-    }
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
-    for (int i = 0; e == cudaSuccess && known && i < kKernels; ++i) {
-        const void *at = nullptr;
-        if (done[dev][i].compare_exchange_strong(at, kernel, std::memory_order_acq_rel) || at == kernel) break;
-    }
-    return e;
-}
 
 // one query row per sequence, window and sinks, or (weights set) the dense
 // decode that adds up the attention weights, or (pt set) prefix and own tokens,
