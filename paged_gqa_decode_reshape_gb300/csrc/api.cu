@@ -1025,12 +1025,20 @@ bool reads_each(const SubsetArgs &a, int D) {
 // 12.3 and 13.0, one of 64 on 400 (50 MB) 13.7 and 20.3, 8 of 2 on 2000 (62 MB, an SM
 // each) 14.4 and 19.1, on 4000 (125 MB, row tiles by this rule) 20.1 and 28.5, 32 of 2
 // on 500 (64 MB) 16.6 and 14.8.
+//
+// E4M3: by both kernels' times in microseconds. A row by itself takes 3.9e-5 per token and KV head (6.6 TB/s over all SMs,
+// the latency of its warps, not L2); row tiles read the tokens of a sequence once, 1.15e-4 per token and KV head while its
+// rows fit one row tile, with 0.05 for a unit's begin and end and 18 to start (code that is fetched first, merges). Each row and
+// row tiles, 28 / 4 heads: 32 sequences of 2 rows on 500 tokens 16.1 and 18.5 us, of 6 rows 24.3 and 18.7 (each by this
+// rule), on 4000 of 3 rows 63 and 72, of 6 rows 111 and 75, on 16000 of 2 rows 142 and 197, of 4 rows 289 and 199; 128 of 2 rows on
+// 4000 tokens 166 and 232, of 4 rows 314 and 236; one of 8 rows on 16000 26 and 38, of 36 rows 80 and 49.
 constexpr int64_t kEachReadsMany = int64_t(56) << 20;
 
 bool rows_each(const SubsetArgs &a, int D, CacheKind kind, int sms) {
     const double seen = std::min(double(a.MBS) * kBlockSize, double(a.window) + a.sinks + 2 * kBlockSize);
     const int64_t segs = int64_t(a.rows) * a.Hkv;
-    return segs * seen * D * (kind == kCacheBf16 ? 4 : 2) <= double(segs <= sms ? kEachReads : kEachReadsMany);
+    if (kind != kCacheBf16) return 3.9e-5 * segs * seen <= 18 + double(a.nseq) * a.Hkv * (1.15e-4 * seen + 0.05);
+    return segs * seen * D * 4 <= double(segs <= sms ? kEachReads : kEachReadsMany);
 }
 
 // the launches, after the argument checks

@@ -24,9 +24,29 @@ def _cuda():
     b.build()
 
 
-def wide(bt, rows, Hkv):
-    """Tables so wide that a call for these rows shares its reads between rows, however short the lengths are."""
-    return torch.nn.functional.pad(bt, (0, (128 << 20) // (rows * Hkv * BS * D * 2) + 1), value=-1)
+WIDE = 6250  # blocks of a table that makes a call share reads between rows, where sequences have several
+
+
+def filler(rows, nseq, Hkv, window, sinks):
+    """Rows of a further prompt that make the call share its reads between rows: the call's rule is by the rows, the
+    sequences and the most tokens that a row can see (the window, or the width of the tables)."""
+    seen = min(WIDE * BS, window + sinks + 2 * BS)
+    cost = lambda n, s: 3.9e-5 * n * Hkv * seen - 18 - s * Hkv * (1.15e-4 * seen + 0.05)
+    if cost(rows, nseq) > 0:
+        return 0
+    n = 1
+    while cost(rows + n, nseq + 1) <= 0:
+        n += 1 + n // 50
+    return n
+
+
+def sharing(ctx, ql, Hkv, window, sinks):
+    n = filler(sum(ql), len(ql), Hkv, window, sinks)
+    return (ctx + [n], ql + [n]) if n else (ctx, ql)
+
+
+def wide(bt):
+    return torch.nn.functional.pad(bt, (0, WIDE - bt.shape[1]), value=-1)
 
 
 def codes(kc, vc, per_block, Hkv):
@@ -54,7 +74,8 @@ def attend(q, k64, v64, bt, lim, window, sinks, scale):
 
 def check_rows(out, q, k64, v64, bt, cu, ctx, ql, window, sinks, scale, every=1):
     for b, x in enumerate(ctx):
-        for i in list(range(0, ql[b], every)) + ([ql[b] - 1] if ql[b] else []):
+        step = max(every, ql[b] // 200)
+        for i in list(range(0, ql[b], step)) + ([ql[b] - 1] if ql[b] else []):
             r = int(cu[b]) + i
             want, bound, _, _ = attend(q[r], k64, v64, bt[b], x - ql[b] + i + 1, window, sinks, scale)
             ref.check(out[r], want, bound, f"sequence {b} row {i}")
@@ -72,12 +93,14 @@ def test_rows(heads, window, sinks, per_block, share):
     Hq, Hkv = heads
     ctx = [1, 700, 40, 18, 0, 513, 1100]
     ql = [1, 150, 40, 25, 3, 1, 129]  # a sequence all of whose rows are new; one with more rows than tokens
+    if share:
+        ctx, ql = sharing(ctx, ql, Hkv, window, sinks)
     g, kc, vc, bt, _, _ = pool(Hq + window % 97, ctx, Hkv, D)
     k8, v8, ks, vs, k64, v64 = codes(kc, vc, per_block, Hkv)
     cu = offsets(ql)
     T = int(cu[-1]) + 2  # two rows of no sequence
     q, scale = bf16(g, T, Hq, D, std=2.0), D ** -0.5
-    args = dev(q, k8, v8, ks, vs, wide(bt, T, Hkv) if share else bt, cu, torch.tensor(ctx, dtype=torch.int32))
+    args = dev(q, k8, v8, ks, vs, wide(bt) if share else bt, cu, torch.tensor(ctx, dtype=torch.int32))
     out = torch.full_like(args[0], 7.0)
     first = None
     for _ in range(2):
@@ -95,14 +118,15 @@ def test_few_rows(S, q, x, per_block, share):
     Hq, Hkv = 28, 4
     ctx, ql = [max(1, x - 7 * b % x) for b in range(S)], [q] * S
     ql = [min(a, b) for a, b in zip(ql, ctx)]
+    if share:
+        ctx, ql = sharing(ctx, ql, Hkv, 1 << 30, 0)
     g, kc, vc, bt, _, _ = pool(S + x, ctx, Hkv, D)
     k8, v8, ks, vs, k64, v64 = codes(kc, vc, per_block, Hkv)
     cu = offsets(ql)
     rows = bf16(g, int(cu[-1]), Hq, D, std=2.0)
-    args = dev(rows, k8, v8, ks, vs, wide(bt, len(rows), Hkv) if share else bt, cu, torch.tensor(ctx, dtype=torch.int32))
+    args = dev(rows, k8, v8, ks, vs, wide(bt) if share else bt, cu, torch.tensor(ctx, dtype=torch.int32))
     out = torch.full_like(args[0], NAN)
     call(per_block, out, *args, 1 << 30, 0, D ** -0.5)
-    some = slice(None) if S < 50 else slice(0, None)
     check_rows(out, rows, k64, v64, bt, cu, ctx, ql, 1 << 30, 0, D ** -0.5, 1 if S < 50 else 2)
 
 
@@ -115,25 +139,28 @@ def test_bad_metadata(per_block, share):
     bt[1, 3], bt[1, 18], bt[0, 0] = -1, kc.shape[0], 1 << 30
     k8, v8, ks, vs, k64, v64 = codes(kc, vc, per_block, Hkv)
     q = bf16(g, 12, Hq, D)
-    table = wide(bt, 12, Hkv) if share else bt
+    table = wide(bt) if share else bt
     out = torch.zeros(12, Hq, D, dtype=torch.bfloat16, device=DEV)
     a = dev(q, k8, v8, ks, vs, table)
     i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)
     ql, cu = [4, 5, 3], offsets([4, 5, 3])
     call(per_block, out, *a, cu.to(DEV), i32([100, 300, -5]), 1 << 20, 0, 0.1)
     check_rows(out, q, k64, v64, bt, cu, [100, 300, 0], ql, 1 << 20, 0, 0.1)
+    assert not share or (not filler(12, 3, Hkv, 1 << 20, 0) and not filler(12, 3, Hkv, WIDE * BS - 34, 2))
     for bad in ([0, 90, 4, 12], [5, 3, 2, 1], [-4, 1 << 30, -9, 1 << 20]):
-        call(per_block, out, *a, i32(bad), i32([100, 300, 90]), 50, 2, 0.1)
+        call(per_block, out, *a, i32(bad), i32([100, 300, 90]), 50 if not share else WIDE * BS - 34, 2, 0.1)
     torch.cuda.synchronize()
 
 
 @pytest.mark.parametrize("more", [0, 60])  # cut units: merged by a kernel of their own, or by the last CTA
 @pytest.mark.parametrize("per_block", [False, True])
-@pytest.mark.parametrize("window,share", [(64, True), (350, True), (64, False)])
+@pytest.mark.parametrize("window,share", [(64, True), (350, True), (64, False), (1 << 20, True)])
 def test_nan_codes_of_unseen_tokens_stay_out(window, share, per_block, more):
     """A token with a NaN code reaches the rows that see it and no other row, although rows share its products."""
     Hq, Hkv, sinks = 14, 2, 3
     ctx, ql = [400, 300] + [500] * more, [30, 300] + [2] * more
+    if share:
+        ctx, ql = sharing(ctx, ql, Hkv, window, sinks)
     g, kc, vc, bt, _, _ = pool(41, ctx, Hkv, D)
     for b, ts in {0: [390, 399], 1: [1, 40, 200, 299]}.items():
         for n, t in enumerate(ts):
@@ -144,7 +171,7 @@ def test_nan_codes_of_unseen_tokens_stay_out(window, share, per_block, more):
     cu = offsets(ql)
     q = bf16(g, sum(ql), Hq, D)
     out = torch.full((sum(ql), Hq, D), 7.0, dtype=torch.bfloat16, device=DEV)
-    call(per_block, out, *dev(q, k8, v8, ks, vs, wide(bt, len(q), Hkv) if share else bt, cu, torch.tensor(ctx, dtype=torch.int32)),
+    call(per_block, out, *dev(q, k8, v8, ks, vs, wide(bt) if share else bt, cu, torch.tensor(ctx, dtype=torch.int32)),
          window, sinks, 0.1)
     got = out.cpu()
     for b in range(2):
@@ -173,9 +200,10 @@ def test_scales_of_every_size(share):
     k64 = k8.view(torch.float8_e4m3fn).double() * ks.double()[:, None, :, None]
     v64 = (v8.view(torch.float8_e4m3fn).double() * vs.double()[:, :, None, None])[..., inv].permute(0, 3, 1, 2)
     cu = offsets(ql)
+    assert not filler(20, 1, Hkv, 1 << 20, 0)
     q = bf16(g, 20, Hq, D)
     out = torch.full((20, Hq, D), NAN, dtype=torch.bfloat16, device=DEV)
-    call(True, out, *dev(q, k8, v8, ks, vs, wide(bt, 20, Hkv) if share else bt, cu, torch.tensor(ctx, dtype=torch.int32)),
+    call(True, out, *dev(q, k8, v8, ks, vs, wide(bt) if share else bt, cu, torch.tensor(ctx, dtype=torch.int32)),
          1 << 20, 0, 0.05)
     check_rows(out, q, k64, v64, bt, cu, ctx, ql, 1 << 20, 0, 0.05)
 
@@ -203,18 +231,21 @@ def test_sharp_and_growing_logits(scale, std, share):
         kc[bt[0, j]] = (kc[bt[0, j]].float() * (0.2 + j / 60)).to(torch.bfloat16)
     k8, v8, ks, vs, k64, v64 = codes(kc, vc, True, Hkv)
     q, cu = bf16(g, 9, Hq, D, std=std), offsets(ql)
+    assert not filler(9, 1, Hkv, 1 << 20, 0)
     out = torch.full((9, Hq, D), NAN, dtype=torch.bfloat16, device=DEV)
-    call(True, out, *dev(q, k8, v8, ks, vs, wide(bt, 9, Hkv) if share else bt, cu, torch.tensor(ctx, dtype=torch.int32)),
+    call(True, out, *dev(q, k8, v8, ks, vs, wide(bt) if share else bt, cu, torch.tensor(ctx, dtype=torch.int32)),
          1 << 20, 0, scale)
     check_rows(out, q, k64, v64, bt, cu, ctx, ql, 1 << 20, 0, scale)
 
 
-def test_other_stream_and_graph():
+@pytest.mark.parametrize("share", [False, True])
+def test_other_stream_and_graph(share):
     """On a stream of its own, then replayed from a graph with other lengths in the same buffers."""
     Hq, Hkv, S = 28, 4, 5
     lens = [[900, 30, 500, 77, 1200], [100, 800, 3, 1100, 640]]
     ql = [40, 3, 100, 1, 9]
     ql2 = [40, 3, 3, 98, 9]
+    assert not filler(153, 5, Hkv, 1 << 30, 0)
     runs = []
     for n, (ctx, rows) in enumerate(zip(lens, (ql, ql2))):
         g, kc, vc, bt, _, _ = pool(50 + n, ctx, Hkv, D, extra=220 - sum(-(-x // BS) for x in ctx))
@@ -222,6 +253,8 @@ def test_other_stream_and_graph():
         runs.append((ctx, rows, bf16(g, sum(rows), Hq, D), bt, offsets(rows), codes(kc, vc, False, Hkv)))
     bufs = dev(runs[0][2], *runs[0][5][:4], runs[0][3], runs[0][4], torch.tensor(lens[0], dtype=torch.int32))
     out = torch.empty_like(bufs[0])
+    if share:
+        bufs[5] = wide(bufs[5]).contiguous()
     go = lambda: call(False, out, *bufs, 1 << 30, 0, 0.0884)
     st = torch.cuda.Stream()
     st.wait_stream(torch.cuda.current_stream())
@@ -232,7 +265,7 @@ def test_other_stream_and_graph():
     with torch.cuda.graph(graph):
         go()
     for ctx, rows, q, bt, cu, c in (*runs, runs[0]):
-        for buf, new in zip(bufs, (q, *c[:4], bt, cu, torch.tensor(ctx, dtype=torch.int32))):
+        for buf, new in zip(bufs, (q, *c[:4], wide(bt) if share else bt, cu, torch.tensor(ctx, dtype=torch.int32))):
             buf.copy_(new)
         out.fill_(NAN)
         graph.replay()
