@@ -1027,17 +1027,19 @@ bool reads_each(const SubsetArgs &a, int D) {
 // on 500 (64 MB) 16.6 and 14.8.
 //
 // E4M3: by both kernels' times in microseconds. A row by itself takes 3.9e-5 per token and KV head (6.6 TB/s over all SMs,
-// the latency of its warps, not L2); row tiles read the tokens of a sequence once, 1.15e-4 per token and KV head while its
-// rows fit one row tile, with 0.05 for a unit's begin and end and 18 to start (code that is fetched first, merges). Each row and
-// row tiles, 28 / 4 heads: 32 sequences of 2 rows on 500 tokens 16.1 and 18.5 us, of 6 rows 24.3 and 18.7 (each by this
-// rule), on 4000 of 3 rows 63 and 72, of 6 rows 111 and 75, on 16000 of 2 rows 142 and 197, of 4 rows 289 and 199; 128 of 2 rows on
-// 4000 tokens 166 and 232, of 4 rows 314 and 236; one of 8 rows on 16000 26 and 38, of 36 rows 80 and 49.
+// the latency of its warps). Row tiles read the tokens of a sequence once, 1.4e-4 per token and KV head while its rows
+// fit one row tile, and take 20 to start and to merge what is cut where there are fewer units than half the SMs, else 10. Each row
+// and row tiles, 28 / 4 heads: one sequence of 8 rows on 16000 tokens 26 and 37 us, of 16 rows 45 and 38; 4 of 4 rows on 16000 45 and
+// 48, of 6 rows 79 and 47; 32 of 4 rows on 500 20 and 18, of 8 rows 29 and 18, of 3 rows on 4000 63 and 71 (of 1 to 6 rows, the
+// cache not in L2, 49 and 82), of 6 rows 111 and 74, of 2 rows on 16000 142 and 201, of 3 rows 237 and 201 (each by this
+// rule), of 4 rows 289 and 202; 128 of 2 rows on 4000 166 and 229, of 4 rows 314 and 232.
 constexpr int64_t kEachReadsMany = int64_t(56) << 20;
 
 bool rows_each(const SubsetArgs &a, int D, CacheKind kind, int sms) {
     const double seen = std::min(double(a.MBS) * kBlockSize, double(a.window) + a.sinks + 2 * kBlockSize);
     const int64_t segs = int64_t(a.rows) * a.Hkv;
-    if (kind != kCacheBf16) return 3.9e-5 * segs * seen <= 18 + double(a.nseq) * a.Hkv * (1.15e-4 * seen + 0.05);
+    const int64_t units = int64_t(a.nseq) * a.Hkv;
+    if (kind != kCacheBf16) return 3.9e-5 * segs * seen <= (2 * units > sms ? 10 : 20) + 1.4e-4 * units * seen;
     return segs * seen * D * 4 <= double(segs <= sms ? kEachReads : kEachReadsMany);
 }
 

@@ -353,48 +353,73 @@ __device__ __forceinline__ uint4 load_shared16(uint32_t src) {
     return v;
 }
 
-// A query row of 128 bf16 values for products with E4M3 codes: x = 2^k (hi + lo), hi the nearest E4M3 value of x / 2^k (the
-// largest is in [128, 256)) and lo that of what is left. The eight bits of a bf16 value are four and four: exact for values of
-// at least 2^-10 of the row's largest, the others are off by at most 2^-18 of it. Written to rows `to` (hi) and `to` +
-// next (lo), 16-byte chunks swizzled by sw; returns 2^k (1 for a row of zeros or none; NaN for one that is not finite).
-__device__ __forceinline__ float split_query(const uint16_t *q, uint8_t *to, int next, int sw) {
-    uint4 v[16];
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = q ? __ldg(reinterpret_cast<const uint4 *>(q) + i) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m = max(m, max(w[e] & 0x7fff0000u, (w[e] << 16) & 0x7fff0000u));
+__device__ __forceinline__ void store_shared16(uint32_t dst, const uint4 &v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// 16 bytes to shared memory, zeros where there are none
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool any) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(any ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// A warp's 32 query rows of 128 bf16 values, for products with E4M3 codes: x = 2^k (hi + lo), hi the nearest E4M3 value of
+// x / 2^k (the row's largest is in [128, 256)) and lo that of what is left. The eight bits of a bf16 value are four and four:
+// exact for values of at least 2^-10 of the row's largest, the others are off by at most 2^-18 of it. Lane r has the offset of
+// row r in q, < 0: a row of zeros. Written to rows 0 .. 31 at `to` (hi) and `to` + next (lo), 128 bytes each, 16-byte chunks
+// swizzled by the row; returns 2^k of the lane's row (1 for a row of zeros; NaN for one that is not finite).
+// The rows first come to where their parts go, then eight lanes convert a row. Code that runs once per unit has to be fetched
+// first: with a lane per row, unrolled over its registers, 13300 cycles at a CTA's begin instead of 8800. A function of its own:
+// within the kernel it changed how the softmax around it was compiled (long prompt chunks 622 us, inlined 685).
+__device__ __noinline__ float split_queries(const uint16_t *q, int64_t offset, uint32_t to, uint32_t next, int lane) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {  // chunk 16 (2 i + lane / 16) + lane % 16
+        const int r = 2 * i + (lane >> 4), c = lane & 15;
+        const int64_t from = __shfl_sync(0xffffffffu, offset, r);
+        cp_async16(to + r * 128 + (c >> 3) * next + (((c & 7) ^ (r & 7)) << 4), q + max(from, int64_t(0)) + c * 8, from >= 0);
     }
-    const int k = m == 0 ? 0 : max(int(m >> 23) - 127 - 7, -119);
-    const float inv = __uint_as_float(uint32_t(127 - k) << 23);
+    cp_async_wait_all();
+    __syncwarp();
+    float mine = 1.f;
+    const int c = lane & 7;  // 16 values
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + (lane >> 3);
+        const uint32_t row = to + r * 128, at = row + (c >> 2) * next;
+        const uint4 v0 = load_shared16(at + (((2 * c & 7) ^ (r & 7)) << 4)), v1 = load_shared16(at + (((2 * c & 7) + 1 ^ (r & 7)) << 4));
+        const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        uint32_t m = 0;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {  // 16 values
+        for (int e = 0; e < 8; ++e) m = max(m, max(w[e] & 0x7fff0000u, (w[e] << 16) & 0x7fff0000u));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const int k = m == 0 ? 0 : max(int(m >> 23) - 127 - 7, -119);
+        const float inv = __uint_as_float(uint32_t(127 - k) << 23);
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const uint4 &y = v[2 * c + e / 2];
-            const uint32_t w[2] = {e & 1 ? y.z : y.x, e & 1 ? y.w : y.y};
             uint32_t h = 0, l = 0;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float a = bf16_lo(w[j]) * inv, b = bf16_hi(w[j]) * inv;
+                const float a = bf16_lo(w[2 * e + j]) * inv, b = bf16_hi(w[2 * e + j]) * inv;
                 const uint32_t p = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
                 const uint32_t f = e4m3x2_to_f16x2(p);
-                const uint32_t r = __nv_cvt_float2_to_fp8x2(make_float2(a - f16_lo(f), b - f16_hi(f)), __NV_SATFINITE, __NV_E4M3);
+                const uint32_t s = __nv_cvt_float2_to_fp8x2(make_float2(a - f16_lo(f), b - f16_hi(f)), __NV_SATFINITE, __NV_E4M3);
                 h |= p << (16 * j);
-                l |= r << (16 * j);
+                l |= s << (16 * j);
             }
             hi[e] = h;
             lo[e] = l;
         }
-        uint8_t *at = to + ((c ^ sw) << 4);
-        *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4 *>(at + next) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        __syncwarp();  // the row has been read
+        store_shared16(row + ((c ^ (r & 7)) << 4), make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        store_shared16(row + next + ((c ^ (r & 7)) << 4), make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        const float f = m >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(uint32_t(k + 127) << 23);
+        const float of = __shfl_sync(0xffffffffu, f, (lane & 3) * 8);
+        if ((lane >> 2) == i) mine = of;
     }
-    return m >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(uint32_t(k + 127) << 23);
+    return mine;
 }
 
 template <int D, bool PREFIX, CacheKind KIND>
@@ -915,6 +940,7 @@ __global__ void __launch_bounds__(kRowWarps<KIND> * 32, 1)
         const int w = warp >> 2, row = tid & 127;
         const uint32_t lane_base = uint32_t(warp & 3) << 21;  // this warp's 32 of the 128 lanes
         const uint32_t ts = tmem + lane_base + 256 * w, to = ts + 128;
+        const uint32_t queries = base + w * C::TILE + (warp & 3) * 4096;  // of this warp's rows
         const int i = row / G, h = row - i * G;
         uint32_t ph = 0, tile_no = 0, units = 0, merges = 0, pubs = 0;
         if (!PREFIX && a.cuts && tid == 0) a.cuts[blockIdx.x].pieces = 0;  // no unit is cut so far
@@ -933,12 +959,12 @@ __global__ void __launch_bounds__(kRowWarps<KIND> * 32, 1)
                 }
                 const int lim = !act ? 0 : PREFIX ? x.lim1 : max(base + ir, 0);
                 const int S1 = min(work.sinks(), lim), lo = max(S1, work.lower(lim));
-                // E4M3: this thread's query row, as two parts (the last unit's products are complete), and the factor of
+                // E4M3: the query rows, as two parts (the last unit's products are complete), and the factor of
                 // its logits; a scale per KV head goes to the logits and to the output
                 float scale_log2 = a.scale_log2;
                 if constexpr (F8) {
-                    const uint16_t *qrow = a.q + (int64_t(x.r0 + ir) * a.Hq + x.kvh * G + h) * D;
-                    scale_log2 *= split_query(act && lim > 0 ? qrow : nullptr, bp + w * C::TILE + row * 128, C::HALF, row & 7);
+                    const int64_t from = act && lim > 0 ? (int64_t(x.r0 + ir) * a.Hq + x.kvh * G + h) * D : -1;
+                    scale_log2 *= split_queries(a.q, from, queries, C::HALF, lane);
                     if (!PSC) scale_log2 *= __ldg(a.k_scale + x.kvh);
                     fence_proxy_async();
                     mbar_arrive(q_full + 8 * w);

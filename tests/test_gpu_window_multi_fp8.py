@@ -31,7 +31,7 @@ def filler(rows, nseq, Hkv, window, sinks):
     """Rows of a further prompt that make the call share its reads between rows: the call's rule is by the rows, the
     sequences and the most tokens that a row can see (the window, or the width of the tables)."""
     seen = min(WIDE * BS, window + sinks + 2 * BS)
-    cost = lambda n, s: 3.9e-5 * n * Hkv * seen - 18 - s * Hkv * (1.15e-4 * seen + 0.05)
+    cost = lambda n, s: 3.9e-5 * n * Hkv * seen - 20 - 1.4e-4 * s * Hkv * seen
     if cost(rows, nseq) > 0:
         return 0
     n = 1
@@ -138,15 +138,15 @@ def test_bad_metadata(per_block, share):
     g, kc, vc, bt, _, _ = pool(5, [100, 300, 90], Hkv, D)
     bt[1, 3], bt[1, 18], bt[0, 0] = -1, kc.shape[0], 1 << 30
     k8, v8, ks, vs, k64, v64 = codes(kc, vc, per_block, Hkv)
-    q = bf16(g, 12, Hq, D)
+    q = bf16(g, 24, Hq, D)
     table = wide(bt) if share else bt
-    out = torch.zeros(12, Hq, D, dtype=torch.bfloat16, device=DEV)
+    out = torch.zeros(24, Hq, D, dtype=torch.bfloat16, device=DEV)
     a = dev(q, k8, v8, ks, vs, table)
     i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)
-    ql, cu = [4, 5, 3], offsets([4, 5, 3])
+    ql, cu = [8, 10, 6], offsets([8, 10, 6])
     call(per_block, out, *a, cu.to(DEV), i32([100, 300, -5]), 1 << 20, 0, 0.1)
     check_rows(out, q, k64, v64, bt, cu, [100, 300, 0], ql, 1 << 20, 0, 0.1)
-    assert not share or (not filler(12, 3, Hkv, 1 << 20, 0) and not filler(12, 3, Hkv, WIDE * BS - 34, 2))
+    assert not share or (not filler(24, 3, Hkv, 1 << 20, 0) and not filler(24, 3, Hkv, WIDE * BS - 34, 2))
     for bad in ([0, 90, 4, 12], [5, 3, 2, 1], [-4, 1 << 30, -9, 1 << 20]):
         call(per_block, out, *a, i32(bad), i32([100, 300, 90]), 50 if not share else WIDE * BS - 34, 2, 0.1)
     torch.cuda.synchronize()
