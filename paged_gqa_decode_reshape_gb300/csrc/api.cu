@@ -1373,7 +1373,10 @@ int run_rope(RopeArgs a, const RopeShape &s, RopeCache cache, int interleaved, v
     a.naxes = s.axes;
     a.NB = s.NB;
     if (s.axes == 1) a.axis = nullptr;
-    const cudaError_t e = launch_norm_rope(a, s.D, interleaved != 0, cache, static_cast<cudaStream_t>(stream));
+    DecodeGeometry geo;
+    cudaError_t e = decode_geometry(s.D, &geo);
+    if (e == cudaSuccess)  // geo.grid: one CTA per SM
+        e = launch_norm_rope(a, s.D, interleaved != 0, cache, geo.grid, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 

@@ -52,6 +52,6 @@ struct RopeArgs {
 
 enum RopeCache { kRopeNone = 0, kRopeBf16 = 1, kRopeE4m3 = 2 };
 
-cudaError_t launch_norm_rope(const RopeArgs &a, int head_dim, bool interleaved, RopeCache cache, cudaStream_t stream);
+cudaError_t launch_norm_rope(const RopeArgs &a, int head_dim, bool interleaved, RopeCache cache, int sms, cudaStream_t stream);
 
 }  // namespace pa

@@ -157,9 +157,18 @@ def test_cache_fp8(heads, T):
     assert torch.equal(got[rest], kc.view(-1, Hkv, D)[rest])
 
 
-def test_in_place_on_one_projection():
-    """q_out and k_out are the parts of the projection themselves; the rest of it stays."""
-    T, Hq, Hkv, D = 300, 12, 4, 128
+@pytest.mark.parametrize("heads,T", [((1, 1, 128), 4096), ((2, 2, 128), 5003), ((5, 1, 64), 4500), ((9, 3, 64), 3001),
+                                     ((28, 4, 128), 900), ((3, 2, 128), 2500), ((40, 8, 128), 2600)])
+def test_many_tokens(heads, T):
+    """From about 4096 steps of heads on, where warps go over ranges of them; tokens of one step and of many."""
+    for A, interleaved in ((1, False), (3, True), (4, False), (1, True)):
+        test_norm_rope(heads, T, A, True, interleaved)
+    test_cache(heads, T, True)
+
+
+@pytest.mark.parametrize("T", [300, 1500])
+def test_in_place_on_one_projection(T):
+    Hq, Hkv, D = 12, 4, 128
     q, k, v, qw, kw, table, pos, _ = make(3, T, Hq, Hkv, D, D)
     whole = torch.empty(0, dtype=q.dtype).set_(q.untyped_storage()).view(T, Hq + 2 * Hkv + 1, D)
     x = whole.to(DEV)
