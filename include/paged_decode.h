@@ -710,7 +710,12 @@ PA_API int pa_decode_window_multi(pa_bf16 *out, const pa_bf16 *query, const pa_b
 /* pa_decode_window_multi over an 8-bit cache: prompt chunks and speculative
  * rows read K and V as pa_decode_fp8 (scales per KV head) or pa_decode_fp8_block
  * (powers of two per block) do. head_dim 128. With window >= every context a
- * row sees all tokens before it. Workspace: pa_decode_window_multi_workspace_size. */
+ * row sees all tokens before it. Workspace: pa_decode_window_multi_workspace_size.
+ * Queries: small calls round them to f16 (values from 65520 on become infinite,
+ * those below 2^-14 lose bits); calls whose rows share their reads take each
+ * head row as two E4M3 parts and a power of two, exact for values of at least
+ * 2^-10 of the row's largest, the others off by at most 2^-18 of it, and a row
+ * with an element that is not finite gets NaN. */
 PA_API int pa_decode_window_multi_fp8(pa_bf16 *out, const pa_bf16 *query, const pa_e4m3 *key_cache,
                                       const pa_e4m3 *value_cache, const float *k_scale, const float *v_scale,
                                       const int32_t *block_tables, int max_blocks_per_seq,

@@ -10,7 +10,9 @@
 // in fp32, rounded once to bf16 or (keys and values of an 8-bit cache) to the E4M3
 // code of the value over its head's scale.
 //
-// Bound by HBM: a head is read and written once, 8 D flops for 4 D bytes.
+// Bound by HBM: a head is read and written once, 8 D flops for 4 D bytes. Measured (28 / 4 heads of 128): 8191 tokens
+// (156 MB) 28.7 us = 5.4 TB/s, 80 % of the measured copy rate; one token 1.8 us, 128 tokens over the 8-bit cache 3.0:
+// a launch and two dependent reads (position, angles).
 //
 //  * D / 16 lanes per head, each with two chunks of 8 dims whose rotation stays
 //    in the lane (chunks c and c + R / 16; the unrotated ones two by two): 16-byte
@@ -315,7 +317,10 @@ __global__ void __launch_bounds__(kRopeWarps * 32) norm_rope_kernel(const RopeAr
 // ---- many tokens: a warp per range of steps, kRingStages of them on their way in shared memory
 //
 // The heads come by asynchronous copies that hold no registers, 8 KB per warp and 128 KB per SM in flight, angles and
-// slot of a token beside the first of its steps, its position a token ahead. The 8-bit V is for warps of its own.
+// slot of a token beside the first of its steps, its position a token ahead. The 8-bit V is for warps of its own. What is left
+// is issue: two thirds of the slots (8191 tokens 28.7 us; 12 warps 30.8, 20 warps of 6 stages, whose registers spill, 35.4;
+// three steps per warp, each loading its own to registers, 33.4). Ring and a warp per step, 28 / 4 heads of 128: 300 tokens 3.4
+// and 3.0 us, 400 3.5 and 3.4, 500 3.6 and 4.2, 1000 4.9 and 6.5; 8-bit 400 5.5 and 4.9, 500 5.4 and 5.6, 1000 6.1 and 9.2.
 constexpr int kRingWarps = 16, kRingStages = 8;
 // E4M3: warps of a CTA for V, beside the others (one after the other in every warp: 8191 tokens 38.2 us)
 constexpr int kRingV8Warps = 4;

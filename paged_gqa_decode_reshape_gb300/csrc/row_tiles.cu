@@ -46,12 +46,12 @@
 //    is not 0 if V is not finite: a row whose result is not finite, in a unit with
 //    such a token, is computed again, over its own tokens only, at the CTA's end.
 //  * E4M3 caches (query rows over windows): S = Q K^T takes K's codes as they are, by products of E4M3 inputs: a bf16
-//    query is two E4M3 parts (split_query, by the softmax warps: a thread per row), 2 x 128 codes deep at twice the
+//    query is two E4M3 parts (split_queries, by the softmax warps), 2 x 128 codes deep at twice the
 //    rate, from half as much of K. P V takes bf16: P in E4M3 would lose small weights. V's codes become bf16 on
 //    the way: two warps copy blocks of codes into a ring, eight convert them and lay them down dim by token, as the
 //    cache has them, with the contraction over tokens contiguous. A scale per KV head goes to the logits and the output; a
 //    scale per block to the block's 16 logits and, in the conversion, to its V. Chunks of 517 to 2048 rows behind 9000 to
-//    16000 tokens 622 us = 1.28 PFLOP/s, the rate of the bf16 cache. On the way there: K and V converted, by loads to
+//    16000 tokens 625 us = 1.28 PFLOP/s, the rate of the bf16 cache. On the way there: K and V converted, by loads to
 //    registers 1615 us (a loop unrolled over a half step runs out of instruction cache at 7 cycles an instruction), by
 //    asynchronous copies and rolled loops 790; V alone converted, one warp issuing its copies (330 cycles each) 830.
 //  * Units cut between CTAs leave (O, m, l) per row and piece in the workspace;

@@ -238,6 +238,38 @@ def test_sharp_and_growing_logits(scale, std, share):
     check_rows(out, q, k64, v64, bt, cu, ctx, ql, 1 << 20, 0, scale)
 
 
+@pytest.mark.parametrize("power", [-60, 0, 60])
+def test_queries_of_every_size(power):
+    """Shared reads: a query row keeps its values whatever their power of two (as two E4M3 parts and that power), those of
+    less than 2^-10 of its largest to within 2^-18 of it; a row that is not finite gives NaN, the ones beside it their own."""
+    Hq, Hkv, ctx, ql = 8, 2, [1000], [12]
+    assert not filler(12, 1, Hkv, 1 << 20, 0)
+    g, kc, vc, bt, _, _ = pool(77, ctx, Hkv, D)
+    k8, v8, ks, vs, k64, v64 = codes(kc, vc, False, Hkv)
+    q, cu = bf16(g, 12, Hq, D), offsets(ql)
+    q[:, :, 1::2] *= 2.0 ** -12  # bf16, a power of two: exact
+    q[3, :, 5:9] *= 2.0 ** -30
+    q = (q.float() * 2.0 ** power).to(torch.bfloat16)
+    q[4, 1, 7], q[9, 6, 0] = NAN, float("inf")
+    out = torch.zeros((12, Hq, D), dtype=torch.bfloat16, device=DEV)
+    scale = 0.1 * 2.0 ** -power
+    call(False, out, *dev(q, k8, v8, ks, vs, wide(bt), cu, torch.tensor(ctx, dtype=torch.int32)), 1 << 20, 0, scale)
+    got = out.cpu().double()
+    assert torch.isnan(got[4, 1]).all() and torch.isnan(got[9, 6]).all()
+    for i in range(12):
+        heads = [h for h in range(Hq) if (i, h) not in ((4, 1), (9, 6))]
+        rows = torch.nan_to_num(q[i].double(), nan=0.0, posinf=0.0)
+        t = torch.arange(1000 - 12 + i + 1)
+        k, v = ref.rows_at(k64, bt[0], t)[0], ref.rows_at(v64, bt[0], t)[0]
+        # a logit is off by at most e = scale 2^-18 max |q| sum_d |k_d|; weights then change by a factor within e^(+-2 e) in all,
+        # and their average of values by at most 2 e max |v| (e is below 0.01 here)
+        want, bound, _, _ = ref.attend(rows, k, v, scale, 2.0 ** -8, 2.0 ** -11)
+        off = scale * 2.0 ** -18 * rows.abs().amax(1) * k.abs().sum(2).amax(0).repeat_interleave(Hq // Hkv)  # of a logit
+        more = 2 * off[:, None] * v.abs().amax(0).repeat_interleave(Hq // Hkv, 0)  # of an average of values
+        err = (got[i] - want).abs() - bound - more
+        assert (err[heads] <= 0).all(), f"row {i}"
+
+
 @pytest.mark.parametrize("share", [False, True])
 def test_other_stream_and_graph(share):
     """On a stream of its own, then replayed from a graph with other lengths in the same buffers."""
