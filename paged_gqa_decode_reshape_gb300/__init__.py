@@ -1513,9 +1513,8 @@ def _heads(t: torch.Tensor, name: str, rows: Optional[int] = None, device=None):
     try:  # the usual case first
         if t.dtype is torch.bfloat16 and t.ndim == 3:
             (T, H, D), (row, head, one), d = t.shape, t.stride(), t.get_device()
-            if (T > 1 and one == 1 and head == D and d >= 0 and (device is None or d == device.index)
-                    and (rows is None or T == rows)):
-                return H, D, row
+            if one == 1 and head == D and (d >= 0 if device is None else d == device.index) and (rows is None or T == rows):
+                return H, D, row if T > 1 else H * D  # one row: its stride says nothing
     except AttributeError:
         pass
     if not isinstance(t, torch.Tensor):
@@ -1537,7 +1536,10 @@ def _heads(t: torch.Tensor, name: str, rows: Optional[int] = None, device=None):
 
 def _fits(t, dtype, ndim, d) -> bool:
     """The usual case of _need: a contiguous tensor of this type and rank on device number d."""
-    return t.dtype is dtype and t.ndim == ndim and t.get_device() == d and t.is_contiguous()
+    try:
+        return t.dtype is dtype and t.ndim == ndim and t.get_device() == d and t.is_contiguous()
+    except AttributeError:
+        return False
 
 
 def _rope(name, q_out, k_out, query, key, value, cos_sin, positions, q_weight, k_weight, eps, axes, interleaved,
@@ -1558,55 +1560,57 @@ def _rope(name, q_out, k_out, query, key, value, cos_sin, positions, q_weight, k
         if h != Hkv or d2 != D:
             raise ValueError("k_out must have key's shape")
         ko = k_out.data_ptr()
-    if not (isinstance(cos_sin, torch.Tensor) and _fits(cos_sin, torch.float32, 2, d)):
+    bf16, i32 = torch.bfloat16, torch.int32
+    if not _fits(cos_sin, torch.float32, 2, d):
         _need(cos_sin, "cos_sin", torch.float32, 2, dev)
     P, R = cos_sin.shape
     qw = kw = ax = None
     if q_weight is not None:
-        _need(q_weight, "q_weight", torch.bfloat16, 1, dev)
+        if not _fits(q_weight, bf16, 1, d):
+            _need(q_weight, "q_weight", bf16, 1, dev)
         if q_weight.numel() != D:
             raise ValueError("q_weight must be [head_dim]")
         qw = q_weight.data_ptr()
     if k_weight is not None:
-        _need(k_weight, "k_weight", torch.bfloat16, 1, dev)
+        if not _fits(k_weight, bf16, 1, d):
+            _need(k_weight, "k_weight", bf16, 1, dev)
         if k_weight.numel() != D:
             raise ValueError("k_weight must be [head_dim]")
         kw = k_weight.data_ptr()
     A = 1
-    if axes is None:
-        _need(positions, "positions", torch.int32, 1, dev)
-    else:
-        _need(positions, "positions", torch.int32, 2, dev)
+    if not _fits(positions, i32, 1 if axes is None else 2, d):
+        _need(positions, "positions", i32, 1 if axes is None else 2, dev)
+    if axes is not None:
         A = positions.shape[0]
-        _need(axes, "axes", torch.int32, 1, dev)
+        if not _fits(axes, i32, 1, d):
+            _need(axes, "axes", i32, 1, dev)
         if axes.numel() * 2 != R:
             raise ValueError("axes must be [rotary_dim / 2]")
         ax = axes.data_ptr()
     if positions.numel() != A * T:
         raise ValueError("positions must have a column per token")
-    head = q_out.data_ptr(), qos, ko, kos, query.data_ptr(), qs, key.data_ptr(), ks
-    tail = (qw, kw, eps, cos_sin.data_ptr(), P, R, positions.data_ptr(), ax, A, 1 if interleaved else 0)
     if cache is None:
-        _run(name, dev, (*head, *tail, T, Hq, Hkv, D))
+        _run(name, dev, (q_out.data_ptr(), qos, ko, kos, query.data_ptr(), qs, key.data_ptr(), ks, qw, kw, eps,
+                         cos_sin.data_ptr(), P, R, positions.data_ptr(), ax, A, 1 if interleaved else 0, T, Hq, Hkv, D))
         return q_out
     h, d2, vs = _heads(value, "value", T, dev)
     if h != Hkv or d2 != D:
         raise ValueError("value must have key's shape")
     kc, vc, slots, *scales = cache
-    dtype = torch.uint8 if scales else torch.bfloat16
-    _need(kc, "key_cache", dtype, 4, dev)
-    _need(vc, "value_cache", dtype, 4, dev)
-    _need(slots, "slot_mapping", torch.int64, 1, dev)
+    dtype = torch.uint8 if scales else bf16
+    if not (_fits(kc, dtype, 4, d) and _fits(vc, dtype, 4, d) and _fits(slots, torch.int64, 1, d)):
+        _need(kc, "key_cache", dtype, 4, dev)
+        _need(vc, "value_cache", dtype, 4, dev)
+        _need(slots, "slot_mapping", torch.int64, 1, dev)
     NB, BS, h, d2 = kc.shape
     if h != Hkv or d2 != D or vc.shape != ((NB, h, D, BS) if scales else kc.shape) or slots.numel() != T:
         raise ValueError("shape mismatch between key/value, slot_mapping and the caches")
     if scales:
         _scales(*scales, Hkv, dev)
-        _run(name, dev, (*head, value.data_ptr(), vs, *tail, kc.data_ptr(), vc.data_ptr(), scales[0].data_ptr(),
-                         scales[1].data_ptr(), slots.data_ptr(), T, Hq, Hkv, D, BS, NB))
-    else:
-        _run(name, dev, (*head, value.data_ptr(), vs, *tail, kc.data_ptr(), vc.data_ptr(), slots.data_ptr(), T, Hq,
-                         Hkv, D, BS, NB))
+        scales = scales[0].data_ptr(), scales[1].data_ptr()
+    _run(name, dev, (q_out.data_ptr(), qos, ko, kos, query.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs, qw, kw,
+                     eps, cos_sin.data_ptr(), P, R, positions.data_ptr(), ax, A, 1 if interleaved else 0, kc.data_ptr(),
+                     vc.data_ptr(), *scales, slots.data_ptr(), T, Hq, Hkv, D, BS, NB))
     return q_out
 
 
