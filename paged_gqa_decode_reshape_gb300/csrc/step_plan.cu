@@ -10,7 +10,7 @@
 //
 // Bound by latency: the bytes are few, their reads depend on each other (lengths, prefix sums over the batch, free blocks,
 // tables, slots). So one CTA with the sequences in its registers: 16 sequences of a token each 4.1 us, 256 with 9 prompts
-// among them 6.4, 64 prompts of 517 to 16000 rows 11.8 (its rows by a second launch). Releases by one CTA or a cluster: the
+// among them 7.0, 64 prompts of 517 to 16000 rows 11.8 (its rows by a second launch). Releases by one CTA or a cluster: the
 // rejected tokens of 128 sequences 4.8 us, 81000 blocks of 512 sequences 8.6.
 #include "common.cuh"
 #include "kernels.h"
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, bo
                    tid, kPlanThreads);
 }
 
-// Positions and slots of many rows, from what plan_kernel wrote: beyond the 1024 rows that its threads write one each.
+// Positions and slots of many rows, from what plan_kernel wrote.
 constexpr int kRowThreads = 1024;
 
 __global__ void __launch_bounds__(kRowThreads) plan_rows_kernel(const PlanArgs a) {
@@ -303,8 +303,14 @@ __global__ void __launch_bounds__(kPlanThreads) release_kernel(const ReleaseArgs
 
 // Neither kernel lets the next one start early: what they write (lengths, tables, row
 // offsets) is what the attention calls read before they wait for their predecessor.
+//
+// Up to kRowsHere rows are written by the planning CTA itself, else by a second launch, which costs the host 2.5 us. Here and
+// by a second launch (GPU time): 2031 rows of 250 sequences 5.2 and 6.3 us, 2546 of 256 with 9 prompts 7.0 and 6.3, 3256 of 256
+// 4.8 and 5.5.
+constexpr int kRowsHere = 4 * kPlanThreads;
+
 cudaError_t launch_plan(const PlanArgs &a, cudaStream_t stream) {
-    const bool rows_too = a.T <= kPlanThreads;
+    const bool rows_too = a.T <= kRowsHere;
     const size_t smem = (4 * size_t(a.B) + 1) * 4;
     cudaError_t e = smem_once(reinterpret_cast<const void *>(plan_kernel), (4 * size_t(kMaxBatch) + 1) * 4);
     if (e == cudaSuccess) e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), smem, stream, a, rows_too);

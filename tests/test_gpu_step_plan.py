@@ -65,6 +65,7 @@ def same(got, want, names=NAMES):
     ([0], [1], 0), ([15], [1], 0), ([16], [1], 0), ([17], [0], 1), ([0, 0, 0], [0, 0, 0], 2),
     ([5, 0, 31, 100, 16], [1, 17, 1, 0, 33], 0), ([1, 2, 3], [-4, 2, 5000], 3),
     ([700, 0, 33] * 40, [1, 0, 3] * 40, 17), ([9] * 1025, [1] * 1025, 0), ([0, 16] * 2048, [1, 2] * 2048, 5),
+    ([7, 0, 90, 16], [1024] * 4, 0), ([7, 0, 90, 16], [1024] * 4, 1), ([300] * 200, [1] * 199 + [2300], 8),
     ([100, 0, 4], [6000, 9000, 1], 100), ([0] * 3000, [0] * 2999 + [20000], 0),
 ])
 def test_plan(lens, q, pad, in_place):
