@@ -12,7 +12,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
+#include <mutex>
+#include <utility>
+#include <vector>
 
 namespace pa {
 
@@ -484,58 +486,19 @@ __device__ __forceinline__ void cta_topk_emit(KeyOf key_of, int n, uint32_t thr,
     __syncthreads();  // red may be reused by the caller
 }
 
-// Host side: what was done per (device, kernel). Allocates nothing and throws nothing: it runs below C entry points. Beyond
-// its devices and kernels nothing is noted, and the caller does it again.
-struct DoneOnce {
-    static constexpr int kDevices = 64, kKernels = 128;
-    std::atomic<const void *> at[kDevices][kKernels];
-
-    // the slot that holds the kernel, or the free one to note it in (else null)
-    std::atomic<const void *> *find(int dev, const void *kernel, bool &done) noexcept {
-        done = false;
-        if (dev < 0 || dev >= kDevices) return nullptr;
-        const unsigned h = unsigned(reinterpret_cast<uintptr_t>(kernel) >> 4) * 2654435761u >> 25;
-        for (unsigned i = 0; i < kKernels; ++i) {
-            std::atomic<const void *> &s = at[dev][(h + i) % kKernels];
-            const void *k = s.load(std::memory_order_acquire);
-            done = k == kernel;
-            if (done || !k) return &s;
-        }
-        return nullptr;
-    }
-    // a slot that another thread took first is left to it: the kernel is noted at its next call
-    static void note(std::atomic<const void *> *slot, const void *kernel) noexcept {
-        const void *none = nullptr;
-        if (slot) slot->compare_exchange_strong(none, kernel, std::memory_order_acq_rel);
-    }
-};
-
 // Host side: ask once per (device, kernel) for the largest shared-memory
 // carveout, the split the decode kernel needs, so that consecutive kernels of
 // the library never make the SMs reconfigure between them.
-inline void carveout_once(const void *kernel) noexcept {
-    static DoneOnce once;
+inline void carveout_once(const void *kernel) {
+    static std::mutex mu;
+    static std::vector<std::pair<int, const void *>> done;
     int dev = 0;
-    bool done;
     if (cudaGetDevice(&dev) != cudaSuccess) return;
-    std::atomic<const void *> *slot = once.find(dev, kernel, done);
-    if (done) return;
+    std::lock_guard<std::mutex> lock(mu);
+    for (const auto &d : done)
+        if (d.first == dev && d.second == kernel) return;
     cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-    DoneOnce::note(slot, kernel);
-}
-
-// Host side: a kernel's limit of dynamic shared memory, set once per device.
-inline cudaError_t smem_once(const void *kernel, size_t bytes) noexcept {
-    static DoneOnce once;
-    int dev = 0;
-    bool done;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    std::atomic<const void *> *slot = once.find(dev, kernel, done);
-    if (done) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
-    if (e == cudaSuccess) DoneOnce::note(slot, kernel);
-    return e;
+    done.emplace_back(dev, kernel);
 }
 
 // Host side: launch a kernel with programmatic stream serialization allowed.

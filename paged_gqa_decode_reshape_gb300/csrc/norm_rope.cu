@@ -23,6 +23,7 @@
 //  * From kRingFrom steps on: a range of steps per warp (the ring, below).
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.h"
 #include "step.h"
 #include "tcgen05.cuh"
 
@@ -497,11 +498,11 @@ cudaError_t launch_t(const RopeArgs &a, int sms, cudaStream_t stream) {
     if (a.T * steps >= kRingFrom) {
         const auto kernel = norm_rope_ring_kernel<D, INTER, CACHE>;
         const cudaError_t e = smem_once(reinterpret_cast<const void *>(kernel), RingCfg::SMEM);
-        return e != cudaSuccess ? e : launch_pdl(kernel, dim3(sms), dim3(kRingWarps * 32), RingCfg::SMEM, stream, a);
+        return e != cudaSuccess ? e : launch_soon(kernel, dim3(sms), dim3(kRingWarps * 32), RingCfg::SMEM, stream, 1, a);
     }
     const int64_t warps = a.T * (steps + (CACHE == kRopeE4m3 ? 2 * a.Hkv : 0));
-    return launch_pdl(norm_rope_kernel<D, INTER, CACHE>, dim3(unsigned((warps + kRopeWarps - 1) / kRopeWarps)), dim3(kRopeWarps * 32),
-                      0, stream, a);
+    return launch_soon(norm_rope_kernel<D, INTER, CACHE>, dim3(unsigned((warps + kRopeWarps - 1) / kRopeWarps)), dim3(kRopeWarps * 32),
+                      0, stream, 1, a);
 }
 
 template <int D, bool INTER>

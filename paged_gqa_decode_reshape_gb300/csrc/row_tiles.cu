@@ -62,6 +62,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.h"
 #include "subset.h"
 #include "tcgen05.cuh"
 
@@ -1463,11 +1464,11 @@ cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const CUtenso
     const auto kernel = row_tiles_kernel<D, PREFIX, KIND>;
     const cudaError_t e = smem_once(reinterpret_cast<const void *>(kernel), RowCfg<D>::SMEM);
     if (e != cudaSuccess) return e;
-    const cudaError_t f = launch_pdl(kernel, dim3(grid), dim3(kRowWarps<KIND> * 32), RowCfg<D>::SMEM, stream, tk, tv, tq, a);
+    const cudaError_t f = launch_soon(kernel, dim3(grid), dim3(kRowWarps<KIND> * 32), RowCfg<D>::SMEM, stream, 1, tk, tv, tq, a);
     if (PREFIX || f != cudaSuccess || !a.cuts) return f;
     // 32 rows per slice, by the average unit
     const int rows = std::min(2 * (kTileTok / a.G), (a.rows + a.nseq - 1) / a.nseq) * a.G;
-    return launch_pdl(cut_join_kernel<D, KIND>, dim3(grid, (rows + 31) / 32), dim3(256), 0, stream, a);
+    return launch_soon(cut_join_kernel<D, KIND>, dim3(grid, (rows + 31) / 32), dim3(256), 0, stream, 1, a);
 }
 
 }  // namespace

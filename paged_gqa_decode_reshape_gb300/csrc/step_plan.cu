@@ -14,6 +14,7 @@
 // rejected tokens of 128 sequences 4.8 us, 81000 blocks of 512 sequences 8.6.
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.h"
 #include "step.h"
 #include "subset.h"
 
@@ -313,10 +314,10 @@ cudaError_t launch_plan(const PlanArgs &a, cudaStream_t stream) {
     const bool rows_too = a.T <= kRowsHere;
     const size_t smem = (4 * size_t(a.B) + 1) * 4;
     cudaError_t e = smem_once(reinterpret_cast<const void *>(plan_kernel), (4 * size_t(kMaxBatch) + 1) * 4);
-    if (e == cudaSuccess) e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), smem, stream, a, rows_too);
+    if (e == cudaSuccess) e = launch_soon(plan_kernel, dim3(1), dim3(kPlanThreads), smem, stream, 1, a, rows_too);
     if (e != cudaSuccess || rows_too) return e;
     const int grid = (a.T + kRowThreads - 1) / kRowThreads;
-    return launch_pdl(plan_rows_kernel, dim3(unsigned(grid)), dim3(kRowThreads), 0, stream, a);
+    return launch_soon(plan_rows_kernel, dim3(unsigned(grid)), dim3(kRowThreads), 0, stream, 1, a);
 }
 
 // A warp per sequence: one CTA has 32.
@@ -326,21 +327,8 @@ constexpr unsigned kReleaseCtas = 8;
 cudaError_t launch_release(const ReleaseArgs &a, cudaStream_t stream) {
     const cudaError_t e = smem_once(reinterpret_cast<const void *>(release_kernel), 12 * size_t(kMaxBatch) + 8);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
     const unsigned ctas = a.B <= kOneCtaSequences ? 1 : kReleaseCtas;
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kPlanThreads);
-    cfg.dynamicSmemBytes = 12 * size_t(a.B) + 8;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ctas;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, release_kernel, a);
+    return launch_soon(release_kernel, dim3(ctas), dim3(kPlanThreads), 12 * size_t(a.B) + 8, stream, ctas, a);
 }
 
 }  // namespace pa

@@ -47,6 +47,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.h"
 #include "subset.h"
 #include "tcgen05.cuh"
 
@@ -961,7 +962,7 @@ cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const SubsetA
     const auto kernel = stream_decode_kernel<D, KIND, MODE>;
     const cudaError_t e = smem_once(reinterpret_cast<const void *>(kernel), C::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3(grid), dim3(C::THREADS), C::SMEM, stream, tk, tv, a);
+    return launch_soon(kernel, dim3(grid), dim3(C::THREADS), C::SMEM, stream, 1, tk, tv, a);
 }
 
 }  // namespace
@@ -1036,8 +1037,8 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const SubsetArgs a) {
 
 cudaError_t launch_prefix_join(const SubsetArgs &a, int head_dim, cudaStream_t stream) {
     const dim3 grid(unsigned((int64_t(a.rows) * a.Hq + 7) / 8));
-    return head_dim == 128 ? launch_pdl(prefix_join_kernel<128>, grid, dim3(256), 0, stream, a)
-                           : launch_pdl(prefix_join_kernel<64>, grid, dim3(256), 0, stream, a);
+    return head_dim == 128 ? launch_soon(prefix_join_kernel<128>, grid, dim3(256), 0, stream, 1, a)
+                           : launch_soon(prefix_join_kernel<64>, grid, dim3(256), 0, stream, 1, a);
 }
 
 cudaError_t launch_stream_decode(const CUtensorMap &tk, const CUtensorMap &tv, const SubsetArgs &a, int head_dim,
@@ -1050,7 +1051,7 @@ cudaError_t launch_stream_decode(const CUtensorMap &tk, const CUtensorMap &tv, c
         if (e != cudaSuccess || f.fused_add) return e;
         const int per = kAddThreads / (kBlockSize / 4);  // blocks a CTA takes per turn
         const int x = (a.MBS + per - 1) / per;
-        return launch_pdl(weights_add_kernel, dim3(a.nseq * a.Hkv, x < 16 ? x : 16), dim3(kAddThreads), 0, stream, a);
+        return launch_soon(weights_add_kernel, dim3(a.nseq * a.Hkv, x < 16 ? x : 16), dim3(kAddThreads), 0, stream, 1, a);
     }
     if (a.cu_q) {
         SubsetArgs f = a;

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace pa {
 
 constexpr int kMaxWindowRows = 1 << 20;  // query rows of a windowed multi-token call
@@ -54,6 +56,46 @@ struct SubsetArgs {
     int stop_item;                // failure tests: a warp's copies stop at this item (else INT_MAX)
     int min_items;                // row tiles: tiles of a CTA's range at least
 };
+
+// What was done per (device, kernel). Allocates nothing and throws nothing: it runs below C entry points. Beyond
+// its devices and kernels nothing is noted, and the caller does it again.
+struct DoneOnce {
+    static constexpr int kDevices = 64, kKernels = 128;
+    std::atomic<const void *> at[kDevices][kKernels];
+
+    // the slot that holds the kernel, or the free one to note it in (else null)
+    std::atomic<const void *> *find(int dev, const void *kernel, bool &done) noexcept {
+        done = false;
+        if (dev < 0 || dev >= kDevices) return nullptr;
+        const unsigned h = unsigned(reinterpret_cast<uintptr_t>(kernel) >> 4) * 2654435761u >> 25;
+        for (unsigned i = 0; i < kKernels; ++i) {
+            std::atomic<const void *> &s = at[dev][(h + i) % kKernels];
+            const void *k = s.load(std::memory_order_acquire);
+            done = k == kernel;
+            if (done || !k) return &s;
+        }
+        return nullptr;
+    }
+    // a slot that another thread took first is left to it: the kernel is noted at its next call
+    static void note(std::atomic<const void *> *slot, const void *kernel) noexcept {
+        const void *none = nullptr;
+        if (slot) slot->compare_exchange_strong(none, kernel, std::memory_order_acq_rel);
+    }
+};
+
+// A kernel's limit of dynamic shared memory, set once per device.
+inline cudaError_t smem_once(const void *kernel, size_t bytes) noexcept {
+    static DoneOnce once;
+    int dev = 0;
+    bool done;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::atomic<const void *> *slot = once.find(dev, kernel, done);
+    if (done) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    if (e == cudaSuccess) DoneOnce::note(slot, kernel);
+    return e;
+}
 
 // one query row per sequence, window and sinks, or (weights set) the dense
 // decode that adds up the attention weights, or (pt set) prefix and own tokens,
