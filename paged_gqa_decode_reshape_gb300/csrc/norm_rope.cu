@@ -11,7 +11,7 @@
 // code of the value over its head's scale.
 //
 // Bound by HBM: a head is read and written once, 8 D flops for 4 D bytes. Measured (28 / 4 heads of 128): 8191 tokens
-// (156 MB) 28.7 us = 5.4 TB/s, 80 % of the measured copy rate; one token 1.8 us, 128 tokens over the 8-bit cache 3.0:
+// (156 MB) 28.0 us = 5.6 TB/s, 82 % of the measured copy rate; one token 1.8 us, 128 tokens over the 8-bit cache 3.0:
 // a launch and two dependent reads (position, angles).
 //
 //  * D / 16 lanes per head, each with two chunks of 8 dims whose rotation stays
@@ -20,7 +20,7 @@
 //  * A step is 4 (D = 64: 8) heads of a token, 1 KB, all queries, keys or values. Weights and
 //    angles meet once per token and kind: x' = (x A + y B) f with A = w cos, B = -w sin.
 //  * Small calls: a warp per step, its loads issued before the token's position is known.
-//  * From kRingFrom steps on: a range of steps per warp (the ring, below).
+//  * Many tokens: a range of steps per warp (the ring, below).
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.h"
@@ -92,6 +92,7 @@ __device__ __forceinline__ void write_v8(const RopeArgs &a, int64_t t, int64_t s
 
 // V of the rows t .. t + 31 for a half of KV head h's dims, by a warp: rows whose slots follow each other in a block go together, by the
 // first of them (n_rows 1: of row t, if it is such a first one). A run may go on behind the 32.
+template <int LONE>
 __device__ __forceinline__ void write_v8_runs(const RopeArgs &a, int64_t t, int n_rows, int h, int half) {
     constexpr int BS = kBlockSize;
     const int lane = threadIdx.x & 31;
@@ -109,10 +110,38 @@ __device__ __forceinline__ void write_v8_runs(const RopeArgs &a, int64_t t, int 
     const uint32_t on0 = __ballot_sync(0xffffffffu, s0 >= 0 && s0 % BS > 0 && prev == s0 - 1);
     const uint32_t on1 = __ballot_sync(0xffffffffu, s1 >= 0 && s1 % BS > 0 && up == s1 - 1);
     const uint64_t on = on0 | uint64_t(on1 >> 1) << 32;
-    for (uint32_t first = __ballot_sync(0xffffffffu, s0 >= 0 && lane < n_rows) & ~on0; first; first &= first - 1) {
+    uint32_t first = __ballot_sync(0xffffffffu, s0 >= 0 && lane < n_rows) & ~on0, lone = first & ~uint32_t(on >> 1);
+    for (first &= ~lone; first; first &= first - 1) {
         const int l = __ffs(first) - 1;
         const int n = __ffsll(int64_t(~(on >> (l + 1))));
         write_v8(a, t + l, __shfl_sync(0xffffffffu, s0, l), n, h, half);
+    }
+    // rows that are alone in their run: LONE of them on their way at once
+    const int d = half * 64 + 2 * lane;
+    const float scale = __ldg(a.v_scale + h);
+#pragma unroll 1
+    while (lone) {
+        uint32_t x[LONE];
+        const uint32_t these = lone;
+#pragma unroll
+        for (int i = 0; i < LONE; ++i) {
+            const int l = __ffs(lone) - 1;
+            x[i] = lone ? __ldg(reinterpret_cast<const uint32_t *>(a.v + (t + l) * a.vs + h * 128 + d)) : 0u;
+            lone &= lone - 1;
+        }
+        uint32_t rest = these;
+#pragma unroll
+        for (int i = 0; i < LONE; ++i) {
+            if (!rest) break;
+            const int64_t slot = __shfl_sync(0xffffffffu, s0, __ffs(rest) - 1);
+            const int o = int(slot % BS);
+            uint8_t *dst = static_cast<uint8_t *>(a.vc) + (slot / BS * a.Hkv + h) * int64_t(128 * BS) + d * BS +
+                           4 * ((o & 7) >> 1) + 2 * (o >> 3) + (o & 1);
+            const uint32_t code = encode2(bf16_lo(x[i]), bf16_hi(x[i]), scale);
+            dst[0] = uint8_t(code & 0xffu);
+            dst[BS] = uint8_t(code >> 8);
+            rest &= rest - 1;
+        }
     }
 }
 
@@ -146,19 +175,27 @@ struct Steps {
     __device__ __forceinline__ int within(int step) const { return step < q ? step : step < qk ? step - q : step - qk; }
 };
 
+// The norm's weights of a lane's chunks: ones without a norm.
+struct Weights {
+    uint4 w0, w1;
+    template <int D, bool INTER>
+    __device__ __forceinline__ Weights(const uint16_t *w, const Lane<D, INTER> &me) {
+        w0 = w1 = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+        if (w) {
+            w0 = __ldg(reinterpret_cast<const uint4 *>(w) + me.c0);
+            w1 = __ldg(reinterpret_cast<const uint4 *>(w) + me.c1);
+        }
+    }
+};
+
 // Weights and angles of a lane's dims: x' = x A + u B and y' = y C + z E, with x of chunk c0, y of chunk c1, u = y and z = x
 // (INTER: the other of the pair). Each product of a weight and a cosine or sine is rounded once more in fp32.
 struct Turn {
     float2 A[4], B[4], C[4], E[4];
     template <int D, bool INTER>
-    __device__ __forceinline__ void set(const uint16_t *w, const Lane<D, INTER> &me, const float (&c)[8], const float (&s)[8]) {
-        if (w) {
-            unpack8(__ldg(reinterpret_cast<const uint4 *>(w) + me.c0), A);
-            unpack8(__ldg(reinterpret_cast<const uint4 *>(w) + me.c1), C);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) A[i] = C[i] = make_float2(1.f, 1.f);
-        }
+    __device__ __forceinline__ void set(const Weights &w, const Lane<D, INTER> &me, const float (&c)[8], const float (&s)[8]) {
+        unpack8(w.w0, A);
+        unpack8(w.w1, C);
         if (!me.turns) return;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -255,7 +292,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) norm_rope_kernel(const RopeAr
     const int part = int(w - t * all);
     if (t >= a.T) return;
     if (CACHE == kRopeE4m3 && part >= steps.all) {
-        write_v8_runs(a, t, 1, (part - steps.all) >> 1, (part - steps.all) & 1);
+        write_v8_runs<1>(a, t, 1, (part - steps.all) >> 1, (part - steps.all) & 1);
         return;
     }
     const L me(a.R);
@@ -310,7 +347,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) norm_rope_kernel(const RopeAr
                 cs[i] = me.turns ? __ldg(from) : 0.f, sn[i] = me.turns ? __ldg(from + half) : 0.f;
             }
         }
-        turn.set(kind == 0 ? a.qw : a.kw, me, cs, sn);
+        turn.set(Weights(kind == 0 ? a.qw : a.kw, me), me, cs, sn);
     }
     finish_step<D, INTER, CACHE>(a, t, kind, at, slot, me, turn, r0, r1);
 }
@@ -319,13 +356,15 @@ __global__ void __launch_bounds__(kRopeWarps * 32) norm_rope_kernel(const RopeAr
 //
 // The heads come by asynchronous copies that hold no registers, 8 KB per warp and 128 KB per SM in flight, angles and
 // slot of a token beside the first of its steps, its position a token ahead. The 8-bit V is for warps of its own. What is left
-// is issue: two thirds of the slots (8191 tokens 28.7 us; 12 warps 30.8, 20 warps of 6 stages, whose registers spill, 35.4;
-// three steps per warp, each loading its own to registers, 33.4). Ring and a warp per step, 28 / 4 heads of 128: 300 tokens 3.4
-// and 3.0 us, 400 3.5 and 3.4, 500 3.6 and 4.2, 1000 4.9 and 6.5; 8-bit 400 5.5 and 4.9, 500 5.4 and 5.6, 1000 6.1 and 9.2.
+// is issue: two thirds of the slots (8191 tokens 28.0 us; the weights read again at every token 28.7, with that 12 warps 30.8,
+// 20 warps of 6 stages, whose registers spill, 35.4; three steps per warp, each loading its own to registers, 33.4).
 constexpr int kRingWarps = 16, kRingStages = 8;
 // E4M3: warps of a CTA for V, beside the others (one after the other in every warp: 8191 tokens 38.2 us)
 constexpr int kRingV8Warps = 4;
-constexpr int64_t kRingFrom = 4096;
+// Warps of the small form from which on the ring takes over. Ring and small, 28 / 4 heads of 128: 300 tokens 3.3 and 3.0 us,
+// 400 3.5 and 3.4, 500 3.5 and 4.2, 1000 4.7 and 6.5; 8-bit 400 5.5 and 4.9, 600 5.0 and 6.3, 1000 6.1 and 9.5, 1000 of as many
+// sequences 6.5 and 9.8.
+constexpr int64_t kRingFrom = 4096, kRingFromE4m3 = 8192;
 
 struct RingCfg {
     static constexpr int STEP = 1024;              // bytes of a step's heads
@@ -364,7 +403,7 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) norm_rope_ring_kernel(cons
 #pragma unroll 1
         for (int64_t u = int64_t(blockIdx.x) * VW + warp - RW; u < n; u += int64_t(gridDim.x) * VW) {
             const int part = int(u % (2 * a.Hkv));
-            write_v8_runs(a, u / (2 * a.Hkv) * 16, 16, part >> 1, part & 1);
+            write_v8_runs<8>(a, u / (2 * a.Hkv) * 16, 16, part >> 1, part & 1);
         }
         return;
     }
@@ -436,6 +475,7 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) norm_rope_ring_kernel(cons
     copy_commit();
 #pragma unroll 1
     for (int s = 1; s < kRingStages; ++s) copy_commit();
+    const Weights wq(a.qw, me), wk(a.kw, me);
     Turn turn;
     bool known = false;  // turn is of this token and kind
     int64_t slot = -1;
@@ -463,7 +503,7 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) norm_rope_ring_kernel(cons
                         sn[e] = y.x, sn[e + 1] = y.y, sn[e + 2] = y.z, sn[e + 3] = y.w;
                     }
                 }
-                turn.set(kind == 0 ? a.qw : a.kw, me, cs, sn);
+                turn.set(kind == 0 ? wq : wk, me, cs, sn);
             }
             known = true;
         }
@@ -494,15 +534,14 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) norm_rope_ring_kernel(cons
 
 template <int D, bool INTER, RopeCache CACHE>
 cudaError_t launch_t(const RopeArgs &a, int sms, cudaStream_t stream) {
-    const int steps = Steps::of<Lane<D, INTER>::HPS, CACHE>(a.Hq, a.Hkv).all;
-    if (a.T * steps >= kRingFrom) {
+    const int64_t warps = a.T * (Steps::of<Lane<D, INTER>::HPS, CACHE>(a.Hq, a.Hkv).all + (CACHE == kRopeE4m3 ? 2 * a.Hkv : 0));
+    if (warps >= (CACHE == kRopeE4m3 ? kRingFromE4m3 : kRingFrom)) {
         const auto kernel = norm_rope_ring_kernel<D, INTER, CACHE>;
         const cudaError_t e = smem_once(reinterpret_cast<const void *>(kernel), RingCfg::SMEM);
         return e != cudaSuccess ? e : launch_soon(kernel, dim3(sms), dim3(kRingWarps * 32), RingCfg::SMEM, stream, 1, a);
     }
-    const int64_t warps = a.T * (steps + (CACHE == kRopeE4m3 ? 2 * a.Hkv : 0));
     return launch_soon(norm_rope_kernel<D, INTER, CACHE>, dim3(unsigned((warps + kRopeWarps - 1) / kRopeWarps)), dim3(kRopeWarps * 32),
-                      0, stream, 1, a);
+                       0, stream, 1, a);
 }
 
 template <int D, bool INTER>

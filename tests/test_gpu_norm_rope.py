@@ -164,6 +164,8 @@ def test_many_tokens(heads, T):
     for A, interleaved in ((1, False), (3, True), (4, False), (1, True)):
         test_norm_rope(heads, T, A, True, interleaved)
     test_cache(heads, T, True)
+    if heads[2] == 128:
+        test_cache_fp8(heads[:2], T)
 
 
 @pytest.mark.parametrize("T", [300, 1500])
