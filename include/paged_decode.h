@@ -859,7 +859,8 @@ PA_API int pa_release_blocks(const int32_t *block_tables, int max_blocks_per_seq
  * fp32. p = positions[token], or with num_axes > 1 (time, height, width of
  * images and video) positions[axes[i]][token]: positions [num_axes][num_tokens],
  * axes [R / 2] int32. Positions outside the table and axes outside
- * [0, num_axes) are clamped. Everything in fp32, rounded once to bf16.
+ * [0, num_axes) are clamped. Everything in fp32, rounded once to bf16 (squares
+ * too: a normed head with values from about 1e18 on becomes zeros).
  * Row strides (in elements, from one token to the next) may be larger than a
  * row's heads, so q, k and v may be parts of one projection's output; q_out and
  * k_out may be query and key themselves (with the same strides), else no output

@@ -221,6 +221,27 @@ def test_whole_prompt(T, window, sinks, per_block):
     check_rows(out, q, k64, v64, bt, cu, [T], [T], window, sinks, D ** -0.5, 173)
 
 
+@pytest.mark.parametrize("share", [False, True])
+@pytest.mark.parametrize("per_block", [False, True])
+def test_padded_batch(per_block, share):
+    """Sequences without rows, first, last and in long runs between; with lengths of their own and without."""
+    Hq, Hkv = 28, 4
+    ctx = [0, 300, 50, 0, 700] + [33, 0] * 150 + [129, 16, 0]
+    ql = [0, 9, 0, 0, 40] + [0, 0] * 150 + [5, 0, 0]
+    if share:  # rows first: the call's rule counts the sequences, too
+        n = filler(sum(ql), len(ql), Hkv, 1 << 30, 0)
+        ctx, ql = [n] + ctx, [n] + ql
+    g, kc, vc, bt, _, _ = pool(19, ctx, Hkv, D)
+    k8, v8, ks, vs, k64, v64 = codes(kc, vc, per_block, Hkv)
+    cu = offsets(ql)
+    q = bf16(g, sum(ql) + 3, Hq, D, std=2.0)
+    out = torch.full((len(q), Hq, D), 7.0, dtype=torch.bfloat16, device=DEV)
+    call(per_block, out, *dev(q, k8, v8, ks, vs, wide(bt) if share else bt, cu, torch.tensor(ctx, dtype=torch.int32)),
+         1 << 30, 0, D ** -0.5)
+    assert (out[-3:] == 7.0).all()
+    check_rows(out, q, k64, v64, bt, cu, ctx, ql, 1 << 30, 0, D ** -0.5)
+
+
 @pytest.mark.parametrize("scale,std", [(0.0884, 12.0), (3.0, 4.0)])
 @pytest.mark.parametrize("share", [False, True])
 def test_sharp_and_growing_logits(scale, std, share):
