@@ -25,6 +25,15 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanPer = kMaxBatch / kPlanThreads;  // sequences of a thread at most
 constexpr int kFewBlocks = 4;                       // new blocks of a sequence that its thread writes itself
 
+// A value that the same call may write in its place (context_lens by new_lens, *num_free by *new_free), read exactly
+// once and here: a read-only load (__ldg) may only be of what nobody writes while the kernel runs, and the compiler
+// may move or repeat it behind the write.
+__device__ __forceinline__ int32_t load_once(const int32_t *p) {
+    int32_t v;
+    asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
 // Inclusive prefix sums of two values over the CTA's 1024 threads, the sums of all in `u` and `v`.
 struct Pair {
     int64_t u, v;
@@ -112,7 +121,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, bo
     __shared__ int most;
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, lim = a.MBS * kBlockSize;
-    const int nf = int(min(max(int64_t(__ldg(a.num_free)), int64_t(0)), a.F));
+    const int nf = int(min(max(int64_t(load_once(a.num_free)), int64_t(0)), a.F));
     const int per = (a.B + kPlanThreads - 1) / kPlanThreads, b0 = tid * per;
     int c[kPlanPer], q[kPlanPer], need[kPlanPer];
     bool fits[kPlanPer];
@@ -120,7 +129,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, bo
 #pragma unroll
     for (int i = 0; i < kPlanPer; ++i) {
         const bool in = i < per && b0 + i < a.B;
-        c[i] = in ? min(max(__ldg(a.ctx + b0 + i), 0), lim) : 0;
+        c[i] = in ? min(max(load_once(a.ctx + b0 + i), 0), lim) : 0;
         q[i] = in ? max(__ldg(a.q + b0 + i), 0) : 0;
         fits[i] = int64_t(c[i]) + q[i] <= lim;
         need[i] = fits[i] ? (c[i] + q[i] + kBlockSize - 1) / kBlockSize - (c[i] + kBlockSize - 1) / kBlockSize : 0;
@@ -217,14 +226,14 @@ __global__ void __launch_bounds__(kPlanThreads) release_kernel(const ReleaseArgs
     const int rank = int(cluster_rank()), ctas = int(cluster_size());
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, lim = a.MBS * kBlockSize;
-    const int nf = int(min(max(int64_t(__ldg(a.num_free)), int64_t(0)), a.F));
+    const int nf = int(min(max(int64_t(load_once(a.num_free)), int64_t(0)), a.F));
     const int per = (a.B + kPlanThreads - 1) / kPlanThreads, b0 = tid * per;
     int c[kPlanPer], k[kPlanPer];
     Pair sum = {0, 0}, all;
 #pragma unroll
     for (int i = 0; i < kPlanPer; ++i) {
         const bool in = i < per && b0 + i < a.B;
-        c[i] = in ? min(max(__ldg(a.ctx + b0 + i), 0), lim) : 0;
+        c[i] = in ? min(max(load_once(a.ctx + b0 + i), 0), lim) : 0;
         k[i] = in ? min(max(__ldg(a.keep + b0 + i), 0), c[i]) : 0;
         sum.u += (c[i] + kBlockSize - 1) / kBlockSize - (k[i] + kBlockSize - 1) / kBlockSize;
     }
