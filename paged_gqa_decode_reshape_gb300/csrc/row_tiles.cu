@@ -965,8 +965,10 @@ __global__ void __launch_bounds__(kRowWarps<KIND> * 32, 1)
                 float scale_log2 = a.scale_log2;
                 if constexpr (F8) {
                     const int64_t from = act && lim > 0 ? (int64_t(x.r0 + ir) * a.Hq + x.kvh * G + h) * D : -1;
-                    scale_log2 *= split_queries(a.q, from, queries, C::HALF, lane);
                     if (!PSC) scale_log2 *= __ldg(a.k_scale + x.kvh);
+                    scale_log2 *= split_queries(a.q, from, queries, C::HALF, lane);
+                    // scales and queries too small for fp32: logits of 0 either way, but a masked one is -inf times this
+                    if (scale_log2 == 0.f) scale_log2 = __uint_as_float(1u);
                     fence_proxy_async();
                     mbar_arrive(q_full + 8 * w);
                 }
