@@ -714,8 +714,11 @@ PA_API int pa_decode_window_multi(pa_bf16 *out, const pa_bf16 *query, const pa_b
  * Queries: small calls round them to f16 (values from 65520 on become infinite,
  * those below 2^-14 lose bits); calls whose rows share their reads take each
  * head row as two E4M3 parts and a power of two, exact for values of at least
- * 2^-10 of the row's largest, the others off by at most 2^-18 of it, and a row
- * with an element that is not finite gets NaN. */
+ * 2^-9 of the row's largest, the others off by at most 2^-17 of it (a largest
+ * below 2^-112 counts as 2^-112), and a row with an element that is not finite
+ * gets NaN. The weights are rounded to f16 (small calls) or bf16 (shared reads)
+ * before they meet V. Which of the two serves a call goes by its rows, its
+ * sequences, and the width of its tables or the window. */
 PA_API int pa_decode_window_multi_fp8(pa_bf16 *out, const pa_bf16 *query, const pa_e4m3 *key_cache,
                                       const pa_e4m3 *value_cache, const float *k_scale, const float *v_scale,
                                       const int32_t *block_tables, int max_blocks_per_seq,

@@ -366,8 +366,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool a
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // A warp's 32 query rows of 128 bf16 values, for products with E4M3 codes: x = 2^k (hi + lo), hi the nearest E4M3 value of
-// x / 2^k (the row's largest is in [128, 256)) and lo that of what is left. The eight bits of a bf16 value are four and four:
-// exact for values of at least 2^-10 of the row's largest, the others are off by at most 2^-18 of it. Lane r has the offset of
+// x / 2^k (the row's largest is in [128, 256)) and lo that of what is left. The eight bits of a bf16 value are four and four,
+// but for what is below lo's smallest step, 2^-9: from 2^-2 on, 2^-9 of the row's largest, values are exact, the others off
+// by at most 2^-10, 2^-17 of it (k stays above -120: a largest below 2^-112 counts as 2^-112). Lane r has the offset of
 // row r in q, < 0: a row of zeros. Written to rows 0 .. 31 at `to` (hi) and `to` + next (lo), 128 bytes each, 16-byte chunks
 // swizzled by the row; returns 2^k of the lane's row (1 for a row of zeros; NaN for one that is not finite).
 // The rows first come to where their parts go, then eight lanes convert a row. Code that runs once per unit has to be fetched
