@@ -1032,7 +1032,10 @@ bool reads_each(const SubsetArgs &a, int D) {
 // and row tiles, 28 / 4 heads: one sequence of 8 rows on 16000 tokens 26 and 37 us, of 16 rows 45 and 38; 4 of 4 rows on 16000 45 and
 // 48, of 6 rows 79 and 47; 32 of 4 rows on 500 20 and 18, of 8 rows 29 and 18, of 3 rows on 4000 63 and 71 (of 1 to 6 rows, the
 // cache not in L2, 49 and 82), of 6 rows 111 and 74, of 2 rows on 16000 142 and 201, of 3 rows 237 and 201 (each by this
-// rule), of 4 rows 289 and 202; 128 of 2 rows on 4000 166 and 229, of 4 rows 314 and 232.
+// rule), of 4 rows 289 and 202; 128 of 2 rows on 4000 166 and 229, of 4 rows 314 and 232. (Row tiles get quicker per token with
+// length, 0.9e-4 on 16000 tokens: the rule leans to each row by itself.) By averages, as the lengths are not known here: a chunk of
+// 512 rows behind 16000 tokens beside 256 sequences of one row goes row by row, 1133 us; in calls of their own 98 and 119. Sequences
+// of one row on 400 tokens, each by itself, as the rows grow past the table of segments: 500 46 us, 1000 81, 4000 326.
 constexpr int64_t kEachReadsMany = int64_t(56) << 20;
 
 bool rows_each(const SubsetArgs &a, int D, CacheKind kind, int sms) {

@@ -359,7 +359,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32) norm_rope_kernel(const RopeAr
 // is issue: two thirds of the slots (8191 tokens 28.0 us; the weights read again at every token 28.7, with that 12 warps 30.8,
 // 20 warps of 6 stages, whose registers spill, 35.4; three steps per warp, each loading its own to registers, 33.4).
 constexpr int kRingWarps = 16, kRingStages = 8;
-// E4M3: warps of a CTA for V, beside the others (one after the other in every warp: 8191 tokens 38.2 us)
+// E4M3: warps of a CTA for V, beside the others: 8191 tokens (148 MB) 33.4 us = 4.4 TB/s, 65 % of the measured copy rate (one
+// after the other in every warp 38.2)
 constexpr int kRingV8Warps = 4;
 // Warps of the small form from which on the ring takes over. Ring and small, 28 / 4 heads of 128: 300 tokens 3.3 and 3.0 us,
 // 400 3.5 and 3.4, 500 3.5 and 4.2, 1000 4.7 and 6.5; 8-bit 400 5.5 and 4.9, 600 5.0 and 6.3, 1000 6.1 and 9.5, 1000 of as many

@@ -51,7 +51,8 @@
 //    the way: two warps copy blocks of codes into a ring, eight convert them and lay them down dim by token, as the
 //    cache has them, with the contraction over tokens contiguous. A scale per KV head goes to the logits and the output; a
 //    scale per block to the block's 16 logits and, in the conversion, to its V. Chunks of 517 to 2048 rows behind 9000 to
-//    16000 tokens 625 us = 1.28 PFLOP/s, the rate of the bf16 cache. On the way there: K and V converted, by loads to
+//    16000 tokens 625 us = 1.28 PFLOP/s, the rate of the bf16 cache; with scales per block 810, as every logit meets its
+//    block's before the maximum. (96 registers: 280 and 268 bytes spilled, bf16 228 of 168 registers.) On the way there: K and V converted, by loads to
 //    registers 1615 us (a loop unrolled over a half step runs out of instruction cache at 7 cycles an instruction), by
 //    asynchronous copies and rolled loops 790; V alone converted, one warp issuing its copies (330 cycles each) 830.
 //  * Units cut between CTAs leave (O, m, l) per row and piece in the workspace;
@@ -373,7 +374,7 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 // swizzled by the row; returns 2^k of the lane's row (1 for a row of zeros; NaN for one that is not finite).
 // The rows first come to where their parts go, then eight lanes convert a row. Code that runs once per unit has to be fetched
 // first: with a lane per row, unrolled over its registers, 13300 cycles at a CTA's begin instead of 8800. A function of its own:
-// within the kernel it changed how the softmax around it was compiled (long prompt chunks 622 us, inlined 685).
+// within the kernel it changed how the softmax around it was compiled (long prompt chunks 625 us, inlined 63 more).
 __device__ __noinline__ float split_queries(const uint16_t *q, int64_t offset, uint32_t to, uint32_t next, int lane) {
 #pragma unroll 1
     for (int i = 0; i < 16; ++i) {  // chunk 16 (2 i + lane / 16) + lane % 16
